@@ -24,6 +24,14 @@
  *   lrmoe_backward_bytes,  host-only: the device bytes a backward holds, and quota
  *   lrmoe_plan_quotas      admission on one GPU (Algorithm 1's admission, section 3.3)
  *
+ * Around the experts (the router that feeds them, and the update that follows the backward):
+ *
+ *   lrmoe_route            logits -> experts, routing weights, expert-major pair lists
+ *   lrmoe_balance_loss     per-expert counts and the balance loss of every sequence
+ *   lrmoe_alpha_grad       gradient of the routing weights from the saved output rows
+ *   lrmoe_route_bwd        gradient of the logits: routing weights and balance loss
+ *   lrmoe_adamw            AdamW step over many tensors, states in 32 or 8 bits
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  * - Pairs are stored expert-major: expert e owns pair rows [seg_off[e], seg_off[e+1]).
@@ -353,6 +361,151 @@ lrmoe_status lrmoe_expert_forward(const lrmoe_problem* p, const int64_t* seg_off
 lrmoe_status lrmoe_scatter(const lrmoe_problem* p, lrmoe_scatter_mode mode, int64_t n_rows, int32_t width,
                            int32_t rows_dtype, const void* rows, const int32_t* ctok, const int32_t* cslot,
                            const int32_t* pmap, float* out, void* ws, size_t ws_bytes, lrmoe_stream_t stream);
+
+/* ---------------------------------------------------------------- the router
+ *
+ * lrmoe_router describes the router of one layer: T tokens, E experts of the whole layer (all
+ * GPUs), K slots per token, and the experts [first, first + local) that this GPU's pair lists
+ * cover. Logits are [T x E] of `dtype` (f32 or bf16), and are read by these rules everywhere:
+ * a NaN counts as -inf, +inf as the largest finite f32. mask [T] uint8 (NULL: all ones) leaves
+ * the tokens with a zero out. A token is live if it is not masked and has a logit over -inf.
+ * T * K must be under 2^31, E at most 1024, K at most min(E, 32). */
+typedef struct lrmoe_router {
+  int32_t T;        /* tokens                                                        */
+  int32_t E;        /* experts of the layer                                          */
+  int32_t K;        /* routing slots per token                                       */
+  int32_t first;    /* first expert of this GPU's pair lists                         */
+  int32_t local;    /* how many experts the pair lists cover                         */
+  int32_t dtype;    /* lrmoe_dtype of the logits and of their gradient               */
+  int32_t renorm;   /* 1: a token's weights sum to scale; 0: scale * softmax over E  */
+  int32_t reserved; /* must be 0                                                     */
+  float scale;      /* factor of the routing weights                                 */
+} lrmoe_router;
+
+/* Host-only. Bytes of scratch that lrmoe_route and lrmoe_balance_loss (with n_seq sequences)
+ * need; calls in order on one stream may share one buffer. */
+lrmoe_status lrmoe_router_workspace_size(const lrmoe_router* r, int32_t n_seq, size_t* bytes);
+
+/* Top-K routing. For every live token t: idx[t, 0..K) = the experts of its K largest logits over
+ * -inf, in decreasing order, among equal ones the lower index first; -1 in slots without one.
+ *   w[t, k] = scale * exp(x_k - max) / Z      f32, Z = the sum of exp(x - max) over all experts,
+ *                                             or over the token's chosen ones (renorm)
+ * and 0 in empty slots. counts [E] int32: tokens per expert over the whole layer.
+ * Pair lists of the local experts in the order every other call uses: expert-major, by token
+ * inside an expert. seg_off [local + 1] int64 (device; its host copy goes into lrmoe_problem),
+ * tok, slot [T*K] int32, alpha [T*K] f32 = w of the pair; rows at and after seg_off[local] are
+ * left as they were. pmap [T x K] int32: the pair row of (t, k), -1 where there is none or its
+ * expert is not local. All outputs are required. Deterministic. */
+lrmoe_status lrmoe_route(const lrmoe_router* r, const void* logits, const uint8_t* mask, int32_t* idx, float* w,
+                         int32_t* counts, int64_t* seg_off, int32_t* tok, int32_t* slot, float* alpha,
+                         int32_t* pmap, void* ws, size_t ws_bytes, lrmoe_stream_t stream);
+
+/* Balance loss and per-expert counts. Sequence s holds the tokens [seq_off[s], seq_off[s+1])
+ * (seq_off_d: device int64 [n_seq + 1], not decreasing, inside [0, T]; NULL with n_seq = 1: all
+ * T tokens). Over the n_s live tokens of sequence s, with p = softmax of a token's logits:
+ *   counts[s, e] = slots idx[t, k] = e        int32 [n_seq x E]
+ *   psum[s, e]   = sum of p[t, e]             f32 [n_seq x E]
+ *   norm[s]      = coef * E / (S' K n_s^2)    f32 [n_seq], 0 where n_s = 0; S' = sequences with
+ *                                             n_s > 0
+ *   loss[0]      = sum_s norm[s] sum_e counts[s, e] psum[s, e]
+ * i.e. coef times the mean over the sequences of E * sum_e f_e P_e, with f_e the share of the
+ * slots and P_e the mean probability of expert e. idx [T x K] as lrmoe_route wrote it; an entry
+ * outside [0, E) counts nowhere. Sums of probabilities are joined in fp64. Deterministic. */
+lrmoe_status lrmoe_balance_loss(const lrmoe_router* r, const void* logits, const uint8_t* mask, const int32_t* idx,
+                                const int64_t* seq_off_d, int32_t n_seq, float coef, int32_t* counts, float* psum,
+                                float* norm, float* loss, void* ws, size_t ws_bytes, lrmoe_stream_t stream);
+
+/* Gradient of the logits, dlogits [T x E] of r->dtype, every element written (0 for tokens that
+ * are not live). Two parts, either of which may be left out:
+ * - routing weights, if dalpha is not NULL: with pmap, dalpha is [n_pairs] by pair row (as
+ *   lrmoe_alpha_grad gives it) and a slot whose pmap is outside [0, n_pairs) has gradient 0;
+ *   with pmap NULL, dalpha is [T x K] by slot and n_pairs is not used. With y = scale * dalpha:
+ *     renorm = 0: dx_e    = p_e (y_k [e = idx_k] - sum_k p_k y_k)
+ *     renorm = 1: dx_idx_k = q_k (y_k - sum_j q_j y_j), q = softmax over the token's chosen experts
+ *   With experts on several GPUs the parts of their pairs add up to the whole gradient.
+ * - balance loss, if norm is not NULL (counts, norm, seq_off_d and n_seq as in
+ *   lrmoe_balance_loss; tokens outside every sequence get none):
+ *     dx_e += gloss[0] * norm[s] * p_e (counts[s, e] - sum_e' counts[s, e'] p_e')
+ *   with gloss a device f32 (NULL: 1), the gradient of the loss value.
+ * A token's idx entries have to be different; an entry outside [0, E) is an empty slot. */
+lrmoe_status lrmoe_route_bwd(const lrmoe_router* r, const void* logits, const uint8_t* mask, const int32_t* idx,
+                             const float* dalpha, const int32_t* pmap, int64_t n_pairs, const int64_t* seq_off_d,
+                             int32_t n_seq, const int32_t* counts, const float* norm, const float* gloss,
+                             void* dlogits, lrmoe_stream_t stream);
+
+/* Gradient of the routing weights of the N pairs: the layer output is the token sum of the saved
+ * rows Y[j] = alpha[j] * u_j (lrmoe_expert_forward), so with G the output's gradient
+ *   dalpha[j] = <G[tok_j], u_j> = <G[tok_j], Y[j]> / alpha[j]      f32 [N]
+ * 0 where alpha[j] = 0 (u_j cannot be had from Y then) or keep[j] = 0 (keep [N] uint8, NULL: all
+ * kept; the selection's keep gives the gradient of the retained pairs). G [T x D], Y [N x D] of
+ * the storage dtype. pmap [T x K]: the pair row of each (token, slot) position, as lrmoe_route
+ * wrote it; each pair has one position. An entry outside [0, N) is none, and pairs without a
+ * position keep what dalpha held. Products and sums in fp64. No workspace. */
+lrmoe_status lrmoe_alpha_grad(const lrmoe_problem* p, const void* G, const void* Y, const float* alpha,
+                              const int32_t* pmap, const uint8_t* keep, float* dalpha, lrmoe_stream_t stream);
+
+/* ---------------------------------------------------------------- the weight update
+ *
+ * One tensor of a lrmoe_adamw call, n elements each. All pointers are device pointers, 16-byte
+ * aligned (the scales and 8-bit states 4-byte), of buffers that do not overlap. */
+typedef struct lrmoe_adamw_tensor {
+  void* w;          /* weights, config.w_dtype                                              */
+  float* master;    /* f32 weights (config.master = 1: w is their rounded copy), else NULL  */
+  const void* grad; /* gradient, config.grad_dtype                                          */
+  void* m;          /* first moment: f32, or e4m3 codes                                     */
+  void* v;          /* second moment: f32, or e4m3 codes of its square root                 */
+  float* m_scale;   /* 8 bits: f32 per 256 elements [ceil(n / 256)], else NULL              */
+  float* v_scale;   /* the same for v                                                       */
+  int64_t n;        /* elements, >= 0                                                       */
+  int64_t first;    /* 8 bits: counter of element 0 for the random rounding, a multiple of  */
+                    /* 256, so that shards of one tensor round as the whole would           */
+} lrmoe_adamw_tensor;
+
+typedef struct lrmoe_adamw_config {
+  int32_t w_dtype;     /* lrmoe_dtype of w                                                 */
+  int32_t grad_dtype;  /* lrmoe_dtype of grad                                              */
+  int32_t master;      /* 1: every tensor has f32 master weights                           */
+  int32_t state_bits;  /* 32 or 8                                                          */
+  double lr, beta1, beta2, eps, weight_decay;
+  double grad_scale;   /* factor of every gradient (1 / loss scale, or a clipping factor)  */
+  int64_t step;        /* number of this step, from 1                                      */
+  uint32_t seed;       /* of the random rounding of 8-bit states                           */
+  uint32_t reserved;   /* must be 0                                                        */
+} lrmoe_adamw_config;
+
+/* What changes from step to step, as the kernel takes it. */
+typedef struct lrmoe_adamw_scalars {
+  float decay;      /* 1 - lr * weight_decay     */
+  float lr;
+  float c1;         /* 1 / (1 - beta1^step)      */
+  float c2;         /* 1 / sqrt(1 - beta2^step)  */
+  float grad_scale;
+  uint32_t key;     /* mix(seed + mix(step))     */
+  uint32_t reserved[2];
+} lrmoe_adamw_scalars;
+
+/* Host-only: the scalars of a config. */
+lrmoe_status lrmoe_adamw_step_scalars(const lrmoe_adamw_config* c, lrmoe_adamw_scalars* out);
+
+/* One AdamW step over n_tensors tensors (a host array; nothing of it is read after the call):
+ *   g = grad_scale * grad;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   w = w * decay - lr * (m c1) / (sqrt(v) c2 + eps)
+ * in f32 with a rounding at each operation; w of bf16 without a master is rounded to nearest
+ * even, with a master the master takes the f32 result and w its rounded copy.
+ * 8-bit states: m and r = sqrt(v) are e4m3 codes times one power of two per 256 elements,
+ * 2^(floor(log2(0.8164966 a)) - 7) with a the block's largest finite magnitude (1 where a = 0).
+ * The update uses m and v before they are rounded. Magnitudes are rounded at random,
+ * floor(x / u + (b + 0.5) / 65536) * u with u the spacing of e4m3 at x: rounding to nearest
+ * would keep v where it is, as a step changes it by less than half a spacing. b are the low (m)
+ * and high (r) 16 bits of mix(lo + mix(key + hi * 0x9E3779B1)) with hi, lo the 32-bit halves of
+ * first + i and mix(x): x ^= x >> 16; x *= 0x9E3779B1; x ^= x >> 15; x *= 0x85EBCA77;
+ * x ^= x >> 13. A positive r is never rounded to 0 (a root of 0 beside a first moment that is
+ * not 0 would make a step of m / eps). What is not finite becomes the NaN code.
+ * scalars_d (may be NULL: computed from the config here): the scalars in device memory, read when
+ * the kernel runs, for calls captured into a graph; step, lr, weight_decay, grad_scale and seed of
+ * the config are then not used. No workspace. Several launches for more than 48 tensors. */
+lrmoe_status lrmoe_adamw(const lrmoe_adamw_tensor* tensors, int32_t n_tensors, const lrmoe_adamw_config* c,
+                         const lrmoe_adamw_scalars* scalars_d, lrmoe_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -9,8 +9,10 @@ section 3.3) are calls into ``liblrmoe.so`` (hand-written HIP for gfx950):
 
 The functions here have the C entry points' names and only marshal arguments:
 torch tensors supply device memory and the current HIP stream. ``backward`` chains
-the five calls. Nothing falls back to another implementation; if the library is
-not built, the first call raises ImportError.
+the five calls. Around the experts, ``Router`` with route, balance_loss, alpha_grad and
+route_bwd makes the pair lists and trains the router, and ``AdamW`` applies the gradients.
+Nothing falls back to another implementation; if the library is not built, the first call
+raises ImportError.
 """
 from __future__ import annotations
 
@@ -26,7 +28,7 @@ from ._lib import (BF16, COMPACT_PHYSICAL, COMPACT_ZERO_MASKED, F32, SCATTER_SLO
 
 __all__ = ["Problem", "score", "select", "select_noalloc", "compact", "compact_weighted", "grouped_gemm_bwd",
            "grouped_gemm_bwd_gathered", "expert_forward", "scatter", "backward", "backward_bytes", "plan_quotas",
-           "library", "BF16", "F32", "COMPACT_PHYSICAL", "COMPACT_ZERO_MASKED", "SCATTER_TOKEN",
+           "Router", "route", "balance_loss", "route_bwd", "alpha_grad", "AdamW", "library", "BF16", "F32", "COMPACT_PHYSICAL", "COMPACT_ZERO_MASKED", "SCATTER_TOKEN",
            "SCATTER_SLOT", "SCATTER_TOKEN_BESIDE", "LrmoeError", "InfeasibleQuotaError"]
 
 
@@ -417,3 +419,302 @@ def backward(p: Problem, *, G, Phi, alpha, tok, slot, W2, X=None, H=None, W1=Non
                       pmap=pmap, stream=main)
     b.setdefault("out", out)
     return {"R": b["R"], "sel": sel, "keep": keep, **c, **g, "out": out}
+
+
+class Router:
+    """The router of one layer: T tokens, E experts of the whole layer, K slots per token, and the
+    experts [first, first + local) that this GPU's pair lists cover (local=None: all from first).
+    ``dtype``: F32 or BF16 logits. ``renorm``: a token's weights sum to ``scale``."""
+
+    def __init__(self, *, T, E, K, dtype=F32, first=0, local=None, renorm=False, scale=1.0, device="cuda"):
+        self.T, self.E, self.K, self.dtype = int(T), int(E), int(K), int(dtype)
+        self.first, self.local = int(first), int(E) - int(first) if local is None else int(local)
+        self.renorm, self.scale = bool(renorm), float(scale)
+        self.c = _lib.CRouter(T=self.T, E=self.E, K=self.K, first=self.first, local=self.local, dtype=self.dtype,
+                              renorm=int(self.renorm), reserved=0, scale=self.scale)
+        self.ref = ctypes.byref(self.c)
+        self.device = torch.device(device)
+        self.torch_dtype = torch.bfloat16 if self.dtype == BF16 else torch.float32
+        T, E, K, i32, f32 = self.T, self.E, self.K, torch.int32, torch.float32
+        self._route_out = (("idx", (T, K), i32), ("w", (T, K), f32), ("counts", (E,), i32),
+                           ("seg_off", (self.local + 1,), torch.int64), ("tok", (T * K,), i32),
+                           ("slot", (T * K,), i32), ("alpha", (T * K,), f32), ("pmap", (T, K), i32))
+        self._ws, self._ws_size = None, {}
+        self.workspace_size()  # checks the router
+
+    def workspace_size(self, n_seq=1) -> int:
+        """lrmoe_router_workspace_size, asked once per number of sequences."""
+        if n_seq not in self._ws_size:
+            n = ctypes.c_size_t(0)
+            _lib.check(library().lrmoe_router_workspace_size(self.ref, n_seq, ctypes.byref(n)),
+                       "lrmoe_router_workspace_size")
+            self._ws_size[n_seq] = int(n.value)
+        return self._ws_size[n_seq]
+
+    def workspace(self, n_seq=1) -> torch.Tensor:
+        """The router's scratch buffer. Calls that overlap on several streams, or graphs that
+        may replay at the same time, need a Router each."""
+        n = self.workspace_size(n_seq)
+        if self._ws is None or self._ws.numel() < n:
+            self._ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+        return self._ws
+
+
+def _want(t, name, shape, dtype, here):
+    """Pointer of a tensor after its shape, type and place (the current device) are checked
+    (None -> NULL)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.get_device() != here:
+        raise ValueError(f"{name}: expected {dtype} of shape {tuple(shape)} on the current device, "
+                         f"got {t.dtype} of {tuple(t.shape)} on {t.device}")
+    return _ptr(t)
+
+
+def _flags(t, name, n, here):
+    """Pointer of a tensor of at least n zeros and ones (None -> NULL)."""
+    if t is None:
+        return None
+    if t.dtype not in (torch.uint8, torch.bool) or t.numel() < n or t.get_device() != here:
+        raise ValueError(f"{name}: expected {n} uint8 or bool entries on the current device")
+    return _ptr(t)
+
+
+def _outputs(given, wanted, device, here):
+    """(dict of outputs, their pointers): the given ones checked, the others allocated."""
+    o = dict(given) if given else {}
+    ptrs = []
+    for name, shape, dt in wanted:
+        t = o.get(name)
+        if t is None:
+            t = o[name] = torch.empty(shape, dtype=dt, device=device)
+        ptrs.append(_want(t, name, shape, dt, here))
+    return o, ptrs
+
+
+def route(r: Router, logits, mask=None, out=None, stream=None):
+    """Top-K routing of ``logits`` [T, E] (lrmoe_route): a dict of idx, w [T, K], counts [E],
+    seg_off [local + 1] (device; ``.cpu()`` of it is Problem's seg_off), tok, slot, alpha [T*K] (rows
+    at and after seg_off[local] are not written) and pmap [T, K]. ``mask`` [T] uint8 or bool: 0
+    leaves a token out. ``out`` reuses buffers."""
+    here = torch.cuda.current_device()
+    o, ptrs = _outputs(out, r._route_out, r.device, here)
+    ws = r.workspace()
+    _lib.check(library().lrmoe_route(r.ref, _want(logits, "logits", (r.T, r.E), r.torch_dtype, here),
+                                     _flags(mask, "mask", r.T, here), *ptrs, ws.data_ptr(), ws.numel(),
+                                     _stream(stream)), "lrmoe_route")
+    return o
+
+
+def _sequences(r, seq_off, here):
+    """(device offsets or None, number of sequences). Offsets on the host are checked and copied."""
+    if seq_off is None:
+        return None, 1
+    if not isinstance(seq_off, torch.Tensor):
+        seq_off = torch.as_tensor(seq_off, dtype=torch.int64)
+    if seq_off.dtype != torch.int64 or seq_off.dim() != 1 or seq_off.numel() < 2:
+        raise ValueError("seq_off must be int64 [n_seq + 1]")
+    if not seq_off.is_cuda:
+        a = seq_off.tolist()
+        if a[0] < 0 or a[-1] > r.T or any(x > y for x, y in zip(a, a[1:])):
+            raise ValueError("seq_off must not decrease and stay inside [0, T]")
+        seq_off = seq_off.to(r.device)
+    elif seq_off.get_device() != here:
+        raise ValueError("seq_off must be on the current device")
+    return seq_off, seq_off.numel() - 1
+
+
+def balance_loss(r: Router, logits, idx, coef=1.0, mask=None, seq_off=None, out=None, stream=None):
+    """Per-expert counts and the balance loss of every sequence (lrmoe_balance_loss): a dict of loss
+    [1], counts, psum [n_seq, E] and norm [n_seq]. ``seq_off`` (int64 [n_seq + 1], host or device;
+    None: one sequence of all tokens). ``route_bwd`` takes the result as ``balance``."""
+    here = torch.cuda.current_device()
+    off, S = _sequences(r, seq_off, here)
+    o, ptrs = _outputs(out, (("counts", (S, r.E), torch.int32), ("psum", (S, r.E), torch.float32),
+                             ("norm", (S,), torch.float32), ("loss", (1,), torch.float32)), r.device, here)
+    ws = r.workspace(S)
+    _lib.check(library().lrmoe_balance_loss(r.ref, _want(logits, "logits", (r.T, r.E), r.torch_dtype, here),
+                                            _flags(mask, "mask", r.T, here),
+                                            _want(idx, "idx", (r.T, r.K), torch.int32, here), _ptr(off), S,
+                                            float(coef), *ptrs, ws.data_ptr(), ws.numel(), _stream(stream)),
+               "lrmoe_balance_loss")
+    return o
+
+
+def route_bwd(r: Router, logits, idx, dalpha=None, pmap=None, balance=None, gloss=None, mask=None, seq_off=None,
+              out=None, stream=None):
+    """Gradient of the logits [T, E] (lrmoe_route_bwd). ``dalpha``: the routing weights' gradient, by
+    pair row with ``pmap`` (alpha_grad's result and route's map), else [T, K]. ``balance``: what
+    balance_loss returned for these logits, with the same ``seq_off`` and ``mask``; ``gloss`` (device
+    f32 [1] or None = 1): the gradient of its loss. Either part may be None."""
+    here = torch.cuda.current_device()
+    shape = (r.T, r.E)
+    off, S = _sequences(r, seq_off, here) if balance is not None else (None, 1)
+    if out is None:
+        out = torch.empty(shape, dtype=r.torch_dtype, device=r.device)
+    n_pairs, d = 0, None
+    if dalpha is not None:
+        n_pairs = dalpha.numel()
+        d = _want(dalpha, "dalpha", (n_pairs,) if pmap is not None else (r.T, r.K), torch.float32, here)
+    counts = norm = None
+    if balance is not None:
+        counts = _want(balance["counts"], "counts", (S, r.E), torch.int32, here)
+        norm = _want(balance["norm"], "norm", (S,), torch.float32, here)
+    _lib.check(library().lrmoe_route_bwd(r.ref, _want(logits, "logits", shape, r.torch_dtype, here),
+                                         _flags(mask, "mask", r.T, here),
+                                         _want(idx, "idx", (r.T, r.K), torch.int32, here), d,
+                                         _want(pmap, "pmap", (r.T, r.K), torch.int32, here), n_pairs, _ptr(off), S,
+                                         counts, norm, _want(gloss, "gloss", (1,), torch.float32, here),
+                                         _want(out, "out", shape, r.torch_dtype, here), _stream(stream)),
+               "lrmoe_route_bwd")
+    return out
+
+
+def alpha_grad(p: Problem, G, Y, alpha, pmap, keep=None, out=None, stream=None):
+    """Gradient of the N pairs' routing weights from expert_forward's rows Y and the output's
+    gradient G (lrmoe_alpha_grad); ``pmap`` [T, K] from route, ``keep`` [N] uint8 from select."""
+    here = torch.cuda.current_device()
+    if out is None:
+        out = torch.empty(p.N, dtype=torch.float32, device=p.device)
+    for name, t in (("alpha", alpha), ("out", out)):
+        if t.dtype != torch.float32 or t.numel() < p.N or t.get_device() != here:
+            raise ValueError(f"{name}: expected f32 of at least N elements on the current device")
+    for name, t, rows in (("G", G, p.T), ("Y", Y, p.N)):
+        if t.dtype != p.torch_dtype or t.dim() != 2 or t.shape[0] < rows or t.shape[1] != p.D or t.get_device() != here:
+            raise ValueError(f"{name}: expected {p.torch_dtype} of {rows} rows of {p.D} on the current device")
+    _lib.check(library().lrmoe_alpha_grad(ctypes.byref(p.c), _ptr(G), _ptr(Y), _ptr(alpha),
+                                          _want(pmap, "pmap", (p.T, p.K), torch.int32, here),
+                                          _flags(keep, "keep", p.N, here), _ptr(out), _stream(stream)),
+               "lrmoe_alpha_grad")
+    return out
+
+
+class AdamW:
+    """AdamW over a list of tensors, updated in place by one call (lrmoe_adamw).
+
+    ``weights``: f32 or bf16 tensors, all of one type; ``masters``: their f32 masters (bf16 weights
+    only), or None; ``grads``: the gradient buffers the backward writes (f32 or bf16, all of one
+    type; they can also be given to each ``step``). ``bits``: 32 or 8 bits of state per moment. The
+    states ``m``, ``v`` (8 bits: e4m3 codes, v's of its square root, with ``m_scale``, ``v_scale`` per 256
+    elements) start at zero unless given. ``first``: 8 bits, the counter of each tensor's first
+    element for the random rounding (multiples of 256; None: one tensor behind the other).
+    ``t`` counts the steps taken. Buffers must not overlap."""
+
+    def __init__(self, weights, grads=None, masters=None, m=None, v=None, m_scale=None, v_scale=None, *, lr=1e-3,
+                 betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, bits=32, first=None, step=0, seed=0):
+        self.w, self.masters = list(weights), None if masters is None else list(masters)
+        if not self.w:
+            raise ValueError("AdamW needs at least one tensor")
+        dev = self.w[0].device
+        sizes = [t.numel() for t in self.w]
+        if bits not in (32, 8):
+            raise ValueError("bits must be 32 or 8")
+        st = torch.float8_e4m3fn if bits == 8 else torch.float32
+
+        def states(given, dt, n, fill=0):
+            if given is not None:
+                return list(given)
+            return [torch.full((k,), fill, dtype=torch.uint8 if dt == torch.float8_e4m3fn else dt,
+                               device=dev).view(dt) for k in n]
+
+        blocks = [(k + 255) // 256 for k in sizes]
+        self.m, self.v = states(m, st, sizes), states(v, st, sizes)
+        self.m_scale = states(m_scale, torch.float32, blocks, 1) if bits == 8 else None
+        self.v_scale = states(v_scale, torch.float32, blocks, 1) if bits == 8 else None
+        at = 0
+        if first is None:
+            first = []
+            for b in blocks:
+                first.append(at)
+                at += b * 256
+        self.t, self.lr, self.weight_decay = int(step), lr, weight_decay
+        wt = self.w[0].dtype
+        if wt not in (torch.float32, torch.bfloat16):
+            raise ValueError("weights must be f32 or bf16")
+        for name, ts, dt, n in (("weights", self.w, wt, sizes), ("masters", self.masters, torch.float32, sizes),
+                                ("m", self.m, st, sizes), ("v", self.v, st, sizes),
+                                ("m_scale", self.m_scale, torch.float32, blocks),
+                                ("v_scale", self.v_scale, torch.float32, blocks)):
+            if ts is not None and (len(ts) != len(sizes) or any(
+                    t.dtype != dt or t.numel() != k or t.device != dev for t, k in zip(ts, n))):
+                raise ValueError(f"{name}: one tensor of {dt} per weight, of its size, on {dev}")
+        if len(first) != len(sizes):
+            raise ValueError("first: one counter per weight")
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+                       for ts in (self.w, self.masters, self.m, self.v, self.m_scale, self.v_scale)
+                       if ts is not None for t in ts if t.numel())
+        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+            raise ValueError("AdamW's buffers overlap")
+        self.c = _lib.CAdamwConfig(w_dtype=BF16 if wt == torch.bfloat16 else F32, grad_dtype=F32,
+                                   master=int(masters is not None), state_bits=bits, lr=lr, beta1=betas[0],
+                                   beta2=betas[1], eps=eps, weight_decay=weight_decay, grad_scale=1.0, step=1,
+                                   seed=int(seed), reserved=0)
+        self._table = (_lib.CAdamwTensor * len(sizes))()
+        for i, k in enumerate(sizes):
+            e = self._table[i]
+            e.w, e.master = _ptr(self.w[i]), _ptr(self.masters[i]) if masters is not None else None
+            e.m, e.v, e.n, e.first = _ptr(self.m[i]), _ptr(self.v[i]), k, int(first[i])
+            if bits == 8:
+                e.m_scale, e.v_scale = _ptr(self.m_scale[i]), _ptr(self.v_scale[i])
+        self._scalars = None
+        self.grads = None
+        if grads is not None:
+            self.bind(grads)
+        _lib.check(library().lrmoe_adamw_step_scalars(ctypes.byref(self.c), ctypes.byref(_lib.CAdamwScalars())),
+                   "lrmoe_adamw_step_scalars")
+
+    def bind(self, grads):
+        """Takes these tensors as the gradient buffers from now on."""
+        grads = list(grads)
+        dt = grads[0].dtype if grads else None
+        if len(grads) != len(self.w) or dt not in (torch.float32, torch.bfloat16) or any(
+                g.dtype != dt or g.numel() != w.numel() or g.device != w.device for g, w in zip(grads, self.w)):
+            raise ValueError("grads: one f32 or bf16 tensor per weight, of its size, all of one type")
+        for e, g in zip(self._table, grads):
+            e.grad = _ptr(g)
+        self.c.grad_dtype = BF16 if dt == torch.bfloat16 else F32
+        self.grads = grads
+
+    def _config(self, grad_scale):
+        self.c.step, self.c.lr, self.c.weight_decay, self.c.grad_scale = self.t, self.lr, self.weight_decay, grad_scale
+
+    def _check_place(self):
+        if self.w[0].get_device() != torch.cuda.current_device():
+            raise ValueError("AdamW's tensors must be on the current device")
+
+    def step(self, grads=None, grad_scale=1.0, stream=None):
+        """One step. Inside a captured graph call ``step_captured`` instead."""
+        if grads is not None:
+            self.bind(grads)
+        if self.grads is None:
+            raise ValueError("AdamW has no gradient buffers: pass grads")
+        self._check_place()
+        self.t += 1
+        self._config(grad_scale)
+        try:
+            _lib.check(library().lrmoe_adamw(self._table, len(self.w), ctypes.byref(self.c), None, _stream(stream)),
+                       "lrmoe_adamw")
+        except LrmoeError:
+            self.t -= 1
+            raise
+
+    def advance(self, grad_scale=1.0):
+        """Counts one step and copies its scalars (step, lr, weight_decay, grad_scale) to the device, on
+        the current stream. Call it before each replay of a graph that holds ``step_captured``."""
+        host = _lib.CAdamwScalars()
+        self.t += 1
+        self._config(grad_scale)
+        _lib.check(library().lrmoe_adamw_step_scalars(ctypes.byref(self.c), ctypes.byref(host)),
+                   "lrmoe_adamw_step_scalars")
+        values = torch.frombuffer(bytearray(host), dtype=torch.int32)
+        if self._scalars is None:
+            self._scalars = torch.empty(8, dtype=torch.int32, device=self.w[0].device)
+        self._scalars.copy_(values)
+
+    def step_captured(self, stream=None):
+        """The update with the scalars of the last ``advance``, for capture into a graph."""
+        if self._scalars is None or self.grads is None:
+            raise ValueError("call advance (and bind the gradient buffers) before step_captured")
+        self._check_place()
+        _lib.check(library().lrmoe_adamw(self._table, len(self.w), ctypes.byref(self.c), _ptr(self._scalars),
+                                         _stream(stream)), "lrmoe_adamw")

@@ -23,7 +23,9 @@ SCATTER_TOKEN, SCATTER_SLOT, SCATTER_TOKEN_BESIDE = 0, 1, 2
 EXPORTS = ("lrmoe_status_string", "lrmoe_version", "lrmoe_validate", "lrmoe_workspace_size",
            "lrmoe_backward_bytes", "lrmoe_plan_quotas", "lrmoe_score", "lrmoe_score_criterion", "lrmoe_select",
            "lrmoe_compact", "lrmoe_grouped_gemm_bwd", "lrmoe_scatter", "lrmoe_expert_forward",
-           "lrmoe_select_noalloc", "lrmoe_compact_weighted", "lrmoe_grouped_gemm_bwd_gathered")
+           "lrmoe_select_noalloc", "lrmoe_compact_weighted", "lrmoe_grouped_gemm_bwd_gathered",
+           "lrmoe_router_workspace_size", "lrmoe_route", "lrmoe_balance_loss", "lrmoe_route_bwd", "lrmoe_alpha_grad",
+           "lrmoe_adamw_step_scalars", "lrmoe_adamw")
 
 
 class LrmoeError(RuntimeError):
@@ -41,6 +43,28 @@ class CProblem(ctypes.Structure):
                 ("D", ctypes.c_int32), ("F", ctypes.c_int32), ("swiglu", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32), ("N", ctypes.c_int64),
                 ("seg_off", ctypes.POINTER(ctypes.c_int64)), ("quota", ctypes.POINTER(ctypes.c_int32))]
+
+
+class CRouter(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("K", ctypes.c_int32), ("first", ctypes.c_int32),
+                ("local", ctypes.c_int32), ("dtype", ctypes.c_int32), ("renorm", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class CAdamwTensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("w", "master", "grad", "m", "v", "m_scale", "v_scale")] + [
+        ("n", ctypes.c_int64), ("first", ctypes.c_int64)]
+
+
+class CAdamwConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("w_dtype", "grad_dtype", "master", "state_bits")] + [
+        (n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay", "grad_scale")] + [
+        ("step", ctypes.c_int64), ("seed", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+class CAdamwScalars(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_float) for n in ("decay", "lr", "c1", "c2", "grad_scale")] + [
+        ("key", ctypes.c_uint32), ("reserved", ctypes.c_uint32 * 2)]
 
 
 _lib = None
@@ -79,6 +103,14 @@ def load() -> ctypes.CDLL:
                                             vp, vp],
         "lrmoe_scatter": [P, ctypes.c_int, i64, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp],
         "lrmoe_expert_forward": [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp],
+        "lrmoe_router_workspace_size": [ctypes.POINTER(CRouter), i32, ctypes.POINTER(sz)],
+        "lrmoe_route": [ctypes.POINTER(CRouter)] + [vp] * 11 + [sz, vp],
+        "lrmoe_balance_loss": [ctypes.POINTER(CRouter), vp, vp, vp, vp, i32, ctypes.c_float, vp, vp, vp, vp, vp, sz,
+                               vp],
+        "lrmoe_route_bwd": [ctypes.POINTER(CRouter), vp, vp, vp, vp, vp, i64, vp, i32, vp, vp, vp, vp, vp],
+        "lrmoe_alpha_grad": [P, vp, vp, vp, vp, vp, vp, vp],
+        "lrmoe_adamw_step_scalars": [ctypes.POINTER(CAdamwConfig), ctypes.POINTER(CAdamwScalars)],
+        "lrmoe_adamw": [ctypes.POINTER(CAdamwTensor), i32, ctypes.POINTER(CAdamwConfig), vp, vp],
     }
     for name, args in sigs.items():
         f = getattr(lib, name)

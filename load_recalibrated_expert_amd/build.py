@@ -15,7 +15,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "liblrmoe.so")
-SOURCES = ["lrmoe_abi.hip", "score.hip", "select.hip", "compact.hip", "gemm.hip", "scatter.hip"]
+SOURCES = ["lrmoe_abi.hip", "score.hip", "select.hip", "compact.hip", "gemm.hip", "scatter.hip",
+           "router.hip", "adamw.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -1,0 +1,260 @@
+// AdamW over many tensors in one launch, first and second moments in 32 or in 8 bits.
+//
+// Elementwise over [n]: HBM-bound, every array read and written once. A launch takes the tensors
+// from a table in its arguments (nothing is copied to the device), cut into chunks of kChunk
+// elements; a block finds its chunk's tensor by bisection of the chunk counts.
+#include <algorithm>
+
+#include "common.h"
+
+#pragma clang fp contract(off)  // a rounding at each operation, as the header says
+
+namespace lrmoe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBlock = 256;   // elements that share a scale: four to a lane of one wavefront
+constexpr int kChunk = 4096;  // elements of one thread block
+
+struct AdamwTable {
+  lrmoe_adamw_tensor t[kAdamwTensors];
+  uint32_t chunk[kAdamwTensors + 1];  // first chunk of each tensor
+  int32_t n;
+};
+
+struct AdamwArgs {
+  float b1, a1, b2, a2, eps;  // beta, 1 - beta
+  lrmoe_adamw_scalars s;
+  const lrmoe_adamw_scalars* dyn;
+};
+
+__device__ __forceinline__ uint32_t mix(uint32_t x) {
+  x ^= x >> 16;
+  x *= 0x9E3779B1u;
+  x ^= x >> 15;
+  x *= 0x85EBCA77u;
+  return x ^ (x >> 13);
+}
+
+__device__ __forceinline__ float pow2(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
+
+// |x| rounded to e4m3 at random by the 16 bits b: to a multiple of the spacing at x, 2^(e - 3)
+// with e at least -6. The result is an e4m3 value, so its conversion is exact.
+__device__ __forceinline__ float round_e4m3(float x, uint32_t b) {
+  const int e = max((int)(__float_as_uint(x) >> 23) - 127, -6);
+  return floorf(x * pow2(3 - e) + ((float)b + 0.5f) * 0x1p-16f) * pow2(e - 3);
+}
+
+// Exponent of a block's scale for its largest finite magnitude: the scaled maximum is in
+// [156.8, 313.6), under e4m3's 448 also after rounding up.
+__device__ __forceinline__ int scale_exp(float amax) {
+  return max((int)(__float_as_uint(amax * 0.8164966f) >> 23) - 127 - 7, -126);
+}
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, kWave));
+  return v;
+}
+
+__device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u; }
+
+// Four elements at i, of which `left` are inside the tensor.
+template <bool BF16>
+__device__ __forceinline__ void load4(const void* __restrict__ p, int64_t i, int left, float v[4]) {
+  if (left >= 4) {
+    if (BF16) {
+      const uint2 x = *(const uint2*)((const uint16_t*)p + i);
+      v[0] = bf16_lo(x.x);
+      v[1] = bf16_hi(x.x);
+      v[2] = bf16_lo(x.y);
+      v[3] = bf16_hi(x.y);
+    } else {
+      const float4 x = *(const float4*)((const float*)p + i);
+      v[0] = x.x;
+      v[1] = x.y;
+      v[2] = x.z;
+      v[3] = x.w;
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      v[q] = q >= left ? 0.0f
+             : BF16    ? __uint_as_float((uint32_t)((const uint16_t*)p)[i + q] << 16)
+                       : ((const float*)p)[i + q];
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store4(void* __restrict__ p, int64_t i, int left, const float v[4]) {
+  if (left >= 4) {
+    if (BF16) *(uint2*)((uint16_t*)p + i) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    else *(float4*)((float*)p + i) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (q < left) {
+        if (BF16) ((uint16_t*)p)[i + q] = (uint16_t)pack_bf16x2(v[q], 0.0f);
+        else ((float*)p)[i + q] = v[q];
+      }
+  }
+}
+
+__device__ __forceinline__ void load_codes(const void* __restrict__ p, int64_t i, int left, float scale, float v[4]) {
+  uint32_t c = 0;
+  if (left >= 4) {
+    c = *(const uint32_t*)((const uint8_t*)p + i);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (q < left) c |= (uint32_t)((const uint8_t*)p)[i + q] << (8 * q);
+  }
+  const f32x2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8(c, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(c, true);
+  v[0] = lo[0] * scale;
+  v[1] = lo[1] * scale;
+  v[2] = hi[0] * scale;
+  v[3] = hi[1] * scale;
+}
+
+// One wavefront's block of 256: scale, codes, and the scale's store by lane 0. SIGNED: the first
+// moment; else the root of the second, whose positive values stay positive.
+template <bool SIGNED>
+__device__ __forceinline__ void store_codes(void* __restrict__ p, float* __restrict__ scales, int64_t i, int left,
+                                            const float v[4], const uint32_t rnd[4]) {
+  float amax = 0.0f;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) amax = fmaxf(amax, q < left && finite(v[q]) ? fabsf(v[q]) : 0.0f);
+  amax = wave_max(amax);
+  const int k = amax > 0.0f ? scale_exp(amax) : 0;
+  const float inv = pow2(-k);
+  float c[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float x = round_e4m3(fabsf(v[q]) * inv, rnd[q]);
+    if (!SIGNED && v[q] > 0.0f) x = fmaxf(x, 0x1p-9f);
+    if (SIGNED && v[q] < 0.0f) x = -x;
+    c[q] = finite(v[q]) ? x : __uint_as_float(0x7FC00000u);
+  }
+  int code = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
+  code = __builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], code, true);
+  if (left >= 4) {
+    *(uint32_t*)((uint8_t*)p + i) = (uint32_t)code;
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (q < left) ((uint8_t*)p)[i + q] = (uint8_t)((uint32_t)code >> (8 * q));
+  }
+  if ((threadIdx.x & (kWave - 1)) == 0 && left > 0) scales[i / kBlock] = pow2(k);
+}
+
+template <bool Q8, bool W16, bool G16, bool MASTER>
+__global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwTable tab, AdamwArgs a) {
+  int lo = 0, hi = tab.n - 1;
+  while (lo < hi) {  // the last tensor whose first chunk is at or before this one
+    const int m = (lo + hi + 1) / 2;
+    if (tab.chunk[m] <= blockIdx.x) lo = m;
+    else hi = m - 1;
+  }
+  const lrmoe_adamw_tensor t = tab.t[lo];
+  const lrmoe_adamw_scalars s = a.dyn ? *a.dyn : a.s;
+  const int64_t i0 = (int64_t)(blockIdx.x - tab.chunk[lo]) * kChunk;
+  for (int u = 0; u < kChunk / (4 * kThreads); ++u) {
+    const int64_t i = i0 + (int64_t)u * 4 * kThreads + threadIdx.x * 4;
+    const int left = (int)max((int64_t)0, min((int64_t)4, t.n - i));
+    float w[4], g[4], m[4], v[4];
+    load4<G16>(t.grad, i, left, g);
+    if (MASTER) load4<false>(t.master, i, left, w);
+    else load4<W16>(t.w, i, left, w);
+    if (Q8) {
+      const float sm = left > 0 ? t.m_scale[i / kBlock] : 1.0f, sv = left > 0 ? t.v_scale[i / kBlock] : 1.0f;
+      load_codes(t.m, i, left, sm, m);
+      load_codes(t.v, i, left, sv, v);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = v[q] * v[q];
+    } else {
+      load4<false>(t.m, i, left, m);
+      load4<false>(t.v, i, left, v);
+    }
+    float r[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float x = g[q] * s.grad_scale;
+      m[q] = m[q] * a.b1 + x * a.a1;
+      v[q] = v[q] * a.b2 + (x * x) * a.a2;
+      r[q] = sqrtf(v[q]);
+      w[q] = w[q] * s.decay - (m[q] * s.c1) / (r[q] * s.c2 + a.eps) * s.lr;
+    }
+    if (MASTER) store4<false>(t.master, i, left, w);
+    store4<W16>(t.w, i, left, w);
+    if (Q8) {
+      uint32_t rm[4], rr[4];
+      const uint64_t c0 = (uint64_t)(t.first + i);  // a multiple of 4: the four share the high half
+      const uint32_t base = mix(s.key + (uint32_t)(c0 >> 32) * 0x9E3779B1u) + (uint32_t)c0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t h = mix(base + q);
+        rm[q] = h & 0xFFFFu;
+        rr[q] = h >> 16;
+      }
+      store_codes<true>(t.m, t.m_scale, i, left, m, rm);
+      store_codes<false>(t.v, t.v_scale, i, left, r, rr);
+    } else {
+      store4<false>(t.m, i, left, m);
+      store4<false>(t.v, i, left, v);
+    }
+  }
+}
+
+template <bool Q8, bool W16, bool G16, bool MASTER>
+void run(unsigned grid, const AdamwTable& tab, const AdamwArgs& a, hipStream_t s) {
+  adamw_kernel<Q8, W16, G16, MASTER><<<grid, kThreads, 0, s>>>(tab, a);
+}
+
+}  // namespace
+
+lrmoe_status launch_adamw(const lrmoe_adamw_tensor* tensors, int32_t n_tensors, const lrmoe_adamw_config* c,
+                          const lrmoe_adamw_scalars& host, const lrmoe_adamw_scalars* scalars_d, hipStream_t s) {
+  AdamwArgs a;
+  a.b1 = (float)c->beta1;
+  a.a1 = (float)(1.0 - c->beta1);
+  a.b2 = (float)c->beta2;
+  a.a2 = (float)(1.0 - c->beta2);
+  a.eps = (float)c->eps;
+  a.s = host;
+  a.dyn = scalars_d;
+  const bool q = c->state_bits == 8, w16 = c->w_dtype == LRMOE_BF16, g16 = c->grad_dtype == LRMOE_BF16;
+  int32_t i = 0;
+  while (i < n_tensors) {
+    AdamwTable tab;
+    tab.n = 0;
+    uint32_t chunks = 0;
+    for (; i < n_tensors && tab.n < kAdamwTensors; ++i) {
+      if (tensors[i].n == 0) continue;
+      tab.t[tab.n] = tensors[i];
+      tab.chunk[tab.n++] = chunks;
+      chunks += (uint32_t)ceil_div(tensors[i].n, kChunk);
+    }
+    if (tab.n == 0) break;
+    tab.chunk[tab.n] = chunks;
+    const int kind = (q ? 8 : 0) + (w16 ? 4 : 0) + (g16 ? 2 : 0) + (c->master ? 1 : 0);
+    switch (kind) {
+      case 0: run<false, false, false, false>(chunks, tab, a, s); break;
+      case 2: run<false, false, true, false>(chunks, tab, a, s); break;
+      case 4: run<false, true, false, false>(chunks, tab, a, s); break;
+      case 5: run<false, true, false, true>(chunks, tab, a, s); break;
+      case 6: run<false, true, true, false>(chunks, tab, a, s); break;
+      case 7: run<false, true, true, true>(chunks, tab, a, s); break;
+      case 8: run<true, false, false, false>(chunks, tab, a, s); break;
+      case 10: run<true, false, true, false>(chunks, tab, a, s); break;
+      case 12: run<true, true, false, false>(chunks, tab, a, s); break;
+      case 13: run<true, true, false, true>(chunks, tab, a, s); break;
+      case 14: run<true, true, true, false>(chunks, tab, a, s); break;
+      case 15: run<true, true, true, true>(chunks, tab, a, s); break;
+      default: return LRMOE_ERR_UNSUPPORTED;
+    }
+    if (launch_status() != LRMOE_OK) return LRMOE_ERR_HIP;
+  }
+  return LRMOE_OK;
+}
+
+}  // namespace lrmoe

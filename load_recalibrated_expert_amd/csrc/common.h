@@ -143,4 +143,23 @@ lrmoe_status launch_scatter(const lrmoe_problem* p, int mode, int64_t n_rows, in
                             const void* rows, const int32_t* ctok, const int32_t* cslot, const int32_t* pmap,
                             float* out, void* ws, hipStream_t s);
 
+size_t route_ws_bytes(const lrmoe_router* r);
+lrmoe_status launch_route(const lrmoe_router* r, const void* logits, const uint8_t* mask, int32_t* idx, float* w,
+                          int32_t* counts, int64_t* seg_off, int32_t* tok, int32_t* slot, float* alpha,
+                          int32_t* pmap, void* ws, hipStream_t s);
+size_t balance_ws_bytes(const lrmoe_router* r, int32_t n_seq);
+lrmoe_status launch_balance_loss(const lrmoe_router* r, const void* logits, const uint8_t* mask, const int32_t* idx,
+                                 const int64_t* seq_off_d, int32_t n_seq, float coef, int32_t* counts, float* psum,
+                                 float* norm, float* loss, void* ws, hipStream_t s);
+lrmoe_status launch_route_bwd(const lrmoe_router* r, const void* logits, const uint8_t* mask, const int32_t* idx,
+                              const float* dalpha, const int32_t* pmap, int64_t n_pairs, const int64_t* seq_off_d,
+                              int32_t n_seq, const int32_t* counts, const float* norm, const float* gloss,
+                              void* dlogits, hipStream_t s);
+lrmoe_status launch_alpha_grad(const lrmoe_problem* p, const void* G, const void* Y, const float* alpha,
+                               const int32_t* pmap, const uint8_t* keep, float* dalpha, hipStream_t s);
+
+constexpr int kAdamwTensors = 48;  // tensors of one launch: their table travels in the kernel arguments
+lrmoe_status launch_adamw(const lrmoe_adamw_tensor* tensors, int32_t n_tensors, const lrmoe_adamw_config* c,
+                          const lrmoe_adamw_scalars& host, const lrmoe_adamw_scalars* scalars_d, hipStream_t s);
+
 }  // namespace lrmoe

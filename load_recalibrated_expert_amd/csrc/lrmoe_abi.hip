@@ -2,6 +2,7 @@
 // kernels of each step. Every check runs before any launch; nothing here allocates,
 // synchronises or keeps state.
 #include <algorithm>
+#include <cmath>
 #include <vector>
 
 #include "common.h"
@@ -74,6 +75,47 @@ size_t backward_estimate(const lrmoe_problem* p, int64_t K_tot, bool packed) {
   return backward_buffer_bytes(p, K_tot, packed) + ws_need(p, LRMOE_COMPACT_PHYSICAL) +
          sizeof(int32_t) * (size_t)p->T * p->K;
 }
+
+lrmoe_status check_router(const lrmoe_router* r) {
+  if (!r || r->reserved != 0) return LRMOE_ERR_INVALID_ARG;
+  if (r->T < 0 || r->E < 1 || r->K < 1 || r->K > r->E) return LRMOE_ERR_INVALID_ARG;
+  if (r->first < 0 || r->local < 1 || r->local > r->E || r->first > r->E - r->local) return LRMOE_ERR_INVALID_ARG;
+  if ((r->renorm != 0 && r->renorm != 1) || !std::isfinite(r->scale)) return LRMOE_ERR_INVALID_ARG;
+  if (r->dtype != LRMOE_F32 && r->dtype != LRMOE_BF16) return LRMOE_ERR_UNSUPPORTED;
+  if (r->E > 1024 || r->K > 32) return LRMOE_ERR_UNSUPPORTED;
+  if ((int64_t)r->T * r->K >= ((int64_t)1 << 31)) return LRMOE_ERR_UNSUPPORTED;
+  return LRMOE_OK;
+}
+
+// Sequences of the balance loss: without offsets there is one, of all tokens.
+lrmoe_status check_sequences(const lrmoe_router* r, const int64_t* seq_off_d, int32_t n_seq) {
+  if (n_seq < 1 || (!seq_off_d && n_seq != 1)) return LRMOE_ERR_INVALID_ARG;
+  if ((int64_t)n_seq * r->E >= ((int64_t)1 << 31)) return LRMOE_ERR_UNSUPPORTED;
+  return LRMOE_OK;
+}
+
+uint32_t mix32(uint32_t x) {
+  x ^= x >> 16;
+  x *= 0x9E3779B1u;
+  x ^= x >> 15;
+  x *= 0x85EBCA77u;
+  return x ^ (x >> 13);
+}
+
+lrmoe_status check_adamw(const lrmoe_adamw_config* c) {
+  if (!c || c->reserved != 0 || (c->master != 0 && c->master != 1)) return LRMOE_ERR_INVALID_ARG;
+  for (int32_t t : {c->w_dtype, c->grad_dtype})
+    if (t != LRMOE_F32 && t != LRMOE_BF16) return LRMOE_ERR_UNSUPPORTED;
+  if (c->state_bits != 32 && c->state_bits != 8) return LRMOE_ERR_UNSUPPORTED;
+  if (c->master && c->w_dtype != LRMOE_BF16) return LRMOE_ERR_UNSUPPORTED;  // an f32 w is its own master
+  for (double x : {c->lr, c->eps, c->weight_decay, c->grad_scale})
+    if (!std::isfinite(x)) return LRMOE_ERR_INVALID_ARG;
+  if (!(c->beta1 >= 0 && c->beta1 < 1) || !(c->beta2 >= 0 && c->beta2 < 1) || c->eps < 0) return LRMOE_ERR_INVALID_ARG;
+  if (c->step < 1) return LRMOE_ERR_INVALID_ARG;
+  return LRMOE_OK;
+}
+
+bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 #define LRMOE_TRY(x)                      \
   do {                                    \
@@ -339,6 +381,99 @@ lrmoe_status lrmoe_scatter(const lrmoe_problem* p, lrmoe_scatter_mode mode, int6
     if (!ws || ws_bytes < scatter_ws_bytes(p)) return LRMOE_ERR_WORKSPACE;
   }
   return launch_scatter(p, mode, n_rows, width, rows_dtype, rows, ctok, cslot, pmap, out, ws, (hipStream_t)stream);
+}
+
+lrmoe_status lrmoe_router_workspace_size(const lrmoe_router* r, int32_t n_seq, size_t* bytes) {
+  if (!bytes) return LRMOE_ERR_INVALID_ARG;
+  LRMOE_TRY(check_router(r));
+  if (n_seq < 1) return LRMOE_ERR_INVALID_ARG;
+  if ((int64_t)n_seq * r->E >= ((int64_t)1 << 31)) return LRMOE_ERR_UNSUPPORTED;
+  *bytes = std::max<size_t>(256, std::max(route_ws_bytes(r), balance_ws_bytes(r, n_seq)));
+  return LRMOE_OK;
+}
+
+lrmoe_status lrmoe_route(const lrmoe_router* r, const void* logits, const uint8_t* mask, int32_t* idx, float* w,
+                         int32_t* counts, int64_t* seg_off, int32_t* tok, int32_t* slot, float* alpha,
+                         int32_t* pmap, void* ws, size_t ws_bytes, lrmoe_stream_t stream) {
+  LRMOE_TRY(check_router(r));
+  if (!counts || !seg_off) return LRMOE_ERR_INVALID_ARG;
+  if (r->T > 0 && (!logits || !idx || !w || !tok || !slot || !alpha || !pmap)) return LRMOE_ERR_INVALID_ARG;
+  if (!aligned(logits, 16)) return LRMOE_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < route_ws_bytes(r)) return LRMOE_ERR_WORKSPACE;
+  return launch_route(r, logits, mask, idx, w, counts, seg_off, tok, slot, alpha, pmap, ws, (hipStream_t)stream);
+}
+
+lrmoe_status lrmoe_balance_loss(const lrmoe_router* r, const void* logits, const uint8_t* mask, const int32_t* idx,
+                                const int64_t* seq_off_d, int32_t n_seq, float coef, int32_t* counts, float* psum,
+                                float* norm, float* loss, void* ws, size_t ws_bytes, lrmoe_stream_t stream) {
+  LRMOE_TRY(check_router(r));
+  LRMOE_TRY(check_sequences(r, seq_off_d, n_seq));
+  if (!std::isfinite(coef)) return LRMOE_ERR_INVALID_ARG;
+  if (!counts || !psum || !norm || !loss || (r->T > 0 && (!logits || !idx))) return LRMOE_ERR_INVALID_ARG;
+  if (!aligned(logits, 16)) return LRMOE_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < balance_ws_bytes(r, n_seq)) return LRMOE_ERR_WORKSPACE;
+  return launch_balance_loss(r, logits, mask, idx, seq_off_d, n_seq, coef, counts, psum, norm, loss, ws,
+                             (hipStream_t)stream);
+}
+
+lrmoe_status lrmoe_route_bwd(const lrmoe_router* r, const void* logits, const uint8_t* mask, const int32_t* idx,
+                             const float* dalpha, const int32_t* pmap, int64_t n_pairs, const int64_t* seq_off_d,
+                             int32_t n_seq, const int32_t* counts, const float* norm, const float* gloss,
+                             void* dlogits, lrmoe_stream_t stream) {
+  LRMOE_TRY(check_router(r));
+  if (norm) {
+    LRMOE_TRY(check_sequences(r, seq_off_d, n_seq));
+    if (!counts) return LRMOE_ERR_INVALID_ARG;
+  }
+  if (dalpha && pmap && n_pairs < 0) return LRMOE_ERR_INVALID_ARG;
+  if (r->T == 0) return LRMOE_OK;
+  if (!logits || !dlogits || (dalpha && !idx)) return LRMOE_ERR_INVALID_ARG;
+  if (!aligned(logits, 16) || !aligned(dlogits, 16)) return LRMOE_ERR_INVALID_ARG;
+  return launch_route_bwd(r, logits, mask, idx, dalpha, pmap, n_pairs, seq_off_d, n_seq, counts, norm, gloss, dlogits,
+                          (hipStream_t)stream);
+}
+
+lrmoe_status lrmoe_alpha_grad(const lrmoe_problem* p, const void* G, const void* Y, const float* alpha,
+                              const int32_t* pmap, const uint8_t* keep, float* dalpha, lrmoe_stream_t stream) {
+  LRMOE_TRY(check_problem(p, nullptr, nullptr));
+  if (p->N == 0) return LRMOE_OK;
+  if (!G || !Y || !alpha || !pmap || !dalpha) return LRMOE_ERR_INVALID_ARG;
+  if (!aligned(G, 16) || !aligned(Y, 16)) return LRMOE_ERR_INVALID_ARG;
+  return launch_alpha_grad(p, G, Y, alpha, pmap, keep, dalpha, (hipStream_t)stream);
+}
+
+lrmoe_status lrmoe_adamw_step_scalars(const lrmoe_adamw_config* c, lrmoe_adamw_scalars* out) {
+  if (!out) return LRMOE_ERR_INVALID_ARG;
+  LRMOE_TRY(check_adamw(c));
+  out->decay = (float)(1.0 - c->lr * c->weight_decay);
+  out->lr = (float)c->lr;
+  out->c1 = (float)(1.0 / (1.0 - std::pow(c->beta1, (double)c->step)));
+  out->c2 = (float)(1.0 / std::sqrt(1.0 - std::pow(c->beta2, (double)c->step)));
+  out->grad_scale = (float)c->grad_scale;
+  out->key = mix32(c->seed + mix32((uint32_t)c->step));
+  out->reserved[0] = out->reserved[1] = 0;
+  return LRMOE_OK;
+}
+
+lrmoe_status lrmoe_adamw(const lrmoe_adamw_tensor* tensors, int32_t n_tensors, const lrmoe_adamw_config* c,
+                         const lrmoe_adamw_scalars* scalars_d, lrmoe_stream_t stream) {
+  lrmoe_adamw_scalars host;
+  LRMOE_TRY(lrmoe_adamw_step_scalars(c, &host));
+  if (n_tensors < 0 || (n_tensors > 0 && !tensors)) return LRMOE_ERR_INVALID_ARG;
+  const bool q = c->state_bits == 8;
+  for (int32_t i = 0; i < n_tensors; ++i) {
+    const lrmoe_adamw_tensor& t = tensors[i];
+    if (t.n < 0 || t.first < 0 || (q && t.first % 256 != 0)) return LRMOE_ERR_INVALID_ARG;
+    if (t.n > ((int64_t)1 << 36)) return LRMOE_ERR_UNSUPPORTED;
+    if (t.n == 0) continue;
+    if (!t.w || !t.grad || !t.m || !t.v || (c->master != 0) != (t.master != nullptr)) return LRMOE_ERR_INVALID_ARG;
+    if (q != (t.m_scale != nullptr) || q != (t.v_scale != nullptr)) return LRMOE_ERR_INVALID_ARG;
+    const uintptr_t a = q ? 4 : 16;
+    if (!aligned(t.w, 16) || !aligned(t.master, 16) || !aligned(t.grad, 16) || !aligned(t.m, a) || !aligned(t.v, a) ||
+        !aligned(t.m_scale, 4) || !aligned(t.v_scale, 4))
+      return LRMOE_ERR_INVALID_ARG;
+  }
+  return launch_adamw(tensors, n_tensors, c, host, scalars_d, (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,316 @@
+"""GPU parity of the router's operators against their fp64 definitions (oracle/router_oracle.py,
+which also gives each value's error bound in fp32 arithmetic): routing and pair lists, balance
+loss, both gradients, at the sizes, masks and values where they can go wrong."""
+import numpy as np
+import pytest
+import torch
+
+import load_recalibrated_expert_amd as lr
+from oracle import router_oracle as ro
+
+from gpu_util import DEV, as_f64, log
+
+pytestmark = pytest.mark.gpu
+
+# T, E, K, first, local, dtype, renorm, mask share, what the logits hold
+CASES = {
+    "one_token": (1, 8, 2, 0, 8, "f32", False, 0.0, "normal"),
+    "one_expert": (37, 1, 1, 0, 1, "f32", True, 0.0, "normal"),
+    "all_chosen": (50, 7, 7, 0, 7, "f32", True, 0.0, "normal"),
+    "share": (1111, 128, 8, 0, 128, "f32", True, 0.0, "normal"),
+    "share_bf16": (1111, 128, 8, 16, 16, "bf16", False, 0.2, "normal"),
+    "odd_bf16": (300, 61, 5, 7, 20, "bf16", True, 0.3, "normal"),
+    "odd_f32": (515, 257, 6, 200, 57, "f32", False, 0.1, "normal"),
+    "two_groups": (130, 66, 32, 0, 66, "f32", False, 0.0, "normal"),
+    "wide": (129, 600, 16, 3, 590, "bf16", False, 0.0, "normal"),
+    "widest": (77, 1024, 32, 0, 1024, "f32", True, 0.1, "normal"),
+    "ties": (400, 48, 6, 0, 48, "bf16", True, 0.0, "ties"),
+    "constant": (70, 16, 4, 2, 9, "f32", False, 0.0, "constant"),
+    "bad_values": (333, 40, 6, 0, 40, "f32", False, 0.1, "bad"),
+    "bad_values_bf16": (333, 40, 6, 0, 40, "bf16", True, 0.1, "bad"),
+    "all_masked": (90, 12, 3, 0, 12, "f32", True, 1.0, "normal"),
+    "few_left": (64, 24, 8, 4, 16, "f32", True, 0.0, "few"),
+    "lowest": (64, 24, 8, 0, 24, "f32", True, 0.0, "lowest"),
+    "large": (96, 32, 4, 0, 32, "f32", False, 0.0, "large"),
+    "many_chunks": (40000, 5, 2, 1, 3, "f32", False, 0.1, "normal"),
+    "two_chunks": (129, 20, 3, 0, 20, "f32", False, 0.0, "normal"),
+}
+
+
+def _inputs(name):
+    T, E, K, first, local, dt, renorm, masked, kind = CASES[name]
+    rng = np.random.default_rng(sum(map(ord, name)))
+    x = rng.standard_normal((T, E)) * 2
+    if kind == "ties":
+        x = np.round(x)
+        x[::7] = np.where(rng.random((len(x[::7]), E)) < 0.5, 0.0, -0.0)
+    elif kind == "constant":
+        x[:] = 1.5
+    elif kind == "bad":
+        for v, share in ((np.nan, 0.1), (np.inf, 0.02), (-np.inf, 0.2), (-3e38, 0.1), (3e38, 0.02)):
+            x[rng.random((T, E)) < share] = v
+        x[5], x[6], x[7] = np.nan, -np.inf, np.inf
+        x[8] = -3.3e38
+    elif kind == "few":
+        x[rng.random((T, E)) < 0.85] = -np.inf
+    elif kind == "lowest":  # masked by the type's lowest value instead of -inf
+        x[rng.random((T, E)) < 0.85] = np.finfo(np.float32).min
+    elif kind == "large":
+        x *= 40
+    t = torch.from_numpy(x.astype(np.float32))
+    t = (t.bfloat16() if dt == "bf16" else t).to(DEV)
+    mask = None
+    if masked:
+        mask = (torch.from_numpy(rng.random(T)) >= masked).to(torch.uint8).to(DEV)
+    r = lr.Router(T=T, E=E, K=K, dtype=lr.BF16 if dt == "bf16" else lr.F32, first=first, local=local, renorm=renorm,
+                  scale=1.25, device=DEV)
+    return r, t, mask, rng
+
+
+def _host(t):
+    return None if t is None else as_f64(t)
+
+
+def _outs(r, fill=-7):
+    i32 = lambda *s: torch.full(s, fill, dtype=torch.int32, device=DEV)  # noqa: E731
+    f32 = lambda *s: torch.full(s, float(fill), device=DEV)  # noqa: E731
+    return {"idx": i32(r.T, r.K), "w": f32(r.T, r.K), "counts": i32(r.E),
+            "seg_off": torch.full((r.local + 1,), fill, dtype=torch.int64, device=DEV), "tok": i32(r.T * r.K),
+            "slot": i32(r.T * r.K), "alpha": f32(r.T * r.K), "pmap": i32(r.T, r.K)}
+
+
+def _check_route(r, o, ref):
+    for k in ("idx", "counts", "seg_off", "pmap"):
+        assert np.array_equal(o[k].cpu().numpy(), ref[k]), k
+    N = int(ref["seg_off"][-1])
+    for k in ("tok", "slot"):
+        assert np.array_equal(o[k][:N].cpu().numpy(), ref[k]), k
+        assert torch.all(o[k][N:] == -7), k  # rows behind the last pair are left as they were
+    assert torch.all(o["alpha"][N:] == -7)
+    w = as_f64(o["w"])
+    assert np.all(np.abs(w - ref["w"]) <= ref["w_err"]), np.max(np.abs(w - ref["w"]) / ref["w_err"])
+    t, k = np.nonzero(ref["pmap"] >= 0)
+    alpha = as_f64(o["alpha"])
+    assert np.array_equal(alpha[ref["pmap"][t, k]], w[t, k])
+
+
+@pytest.mark.parametrize("name", sorted(CASES))
+def test_route(name):
+    r, x, mask, _ = _inputs(name)
+    log(f"route {name}")
+    ref = ro.route(_host(x), r.K, _host(mask), r.first, r.local, r.renorm, r.scale)
+    o = lr.route(r, x, mask=mask, out=_outs(r))
+    torch.cuda.synchronize()
+    _check_route(r, o, ref)
+    again = lr.route(r, x, mask=mask, out=_outs(r))
+    for k in o:
+        assert torch.equal(o[k], again[k]), k
+
+
+def test_route_no_tokens():
+    r = lr.Router(T=0, E=9, K=2, first=3, local=4, device=DEV)
+    log("route without tokens")
+    o = lr.route(r, torch.empty(0, 9, device=DEV))
+    assert o["counts"].tolist() == [0] * 9 and o["seg_off"].tolist() == [0] * 5
+    b = lr.balance_loss(r, torch.empty(0, 9, device=DEV), o["idx"], seq_off=[0, 0, 0])
+    assert b["loss"].item() == 0 and not b["counts"].any() and not b["psum"].any() and not b["norm"].any()
+    assert lr.route_bwd(r, torch.empty(0, 9, device=DEV), o["idx"], balance=b, seq_off=[0, 0, 0]).shape == (0, 9)
+
+
+def _sequences(name, T, rng):
+    yield None
+    yield [0, T]
+    yield sorted([0, 0, T, T] + rng.integers(0, T + 1, size=9).tolist())
+    if T > 3:
+        yield [1, T // 2, T - 1]  # tokens before the first and behind the last sequence
+
+
+@pytest.mark.parametrize("name", sorted(CASES))
+def test_balance_and_gradient(name):
+    r, x, mask, rng = _inputs(name)
+    X, M = _host(x), _host(mask)
+    idx = lr.route(r, x, mask=mask)["idx"]
+    I = idx.cpu().numpy()
+    dalpha = torch.from_numpy(rng.standard_normal((r.T, r.K)).astype(np.float32)).to(DEV)
+    gloss = torch.tensor([0.7], device=DEV)
+    g7 = float(np.float32(0.7))
+    for off in _sequences(name, r.T, rng):
+        log(f"balance {name} {None if off is None else len(off) - 1}")
+        ref = ro.balance(X, I, float(np.float32(0.3)), M, off)
+        b = lr.balance_loss(r, x, idx, coef=0.3, mask=mask, seq_off=off)
+        again = lr.balance_loss(r, x, idx, coef=0.3, mask=mask, seq_off=off)
+        assert all(torch.equal(b[k], again[k]) for k in b)
+        assert np.array_equal(b["counts"].cpu().numpy(), ref["counts"])
+        assert np.all(np.abs(as_f64(b["psum"]) - ref["psum"]) <= ref["psum_err"])
+        assert np.all(np.abs(as_f64(b["norm"]) - ref["norm"]) <= 2 * ro.U * ref["norm"])
+        assert abs(float(b["loss"]) - ref["loss"]) <= ref["loss_err"] + 1e-37
+        N = as_f64(b["norm"])
+        for y, bal in ((None, True), (dalpha, False), (dalpha, True)):
+            got = lr.route_bwd(r, x, idx, dalpha=y, balance=b if bal else None, gloss=gloss, mask=mask, seq_off=off)
+            dx, err = ro.route_bwd(X, I, y=None if y is None else as_f64(y), counts=ref["counts"],
+                                   norm=N if bal else None, gloss=g7, mask=M, seq_off=off, renorm=r.renorm,
+                                   scale=r.scale)
+            if x.dtype == torch.bfloat16:
+                err = err + np.abs(dx) * 2.0 ** -8
+            d = np.abs(as_f64(got) - dx)
+            assert np.all(d <= err), (off, y is None, bal, np.max(d / err))
+
+
+def test_gradient_through_pair_rows():
+    """dalpha by pair row: local pairs through pmap, the others and rows past the end give nothing."""
+    r, x, mask, rng = _inputs("share_bf16")
+    o = lr.route(r, x, mask=mask)
+    n = int(o["seg_off"][-1])
+    d = torch.from_numpy(rng.standard_normal(n).astype(np.float32)).to(DEV)
+    slots = torch.where(o["pmap"] >= 0, d[o["pmap"].clamp(min=0).long()], 0.0)
+    log("gradient by pair row")
+    a = lr.route_bwd(r, x, o["idx"], dalpha=d, pmap=o["pmap"], mask=mask)
+    b = lr.route_bwd(r, x, o["idx"], dalpha=slots, mask=mask)
+    assert torch.equal(a, b)
+    short = lr.route_bwd(r, x, o["idx"], dalpha=d[:n // 2].contiguous(), pmap=o["pmap"], mask=mask)
+    cut = torch.where(o["pmap"] < n // 2, slots, 0.0)
+    assert torch.equal(short, lr.route_bwd(r, x, o["idx"], dalpha=cut, mask=mask))
+
+
+def test_indexes_outside_the_experts_are_empty_slots():
+    r, x, mask, rng = _inputs("odd_f32")
+    idx = lr.route(r, x, mask=mask)["idx"].clone()
+    idx[::3, 2], idx[1::5, 0] = r.E, -5
+    idx[4, 1] = 2 ** 31 - 1
+    I = np.where((idx.cpu().numpy() < 0) | (idx.cpu().numpy() >= r.E), -1, idx.cpu().numpy())
+    y = torch.from_numpy(rng.standard_normal((r.T, r.K)).astype(np.float32)).to(DEV)
+    log("indexes outside the experts")
+    b = lr.balance_loss(r, x, idx, mask=mask)
+    assert np.array_equal(b["counts"].cpu().numpy(), ro.balance(_host(x), I, 1.0, _host(mask))["counts"])
+    dx, err = ro.route_bwd(_host(x), I, y=as_f64(y), mask=_host(mask), scale=r.scale)
+    assert np.all(np.abs(as_f64(lr.route_bwd(r, x, idx, dalpha=y, mask=mask)) - dx) <= err)
+
+
+def test_offsets_outside_the_tokens_are_clamped():
+    r, x, _, _ = _inputs("odd_f32")
+    idx = lr.route(r, x)["idx"]
+    log("device offsets outside [0, T]")
+    wild = torch.tensor([-9, 100, 10 ** 12], device=DEV)
+    a = lr.balance_loss(r, x, idx, seq_off=wild)
+    b = lr.balance_loss(r, x, idx, seq_off=[0, 100, r.T])
+    assert all(torch.equal(a[k], b[k]) for k in a)
+    with pytest.raises(ValueError):
+        lr.balance_loss(r, x, idx, seq_off=[0, 10 ** 12])
+    with pytest.raises(ValueError):
+        lr.balance_loss(r, x, idx, seq_off=[0, 9, 3, r.T])
+
+
+def test_gradients_add_over_the_expert_shares():
+    """Each GPU's pairs give a part of the routing gradient; the parts add up to the whole."""
+    _, x, _, rng = _inputs("share")
+    T, E, K = 1111, 128, 8
+    whole = lr.Router(T=T, E=E, K=K, renorm=True, device=DEV)
+    o = lr.route(whole, x)
+    y = torch.from_numpy(rng.standard_normal((T, K)).astype(np.float32)).to(DEV)
+    parts = np.zeros((T, E))
+    log("expert shares")
+    for first in range(0, E, 32):
+        r = lr.Router(T=T, E=E, K=K, renorm=True, first=first, local=32, device=DEV)
+        p = lr.route(r, x)
+        n = int(p["seg_off"][-1])
+        row = p["pmap"].long()
+        d = torch.zeros(n, device=DEV)
+        d[row[row >= 0]] = y[row >= 0]
+        parts += as_f64(lr.route_bwd(r, x, p["idx"], dalpha=d, pmap=p["pmap"]))
+    X, I = _host(x), o["idx"].cpu().numpy()
+    dx, err = ro.route_bwd(X, I, y=as_f64(y), renorm=True)
+    bound = sum(ro.route_bwd(X, I, y=np.where((I >= f) & (I < f + 32), as_f64(y), 0), renorm=True)[1]
+                for f in range(0, E, 32))
+    assert np.all(np.abs(parts - dx) <= bound)
+
+
+@pytest.mark.parametrize("T,K,D,dt,keep", [(1, 1, 8, "f32", None), (37, 3, 8, "bf16", 0.5), (200, 8, 520, "bf16", None),
+                                           (90, 10, 2048, "f32", 0.6), (65, 4, 4104, "bf16", 0.9),
+                                           (130, 17, 264, "f32", None), (700, 2, 1032, "bf16", 0.0)])
+def test_alpha_grad(T, K, D, dt, keep):
+    rng = np.random.default_rng(T + D)
+    E = K + 3
+    x = torch.from_numpy(rng.standard_normal((T, E)).astype(np.float32)).to(DEV)
+    r = lr.Router(T=T, E=E, K=K, first=1, local=E - 1, device=DEV)
+    o = lr.route(r, x)
+    seg = o["seg_off"].cpu().numpy()
+    N = int(seg[-1])
+    p = lr.Problem(E=E - 1, T=T, K=K, D=D, F=8, swiglu=True, dtype=lr.BF16 if dt == "bf16" else lr.F32, seg_off=seg,
+                   quota=np.zeros(E - 1, np.int32), device=DEV)
+    td = torch.bfloat16 if dt == "bf16" else torch.float32
+    G = torch.from_numpy(rng.standard_normal((T, D)).astype(np.float32)).to(DEV).to(td)
+    Y = torch.from_numpy(rng.standard_normal((max(N, 1), D)).astype(np.float32)).to(DEV).to(td)
+    alpha = o["alpha"].clone()
+    alpha[:N][::5] = 0
+    k = None if keep is None else torch.from_numpy((rng.random(max(N, 1)) < keep).astype(np.uint8)).to(DEV)
+    log(f"alpha gradient T={T} K={K} D={D} {dt}")
+    out = torch.full((N + 3,), -7.0, device=DEV)
+    lr.alpha_grad(p, G, Y, alpha, o["pmap"], keep=k, out=out)
+    ref, err = ro.alpha_grad(as_f64(G), as_f64(Y)[:N], as_f64(alpha)[:N], o["tok"][:N].cpu().numpy(),
+                             None if k is None else k.cpu().numpy()[:N])
+    assert np.all(np.abs(as_f64(out[:N]) - ref) <= err + 1e-37)
+    assert torch.all(out[N:] == -7)
+
+
+def test_alpha_grad_leaves_pairs_without_a_position():
+    p = lr.Problem(E=1, T=2, K=2, D=8, F=8, swiglu=True, dtype=lr.F32, seg_off=[0, 4], quota=[4], device=DEV)
+    one = torch.ones(4, 8, device=DEV)
+    out = torch.full((4,), -7.0, device=DEV)
+    pmap = torch.tensor([[3, -1], [4, 1]], dtype=torch.int32, device=DEV)  # 4 is past the last pair
+    log("pairs without a position")
+    lr.alpha_grad(p, one[:2], one, torch.full((4,), 0.5, device=DEV), pmap, out=out)
+    assert out.tolist() == [-7.0, 16.0, -7.0, 16.0]
+
+
+def test_python_checks():
+    r, x, mask, _ = _inputs("share")
+    idx = lr.route(r, x)["idx"]
+    b = lr.balance_loss(r, x, idx)
+    for call in (lambda: lr.route(r, x.bfloat16()), lambda: lr.route(r, x[:-1]), lambda: lr.route(r, x.t()),
+                 lambda: lr.route(r, x.cpu()), lambda: lr.route(r, x, mask=torch.ones(3, dtype=torch.uint8, device=DEV)), lambda: lr.route(r, x, mask=torch.ones(r.T, dtype=torch.uint8)),
+                 lambda: lr.route(r, x, mask=torch.ones(r.T, device=DEV)),
+                 lambda: lr.route(r, x, out={"idx": idx.long()}), lambda: lr.route(r, x, out={"tok": idx}),
+                 lambda: lr.balance_loss(r, x, idx[:5]), lambda: lr.balance_loss(r, x, idx.float()),
+                 lambda: lr.balance_loss(r, x, idx, seq_off=[0]), lambda: lr.balance_loss(r, x, idx, out={"loss": x}),
+                 lambda: lr.route_bwd(r, x, idx, dalpha=b["psum"]), lambda: lr.route_bwd(r, x, idx, dalpha=x.double()),
+                 lambda: lr.route_bwd(r, x, idx, balance=b, seq_off=[0, 4, 9]),
+                 lambda: lr.route_bwd(r, x, idx, balance=b, gloss=torch.ones((), device=DEV)),
+                 lambda: lr.route_bwd(r, x, idx, balance=b, out=x.bfloat16())):
+        with pytest.raises(ValueError):
+            call()
+
+
+def test_replayed_graph_and_other_stream():
+    """Routing, loss and gradient captured on a side stream: every replay on new logits equals the eager
+    calls, with eager work of another Router between the replays."""
+    r, x, mask, rng = _inputs("share_bf16")
+    off = torch.tensor([0, 400, 400, 900, r.T], device=DEV)
+    y = torch.from_numpy(rng.standard_normal((r.T, r.K)).astype(np.float32)).to(DEV)
+
+    def step(rt):
+        o = lr.route(rt, x, mask=mask)
+        b = lr.balance_loss(rt, x, o["idx"], mask=mask, seq_off=off)
+        return {**o, **b, "dx": lr.route_bwd(rt, x, o["idx"], dalpha=y, balance=b, mask=mask, seq_off=off)}
+
+    eager = lr.Router(T=r.T, E=r.E, K=r.K, dtype=r.dtype, first=r.first, local=r.local, scale=r.scale, device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(r)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            got = step(r)
+    for rep in range(4):
+        x.copy_(torch.from_numpy(rng.standard_normal(tuple(x.shape)).astype(np.float32)).to(DEV))
+        for t in got.values():
+            t.fill_(3)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        want = step(eager)
+        n = int(want["seg_off"][-1])
+        log(f"replay {rep}: {n} pairs")
+        for k in want:
+            a, b = (t[k][:n] if k in ("tok", "slot", "alpha") else t[k] for t in (got, want))
+            assert torch.equal(a, b), (rep, k)
