@@ -6,6 +6,7 @@
 // [N x D] output rows), so memory bounds it at large T and launch latency at small T. A group
 // of L lanes holds one token's logits in registers, V to a lane.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.h"
 
@@ -19,49 +20,110 @@ __device__ __forceinline__ float clean(float x) {  // NaN -> -inf, +inf -> FLT_M
   return x != x ? kNegInf : fminf(x, kFltMax);
 }
 
-template <bool BF16>
-__device__ __forceinline__ float load_logit(const void* __restrict__ logits, int64_t i) {
-  if (BF16) return __uint_as_float((uint32_t)((const uint16_t*)logits)[i] << 16);
-  return ((const float*)logits)[i];
+// Reductions over the L lanes of a token's group; every lane gets the result, the same bits in each.
+// Sixteen lanes are a DPP row: four rotations at register speed instead of cross-lane permutes
+// through LDS (an 8-slot top-K over 128 experts: 46 us with permutes, 17 us so, T = 32768).
+template <int N>
+__device__ __forceinline__ int row_ror(int v) {
+  return __builtin_amdgcn_update_dpp(v, v, 0x120 + N, 0xF, 0xF, false);
 }
-
-// Reductions over the L lanes of a token's group; every lane gets the result.
+template <int L, class Op>
+__device__ __forceinline__ int group_reduce(int v, Op op) {
+  v = op(v, row_ror<8>(v));
+  v = op(v, row_ror<4>(v));
+  v = op(v, row_ror<2>(v));
+  v = op(v, row_ror<1>(v));
+#pragma unroll
+  for (int o = 16; o < L; o <<= 1) v = op(v, __shfl_xor(v, o, kWave));
+  return v;
+}
 template <int L>
 __device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, kWave));
-  return v;
+  return __int_as_float(group_reduce<L>(__float_as_int(v), [](int a, int b) {
+    return __float_as_int(fmaxf(__int_as_float(a), __int_as_float(b)));
+  }));
 }
 template <int L>
 __device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
-  return v;
+  return __int_as_float(group_reduce<L>(__float_as_int(v), [](int a, int b) {
+    return __float_as_int(__int_as_float(a) + __int_as_float(b));
+  }));
 }
 template <int L>
 __device__ __forceinline__ int group_min(int v) {
-#pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) v = min(v, __shfl_xor(v, o, kWave));
-  return v;
+  return group_reduce<L>(v, [](int a, int b) { return min(a, b); });
 }
 
-// Expert of value v of a lane.
-template <int L, int V>
-__device__ __forceinline__ int expert_of(int lane, int v) {
-  return v * L + lane;
-}
-
-// A token's logits by the rules of the header; -inf beyond E and for a masked token.
-template <int L, int V, bool BF16>
-__device__ __forceinline__ void load_row(const void* __restrict__ logits, const uint8_t* __restrict__ mask, int64_t t,
-                                         int E, bool in, int lane, float x[V]) {
-  const bool on = in && (!mask || mask[t] != 0);
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = expert_of<L, V>(lane, v);
-    x[v] = on && e < E ? clean(load_logit<BF16>(logits, t * E + e)) : kNegInf;
+// How a token's E logits lie over the L lanes of its group, V to a lane, ascending in each lane.
+// VEC (E a multiple of 4, so rows are aligned): runs of four, one 16-byte (f32) or 8-byte (bf16)
+// load each; else single logits, L apart.
+template <int L_, int V_, bool BF16_, bool VEC_>
+struct Layout {
+  static constexpr int L = L_, V = V_;
+  static constexpr bool BF16 = BF16_, VEC = VEC_;
+  static __device__ __forceinline__ int expert(int lane, int v) {
+    return VEC ? (v >> 2) * (4 * L) + lane * 4 + (v & 3) : v * L + lane;
   }
-}
+  // Token t by the rules of the header; -inf beyond E, and everywhere if `on` is false.
+  static __device__ __forceinline__ void load(const void* __restrict__ logits, int64_t t, int E, bool on, int lane,
+                                              float x[V]) {
+    if (VEC) {
+#pragma unroll
+      for (int q = 0; q < V; q += 4) {
+        const int e = expert(lane, q);
+        if (on && e < E) {
+          if (BF16) {
+            const uint2 r = *(const uint2*)((const uint16_t*)logits + t * E + e);
+            x[q] = clean(bf16_lo(r.x));
+            x[q + 1] = clean(bf16_hi(r.x));
+            x[q + 2] = clean(bf16_lo(r.y));
+            x[q + 3] = clean(bf16_hi(r.y));
+          } else {
+            const float4 r = *(const float4*)((const float*)logits + t * E + e);
+            x[q] = clean(r.x);
+            x[q + 1] = clean(r.y);
+            x[q + 2] = clean(r.z);
+            x[q + 3] = clean(r.w);
+          }
+        } else {
+          x[q] = x[q + 1] = x[q + 2] = x[q + 3] = kNegInf;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int e = expert(lane, v);
+        x[v] = kNegInf;
+        if (on && e < E)
+          x[v] = clean(BF16 ? __uint_as_float((uint32_t)((const uint16_t*)logits)[t * E + e] << 16)
+                            : ((const float*)logits)[t * E + e]);
+      }
+    }
+  }
+  static __device__ __forceinline__ void store(void* __restrict__ out, int64_t t, int E, int lane, const float x[V]) {
+    if (VEC) {
+#pragma unroll
+      for (int q = 0; q < V; q += 4) {
+        const int e = expert(lane, q);
+        if (e >= E) continue;
+        if (BF16)
+          *(uint2*)((uint16_t*)out + t * E + e) = make_uint2(pack_bf16x2(x[q], x[q + 1]), pack_bf16x2(x[q + 2], x[q + 3]));
+        else
+          *(float4*)((float*)out + t * E + e) = make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int e = expert(lane, v);
+        if (e >= E) continue;
+        if (BF16) ((uint16_t*)out)[t * E + e] = (uint16_t)pack_bf16x2(x[v], 0.0f);
+        else ((float*)out)[t * E + e] = x[v];
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ bool unmasked(const uint8_t* __restrict__ mask, int64_t t) { return !mask || mask[t] != 0; }
 
 // ---------------------------------------------------------------- routing
 
@@ -75,132 +137,174 @@ int route_chunk(const lrmoe_router* r) {
   return c;
 }
 
-// One block per chunk of tokens: the K largest logits of each, their weights, and how often the
-// chunk chose each expert.
-template <int L, int V, bool BF16>
-__global__ __launch_bounds__(kRouteThreads) void route_topk_kernel(int T, int E, int K, int C, int renorm, float scale,
-                                                                   const void* __restrict__ logits,
-                                                                   const uint8_t* __restrict__ mask,
-                                                                   int32_t* __restrict__ idx, float* __restrict__ w,
-                                                                   int32_t* __restrict__ hist) {
-  __shared__ int cnt[1024];
-  for (int e = threadIdx.x; e < E; e += kRouteThreads) cnt[e] = 0;
-  __syncthreads();
-  const int lane = threadIdx.x & (L - 1), group = threadIdx.x / L;
-  constexpr int kGroups = kRouteThreads / L;
-  const int64_t t0 = (int64_t)blockIdx.x * C, t1 = min(t0 + C, (int64_t)T);
-  for (int64_t tb = t0; tb < t1; tb += kGroups) {
-    const int64_t t = tb + group;
-    const bool in = t < t1;
-    float x[V];
-    load_row<L, V, BF16>(logits, mask, t, E, in, lane, x);
-    float top = kNegInf;
-#pragma unroll
-    for (int v = 0; v < V; ++v) top = fmaxf(top, x[v]);
-    top = group_max<L>(top);
-    float Z = 0.0f;
-    if (!renorm) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) Z += x[v] > kNegInf ? expf(x[v] - top) : 0.0f;
-      Z = group_sum<L>(Z);
-    }
-    // slot k: the largest value left, the lowest index that has it
-    int my_e = -1;
-    float my_x = kNegInf;
-    for (int k = 0; k < K; ++k) {
-      float best = kNegInf;
-#pragma unroll
-      for (int v = 0; v < V; ++v) best = fmaxf(best, x[v]);
-      best = group_max<L>(best);
-      int at = 1 << 30;
-#pragma unroll
-      for (int v = V - 1; v >= 0; --v)
-        if (x[v] == best && best > kNegInf) at = expert_of<L, V>(lane, v);
-      at = group_min<L>(at);
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (expert_of<L, V>(lane, v) == at) x[v] = kNegInf;
-      if (lane == k) {
-        my_e = at < (1 << 30) ? at : -1;
-        my_x = best;
-      }
-    }
-    const float p = my_e >= 0 ? expf(my_x - top) : 0.0f;
-    if (renorm) Z = group_sum<L>(p);
-    if (in && lane < K) {
-      idx[t * K + lane] = my_e;
-      w[t * K + lane] = my_e >= 0 ? scale * (p / Z) : 0.0f;
-      if (my_e >= 0) atomicAdd(&cnt[my_e], 1);
-    }
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < E; e += kRouteThreads) hist[(int64_t)blockIdx.x * E + e] = cnt[e];
-}
+struct RouteArgs {
+  int T, E, K, C, chunks, first, local, renorm;
+  float scale;
+  const void* logits;
+  const uint8_t* mask;
+  int32_t* hist;  // [chunks][E] tokens of each chunk per expert
+  int32_t *idx, *counts, *tok, *slot, *pmap;
+  float *w, *alpha;
+  int64_t* seg_off;
+};
 
-// One block per chunk: where each expert's pairs start and how many earlier chunks hold (from
-// all chunks' histograms), then the rank of a pair in its chunk as the number of lower set bits
-// of its expert's token bits: no order of atomics enters the result.
-__global__ __launch_bounds__(kRouteThreads) void route_place_kernel(
-    int T, int E, int K, int C, int chunks, int first, int local, const int32_t* __restrict__ hist,
-    const int32_t* __restrict__ idx, const float* __restrict__ w, int32_t* __restrict__ counts,
-    int64_t* __restrict__ seg_off, int32_t* __restrict__ tok, int32_t* __restrict__ slot, float* __restrict__ alpha,
-    int32_t* __restrict__ pmap) {
-  __shared__ int total[1024], before[1024];
+// Pair rows of one chunk. total, before (LDS, [E]): tokens per expert in all chunks and in the
+// chunks before this one; before becomes the first row of (chunk, expert). The rank of a pair in
+// its chunk is the number of lower set bits among its expert's token bits, so no order of atomics
+// enters the result.
+__device__ __forceinline__ void place_chunk(const RouteArgs& a, int c, const int* total, int* before, uint32_t* bits) {
   __shared__ int wave_total[kRouteThreads / kWave];
-  extern __shared__ uint32_t bits[];  // [C / 32][local]
-  const int tid = threadIdx.x, c = blockIdx.x;
-  for (int e = tid; e < E; e += kRouteThreads) total[e] = before[e] = 0;
-  for (int i = tid; i < C / 32 * local; i += kRouteThreads) bits[i] = 0;
-  __syncthreads();
-  for (int64_t i = tid; i < (int64_t)chunks * E; i += kRouteThreads) {
-    const int ch = (int)(i / E), e = (int)(i - (int64_t)ch * E), h = hist[i];
-    if (h) {
-      atomicAdd(&total[e], h);
-      if (ch < c) atomicAdd(&before[e], h);
-    }
-  }
-  __syncthreads();
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
   if (c == 0)
-    for (int e = tid; e < E; e += kRouteThreads) counts[e] = total[e];
+    for (int e = tid; e < a.E; e += kRouteThreads) a.counts[e] = total[e];
   // exclusive scan of the local experts' totals (local <= 1024 = one value per thread)
-  const int mine = tid < local ? total[first + tid] : 0;
+  const int mine = tid < a.local ? total[a.first + tid] : 0;
   int inc = mine;
 #pragma unroll
   for (int o = 1; o < kWave; o <<= 1) {
     const int up = __shfl_up(inc, o, kWave);
-    if ((tid & (kWave - 1)) >= o) inc += up;
+    if (lane >= o) inc += up;
   }
-  if ((tid & (kWave - 1)) == kWave - 1) wave_total[tid / kWave] = inc;
+  if (lane == kWave - 1) wave_total[tid / kWave] = inc;
+  for (int i = tid; i < a.C / 32 * a.local; i += kRouteThreads) bits[i] = 0;
   __syncthreads();
   int base = inc - mine;
   for (int q = 0; q < tid / kWave; ++q) base += wave_total[q];
-  if (tid < local) {
+  if (tid < a.local) {
     if (c == 0) {
-      seg_off[tid] = base;
-      if (tid == local - 1) seg_off[local] = base + mine;
+      a.seg_off[tid] = base;
+      if (tid == a.local - 1) a.seg_off[a.local] = base + mine;
     }
-    before[first + tid] += base;  // first pair row of (this chunk, expert)
+    before[a.first + tid] += base;
+  }
+  const int64_t t0 = (int64_t)c * a.C;
+  const int n = (int)(min(t0 + a.C, (int64_t)a.T) - t0) * a.K;
+  for (int i = tid; i < n; i += kRouteThreads) {
+    const int e = a.idx[t0 * a.K + i], l = e - a.first, t = i / a.K;
+    if (e >= 0 && l >= 0 && l < a.local) atomicOr(&bits[(t >> 5) * a.local + l], 1u << (t & 31));
   }
   __syncthreads();
-  const int64_t t0 = (int64_t)c * C;
-  const int n = (int)(min(t0 + C, (int64_t)T) - t0) * K;
   for (int i = tid; i < n; i += kRouteThreads) {
-    const int e = idx[t0 * K + i], l = e - first, t = i / K;
-    if (e >= 0 && l >= 0 && l < local) atomicOr(&bits[(t >> 5) * local + l], 1u << (t & 31));
-  }
-  __syncthreads();
-  for (int i = tid; i < n; i += kRouteThreads) {
-    const int e = idx[t0 * K + i], l = e - first, t = i / K;
+    const int e = a.idx[t0 * a.K + i], l = e - a.first, t = i / a.K;
     int row = -1;
-    if (e >= 0 && l >= 0 && l < local) {
-      row = before[e] + __popc(bits[(t >> 5) * local + l] & ((1u << (t & 31)) - 1u));
-      for (int q = 0; q < (t >> 5); ++q) row += __popc(bits[q * local + l]);
-      tok[row] = (int32_t)(t0 + t);
-      slot[row] = i - t * K;
-      alpha[row] = w[t0 * K + i];
+    if (e >= 0 && l >= 0 && l < a.local) {
+      row = before[e] + __popc(bits[(t >> 5) * a.local + l] & ((1u << (t & 31)) - 1u));
+      for (int q = 0; q < (t >> 5); ++q) row += __popc(bits[q * a.local + l]);
+      a.tok[row] = (int32_t)(t0 + t);
+      a.slot[row] = i - t * a.K;
+      a.alpha[row] = a.w[t0 * a.K + i];
     }
-    pmap[t0 * K + i] = row;
+    a.pmap[t0 * a.K + i] = row;
   }
+}
+
+// One block per chunk of tokens: the K largest logits of each, their weights, and how often the
+// chunk chose each expert. With a single chunk (ONE) the block places the pairs itself.
+template <class Lay, bool ONE>
+__global__ __launch_bounds__(kRouteThreads) void route_topk_kernel(RouteArgs a) {
+  constexpr int L = Lay::L, V = Lay::V, kGroups = kRouteThreads / L;
+  constexpr int S = (32 + L - 1) / L;  // slots that a lane keeps: k = lane, lane + L
+  __shared__ int cnt[1024];
+  for (int e = threadIdx.x; e < a.E; e += kRouteThreads) cnt[e] = 0;
+  __syncthreads();
+  const int lane = threadIdx.x & (L - 1), group = threadIdx.x / L;
+  const int64_t t0 = (int64_t)blockIdx.x * a.C, t1 = min(t0 + a.C, (int64_t)a.T);
+  for (int64_t tb = t0; tb < t1; tb += kGroups) {
+    const int64_t t = tb + group;
+    const bool in = t < t1;
+    float x[V];
+    Lay::load(a.logits, t, a.E, in && unmasked(a.mask, t), lane, x);
+    float top = kNegInf, Z = 0.0f;
+    if (!a.renorm) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) top = fmaxf(top, x[v]);
+      top = group_max<L>(top);
+#pragma unroll
+      for (int v = 0; v < V; ++v) Z += x[v] > kNegInf ? expf(x[v] - top) : 0.0f;
+      Z = group_sum<L>(Z);
+    }
+    // slot k: the largest value left, and the lowest index that has it
+    int my_e[S];
+    float my_x[S];
+#pragma unroll
+    for (int q = 0; q < S; ++q) my_e[q] = -1, my_x[q] = kNegInf;
+    for (int k = 0; k < a.K; ++k) {
+      float best = kNegInf;
+#pragma unroll
+      for (int v = 0; v < V; ++v) best = fmaxf(best, x[v]);
+      best = group_max<L>(best);
+      if (k == 0) top = best;
+      int at = 1 << 30;
+      bool hit[V], found = false;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {  // the lane's first value that is the best
+        const bool eq = x[v] == best;
+        hit[v] = eq && !found;
+        found = found || eq;
+        at = hit[v] ? Lay::expert(lane, v) : at;
+      }
+      const int win = group_min<L>(at);
+      const bool mine = at == win;
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[v] = hit[v] && mine ? kNegInf : x[v];
+#pragma unroll
+      for (int q = 0; q < S; ++q)
+        if (lane + q * L == k) {
+          my_e[q] = best > kNegInf ? win : -1;
+          my_x[q] = best;
+        }
+    }
+    float p[S], sum = 0.0f;
+#pragma unroll
+    for (int q = 0; q < S; ++q) {
+      p[q] = my_e[q] >= 0 ? expf(my_x[q] - top) : 0.0f;
+      sum += p[q];
+    }
+    if (a.renorm) Z = group_sum<L>(sum);
+#pragma unroll
+    for (int q = 0; q < S; ++q) {
+      const int k = lane + q * L;
+      if (in && k < a.K) {
+        a.idx[t * a.K + k] = my_e[q];
+        a.w[t * a.K + k] = my_e[q] >= 0 ? a.scale * (p[q] / Z) : 0.0f;
+        if (my_e[q] >= 0) atomicAdd(&cnt[my_e[q]], 1);
+      }
+    }
+  }
+  __syncthreads();
+  if (ONE) {
+    __shared__ int before[1024];
+    extern __shared__ uint32_t bits[];
+    for (int e = threadIdx.x; e < a.E; e += kRouteThreads) before[e] = 0;
+    __syncthreads();
+    place_chunk(a, 0, cnt, before, bits);
+  } else {
+    for (int e = threadIdx.x; e < a.E; e += kRouteThreads) a.hist[(int64_t)blockIdx.x * a.E + e] = cnt[e];
+  }
+}
+
+// One block per chunk: sums every chunk's histogram itself (they are in L2, at most 256 of them up
+// to T = 262144), which saves a launch that scans them. Thread: one expert, every stripes-th chunk.
+__global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs a, int log_e) {
+  __shared__ int total[1024], before[1024];
+  extern __shared__ uint32_t bits[];  // [C / 32][local]
+  const int tid = threadIdx.x, c = blockIdx.x;
+  for (int e = tid; e < a.E; e += kRouteThreads) total[e] = before[e] = 0;
+  __syncthreads();
+  const int e = tid & ((1 << log_e) - 1), stripes = kRouteThreads >> log_e;
+  if (e < a.E) {
+    int sum = 0, low = 0;
+#pragma unroll 8
+    for (int ch = tid >> log_e; ch < a.chunks; ch += stripes) {
+      const int h = a.hist[(int64_t)ch * a.E + e];
+      sum += h;
+      low += ch < c ? h : 0;
+    }
+    atomicAdd(&total[e], sum);
+    atomicAdd(&before[e], low);
+  }
+  __syncthreads();
+  place_chunk(a, c, total, before, bits);
 }
 
 // ---------------------------------------------------------------- balance loss
@@ -240,14 +344,15 @@ struct BalanceWs {
   float* psum;     // [tiles][E] sums of probabilities
   int32_t* count;  // [tiles][E]
   int32_t* live;   // [tiles]
-  double* dot;     // [n_seq] sum_e counts psum
+  double* dot;     // [n_seq][parts] sum_e counts psum over 64 experts
   int32_t* n;      // [n_seq] live tokens
+  uint32_t* done;  // join blocks that are through
 };
 
 int64_t balance_tiles(const lrmoe_router* r, int32_t n_seq) { return r->T / kBalTile + n_seq; }
 
 size_t balance_layout(const lrmoe_router* r, int32_t n_seq, char* base, BalanceWs* out) {
-  const size_t tiles = (size_t)balance_tiles(r, n_seq);
+  const size_t tiles = (size_t)balance_tiles(r, n_seq), parts = (size_t)ceil_div(r->E, kWave);
   size_t at = 0;
   auto take = [&](size_t b) {
     char* p = base + at;
@@ -258,23 +363,25 @@ size_t balance_layout(const lrmoe_router* r, int32_t n_seq, char* base, BalanceW
   w.psum = (float*)take(tiles * r->E * 4);
   w.count = (int32_t*)take(tiles * r->E * 4);
   w.live = (int32_t*)take(tiles * 4);
-  w.dot = (double*)take((size_t)n_seq * 8);
+  w.dot = (double*)take((size_t)n_seq * parts * 8);
   w.n = (int32_t*)take((size_t)n_seq * 4);
+  w.done = (uint32_t*)take(4);
   if (out) *out = w;
   return at;
 }
 
-template <int L, int V, bool BF16>
+template <class Lay>
 __global__ __launch_bounds__(kBalThreads) void balance_tile_kernel(int T, int E, int K, int n_seq,
                                                                    const void* __restrict__ logits,
                                                                    const uint8_t* __restrict__ mask,
                                                                    const int32_t* __restrict__ idx,
                                                                    const int64_t* __restrict__ off, BalanceWs ws) {
-  constexpr int kGroups = kBalThreads / L;
+  constexpr int L = Lay::L, V = Lay::V, kGroups = kBalThreads / L;
   __shared__ int cnt[1024];
   __shared__ float part[kGroups][L * V];
   __shared__ int live_of[kBalTile];
   const int64_t b = blockIdx.x;
+  if (b == 0 && threadIdx.x == 0) *ws.done = 0;
   const int s = off ? seq_of_tile(off, n_seq, T, b) : 0;
   int64_t lo, hi;
   seq_range(off, s, T, &lo, &hi);
@@ -289,7 +396,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_tile_kernel(int T, int E,
   for (int64_t tb = lo; tb < hi; tb += kGroups) {
     const int64_t t = tb + group;
     float x[V], top = kNegInf, Z = 0.0f;
-    load_row<L, V, BF16>(logits, mask, t, E, t < hi, lane, x);
+    Lay::load(logits, t, E, t < hi && unmasked(mask, t), lane, x);
 #pragma unroll
     for (int v = 0; v < V; ++v) top = fmaxf(top, x[v]);
     top = group_max<L>(top);
@@ -306,7 +413,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_tile_kernel(int T, int E,
     if (lane == 0 && t < hi) live_of[t - lo] = live ? 1 : 0;
   }
 #pragma unroll
-  for (int v = 0; v < V; ++v) part[group][expert_of<L, V>(lane, v)] = acc[v];
+  for (int v = 0; v < V; ++v) part[group][Lay::expert(lane, v)] = acc[v];
   __syncthreads();
   const int n = (int)(hi - lo) * K;
   for (int i = threadIdx.x; i < n; i += kBalThreads) {
@@ -321,67 +428,91 @@ __global__ __launch_bounds__(kBalThreads) void balance_tile_kernel(int T, int E,
     ws.psum[b * E + e] = a;
     ws.count[b * E + e] = cnt[e];
   }
-  if (threadIdx.x == 0) {
-    int a = 0;
-    for (int i = 0; i < (int)(hi - lo); ++i) a += live_of[i];
-    ws.live[b] = a;
+  if (threadIdx.x < kBalTile) {
+    const unsigned long long on = __ballot(threadIdx.x < hi - lo && live_of[threadIdx.x] != 0);
+    if (threadIdx.x == 0) ws.live[b] = __popcll(on);
   }
 }
 
-__device__ __forceinline__ double block_sum(double v, double* sh) {  // kBalThreads threads, all get the sum
+constexpr int kJoinThreads = 1024, kJoinWaves = kJoinThreads / kWave;
+
+__device__ __forceinline__ double block_sum(double v, double* sh) {  // kJoinThreads threads, all get the sum
   v = wave_sum(v);
   if ((threadIdx.x & (kWave - 1)) == 0) sh[threadIdx.x / kWave] = v;
   __syncthreads();
   double a = 0.0;
-  for (int i = 0; i < kBalThreads / kWave; ++i) a += sh[i];
+  for (int i = 0; i < kJoinWaves; ++i) a += sh[i];
   __syncthreads();
   return a;
 }
 
-// One block per sequence: its tiles joined in order.
-__global__ __launch_bounds__(kBalThreads) void balance_join_kernel(int T, int E, const int64_t* __restrict__ off,
-                                                                   BalanceWs ws, int32_t* __restrict__ counts,
-                                                                   float* __restrict__ psum) {
-  __shared__ double sh[kBalThreads / kWave];
-  const int s = blockIdx.x;
+// Grid (sequence, 64 experts): the sequence's tiles joined, wavefront by wavefront and then over
+// the wavefronts, always in the same order. The block that finishes last sums the loss; it reads
+// what the others wrote behind their release, in a fixed order, so the result does not depend on
+// which block it is.
+__global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(int T, int E, int K, int n_seq, float coef,
+                                                                    const int64_t* __restrict__ off, BalanceWs ws,
+                                                                    int32_t* __restrict__ counts,
+                                                                    float* __restrict__ psum, float* __restrict__ norm,
+                                                                    float* __restrict__ loss) {
+  __shared__ double sh[kJoinWaves], sum_of[kJoinWaves][kWave];
+  __shared__ int n_of[kJoinWaves][kWave];
+  __shared__ bool last;
+  const int s = blockIdx.x, part = blockIdx.y, parts = gridDim.y;
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, e = part * kWave + lane;
   int64_t lo, hi;
   seq_range(off, s, T, &lo, &hi);
   const int64_t b0 = first_tile(lo, s);
   const int tiles = (int)((hi - lo + kBalTile - 1) / kBalTile);
-  double dot = 0.0;
-  for (int e = threadIdx.x; e < E; e += kBalThreads) {
-    double a = 0.0;
-    int n = 0;
-    for (int i = 0; i < tiles; ++i) {
+  double a = 0.0;
+  int n = 0;
+  if (e < E) {
+#pragma unroll 8
+    for (int i = wave; i < tiles; i += kJoinWaves) {
       a += (double)ws.psum[(b0 + i) * E + e];
       n += ws.count[(b0 + i) * E + e];
     }
+  }
+  sum_of[wave][lane] = a;
+  n_of[wave][lane] = n;
+  int live = 0;
+  if (part == 0)
+    for (int i = threadIdx.x; i < tiles; i += kJoinThreads) live += ws.live[b0 + i];
+  __syncthreads();
+  double dot = 0.0;
+  if (wave == 0 && e < E) {
+    a = 0.0;
+    n = 0;
+    for (int q = 0; q < kJoinWaves; ++q) {
+      a += sum_of[q][lane];
+      n += n_of[q][lane];
+    }
     psum[(int64_t)s * E + e] = (float)a;
     counts[(int64_t)s * E + e] = n;
-    dot += a * n;
+    dot = a * n;
   }
-  double live = 0.0;
-  for (int i = threadIdx.x; i < tiles; i += kBalThreads) live += ws.live[b0 + i];
-  dot = block_sum(dot, sh);
-  live = block_sum(live, sh);
+  dot = wave_sum(dot);
+  const double alive_tokens = block_sum((double)live, sh);  // exact: whole numbers
   if (threadIdx.x == 0) {
-    ws.dot[s] = dot;
-    ws.n[s] = (int)live;
+    __hip_atomic_store(&ws.dot[(int64_t)s * parts + part], dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (part == 0) __hip_atomic_store(&ws.n[s], (int)alive_tokens, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const uint32_t before = __hip_atomic_fetch_add(ws.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    last = before == gridDim.x * gridDim.y - 1;
   }
-}
-
-__global__ __launch_bounds__(kBalThreads) void balance_loss_kernel(int E, int K, int n_seq, float coef, BalanceWs ws,
-                                                                   float* __restrict__ norm,
-                                                                   float* __restrict__ loss) {
-  __shared__ double sh[kBalThreads / kWave];
+  __syncthreads();
+  if (!last) return;
   double alive = 0.0, sum = 0.0;
-  for (int s = threadIdx.x; s < n_seq; s += kBalThreads) alive += ws.n[s] > 0 ? 1.0 : 0.0;
+  for (int i = threadIdx.x; i < n_seq; i += kJoinThreads)
+    alive += __hip_atomic_load(&ws.n[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) > 0 ? 1.0 : 0.0;
   alive = block_sum(alive, sh);
-  for (int s = threadIdx.x; s < n_seq; s += kBalThreads) {
-    const double n = ws.n[s];
-    const double f = n > 0 ? (double)coef * E / (alive * K * n * n) : 0.0;
-    norm[s] = (float)f;
-    sum += f * ws.dot[s];
+  for (int i = threadIdx.x; i < n_seq; i += kJoinThreads) {
+    const double m = __hip_atomic_load(&ws.n[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const double f = m > 0 ? (double)coef * E / (alive * K * m * m) : 0.0;
+    norm[i] = (float)f;
+    double d = 0.0;
+    for (int q = 0; q < parts; ++q)
+      d += __hip_atomic_load(&ws.dot[(int64_t)i * parts + q], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    sum += f * d;
   }
   sum = block_sum(sum, sh);
   if (threadIdx.x == 0) loss[0] = (float)sum;
@@ -391,17 +522,18 @@ __global__ __launch_bounds__(kBalThreads) void balance_loss_kernel(int E, int K,
 
 constexpr int kGradThreads = 256;
 
-template <int L, int V, bool BF16>
+template <class Lay>
 __global__ __launch_bounds__(kGradThreads) void route_bwd_kernel(
     int T, int E, int K, int renorm, float scale, const void* __restrict__ logits, const uint8_t* __restrict__ mask,
     const int32_t* __restrict__ idx, const float* __restrict__ dalpha, const int32_t* __restrict__ pmap,
     int64_t n_pairs, const int64_t* __restrict__ off, int n_seq, const int32_t* __restrict__ counts,
     const float* __restrict__ norm, const float* __restrict__ gloss, void* __restrict__ dlogits) {
+  constexpr int L = Lay::L, V = Lay::V;
   const int lane = threadIdx.x & (L - 1);
   const int64_t t = (int64_t)blockIdx.x * (kGradThreads / L) + threadIdx.x / L;
   const bool in = t < T;
   float x[V], p[V], dx[V], top = kNegInf, Z = 0.0f;
-  load_row<L, V, BF16>(logits, mask, t, E, in, lane, x);
+  Lay::load(logits, t, E, in && unmasked(mask, t), lane, x);
 #pragma unroll
   for (int v = 0; v < V; ++v) top = fmaxf(top, x[v]);
   top = group_max<L>(top);
@@ -435,7 +567,7 @@ __global__ __launch_bounds__(kGradThreads) void route_bwd_kernel(
       }
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        if (e >= 0 && expert_of<L, V>(lane, v) == e && x[v] > kNegInf) {
+        if (e >= 0 && Lay::expert(lane, v) == e && x[v] > kNegInf) {
           y[v] = scale * d;
           chosen |= 1u << v;
         }
@@ -481,7 +613,7 @@ __global__ __launch_bounds__(kGradThreads) void route_bwd_kernel(
     float c[V], dot = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int e = expert_of<L, V>(lane, v);
+      const int e = Lay::expert(lane, v);
       c[v] = on && e < E ? (float)counts[(int64_t)s * E + e] : 0.0f;
       dot += p[v] * c[v];
     }
@@ -494,13 +626,8 @@ __global__ __launch_bounds__(kGradThreads) void route_bwd_kernel(
   }
   if (!in) return;
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = expert_of<L, V>(lane, v);
-    if (e >= E) continue;
-    const float d = live ? dx[v] : 0.0f;
-    if (BF16) ((uint16_t*)dlogits)[t * E + e] = (uint16_t)pack_bf16x2(d, 0.0f);
-    else ((float*)dlogits)[t * E + e] = d;
-  }
+  for (int v = 0; v < V; ++v) dx[v] = live ? dx[v] : 0.0f;
+  Lay::store(dlogits, t, E, lane, dx);
 }
 
 // ---------------------------------------------------------------- gradient of the routing weights
@@ -546,15 +673,22 @@ __global__ __launch_bounds__(kAlphaThreads) void alpha_grad_kernel(int T, int K,
   }
 }
 
-// Calls f(L, V) as compile-time values for E experts.
+// Calls f with the layout for E experts and the logits' type: sixteen lanes to a token up to 256
+// experts (16 in each lane), so that a wavefront takes four tokens and reduces them together.
+template <bool BF16, bool VEC, class F>
+void by_experts(int E, F&& f) {
+  if (E <= 64) f(Layout<16, 4, BF16, VEC>());
+  else if (E <= 128) f(Layout<16, 8, BF16, VEC>());
+  else if (E <= 256) f(Layout<16, 16, BF16, VEC>());
+  else if (E <= 512) f(Layout<32, 16, BF16, VEC>());
+  else f(Layout<64, 16, BF16, VEC>());
+}
 template <class F>
-lrmoe_status by_experts(int E, F&& f) {
-  const int v = (int)ceil_div(E, kWave);
-  if (v <= 1) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 1>());
-  if (v <= 2) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 2>());
-  if (v <= 4) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 4>());
-  if (v <= 8) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 8>());
-  return f(std::integral_constant<int, 64>(), std::integral_constant<int, 16>());
+lrmoe_status by_layout(const lrmoe_router* r, F&& f) {
+  const bool vec = r->E % 4 == 0;
+  if (r->dtype == LRMOE_BF16) vec ? by_experts<true, true>(r->E, f) : by_experts<true, false>(r->E, f);
+  else vec ? by_experts<false, true>(r->E, f) : by_experts<false, false>(r->E, f);
+  return launch_status();
 }
 
 }  // namespace
@@ -568,22 +702,18 @@ lrmoe_status launch_route(const lrmoe_router* r, const void* logits, const uint8
                           int32_t* pmap, void* ws, hipStream_t s) {
   const int C = route_chunk(r);
   const int chunks = (int)ceil_div(r->T, C);
-  int32_t* hist = (int32_t*)ws;
-  if (chunks > 0) {
-    by_experts(r->E, [&](auto l, auto v) {
-      constexpr int L = decltype(l)::value, V = decltype(v)::value;
-      if (r->dtype == LRMOE_BF16)
-        route_topk_kernel<L, V, true><<<chunks, kRouteThreads, 0, s>>>(r->T, r->E, r->K, C, r->renorm, r->scale,
-                                                                       logits, mask, idx, w, hist);
-      else
-        route_topk_kernel<L, V, false><<<chunks, kRouteThreads, 0, s>>>(r->T, r->E, r->K, C, r->renorm, r->scale,
-                                                                        logits, mask, idx, w, hist);
-      return LRMOE_OK;
-    });
-    if (launch_status() != LRMOE_OK) return LRMOE_ERR_HIP;
-  }
-  route_place_kernel<<<std::max(1, chunks), kRouteThreads, (size_t)C / 8 * r->local, s>>>(
-      r->T, r->E, r->K, C, chunks, r->first, r->local, hist, idx, w, counts, seg_off, tok, slot, alpha, pmap);
+  const RouteArgs a{r->T, r->E, r->K, C, chunks, r->first, r->local, r->renorm, r->scale, logits, mask, (int32_t*)ws,
+                    idx, counts, tok, slot, pmap, w, alpha, seg_off};
+  const size_t bits = (size_t)C / 8 * r->local;
+  if (chunks == 1)
+    return by_layout(r, [&](auto lay) { route_topk_kernel<decltype(lay), true><<<1, kRouteThreads, bits, s>>>(a); });
+  if (chunks > 1 &&
+      by_layout(r, [&](auto lay) { route_topk_kernel<decltype(lay), false><<<chunks, kRouteThreads, 0, s>>>(a); }) !=
+          LRMOE_OK)
+    return LRMOE_ERR_HIP;
+  int log_e = 0;
+  while ((1 << log_e) < r->E) ++log_e;
+  route_place_kernel<<<std::max(1, chunks), kRouteThreads, bits, s>>>(a, log_e);
   return launch_status();
 }
 
@@ -594,23 +724,13 @@ lrmoe_status launch_balance_loss(const lrmoe_router* r, const void* logits, cons
                                  float* norm, float* loss, void* ws, hipStream_t s) {
   BalanceWs b;
   balance_layout(r, n_seq, (char*)ws, &b);
-  if (r->T > 0) {
-    const unsigned tiles = (unsigned)balance_tiles(r, n_seq);
-    by_experts(r->E, [&](auto l, auto v) {
-      constexpr int L = decltype(l)::value, V = decltype(v)::value;
-      if (r->dtype == LRMOE_BF16)
-        balance_tile_kernel<L, V, true><<<tiles, kBalThreads, 0, s>>>(r->T, r->E, r->K, n_seq, logits, mask, idx,
-                                                                      seq_off_d, b);
-      else
-        balance_tile_kernel<L, V, false><<<tiles, kBalThreads, 0, s>>>(r->T, r->E, r->K, n_seq, logits, mask, idx,
-                                                                       seq_off_d, b);
-      return LRMOE_OK;
-    });
-    if (launch_status() != LRMOE_OK) return LRMOE_ERR_HIP;
-  }
-  balance_join_kernel<<<n_seq, kBalThreads, 0, s>>>(r->T, r->E, seq_off_d, b, counts, psum);
-  if (launch_status() != LRMOE_OK) return LRMOE_ERR_HIP;
-  balance_loss_kernel<<<1, kBalThreads, 0, s>>>(r->E, r->K, n_seq, coef, b, norm, loss);
+  if (by_layout(r, [&](auto lay) {
+        balance_tile_kernel<decltype(lay)><<<(unsigned)balance_tiles(r, n_seq), kBalThreads, 0, s>>>(
+            r->T, r->E, r->K, n_seq, logits, mask, idx, seq_off_d, b);
+      }) != LRMOE_OK)
+    return LRMOE_ERR_HIP;
+  balance_join_kernel<<<dim3((unsigned)n_seq, (unsigned)ceil_div(r->E, kWave)), kJoinThreads, 0, s>>>(
+      r->T, r->E, r->K, n_seq, coef, seq_off_d, b, counts, psum, norm, loss);
   return launch_status();
 }
 
@@ -618,20 +738,12 @@ lrmoe_status launch_route_bwd(const lrmoe_router* r, const void* logits, const u
                               const float* dalpha, const int32_t* pmap, int64_t n_pairs, const int64_t* seq_off_d,
                               int32_t n_seq, const int32_t* counts, const float* norm, const float* gloss,
                               void* dlogits, hipStream_t s) {
-  by_experts(r->E, [&](auto l, auto v) {
-    constexpr int L = decltype(l)::value, V = decltype(v)::value;
-    const unsigned g = (unsigned)ceil_div(r->T, kGradThreads / L);
-    if (r->dtype == LRMOE_BF16)
-      route_bwd_kernel<L, V, true><<<g, kGradThreads, 0, s>>>(r->T, r->E, r->K, r->renorm, r->scale, logits, mask, idx,
-                                                              dalpha, pmap, n_pairs, seq_off_d, n_seq, counts, norm,
-                                                              gloss, dlogits);
-    else
-      route_bwd_kernel<L, V, false><<<g, kGradThreads, 0, s>>>(r->T, r->E, r->K, r->renorm, r->scale, logits, mask,
-                                                               idx, dalpha, pmap, n_pairs, seq_off_d, n_seq, counts,
-                                                               norm, gloss, dlogits);
-    return LRMOE_OK;
+  return by_layout(r, [&](auto lay) {
+    using Lay = decltype(lay);
+    route_bwd_kernel<Lay><<<(unsigned)ceil_div(r->T, kGradThreads / Lay::L), kGradThreads, 0, s>>>(
+        r->T, r->E, r->K, r->renorm, r->scale, logits, mask, idx, dalpha, pmap, n_pairs, seq_off_d, n_seq, counts, norm,
+        gloss, dlogits);
   });
-  return launch_status();
 }
 
 lrmoe_status launch_alpha_grad(const lrmoe_problem* p, const void* G, const void* Y, const float* alpha,
