@@ -45,8 +45,10 @@ def _ptr(t):
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # the handle alone: a torch.cuda.Stream object costs 3 us of host time per call
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _event(ev, stream=None):
@@ -465,10 +467,10 @@ def _want(t, name, shape, dtype, here):
     (None -> NULL)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape or t.get_device() != here:
-        raise ValueError(f"{name}: expected {dtype} of shape {tuple(shape)} on the current device, "
+    if t.dtype != dtype or t.shape != shape or t.get_device() != here or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {dtype} of shape {tuple(shape)} on the current device, "
                          f"got {t.dtype} of {tuple(t.shape)} on {t.device}")
-    return _ptr(t)
+    return t.data_ptr()
 
 
 def _flags(t, name, n, here):
@@ -488,7 +490,9 @@ def _outputs(given, wanted, device, here):
         t = o.get(name)
         if t is None:
             t = o[name] = torch.empty(shape, dtype=dt, device=device)
-        ptrs.append(_want(t, name, shape, dt, here))
+            ptrs.append(t.data_ptr())
+        else:
+            ptrs.append(_want(t, name, shape, dt, here))
     return o, ptrs
 
 
@@ -497,7 +501,7 @@ def route(r: Router, logits, mask=None, out=None, stream=None):
     seg_off [local + 1] (device; ``.cpu()`` of it is Problem's seg_off), tok, slot, alpha [T*K] (rows
     at and after seg_off[local] are not written) and pmap [T, K]. ``mask`` [T] uint8 or bool: 0
     leaves a token out. ``out`` reuses buffers."""
-    here = torch.cuda.current_device()
+    here = torch._C._cuda_getDevice()
     o, ptrs = _outputs(out, r._route_out, r.device, here)
     ws = r.workspace()
     _lib.check(library().lrmoe_route(r.ref, _want(logits, "logits", (r.T, r.E), r.torch_dtype, here),
@@ -528,7 +532,7 @@ def balance_loss(r: Router, logits, idx, coef=1.0, mask=None, seq_off=None, out=
     """Per-expert counts and the balance loss of every sequence (lrmoe_balance_loss): a dict of loss
     [1], counts, psum [n_seq, E] and norm [n_seq]. ``seq_off`` (int64 [n_seq + 1], host or device;
     None: one sequence of all tokens). ``route_bwd`` takes the result as ``balance``."""
-    here = torch.cuda.current_device()
+    here = torch._C._cuda_getDevice()
     off, S = _sequences(r, seq_off, here)
     o, ptrs = _outputs(out, (("counts", (S, r.E), torch.int32), ("psum", (S, r.E), torch.float32),
                              ("norm", (S,), torch.float32), ("loss", (1,), torch.float32)), r.device, here)
@@ -547,7 +551,7 @@ def route_bwd(r: Router, logits, idx, dalpha=None, pmap=None, balance=None, glos
     pair row with ``pmap`` (alpha_grad's result and route's map), else [T, K]. ``balance``: what
     balance_loss returned for these logits, with the same ``seq_off`` and ``mask``; ``gloss`` (device
     f32 [1] or None = 1): the gradient of its loss. Either part may be None."""
-    here = torch.cuda.current_device()
+    here = torch._C._cuda_getDevice()
     shape = (r.T, r.E)
     off, S = _sequences(r, seq_off, here) if balance is not None else (None, 1)
     if out is None:
@@ -573,7 +577,7 @@ def route_bwd(r: Router, logits, idx, dalpha=None, pmap=None, balance=None, glos
 def alpha_grad(p: Problem, G, Y, alpha, pmap, keep=None, out=None, stream=None):
     """Gradient of the N pairs' routing weights from expert_forward's rows Y and the output's
     gradient G (lrmoe_alpha_grad); ``pmap`` [T, K] from route, ``keep`` [N] uint8 from select."""
-    here = torch.cuda.current_device()
+    here = torch._C._cuda_getDevice()
     if out is None:
         out = torch.empty(p.N, dtype=torch.float32, device=p.device)
     for name, t in (("alpha", alpha), ("out", out)):

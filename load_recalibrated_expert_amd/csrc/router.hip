@@ -20,6 +20,17 @@ __device__ __forceinline__ float clean(float x) {  // NaN -> -inf, +inf -> FLT_M
   return x != x ? kNegInf : fminf(x, kFltMax);
 }
 
+// exp(d) for d = x - max: d is at most 0, or NaN where both are -inf (a token that is not live). h + l is
+// d log2(e) to about 2^-48, so the error is that of the 2^h instruction and of d itself; below
+// -104 it is 0. Half the instructions of expf, whose range checks are not needed here.
+__device__ __forceinline__ float exp_below(float d) {
+  d = fmaxf(d, -104.0f);
+  const float h = d * 1.44269502f;
+  const float l = __builtin_fmaf(d, 1.92596303e-8f, __builtin_fmaf(d, 1.44269502f, -h));
+  const float r = __builtin_amdgcn_exp2f(h);
+  return __builtin_fmaf(r, l * 0.693147181f, r);
+}
+
 // Reductions over the L lanes of a token's group; every lane gets the result, the same bits in each.
 // Sixteen lanes are a DPP row: four rotations at register speed instead of cross-lane permutes
 // through LDS (an 8-slot top-K over 128 experts: 46 us with permutes, 17 us so, T = 32768).
@@ -94,9 +105,27 @@ struct Layout {
       for (int v = 0; v < V; ++v) {
         const int e = expert(lane, v);
         x[v] = kNegInf;
-        if (on && e < E)
-          x[v] = clean(BF16 ? __uint_as_float((uint32_t)((const uint16_t*)logits)[t * E + e] << 16)
-                            : ((const float*)logits)[t * E + e]);
+        if (on && e < E) x[v] = load_one(logits, t * E + e);
+      }
+    }
+  }
+  static __device__ __forceinline__ float load_one(const void* __restrict__ logits, int64_t i) {
+    return clean(BF16 ? __uint_as_float((uint32_t)((const uint16_t*)logits)[i] << 16) : ((const float*)logits)[i]);
+  }
+  // Row s of the [n_seq x E] counts, zeros beyond E and where `on` is false.
+  static __device__ __forceinline__ void load_counts(const int32_t* __restrict__ counts, int64_t s, int E, bool on,
+                                                     int lane, float c[V]) {
+#pragma unroll
+    for (int q = 0; q < V; q += VEC ? 4 : 1) {
+      const int e = expert(lane, q);
+      if (VEC) {
+        const int4 n = on && e < E ? *(const int4*)(counts + s * E + e) : make_int4(0, 0, 0, 0);
+        c[q] = (float)n.x;
+        c[q + 1] = (float)n.y;
+        c[q + 2] = (float)n.z;
+        c[q + 3] = (float)n.w;
+      } else {
+        c[q] = on && e < E ? (float)counts[s * E + e] : 0.0f;
       }
     }
   }
@@ -128,31 +157,39 @@ __device__ __forceinline__ bool unmasked(const uint8_t* __restrict__ mask, int64
 // ---------------------------------------------------------------- routing
 
 constexpr int kRouteThreads = 1024;
+constexpr int kOneChunk = 128;  // up to so many tokens one block does the whole call
 
-// Tokens per chunk: one bit per (chunk token, local expert) has to fit 48 KB of LDS, and the
-// placing blocks each read the histograms of all chunks, so there are few of them.
-int route_chunk(const lrmoe_router* r) {
-  int c = 128;
-  while (ceil_div(r->T, c) > 256 && c < 1024 && (int64_t)r->local * c * 2 / 8 <= 48 * 1024) c *= 2;
-  return c;
+// Tokens of one top-K block (`sub`, a histogram row each) and of one placing block (`chunk`). A placing
+// block holds a bit per (token, local expert) in 48 KB of LDS and reads all rows, so sub grows
+// until there are at most 512 of them, as far as a chunk may.
+void route_sizes(const lrmoe_router* r, int* sub, int* chunk) {
+  int most = 1024;
+  while (most > 64 && (int64_t)r->local * most / 8 > 48 * 1024) most /= 2;
+  int c = 64;
+  while (c < most && ceil_div(r->T, c) > 512) c *= 2;
+  *sub = c;
+  *chunk = std::min(2 * c, most);
+  if (r->T <= kOneChunk) *sub = *chunk = kOneChunk;
 }
 
 struct RouteArgs {
-  int T, E, K, C, chunks, first, local, renorm;
+  int T, E, K, sub, C, rows, first, local, renorm;
   float scale;
   const void* logits;
   const uint8_t* mask;
-  int32_t* hist;  // [chunks][E] tokens of each chunk per expert
+  int32_t* hist;  // [rows][E4] tokens of each sub-chunk per expert, E4 = E rounded up to 4, zeros behind E
   int32_t *idx, *counts, *tok, *slot, *pmap;
   float *w, *alpha;
   int64_t* seg_off;
 };
 
-// Pair rows of one chunk. total, before (LDS, [E]): tokens per expert in all chunks and in the
-// chunks before this one; before becomes the first row of (chunk, expert). The rank of a pair in
-// its chunk is the number of lower set bits among its expert's token bits, so no order of atomics
-// enters the result.
-__device__ __forceinline__ void place_chunk(const RouteArgs& a, int c, const int* total, int* before, uint32_t* bits) {
+// Pair rows of the n = tokens * K slots of one chunk, whose experts and weights e_of(i), w_of(i) gives.
+// total, before (LDS, [E]): tokens per expert in all chunks and in the chunks before this one; before
+// becomes the first row of (chunk, expert). The rank of a pair in its chunk is the number of lower
+// set bits among its expert's token bits, so no order of atomics enters the result.
+template <class EOf, class WOf>
+__device__ __forceinline__ void place_chunk(const RouteArgs& a, int c, int n, const int* total, int* before,
+                                            uint32_t* bits, EOf e_of, WOf w_of) {
   __shared__ int wave_total[kRouteThreads / kWave];
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   if (c == 0)
@@ -166,7 +203,6 @@ __device__ __forceinline__ void place_chunk(const RouteArgs& a, int c, const int
     if (lane >= o) inc += up;
   }
   if (lane == kWave - 1) wave_total[tid / kWave] = inc;
-  for (int i = tid; i < a.C / 32 * a.local; i += kRouteThreads) bits[i] = 0;
   __syncthreads();
   int base = inc - mine;
   for (int q = 0; q < tid / kWave; ++q) base += wave_total[q];
@@ -177,50 +213,63 @@ __device__ __forceinline__ void place_chunk(const RouteArgs& a, int c, const int
     }
     before[a.first + tid] += base;
   }
-  const int64_t t0 = (int64_t)c * a.C;
-  const int n = (int)(min(t0 + a.C, (int64_t)a.T) - t0) * a.K;
   for (int i = tid; i < n; i += kRouteThreads) {
-    const int e = a.idx[t0 * a.K + i], l = e - a.first, t = i / a.K;
+    const int e = e_of(i), l = e - a.first, t = i / a.K;
     if (e >= 0 && l >= 0 && l < a.local) atomicOr(&bits[(t >> 5) * a.local + l], 1u << (t & 31));
   }
   __syncthreads();
+  const int64_t t0 = (int64_t)c * a.C;
   for (int i = tid; i < n; i += kRouteThreads) {
-    const int e = a.idx[t0 * a.K + i], l = e - a.first, t = i / a.K;
+    const int e = e_of(i), l = e - a.first, t = i / a.K;
     int row = -1;
     if (e >= 0 && l >= 0 && l < a.local) {
       row = before[e] + __popc(bits[(t >> 5) * a.local + l] & ((1u << (t & 31)) - 1u));
       for (int q = 0; q < (t >> 5); ++q) row += __popc(bits[q * a.local + l]);
       a.tok[row] = (int32_t)(t0 + t);
       a.slot[row] = i - t * a.K;
-      a.alpha[row] = a.w[t0 * a.K + i];
+      a.alpha[row] = w_of(i);
     }
     a.pmap[t0 * a.K + i] = row;
   }
 }
 
-// One block per chunk of tokens: the K largest logits of each, their weights, and how often the
-// chunk chose each expert. With a single chunk (ONE) the block places the pairs itself.
-template <class Lay, bool ONE>
+// One block per sub-chunk of tokens: the K largest logits of each, their weights, and how often the
+// sub-chunk chose each expert. With few tokens (rows = 1) the block places the pairs itself.
+template <class Lay>
 __global__ __launch_bounds__(kRouteThreads) void route_topk_kernel(RouteArgs a) {
   constexpr int L = Lay::L, V = Lay::V, kGroups = kRouteThreads / L;
   constexpr int S = (32 + L - 1) / L;  // slots that a lane keeps: k = lane, lane + L
-  __shared__ int cnt[1024];
-  for (int e = threadIdx.x; e < a.E; e += kRouteThreads) cnt[e] = 0;
-  __syncthreads();
+  extern __shared__ uint32_t lds[];
+  // [E] counts; with one block also [E] zeros, [C K] experts, [C K] weights, [C / 32][local] bits
+  int* cnt = (int*)lds;
+  const bool one = a.rows == 1;
+  int* before = cnt + a.E;
+  int* e_of = before + a.E;
+  float* w_of = (float*)(e_of + a.C * a.K);
+  uint32_t* bits = (uint32_t*)(w_of + a.C * a.K);
+  for (int e = threadIdx.x; e < (one ? 2 * a.E : a.E); e += kRouteThreads) cnt[e] = 0;
+  if (one)
+    for (int i = threadIdx.x; i < a.C / 32 * a.local; i += kRouteThreads) bits[i] = 0;
   const int lane = threadIdx.x & (L - 1), group = threadIdx.x / L;
-  const int64_t t0 = (int64_t)blockIdx.x * a.C, t1 = min(t0 + a.C, (int64_t)a.T);
+  const int64_t t0 = (int64_t)blockIdx.x * a.sub, t1 = min(t0 + a.sub, (int64_t)a.T);
+  float next[V];
+  Lay::load(a.logits, t0 + group, a.E, t0 + group < t1 && unmasked(a.mask, t0 + group), lane, next);
+  __syncthreads();
   for (int64_t tb = t0; tb < t1; tb += kGroups) {
     const int64_t t = tb + group;
     const bool in = t < t1;
     float x[V];
-    Lay::load(a.logits, t, a.E, in && unmasked(a.mask, t), lane, x);
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = next[v];
+    if (tb + kGroups < t1)  // the next pass's row, while this one is ranked
+      Lay::load(a.logits, t + kGroups, a.E, t + kGroups < t1 && unmasked(a.mask, t + kGroups), lane, next);
     float top = kNegInf, Z = 0.0f;
     if (!a.renorm) {
 #pragma unroll
       for (int v = 0; v < V; ++v) top = fmaxf(top, x[v]);
       top = group_max<L>(top);
 #pragma unroll
-      for (int v = 0; v < V; ++v) Z += x[v] > kNegInf ? expf(x[v] - top) : 0.0f;
+      for (int v = 0; v < V; ++v) Z += exp_below(x[v] - top);
       Z = group_sum<L>(Z);
     }
     // slot k: the largest value left, and the lowest index that has it
@@ -257,7 +306,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_topk_kernel(RouteArgs a) 
     float p[S], sum = 0.0f;
 #pragma unroll
     for (int q = 0; q < S; ++q) {
-      p[q] = my_e[q] >= 0 ? expf(my_x[q] - top) : 0.0f;
+      p[q] = my_e[q] >= 0 ? exp_below(my_x[q] - top) : 0.0f;
       sum += p[q];
     }
     if (a.renorm) Z = group_sum<L>(sum);
@@ -265,51 +314,65 @@ __global__ __launch_bounds__(kRouteThreads) void route_topk_kernel(RouteArgs a) 
     for (int q = 0; q < S; ++q) {
       const int k = lane + q * L;
       if (in && k < a.K) {
+        const float w = my_e[q] >= 0 ? a.scale * (p[q] / Z) : 0.0f;
         a.idx[t * a.K + k] = my_e[q];
-        a.w[t * a.K + k] = my_e[q] >= 0 ? a.scale * (p[q] / Z) : 0.0f;
+        a.w[t * a.K + k] = w;
+        if (one) {
+          e_of[t * a.K + k] = my_e[q];
+          w_of[t * a.K + k] = w;
+        }
         if (my_e[q] >= 0) atomicAdd(&cnt[my_e[q]], 1);
       }
     }
   }
   __syncthreads();
-  if (ONE) {
-    __shared__ int before[1024];
-    extern __shared__ uint32_t bits[];
-    for (int e = threadIdx.x; e < a.E; e += kRouteThreads) before[e] = 0;
-    __syncthreads();
-    place_chunk(a, 0, cnt, before, bits);
+  if (one) {
+    place_chunk(a, 0, a.T * a.K, cnt, before, bits, [&](int i) { return e_of[i]; }, [&](int i) { return w_of[i]; });
   } else {
-    for (int e = threadIdx.x; e < a.E; e += kRouteThreads) a.hist[(int64_t)blockIdx.x * a.E + e] = cnt[e];
+    const int E4 = (a.E + 3) & ~3;
+    for (int e = threadIdx.x; e < E4; e += kRouteThreads)
+      a.hist[(int64_t)blockIdx.x * E4 + e] = e < a.E ? cnt[e] : 0;
   }
 }
 
-// One block per chunk: sums every chunk's histogram itself (they are in L2, at most 256 of them up
-// to T = 262144), which saves a launch that scans them. Thread: one expert, every stripes-th chunk.
-__global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs a, int log_e) {
+// One block per chunk: sums all histogram rows itself (they are in L2), which saves a launch that scans
+// them. Thread: four experts, every stripes-th row.
+__global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs a, int log_q) {
   __shared__ int total[1024], before[1024];
   extern __shared__ uint32_t bits[];  // [C / 32][local]
   const int tid = threadIdx.x, c = blockIdx.x;
-  for (int e = tid; e < a.E; e += kRouteThreads) total[e] = before[e] = 0;
+  const int64_t i0 = (int64_t)c * a.C * a.K;
+  const int n = (int)(min((int64_t)(c + 1) * a.C, (int64_t)a.T) * a.K - i0);
+  const int e0 = tid < n ? a.idx[i0 + tid] : -1;  // on its way while the rows are summed
+  const float w0 = tid < n ? a.w[i0 + tid] : 0.0f;
+  total[tid] = before[tid] = 0;
+  for (int i = tid; i < a.C / 32 * a.local; i += kRouteThreads) bits[i] = 0;
   __syncthreads();
-  const int e = tid & ((1 << log_e) - 1), stripes = kRouteThreads >> log_e;
-  if (e < a.E) {
-    int sum = 0, low = 0;
+  const int E4 = (a.E + 3) & ~3, e = 4 * (tid & ((1 << log_q) - 1)), stripes = kRouteThreads >> log_q;
+  if (e < E4) {
+    int4 sum = make_int4(0, 0, 0, 0), low = sum;
+    const int mine = c * (a.C / a.sub);
 #pragma unroll 8
-    for (int ch = tid >> log_e; ch < a.chunks; ch += stripes) {
-      const int h = a.hist[(int64_t)ch * a.E + e];
-      sum += h;
-      low += ch < c ? h : 0;
+    for (int r = tid >> log_q; r < a.rows; r += stripes) {
+      const int4 h = *(const int4*)(a.hist + (int64_t)r * E4 + e);
+      const int m = r < mine ? -1 : 0;
+      sum.x += h.x, sum.y += h.y, sum.z += h.z, sum.w += h.w;
+      low.x += h.x & m, low.y += h.y & m, low.z += h.z & m, low.w += h.w & m;
     }
-    atomicAdd(&total[e], sum);
-    atomicAdd(&before[e], low);
+    atomicAdd(&total[e], sum.x), atomicAdd(&total[e + 1], sum.y);
+    atomicAdd(&total[e + 2], sum.z), atomicAdd(&total[e + 3], sum.w);
+    atomicAdd(&before[e], low.x), atomicAdd(&before[e + 1], low.y);
+    atomicAdd(&before[e + 2], low.z), atomicAdd(&before[e + 3], low.w);
   }
   __syncthreads();
-  place_chunk(a, c, total, before, bits);
+  place_chunk(
+      a, c, n, total, before, bits, [&](int i) { return i < kRouteThreads ? e0 : a.idx[i0 + i]; },
+      [&](int i) { return i < kRouteThreads ? w0 : a.w[i0 + i]; });
 }
 
 // ---------------------------------------------------------------- balance loss
 
-constexpr int kBalThreads = 256;
+constexpr int kBalThreads = 1024;
 constexpr int kBalTile = 64;  // tokens of one tile
 
 // Sequence s, clamped into [0, T] whatever the offsets hold.
@@ -370,15 +433,16 @@ size_t balance_layout(const lrmoe_router* r, int32_t n_seq, char* base, BalanceW
   return at;
 }
 
+// One block per tile slot; up to 512 experts every group of lanes has one token.
 template <class Lay>
 __global__ __launch_bounds__(kBalThreads) void balance_tile_kernel(int T, int E, int K, int n_seq,
                                                                    const void* __restrict__ logits,
                                                                    const uint8_t* __restrict__ mask,
                                                                    const int32_t* __restrict__ idx,
                                                                    const int64_t* __restrict__ off, BalanceWs ws) {
-  constexpr int L = Lay::L, V = Lay::V, kGroups = kBalThreads / L;
+  constexpr int L = Lay::L, V = Lay::V, kGroups = kBalThreads / L, kWaves = kBalThreads / kWave;
   __shared__ int cnt[1024];
-  __shared__ float part[kGroups][L * V];
+  __shared__ float part[kWaves][L * V];
   __shared__ int live_of[kBalTile];
   const int64_t b = blockIdx.x;
   if (b == 0 && threadIdx.x == 0) *ws.done = 0;
@@ -389,7 +453,8 @@ __global__ __launch_bounds__(kBalThreads) void balance_tile_kernel(int T, int E,
   hi = min(hi, lo + kBalTile);
   if (lo >= hi) return;  // a slot that no tile uses: the whole block leaves
   for (int e = threadIdx.x; e < E; e += kBalThreads) cnt[e] = 0;
-  const int lane = threadIdx.x & (L - 1), group = threadIdx.x / L;
+  const int lane = threadIdx.x & (L - 1), group = threadIdx.x / L, n = (int)(hi - lo) * K;
+  const int e0 = (int)threadIdx.x < n ? idx[lo * K + threadIdx.x] : -1;  // on its way meanwhile
   float acc[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] = 0.0f;
@@ -403,7 +468,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_tile_kernel(int T, int E,
     const bool live = top > kNegInf;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      x[v] = x[v] > kNegInf ? expf(x[v] - top) : 0.0f;
+      x[v] = exp_below(x[v] - top);
       Z += x[v];
     }
     Z = group_sum<L>(Z);
@@ -412,19 +477,25 @@ __global__ __launch_bounds__(kBalThreads) void balance_tile_kernel(int T, int E,
     for (int v = 0; v < V; ++v) acc[v] += x[v] * rz;
     if (lane == 0 && t < hi) live_of[t - lo] = live ? 1 : 0;
   }
+  // the wavefront's groups, then (below) the wavefronts
 #pragma unroll
-  for (int v = 0; v < V; ++v) part[group][Lay::expert(lane, v)] = acc[v];
+  for (int v = 0; v < V; ++v) {
+#pragma unroll
+    for (int o = L; o < kWave; o <<= 1) acc[v] += __shfl_xor(acc[v], o, kWave);
+  }
+  if ((threadIdx.x & (kWave - 1)) < L)
+#pragma unroll
+    for (int v = 0; v < V; ++v) part[threadIdx.x / kWave][Lay::expert(lane, v)] = acc[v];
   __syncthreads();
-  const int n = (int)(hi - lo) * K;
   for (int i = threadIdx.x; i < n; i += kBalThreads) {
-    const int e = idx[lo * K + i];
+    const int e = i < kBalThreads ? e0 : idx[lo * K + i];
     if (e >= 0 && e < E && live_of[i / K]) atomicAdd(&cnt[e], 1);
   }
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += kBalThreads) {
     float a = 0.0f;
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) a += part[g][e];
+    for (int g = 0; g < kWaves; ++g) a += part[g][e];
     ws.psum[b * E + e] = a;
     ws.count[b * E + e] = cnt[e];
   }
@@ -467,7 +538,7 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(int T, int E
   double a = 0.0;
   int n = 0;
   if (e < E) {
-#pragma unroll 8
+#pragma unroll 16
     for (int i = wave; i < tiles; i += kJoinWaves) {
       a += (double)ws.psum[(b0 + i) * E + e];
       n += ws.count[(b0 + i) * E + e];
@@ -522,6 +593,14 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(int T, int E
 
 constexpr int kGradThreads = 256;
 
+// The wavefront's LDS accesses before this point are done and seen by its other lanes.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// The K slots of a token are worked on in K lanes of its group, whose results reach the lanes that
+// hold their experts through a row of LDS.
 template <class Lay>
 __global__ __launch_bounds__(kGradThreads) void route_bwd_kernel(
     int T, int E, int K, int renorm, float scale, const void* __restrict__ logits, const uint8_t* __restrict__ mask,
@@ -529,18 +608,37 @@ __global__ __launch_bounds__(kGradThreads) void route_bwd_kernel(
     int64_t n_pairs, const int64_t* __restrict__ off, int n_seq, const int32_t* __restrict__ counts,
     const float* __restrict__ norm, const float* __restrict__ gloss, void* __restrict__ dlogits) {
   constexpr int L = Lay::L, V = Lay::V;
+  constexpr int S = (32 + L - 1) / L;  // slots of a lane: k = lane, lane + L
+  __shared__ float rows[kGradThreads / L][L * V];
   const int lane = threadIdx.x & (L - 1);
   const int64_t t = (int64_t)blockIdx.x * (kGradThreads / L) + threadIdx.x / L;
-  const bool in = t < T;
+  const bool in = t < T, on = in && unmasked(mask, t);
+  // the slots' loads start first: three of them depend on each other
+  int e[S];
+  float xe[S], y[S];
+  if (dalpha) {
+#pragma unroll
+    for (int q = 0; q < S; ++q) {
+      const int k = lane + q * L;
+      e[q] = on && k < K ? idx[t * K + k] : -1;
+      y[q] = 0.0f;
+      xe[q] = kNegInf;
+      if (e[q] >= 0 && e[q] < E) {
+        const int64_t j = pmap ? pmap[t * K + k] : t * K + k;
+        if (!pmap || (j >= 0 && j < n_pairs)) y[q] = scale * dalpha[j];
+        xe[q] = Lay::load_one(logits, t * E + e[q]);
+      }
+    }
+  }
   float x[V], p[V], dx[V], top = kNegInf, Z = 0.0f;
-  Lay::load(logits, t, E, in && unmasked(mask, t), lane, x);
+  Lay::load(logits, t, E, on, lane, x);
 #pragma unroll
   for (int v = 0; v < V; ++v) top = fmaxf(top, x[v]);
   top = group_max<L>(top);
   const bool live = top > kNegInf;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    p[v] = x[v] > kNegInf ? expf(x[v] - top) : 0.0f;
+    p[v] = exp_below(x[v] - top);
     Z += p[v];
     dx[v] = 0.0f;
   }
@@ -549,57 +647,45 @@ __global__ __launch_bounds__(kGradThreads) void route_bwd_kernel(
 #pragma unroll
   for (int v = 0; v < V; ++v) p[v] *= rz;
   if (dalpha) {
-    // y of every chosen expert, and which they are
-    float y[V];
-    uint32_t chosen = 0;
+    float* row = rows[threadIdx.x / L];
 #pragma unroll
-    for (int v = 0; v < V; ++v) y[v] = 0.0f;
-    for (int k = 0; k < K; ++k) {
-      const int e = in && live ? idx[t * K + k] : -1;
-      float d = 0.0f;
-      if (e >= 0) {
-        if (pmap) {
-          const int j = pmap[t * K + k];
-          d = j >= 0 && j < n_pairs ? dalpha[j] : 0.0f;
-        } else {
-          d = dalpha[t * K + k];
-        }
-      }
+    for (int v = 0; v < V; ++v) row[Lay::expert(lane, v)] = 0.0f;
+    float ref = top, r = rz, q_of[S], s = 0.0f;
+    if (renorm) {  // softmax over the chosen experts
+      ref = kNegInf;
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (e >= 0 && Lay::expert(lane, v) == e && x[v] > kNegInf) {
-          y[v] = scale * d;
-          chosen |= 1u << v;
-        }
+      for (int q = 0; q < S; ++q) ref = fmaxf(ref, xe[q]);
+      ref = group_max<L>(ref);
+      r = 1.0f;
     }
-    float q[V], s = 0.0f;
+#pragma unroll
+    for (int q = 0; q < S; ++q) q_of[q] = xe[q] > kNegInf ? exp_below(xe[q] - ref) * r : 0.0f;
     if (renorm) {
-      float ct = kNegInf, cz = 0.0f;
+      float z = 0.0f;
 #pragma unroll
-      for (int v = 0; v < V; ++v) ct = fmaxf(ct, (chosen >> v) & 1 ? x[v] : kNegInf);
-      ct = group_max<L>(ct);
+      for (int q = 0; q < S; ++q) z += q_of[q];
+      z = group_sum<L>(z);
+      r = z > 0.0f ? 1.0f / z : 0.0f;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        q[v] = (chosen >> v) & 1 ? expf(x[v] - ct) : 0.0f;
-        cz += q[v];
-      }
-      cz = group_sum<L>(cz);
-      const float rc = cz > 0.0f ? 1.0f / cz : 0.0f;
-#pragma unroll
-      for (int v = 0; v < V; ++v) q[v] *= rc;
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v) q[v] = p[v];
+      for (int q = 0; q < S; ++q) q_of[q] *= r;
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) s += (chosen >> v) & 1 ? q[v] * y[v] : 0.0f;
+    for (int q = 0; q < S; ++q) s += xe[q] > kNegInf ? q_of[q] * y[q] : 0.0f;
     s = group_sum<L>(s);
+    wave_sync();
 #pragma unroll
-    for (int v = 0; v < V; ++v) dx[v] = q[v] * (y[v] - s);
+    for (int q = 0; q < S; ++q)
+      if (xe[q] > kNegInf) row[e[q]] = renorm ? q_of[q] * (y[q] - s) : q_of[q] * y[q];
+    wave_sync();
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      dx[v] = row[Lay::expert(lane, v)];
+      if (!renorm) dx[v] -= p[v] * s;
+    }
   }
   if (norm) {
     int s = 0;
-    bool on = live;
+    bool inside = live;
     if (off && in) {  // the last sequence that starts at or before t
       int a = 0, z = n_seq - 1;
       while (a < z) {
@@ -608,18 +694,15 @@ __global__ __launch_bounds__(kGradThreads) void route_bwd_kernel(
         else z = m - 1;
       }
       s = a;
-      on = live && t >= off[s] && t < off[s + 1];
+      inside = live && t >= off[s] && t < off[s + 1];
     }
     float c[V], dot = 0.0f;
+    Lay::load_counts(counts, s, E, inside, lane, c);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = Lay::expert(lane, v);
-      c[v] = on && e < E ? (float)counts[(int64_t)s * E + e] : 0.0f;
-      dot += p[v] * c[v];
-    }
+    for (int v = 0; v < V; ++v) dot += p[v] * c[v];
     dot = group_sum<L>(dot);
-    const float f = on ? norm[s] * (gloss ? gloss[0] : 1.0f) : 0.0f;
-    if (on) {
+    const float f = inside ? norm[s] * (gloss ? gloss[0] : 1.0f) : 0.0f;
+    if (inside) {
 #pragma unroll
       for (int v = 0; v < V; ++v) dx[v] += f * (p[v] * (c[v] - dot));
     }
@@ -673,14 +756,19 @@ __global__ __launch_bounds__(kAlphaThreads) void alpha_grad_kernel(int T, int K,
   }
 }
 
-// Calls f with the layout for E experts and the logits' type: sixteen lanes to a token up to 256
-// experts (16 in each lane), so that a wavefront takes four tokens and reduces them together.
+// Calls f with the layout for E experts and the logits' type: sixteen lanes to a token up to 512
+// experts, so that a wavefront takes four tokens and reduces them together, with as few values to a
+// lane as hold E (257 experts in bf16: 73 us with 32 lanes of 16, 41 us with 16 lanes of 20).
 template <bool BF16, bool VEC, class F>
 void by_experts(int E, F&& f) {
-  if (E <= 64) f(Layout<16, 4, BF16, VEC>());
+  if (E <= 16) f(Layout<16, 1, BF16, false>());
+  else if (E <= 64) f(Layout<16, 4, BF16, VEC>());
   else if (E <= 128) f(Layout<16, 8, BF16, VEC>());
+  else if (E <= 192) f(Layout<16, 12, BF16, VEC>());
   else if (E <= 256) f(Layout<16, 16, BF16, VEC>());
-  else if (E <= 512) f(Layout<32, 16, BF16, VEC>());
+  else if (E <= 320) f(Layout<16, 20, BF16, VEC>());
+  else if (E <= 384) f(Layout<16, 24, BF16, VEC>());
+  else if (E <= 512) f(Layout<16, 32, BF16, VEC>());
   else f(Layout<64, 16, BF16, VEC>());
 }
 template <class F>
@@ -694,26 +782,30 @@ lrmoe_status by_layout(const lrmoe_router* r, F&& f) {
 }  // namespace
 
 size_t route_ws_bytes(const lrmoe_router* r) {
-  return align_up(std::max<size_t>(1, (size_t)ceil_div(r->T, route_chunk(r)) * r->E * 4), 256);
+  int sub, chunk;
+  route_sizes(r, &sub, &chunk);
+  return align_up(std::max<size_t>(16, (size_t)ceil_div(r->T, sub) * align_up(r->E, 4) * 4), 256);
 }
 
 lrmoe_status launch_route(const lrmoe_router* r, const void* logits, const uint8_t* mask, int32_t* idx, float* w,
                           int32_t* counts, int64_t* seg_off, int32_t* tok, int32_t* slot, float* alpha,
                           int32_t* pmap, void* ws, hipStream_t s) {
-  const int C = route_chunk(r);
-  const int chunks = (int)ceil_div(r->T, C);
-  const RouteArgs a{r->T, r->E, r->K, C, chunks, r->first, r->local, r->renorm, r->scale, logits, mask, (int32_t*)ws,
-                    idx, counts, tok, slot, pmap, w, alpha, seg_off};
-  const size_t bits = (size_t)C / 8 * r->local;
-  if (chunks == 1)
-    return by_layout(r, [&](auto lay) { route_topk_kernel<decltype(lay), true><<<1, kRouteThreads, bits, s>>>(a); });
-  if (chunks > 1 &&
-      by_layout(r, [&](auto lay) { route_topk_kernel<decltype(lay), false><<<chunks, kRouteThreads, 0, s>>>(a); }) !=
-          LRMOE_OK)
-    return LRMOE_ERR_HIP;
-  int log_e = 0;
-  while ((1 << log_e) < r->E) ++log_e;
-  route_place_kernel<<<std::max(1, chunks), kRouteThreads, bits, s>>>(a, log_e);
+  int sub, C;
+  route_sizes(r, &sub, &C);
+  const int rows = (int)ceil_div(r->T, sub);
+  const RouteArgs a{r->T, r->E, r->K, sub, C, rows, r->first, r->local, r->renorm, r->scale, logits, mask,
+                    (int32_t*)ws, idx, counts, tok, slot, pmap, w, alpha, seg_off};
+  const size_t bits = (size_t)C / 8 * r->local, cnt = (size_t)r->E * 4;
+  if (rows > 0) {
+    const size_t lds = rows == 1 ? 2 * cnt + (size_t)C * r->K * 8 + bits : cnt;
+    if (by_layout(r, [&](auto lay) { route_topk_kernel<decltype(lay)><<<rows, kRouteThreads, lds, s>>>(a); }) !=
+        LRMOE_OK)
+      return LRMOE_ERR_HIP;
+    if (rows == 1) return LRMOE_OK;
+  }
+  int log_q = 0;
+  while ((4 << log_q) < r->E) ++log_q;
+  route_place_kernel<<<(unsigned)std::max<int64_t>(1, ceil_div(r->T, C)), kRouteThreads, bits, s>>>(a, log_q);
   return launch_status();
 }
 
