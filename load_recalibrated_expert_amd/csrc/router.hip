@@ -31,22 +31,20 @@ __device__ __forceinline__ float exp_below(float d) {
   return __builtin_fmaf(r, l * 0.693147181f, r);
 }
 
-// Reductions over the L lanes of a token's group; every lane gets the result, the same bits in each.
-// Sixteen lanes are a DPP row: four rotations at register speed instead of cross-lane permutes
-// through LDS (an 8-slot top-K over 128 experts: 46 us with permutes, 17 us so, T = 32768).
-template <int N>
-__device__ __forceinline__ int row_ror(int v) {
-  return __builtin_amdgcn_update_dpp(v, v, 0x120 + N, 0xF, 0xF, false);
+// Reductions over the L lanes of a token's group (4 to 64); every lane gets the result, the same bits
+// in each, as both lanes of a pair compute the same sum. Up to sixteen lanes the partner's value
+// comes by DPP, at register speed, instead of a cross-lane permute through LDS. swap<S> exchanges
+// lanes S apart, or mirrored in 2 S lanes, which is the same once S lanes agree.
+template <int S>
+__device__ __forceinline__ int swap(int v) {
+  constexpr int ctrl = S == 1 ? 0xB1 : S == 2 ? 0x4E : S == 4 ? 0x141 : 0x140;
+  if (S <= 8) return __builtin_amdgcn_update_dpp(0, v, ctrl, 0xF, 0xF, true);
+  return __shfl_xor(v, S, kWave);
 }
-template <int L, class Op>
+template <int L, int S = 1, class Op>
 __device__ __forceinline__ int group_reduce(int v, Op op) {
-  v = op(v, row_ror<8>(v));
-  v = op(v, row_ror<4>(v));
-  v = op(v, row_ror<2>(v));
-  v = op(v, row_ror<1>(v));
-#pragma unroll
-  for (int o = 16; o < L; o <<= 1) v = op(v, __shfl_xor(v, o, kWave));
-  return v;
+  if constexpr (S < L) return group_reduce<L, 2 * S>(op(v, swap<S>(v)), op);
+  else return v;
 }
 template <int L>
 __device__ __forceinline__ float group_max(float v) {
@@ -156,28 +154,25 @@ __device__ __forceinline__ bool unmasked(const uint8_t* __restrict__ mask, int64
 
 // ---------------------------------------------------------------- routing
 
-constexpr int kRouteThreads = 1024;
-constexpr int kOneChunk = 128;  // up to so many tokens one block does the whole call
+constexpr int kRouteThreads = 1024;   // placing blocks, and the top-K blocks of more than 8 slots
+constexpr int kRoute8Threads = 512;   // the top-K blocks of up to 8 slots
+constexpr int kOneChunk = 128;        // up to so many tokens one block does the whole call
 
-// Tokens of one top-K block (`sub`, a histogram row each) and of one placing block (`chunk`). A placing
-// block holds a bit per (token, local expert) in 48 KB of LDS and reads all rows, so sub grows
-// until there are at most 512 of them, as far as a chunk may.
-void route_sizes(const lrmoe_router* r, int* sub, int* chunk) {
-  int most = 1024;
-  while (most > 64 && (int64_t)r->local * most / 8 > 48 * 1024) most /= 2;
-  int c = 64;
-  while (c < most && ceil_div(r->T, c) > 512) c *= 2;
-  *sub = c;
-  *chunk = std::min(2 * c, most);
-  if (r->T <= kOneChunk) *sub = *chunk = kOneChunk;
+// Tokens of one top-K block and of one placing block. Each top-K block writes a row of counts, and a
+// placing block reads all rows and holds a bit per (token, local expert) in 48 KB of LDS: chunks
+// grow until there are at most 512, as far as those bits let them.
+int route_chunk(const lrmoe_router* r) {
+  int c = kOneChunk;
+  while (c < 1024 && ceil_div(r->T, c) > 512 && (int64_t)r->local * c * 2 / 8 <= 48 * 1024) c *= 2;
+  return c;
 }
 
 struct RouteArgs {
-  int T, E, K, sub, C, rows, first, local, renorm;
+  int T, E, K, C, rows, first, local, renorm;
   float scale;
   const void* logits;
   const uint8_t* mask;
-  int32_t* hist;  // [rows][E4] tokens of each sub-chunk per expert, E4 = E rounded up to 4, zeros behind E
+  uint16_t* hist;  // [rows][E8] tokens of each chunk per expert, E8 = E rounded up to 8, zeros behind E
   int32_t *idx, *counts, *tok, *slot, *pmap;
   float *w, *alpha;
   int64_t* seg_off;
@@ -187,15 +182,21 @@ struct RouteArgs {
 // total, before (LDS, [E]): tokens per expert in all chunks and in the chunks before this one; before
 // becomes the first row of (chunk, expert). The rank of a pair in its chunk is the number of lower
 // set bits among its expert's token bits, so no order of atomics enters the result.
-template <class EOf, class WOf>
+template <int NT, class EOf, class WOf>
 __device__ __forceinline__ void place_chunk(const RouteArgs& a, int c, int n, const int* total, int* before,
                                             uint32_t* bits, EOf e_of, WOf w_of) {
-  __shared__ int wave_total[kRouteThreads / kWave];
+  constexpr int kPer = 1024 / NT;  // local experts of one thread in the scan of their totals
+  __shared__ int wave_total[NT / kWave];
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   if (c == 0)
-    for (int e = tid; e < a.E; e += kRouteThreads) a.counts[e] = total[e];
-  // exclusive scan of the local experts' totals (local <= 1024 = one value per thread)
-  const int mine = tid < a.local ? total[a.first + tid] : 0;
+    for (int e = tid; e < a.E; e += NT) a.counts[e] = total[e];
+  int v[kPer], mine = 0;
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    const int l = tid * kPer + q;
+    v[q] = l < a.local ? total[a.first + l] : 0;
+    mine += v[q];
+  }
   int inc = mine;
 #pragma unroll
   for (int o = 1; o < kWave; o <<= 1) {
@@ -206,20 +207,25 @@ __device__ __forceinline__ void place_chunk(const RouteArgs& a, int c, int n, co
   __syncthreads();
   int base = inc - mine;
   for (int q = 0; q < tid / kWave; ++q) base += wave_total[q];
-  if (tid < a.local) {
-    if (c == 0) {
-      a.seg_off[tid] = base;
-      if (tid == a.local - 1) a.seg_off[a.local] = base + mine;
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    const int l = tid * kPer + q;
+    if (l < a.local) {
+      if (c == 0) {
+        a.seg_off[l] = base;
+        if (l == a.local - 1) a.seg_off[a.local] = base + v[q];
+      }
+      before[a.first + l] += base;
+      base += v[q];
     }
-    before[a.first + tid] += base;
   }
-  for (int i = tid; i < n; i += kRouteThreads) {
+  for (int i = tid; i < n; i += NT) {
     const int e = e_of(i), l = e - a.first, t = i / a.K;
     if (e >= 0 && l >= 0 && l < a.local) atomicOr(&bits[(t >> 5) * a.local + l], 1u << (t & 31));
   }
   __syncthreads();
   const int64_t t0 = (int64_t)c * a.C;
-  for (int i = tid; i < n; i += kRouteThreads) {
+  for (int i = tid; i < n; i += NT) {
     const int e = e_of(i), l = e - a.first, t = i / a.K;
     int row = -1;
     if (e >= 0 && l >= 0 && l < a.local) {
@@ -233,25 +239,170 @@ __device__ __forceinline__ void place_chunk(const RouteArgs& a, int c, int n, co
   }
 }
 
-// One block per sub-chunk of tokens: the K largest logits of each, their weights, and how often the
-// sub-chunk chose each expert. With few tokens (rows = 1) the block places the pairs itself.
+// What the two top-K kernels have in common: the block's LDS, one slot's outputs, and the end.
+template <int NT>
+struct RouteBlock {
+  // [E] counts; with one block for all tokens also [E] zeros, [C K] experts, [C K] weights, [C / 32][local] bits
+  int *cnt, *before, *e_of;
+  float* w_of;
+  uint32_t* bits;
+  bool one;
+
+  __device__ __forceinline__ RouteBlock(const RouteArgs& a, uint32_t* lds) : one(a.rows == 1) {
+    cnt = (int*)lds;
+    before = cnt + a.E;
+    e_of = before + a.E;
+    w_of = (float*)(e_of + a.C * a.K);
+    bits = (uint32_t*)(w_of + a.C * a.K);
+    for (int e = threadIdx.x; e < (one ? 2 * a.E : a.E); e += NT) cnt[e] = 0;
+    if (one)
+      for (int i = threadIdx.x; i < a.C / 32 * a.local; i += NT) bits[i] = 0;
+  }
+  __device__ __forceinline__ void put(const RouteArgs& a, int64_t t, int k, int e, float w) {
+    a.idx[t * a.K + k] = e;
+    a.w[t * a.K + k] = w;
+    if (one) {
+      e_of[t * a.K + k] = e;
+      w_of[t * a.K + k] = w;
+    }
+    if (e >= 0) atomicAdd(&cnt[e], 1);
+  }
+  __device__ __forceinline__ void finish(const RouteArgs& a) {
+    __syncthreads();
+    if (one) {
+      place_chunk<NT>(a, 0, a.T * a.K, cnt, before, bits, [&](int i) { return e_of[i]; }, [&](int i) { return w_of[i]; });
+    } else {
+      const int E8 = (a.E + 7) & ~7;
+      for (int e = threadIdx.x; e < E8; e += NT)
+        a.hist[(int64_t)blockIdx.x * E8 + e] = e < a.E ? (uint16_t)cnt[e] : 0;
+    }
+  }
+};
+
+// Up to 8 slots. A logit and its expert make one positive double: the logit's bits, mapped so that
+// they order as unsigned numbers, above 1023 - e, so one f64 maximum compares both and ties go to
+// the lower index. Lanes sort their values in eights (19 exchanges of a maximum and a minimum),
+// and lists of eight are merged, in a lane and then over the token's lanes: the larger halves of
+// one list against the other reversed are the eight largest of both, sorted by 12 more exchanges.
+// With four lanes to a token (up to 128 experts) that is about 45 instructions a token and
+// wavefront, where taking the largest K times over costs 240: 32768 x 128 takes TOPK8_US here and
+// 13.4 us that way.
+#pragma float_control(precise, off, push)  // maxima without NaN handling: there are none among the keys
+__device__ __forceinline__ void exchange(double& a, double& b) {
+  const double hi = __builtin_fmax(a, b), lo = __builtin_fmin(a, b);
+  a = hi;
+  b = lo;
+}
+__device__ __forceinline__ void sort8(double* a) {
+  exchange(a[0], a[1]), exchange(a[2], a[3]), exchange(a[4], a[5]), exchange(a[6], a[7]);
+  exchange(a[0], a[2]), exchange(a[1], a[3]), exchange(a[4], a[6]), exchange(a[5], a[7]);
+  exchange(a[1], a[2]), exchange(a[5], a[6]);
+  exchange(a[0], a[4]), exchange(a[1], a[5]), exchange(a[2], a[6]), exchange(a[3], a[7]);
+  exchange(a[2], a[4]), exchange(a[3], a[5]);
+  exchange(a[1], a[2]), exchange(a[3], a[4]), exchange(a[5], a[6]);
+}
+// a = the eight largest of a and b, both sorted
+__device__ __forceinline__ void merge8(double* a, const double* b) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a[i] = __builtin_fmax(a[i], b[7 - i]);
+  exchange(a[0], a[4]), exchange(a[1], a[5]), exchange(a[2], a[6]), exchange(a[3], a[7]);
+  exchange(a[0], a[2]), exchange(a[1], a[3]), exchange(a[4], a[6]), exchange(a[5], a[7]);
+  exchange(a[0], a[1]), exchange(a[2], a[3]), exchange(a[4], a[5]), exchange(a[6], a[7]);
+}
+#pragma float_control(pop)
+template <int L, int S = 1>
+__device__ __forceinline__ void merge_lanes(double* a) {
+  if constexpr (S < L) {
+    double b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = __hiloint2double(swap<S>(__double2hiint(a[i])), swap<S>(__double2loint(a[i])));
+    merge8(a, b);
+    merge_lanes<L, 2 * S>(a);
+  }
+}
+__device__ __forceinline__ double key_of(float x, int e) {
+  const int u = __float_as_int(x + 0.0f);  // -0 ties with 0
+  const uint32_t k = (uint32_t)u ^ ((uint32_t)(u >> 31) | 0x80000000u);
+  return __hiloint2double((int)(k >> 1), (int)(k << 31 | (uint32_t)(1023 - e)));
+}
+__device__ __forceinline__ void of_key(double d, float* x, int* e) {  // e = -1 for -inf
+  const uint32_t hi = (uint32_t)__double2hiint(d), lo = (uint32_t)__double2loint(d), k = hi << 1 | lo >> 31;
+  *x = __uint_as_float(k >> 31 ? k ^ 0x80000000u : ~k);
+  *e = k > 0x007FFFFFu ? 1023 - (int)(lo & 1023u) : -1;
+}
+
+template <class Lay>
+__global__ __launch_bounds__(kRoute8Threads) void route_topk8_kernel(RouteArgs a) {
+  constexpr int L = Lay::L, V = Lay::V, kGroups = kRoute8Threads / L;
+  constexpr int S = (8 + L - 1) / L;  // slots of a lane: k = lane, lane + L
+  extern __shared__ uint32_t lds[];
+  RouteBlock<kRoute8Threads> blk(a, lds);
+  const int lane = threadIdx.x & (L - 1), group = threadIdx.x / L;
+  const int64_t t0 = (int64_t)blockIdx.x * a.C, t1 = min(t0 + a.C, (int64_t)a.T);
+  __syncthreads();
+  for (int64_t tb = t0; tb < t1; tb += kGroups) {
+    const int64_t t = tb + group;
+    const bool in = t < t1;
+    float x[V];
+    Lay::load(a.logits, t, a.E, in && unmasked(a.mask, t), lane, x);
+    float top = kNegInf, Z = 0.0f;
+    if (!a.renorm) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) top = fmaxf(top, x[v]);
+      top = group_max<L>(top);
+#pragma unroll
+      for (int v = 0; v < V; ++v) Z += exp_below(x[v] - top);
+      Z = group_sum<L>(Z);
+    }
+    double best[8];
+#pragma unroll
+    for (int q = 0; q < V; q += 8) {
+      double d[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d[i] = key_of(x[q + i], Lay::expert(lane, q + i));
+      sort8(d);
+      if (q == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) best[i] = d[i];
+      } else {
+        merge8(best, d);
+      }
+    }
+    merge_lanes<L>(best);
+    int e[S], top_e;
+    float p[S], sum = 0.0f;
+    of_key(best[0], &top, &top_e);
+#pragma unroll
+    for (int q = 0; q < S; ++q) {
+      const int k = lane + q * L;
+      double d = 0.0;
+#pragma unroll
+      for (int i = q * L; i < 8 && i < (q + 1) * L; ++i) d = i == k ? best[i] : d;
+      float xk;
+      of_key(d, &xk, &e[q]);
+      if (k >= a.K) e[q] = -1;
+      p[q] = e[q] >= 0 ? exp_below(xk - top) : 0.0f;
+      sum += p[q];
+    }
+    if (a.renorm) Z = group_sum<L>(sum);
+#pragma unroll
+    for (int q = 0; q < S; ++q) {
+      const int k = lane + q * L;
+      if (in && k < a.K) blk.put(a, t, k, e[q], e[q] >= 0 ? a.scale * (p[q] / Z) : 0.0f);
+    }
+  }
+  blk.finish(a);
+}
+
+// More than 8 slots: the largest value left, K times.
 template <class Lay>
 __global__ __launch_bounds__(kRouteThreads) void route_topk_kernel(RouteArgs a) {
   constexpr int L = Lay::L, V = Lay::V, kGroups = kRouteThreads / L;
   constexpr int S = (32 + L - 1) / L;  // slots that a lane keeps: k = lane, lane + L
   extern __shared__ uint32_t lds[];
-  // [E] counts; with one block also [E] zeros, [C K] experts, [C K] weights, [C / 32][local] bits
-  int* cnt = (int*)lds;
-  const bool one = a.rows == 1;
-  int* before = cnt + a.E;
-  int* e_of = before + a.E;
-  float* w_of = (float*)(e_of + a.C * a.K);
-  uint32_t* bits = (uint32_t*)(w_of + a.C * a.K);
-  for (int e = threadIdx.x; e < (one ? 2 * a.E : a.E); e += kRouteThreads) cnt[e] = 0;
-  if (one)
-    for (int i = threadIdx.x; i < a.C / 32 * a.local; i += kRouteThreads) bits[i] = 0;
+  RouteBlock<kRouteThreads> blk(a, lds);
   const int lane = threadIdx.x & (L - 1), group = threadIdx.x / L;
-  const int64_t t0 = (int64_t)blockIdx.x * a.sub, t1 = min(t0 + a.sub, (int64_t)a.T);
+  const int64_t t0 = (int64_t)blockIdx.x * a.C, t1 = min(t0 + a.C, (int64_t)a.T);
   float next[V];
   Lay::load(a.logits, t0 + group, a.E, t0 + group < t1 && unmasked(a.mask, t0 + group), lane, next);
   __syncthreads();
@@ -313,30 +464,14 @@ __global__ __launch_bounds__(kRouteThreads) void route_topk_kernel(RouteArgs a) 
 #pragma unroll
     for (int q = 0; q < S; ++q) {
       const int k = lane + q * L;
-      if (in && k < a.K) {
-        const float w = my_e[q] >= 0 ? a.scale * (p[q] / Z) : 0.0f;
-        a.idx[t * a.K + k] = my_e[q];
-        a.w[t * a.K + k] = w;
-        if (one) {
-          e_of[t * a.K + k] = my_e[q];
-          w_of[t * a.K + k] = w;
-        }
-        if (my_e[q] >= 0) atomicAdd(&cnt[my_e[q]], 1);
-      }
+      if (in && k < a.K) blk.put(a, t, k, my_e[q], my_e[q] >= 0 ? a.scale * (p[q] / Z) : 0.0f);
     }
   }
-  __syncthreads();
-  if (one) {
-    place_chunk(a, 0, a.T * a.K, cnt, before, bits, [&](int i) { return e_of[i]; }, [&](int i) { return w_of[i]; });
-  } else {
-    const int E4 = (a.E + 3) & ~3;
-    for (int e = threadIdx.x; e < E4; e += kRouteThreads)
-      a.hist[(int64_t)blockIdx.x * E4 + e] = e < a.E ? cnt[e] : 0;
-  }
+  blk.finish(a);
 }
 
-// One block per chunk: sums all histogram rows itself (they are in L2), which saves a launch that scans
-// them. Thread: four experts, every stripes-th row.
+// One block per chunk: sums all rows of counts itself (they are in L2), which saves a launch that scans
+// them. Thread: eight experts, every stripes-th row.
 __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs a, int log_q) {
   __shared__ int total[1024], before[1024];
   extern __shared__ uint32_t bits[];  // [C / 32][local]
@@ -348,24 +483,29 @@ __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs a,
   total[tid] = before[tid] = 0;
   for (int i = tid; i < a.C / 32 * a.local; i += kRouteThreads) bits[i] = 0;
   __syncthreads();
-  const int E4 = (a.E + 3) & ~3, e = 4 * (tid & ((1 << log_q) - 1)), stripes = kRouteThreads >> log_q;
-  if (e < E4) {
-    int4 sum = make_int4(0, 0, 0, 0), low = sum;
-    const int mine = c * (a.C / a.sub);
-#pragma unroll 8
+  const int E8 = (a.E + 7) & ~7, e = 8 * (tid & ((1 << log_q) - 1)), stripes = kRouteThreads >> log_q;
+  if (e < E8) {
+    int sum[8] = {0, 0, 0, 0, 0, 0, 0, 0}, low[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
     for (int r = tid >> log_q; r < a.rows; r += stripes) {
-      const int4 h = *(const int4*)(a.hist + (int64_t)r * E4 + e);
-      const int m = r < mine ? -1 : 0;
-      sum.x += h.x, sum.y += h.y, sum.z += h.z, sum.w += h.w;
-      low.x += h.x & m, low.y += h.y & m, low.z += h.z & m, low.w += h.w & m;
+      const uint4 h = *(const uint4*)(a.hist + (int64_t)r * E8 + e);
+      const uint32_t w[4] = {h.x, h.y, h.z, h.w};
+      const int m = r < c ? -1 : 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int lo = (int)(w[q] & 0xFFFFu), hi = (int)(w[q] >> 16);
+        sum[2 * q] += lo, sum[2 * q + 1] += hi;
+        low[2 * q] += lo & m, low[2 * q + 1] += hi & m;
+      }
     }
-    atomicAdd(&total[e], sum.x), atomicAdd(&total[e + 1], sum.y);
-    atomicAdd(&total[e + 2], sum.z), atomicAdd(&total[e + 3], sum.w);
-    atomicAdd(&before[e], low.x), atomicAdd(&before[e + 1], low.y);
-    atomicAdd(&before[e + 2], low.z), atomicAdd(&before[e + 3], low.w);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      if (sum[q]) atomicAdd(&total[e + q], sum[q]);
+      if (low[q]) atomicAdd(&before[e + q], low[q]);
+    }
   }
   __syncthreads();
-  place_chunk(
+  place_chunk<kRouteThreads>(
       a, c, n, total, before, bits, [&](int i) { return i < kRouteThreads ? e0 : a.idx[i0 + i]; },
       [&](int i) { return i < kRouteThreads ? w0 : a.w[i0 + i]; });
 }
@@ -771,6 +911,25 @@ void by_experts(int E, F&& f) {
   else if (E <= 512) f(Layout<16, 32, BF16, VEC>());
   else f(Layout<64, 16, BF16, VEC>());
 }
+// The same for lists of eight: values by the eight, and as few lanes as hold them in 40 values each.
+template <bool BF16, bool VEC, class F>
+void by_experts8(int E, F&& f) {
+  if (E <= 32) f(Layout<4, 8, BF16, VEC>());
+  else if (E <= 64) f(Layout<4, 16, BF16, VEC>());
+  else if (E <= 128) f(Layout<4, 32, BF16, VEC>());
+  else if (E <= 192) f(Layout<8, 24, BF16, VEC>());
+  else if (E <= 256) f(Layout<8, 32, BF16, VEC>());
+  else if (E <= 320) f(Layout<8, 40, BF16, VEC>());
+  else if (E <= 512) f(Layout<16, 32, BF16, VEC>());
+  else f(Layout<32, 32, BF16, VEC>());
+}
+template <class F>
+lrmoe_status by_layout8(const lrmoe_router* r, F&& f) {
+  const bool vec = r->E % 4 == 0;
+  if (r->dtype == LRMOE_BF16) vec ? by_experts8<true, true>(r->E, f) : by_experts8<true, false>(r->E, f);
+  else vec ? by_experts8<false, true>(r->E, f) : by_experts8<false, false>(r->E, f);
+  return launch_status();
+}
 template <class F>
 lrmoe_status by_layout(const lrmoe_router* r, F&& f) {
   const bool vec = r->E % 4 == 0;
@@ -782,30 +941,27 @@ lrmoe_status by_layout(const lrmoe_router* r, F&& f) {
 }  // namespace
 
 size_t route_ws_bytes(const lrmoe_router* r) {
-  int sub, chunk;
-  route_sizes(r, &sub, &chunk);
-  return align_up(std::max<size_t>(16, (size_t)ceil_div(r->T, sub) * align_up(r->E, 4) * 4), 256);
+  return align_up(std::max<size_t>(16, (size_t)ceil_div(r->T, route_chunk(r)) * align_up(r->E, 8) * 2), 256);
 }
 
 lrmoe_status launch_route(const lrmoe_router* r, const void* logits, const uint8_t* mask, int32_t* idx, float* w,
                           int32_t* counts, int64_t* seg_off, int32_t* tok, int32_t* slot, float* alpha,
                           int32_t* pmap, void* ws, hipStream_t s) {
-  int sub, C;
-  route_sizes(r, &sub, &C);
-  const int rows = (int)ceil_div(r->T, sub);
-  const RouteArgs a{r->T, r->E, r->K, sub, C, rows, r->first, r->local, r->renorm, r->scale, logits, mask,
-                    (int32_t*)ws, idx, counts, tok, slot, pmap, w, alpha, seg_off};
+  const int C = route_chunk(r), rows = (int)ceil_div(r->T, C);
+  const RouteArgs a{r->T, r->E, r->K, C, rows, r->first, r->local, r->renorm, r->scale, logits, mask,
+                    (uint16_t*)ws, idx, counts, tok, slot, pmap, w, alpha, seg_off};
   const size_t bits = (size_t)C / 8 * r->local, cnt = (size_t)r->E * 4;
   if (rows > 0) {
     const size_t lds = rows == 1 ? 2 * cnt + (size_t)C * r->K * 8 + bits : cnt;
-    if (by_layout(r, [&](auto lay) { route_topk_kernel<decltype(lay)><<<rows, kRouteThreads, lds, s>>>(a); }) !=
-        LRMOE_OK)
-      return LRMOE_ERR_HIP;
-    if (rows == 1) return LRMOE_OK;
+    const lrmoe_status st =
+        r->K <= 8
+            ? by_layout8(r, [&](auto lay) { route_topk8_kernel<decltype(lay)><<<rows, kRoute8Threads, lds, s>>>(a); })
+            : by_layout(r, [&](auto lay) { route_topk_kernel<decltype(lay)><<<rows, kRouteThreads, lds, s>>>(a); });
+    if (st != LRMOE_OK || rows == 1) return st;
   }
   int log_q = 0;
-  while ((4 << log_q) < r->E) ++log_q;
-  route_place_kernel<<<(unsigned)std::max<int64_t>(1, ceil_div(r->T, C)), kRouteThreads, bits, s>>>(a, log_q);
+  while ((8 << log_q) < r->E) ++log_q;
+  route_place_kernel<<<(unsigned)std::max(1, rows), kRouteThreads, bits, s>>>(a, log_q);
   return launch_status();
 }
 
