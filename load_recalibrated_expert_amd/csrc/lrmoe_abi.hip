@@ -423,7 +423,7 @@ lrmoe_status lrmoe_route_bwd(const lrmoe_router* r, const void* logits, const ui
   LRMOE_TRY(check_router(r));
   if (norm) {
     LRMOE_TRY(check_sequences(r, seq_off_d, n_seq));
-    if (!counts || !aligned(counts, 16)) return LRMOE_ERR_INVALID_ARG;
+    if (!counts) return LRMOE_ERR_INVALID_ARG;
   }
   if (dalpha && pmap && n_pairs < 0) return LRMOE_ERR_INVALID_ARG;
   if (r->T == 0) return LRMOE_OK;

@@ -31,6 +31,10 @@ __device__ __forceinline__ float exp_below(float d) {
   return __builtin_fmaf(r, l * 0.693147181f, r);
 }
 
+// A term of a sum of exp(d): without the part l. Its relative error of 1.2 |d| 2^-24 falls with the term,
+// so a whole sum over E values is off by less than 2 ln(E) 2^-24 more. NaN if the token is not live.
+__device__ __forceinline__ float exp_term(float d) { return __builtin_amdgcn_exp2f(d * 1.44269502f); }
+
 // Reductions over the L lanes of a token's group (4 to 64); every lane gets the result, the same bits
 // in each, as both lanes of a pair compute the same sum. Up to sixteen lanes the partner's value
 // comes by DPP, at register speed, instead of a cross-lane permute through LDS. swap<S> exchanges
@@ -63,88 +67,85 @@ __device__ __forceinline__ int group_min(int v) {
   return group_reduce<L>(v, [](int a, int b) { return min(a, b); });
 }
 
-// How a token's E logits lie over the L lanes of its group, V to a lane, ascending in each lane.
-// VEC (E a multiple of 4, so rows are aligned): runs of four, one 16-byte (f32) or 8-byte (bf16)
-// load each; else single logits, L apart.
-template <int L_, int V_, bool BF16_, bool VEC_>
+// Four logits from or to any element of a row: rows of an odd number of experts are aligned to their
+// elements only, which vector loads and stores of global memory take.
+typedef float f32x4u_t __attribute__((ext_vector_type(4), aligned(4)));
+typedef int32_t i32x4u_t __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t bf16x4u_t __attribute__((ext_vector_type(2), aligned(2)));
+
+// How a token's E logits lie over the L lanes of its group, V to a lane: runs of four, 4 L apart,
+// ascending in each lane. One 16-byte (f32) or 8-byte (bf16) access takes a run; the run that E
+// cuts is taken singly, so nothing behind the last row is touched.
+template <int L_, int V_, bool BF16_>
 struct Layout {
   static constexpr int L = L_, V = V_;
-  static constexpr bool BF16 = BF16_, VEC = VEC_;
-  static __device__ __forceinline__ int expert(int lane, int v) {
-    return VEC ? (v >> 2) * (4 * L) + lane * 4 + (v & 3) : v * L + lane;
+  static constexpr bool BF16 = BF16_;
+  static __device__ __forceinline__ int expert(int lane, int v) { return (v >> 2) * (4 * L) + lane * 4 + (v & 3); }
+  static __device__ __forceinline__ float load_one(const void* __restrict__ logits, int64_t i) {
+    return clean(BF16 ? __uint_as_float((uint32_t)((const uint16_t*)logits)[i] << 16) : ((const float*)logits)[i]);
   }
   // Token t by the rules of the header; -inf beyond E, and everywhere if `on` is false.
   static __device__ __forceinline__ void load(const void* __restrict__ logits, int64_t t, int E, bool on, int lane,
                                               float x[V]) {
-    if (VEC) {
 #pragma unroll
-      for (int q = 0; q < V; q += 4) {
-        const int e = expert(lane, q);
-        if (on && e < E) {
-          if (BF16) {
-            const uint2 r = *(const uint2*)((const uint16_t*)logits + t * E + e);
-            x[q] = clean(bf16_lo(r.x));
-            x[q + 1] = clean(bf16_hi(r.x));
-            x[q + 2] = clean(bf16_lo(r.y));
-            x[q + 3] = clean(bf16_hi(r.y));
-          } else {
-            const float4 r = *(const float4*)((const float*)logits + t * E + e);
-            x[q] = clean(r.x);
-            x[q + 1] = clean(r.y);
-            x[q + 2] = clean(r.z);
-            x[q + 3] = clean(r.w);
-          }
+    for (int q = 0; q < V; q += 4) {
+      const int e = expert(lane, q);
+      float a = kNegInf, b = kNegInf, c = kNegInf, d = kNegInf;
+      if (on && e + 4 <= E) {
+        if (BF16) {
+          const bf16x4u_t r = *(const bf16x4u_t*)((const uint16_t*)logits + t * E + e);
+          a = bf16_lo(r[0]), b = bf16_hi(r[0]), c = bf16_lo(r[1]), d = bf16_hi(r[1]);
         } else {
-          x[q] = x[q + 1] = x[q + 2] = x[q + 3] = kNegInf;
+          const f32x4u_t r = *(const f32x4u_t*)((const float*)logits + t * E + e);
+          a = r[0], b = r[1], c = r[2], d = r[3];
         }
+      } else if (on && e < E) {
+        a = load_one(logits, t * E + e);
+        if (e + 1 < E) b = load_one(logits, t * E + e + 1);
+        if (e + 2 < E) c = load_one(logits, t * E + e + 2);
       }
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int e = expert(lane, v);
-        x[v] = kNegInf;
-        if (on && e < E) x[v] = load_one(logits, t * E + e);
-      }
+      x[q] = a, x[q + 1] = b, x[q + 2] = c, x[q + 3] = d;
     }
-  }
-  static __device__ __forceinline__ float load_one(const void* __restrict__ logits, int64_t i) {
-    return clean(BF16 ? __uint_as_float((uint32_t)((const uint16_t*)logits)[i] << 16) : ((const float*)logits)[i]);
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = clean(x[v]);
   }
   // Row s of the [n_seq x E] counts, zeros beyond E and where `on` is false.
   static __device__ __forceinline__ void load_counts(const int32_t* __restrict__ counts, int64_t s, int E, bool on,
                                                      int lane, float c[V]) {
 #pragma unroll
-    for (int q = 0; q < V; q += VEC ? 4 : 1) {
+    for (int q = 0; q < V; q += 4) {
       const int e = expert(lane, q);
-      if (VEC) {
-        const int4 n = on && e < E ? *(const int4*)(counts + s * E + e) : make_int4(0, 0, 0, 0);
-        c[q] = (float)n.x;
-        c[q + 1] = (float)n.y;
-        c[q + 2] = (float)n.z;
-        c[q + 3] = (float)n.w;
-      } else {
-        c[q] = on && e < E ? (float)counts[s * E + e] : 0.0f;
+      const int32_t* row = counts + s * E + e;
+      float n0 = 0.0f, n1 = 0.0f, n2 = 0.0f, n3 = 0.0f;
+      if (on && e + 4 <= E) {
+        const i32x4u_t n = *(const i32x4u_t*)row;
+        n0 = (float)n[0], n1 = (float)n[1], n2 = (float)n[2], n3 = (float)n[3];
+      } else if (on && e < E) {
+        n0 = (float)row[0];
+        if (e + 1 < E) n1 = (float)row[1];
+        if (e + 2 < E) n2 = (float)row[2];
       }
+      c[q] = n0, c[q + 1] = n1, c[q + 2] = n2, c[q + 3] = n3;
     }
   }
   static __device__ __forceinline__ void store(void* __restrict__ out, int64_t t, int E, int lane, const float x[V]) {
-    if (VEC) {
 #pragma unroll
-      for (int q = 0; q < V; q += 4) {
-        const int e = expert(lane, q);
-        if (e >= E) continue;
-        if (BF16)
-          *(uint2*)((uint16_t*)out + t * E + e) = make_uint2(pack_bf16x2(x[q], x[q + 1]), pack_bf16x2(x[q + 2], x[q + 3]));
-        else
-          *(float4*)((float*)out + t * E + e) = make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
-      }
-    } else {
+    for (int q = 0; q < V; q += 4) {
+      const int e = expert(lane, q);
+      if (e + 4 <= E) {
+        if (BF16) {
+          *(bf16x4u_t*)((uint16_t*)out + t * E + e) =
+              bf16x4u_t{pack_bf16x2(x[q], x[q + 1]), pack_bf16x2(x[q + 2], x[q + 3])};
+        } else {
+          *(f32x4u_t*)((float*)out + t * E + e) = f32x4u_t{x[q], x[q + 1], x[q + 2], x[q + 3]};
+        }
+      } else if (e < E) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int e = expert(lane, v);
-        if (e >= E) continue;
-        if (BF16) ((uint16_t*)out)[t * E + e] = (uint16_t)pack_bf16x2(x[v], 0.0f);
-        else ((float*)out)[t * E + e] = x[v];
+        for (int i = 0; i < 3; ++i)
+          if (e + i < E) {
+            if (BF16) ((uint16_t*)out)[t * E + e + i] = (uint16_t)pack_bf16x2(x[q + i], 0.0f);
+            else ((float*)out)[t * E + e + i] = x[q + i];
+          }
       }
     }
   }
@@ -172,6 +173,7 @@ struct RouteArgs {
   float scale;
   const void* logits;
   const uint8_t* mask;
+  int *prefix, *total;  // [rows][E8], [E8]: the scan's results, NULL if it does not run
   uint16_t* hist;  // [rows][E8] tokens of each chunk per expert, E8 = E rounded up to 8, zeros behind E
   int32_t *idx, *counts, *tok, *slot, *pmap;
   float *w, *alpha;
@@ -279,21 +281,28 @@ struct RouteBlock {
   }
 };
 
-// Up to 8 slots. A logit and its expert make one positive double: the logit's bits, mapped so that
-// they order as unsigned numbers, above 1023 - e, so one f64 maximum compares both and ties go to
-// the lower index. Lanes sort their values in eights (19 exchanges of a maximum and a minimum),
-// and lists of eight are merged, in a lane and then over the token's lanes: the larger halves of
-// one list against the other reversed are the eight largest of both, sorted by 12 more exchanges.
-// With four lanes to a token (up to 128 experts) that is about 45 instructions a token and
-// wavefront, where taking the largest K times over costs 240: 32768 x 128 takes TOPK8_US here and
-// 13.4 us that way.
+// Up to 8 slots. A logit and its expert make one key: the logit's bits, mapped so that they order as
+// unsigned numbers, above 1023 - e, so one maximum compares both and ties go to the lower index.
+// f32 logits take 63 bits as a positive double (f64 maxima run at full rate), bf16 logits 32. Lanes
+// sort their keys in eights (19 exchanges of a maximum and a minimum), and lists of eight are
+// merged, in a lane and then over the token's lanes: the larger of one list against the other
+// reversed are the eight largest of both, sorted by 12 more exchanges. With four lanes to a token
+// (up to 128 experts) that is a fifth of the instructions of taking the largest K times over:
+// 32768 x 128 f32 takes 8.2 us here and 13.4 us that way.
 #pragma float_control(precise, off, push)  // maxima without NaN handling: there are none among the keys
-__device__ __forceinline__ void exchange(double& a, double& b) {
-  const double hi = __builtin_fmax(a, b), lo = __builtin_fmin(a, b);
+__device__ __forceinline__ double key_max(double a, double b) { return __builtin_fmax(a, b); }
+__device__ __forceinline__ double key_min(double a, double b) { return __builtin_fmin(a, b); }
+#pragma float_control(pop)
+__device__ __forceinline__ uint32_t key_max(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t key_min(uint32_t a, uint32_t b) { return a < b ? a : b; }
+template <class Key>
+__device__ __forceinline__ void exchange(Key& a, Key& b) {
+  const Key hi = key_max(a, b), lo = key_min(a, b);
   a = hi;
   b = lo;
 }
-__device__ __forceinline__ void sort8(double* a) {
+template <class Key>
+__device__ __forceinline__ void sort8(Key* a) {
   exchange(a[0], a[1]), exchange(a[2], a[3]), exchange(a[4], a[5]), exchange(a[6], a[7]);
   exchange(a[0], a[2]), exchange(a[1], a[3]), exchange(a[4], a[6]), exchange(a[5], a[7]);
   exchange(a[1], a[2]), exchange(a[5], a[6]);
@@ -302,33 +311,53 @@ __device__ __forceinline__ void sort8(double* a) {
   exchange(a[1], a[2]), exchange(a[3], a[4]), exchange(a[5], a[6]);
 }
 // a = the eight largest of a and b, both sorted
-__device__ __forceinline__ void merge8(double* a, const double* b) {
+template <class Key>
+__device__ __forceinline__ void merge8(Key* a, const Key* b) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a[i] = __builtin_fmax(a[i], b[7 - i]);
+  for (int i = 0; i < 8; ++i) a[i] = key_max(a[i], b[7 - i]);
   exchange(a[0], a[4]), exchange(a[1], a[5]), exchange(a[2], a[6]), exchange(a[3], a[7]);
   exchange(a[0], a[2]), exchange(a[1], a[3]), exchange(a[4], a[6]), exchange(a[5], a[7]);
   exchange(a[0], a[1]), exchange(a[2], a[3]), exchange(a[4], a[5]), exchange(a[6], a[7]);
 }
-#pragma float_control(pop)
-template <int L, int S = 1>
-__device__ __forceinline__ void merge_lanes(double* a) {
+template <int S>
+__device__ __forceinline__ double swap(double v) {
+  return __hiloint2double(swap<S>(__double2hiint(v)), swap<S>(__double2loint(v)));
+}
+template <int S>
+__device__ __forceinline__ uint32_t swap(uint32_t v) {
+  return (uint32_t)swap<S>((int)v);
+}
+template <int L, int S = 1, class Key>
+__device__ __forceinline__ void merge_lanes(Key* a) {
   if constexpr (S < L) {
-    double b[8];
+    Key b[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = __hiloint2double(swap<S>(__double2hiint(a[i])), swap<S>(__double2loint(a[i])));
+    for (int i = 0; i < 8; ++i) b[i] = swap<S>(a[i]);
     merge8(a, b);
     merge_lanes<L, 2 * S>(a);
   }
 }
-__device__ __forceinline__ double key_of(float x, int e) {
+__device__ __forceinline__ uint32_t ordered(float x) {
   const int u = __float_as_int(x + 0.0f);  // -0 ties with 0
-  const uint32_t k = (uint32_t)u ^ ((uint32_t)(u >> 31) | 0x80000000u);
-  return __hiloint2double((int)(k >> 1), (int)(k << 31 | (uint32_t)(1023 - e)));
+  return (uint32_t)u ^ ((uint32_t)(u >> 31) | 0x80000000u);
 }
+__device__ __forceinline__ void to_key(float x, int e, double* k) {
+  const uint32_t u = ordered(x);
+  *k = __hiloint2double((int)(u >> 1), (int)(u << 31 | (uint32_t)(1023 - e)));
+}
+__device__ __forceinline__ void to_key(float x, int e, uint32_t* k) {  // the low half of a bf16's bits is 0 or, mapped, ones
+  *k = (ordered(x) & 0xFFFF0000u) | (uint32_t)(1023 - e);
+}
+__device__ __forceinline__ float unordered(uint32_t u) { return __uint_as_float(u >> 31 ? u ^ 0x80000000u : ~u); }
 __device__ __forceinline__ void of_key(double d, float* x, int* e) {  // e = -1 for -inf
-  const uint32_t hi = (uint32_t)__double2hiint(d), lo = (uint32_t)__double2loint(d), k = hi << 1 | lo >> 31;
-  *x = __uint_as_float(k >> 31 ? k ^ 0x80000000u : ~k);
-  *e = k > 0x007FFFFFu ? 1023 - (int)(lo & 1023u) : -1;
+  const uint32_t hi = (uint32_t)__double2hiint(d), lo = (uint32_t)__double2loint(d), u = hi << 1 | lo >> 31;
+  *x = unordered(u);
+  *e = u > 0x007FFFFFu ? 1023 - (int)(lo & 1023u) : -1;
+}
+__device__ __forceinline__ void of_key(uint32_t k, float* x, int* e) {
+  const uint32_t u = k >> 31 ? k & 0xFFFF0000u : k | 0xFFFFu;
+  *x = unordered(u);
+  *e = u > 0x007FFFFFu ? 1023 - (int)(k & 1023u) : -1;
 }
 
 template <class Lay>
@@ -351,15 +380,16 @@ __global__ __launch_bounds__(kRoute8Threads) void route_topk8_kernel(RouteArgs a
       for (int v = 0; v < V; ++v) top = fmaxf(top, x[v]);
       top = group_max<L>(top);
 #pragma unroll
-      for (int v = 0; v < V; ++v) Z += exp_below(x[v] - top);
+      for (int v = 0; v < V; ++v) Z += exp_term(x[v] - top);
       Z = group_sum<L>(Z);
     }
-    double best[8];
+    using Key = std::conditional_t<Lay::BF16, uint32_t, double>;
+    Key best[8];
 #pragma unroll
     for (int q = 0; q < V; q += 8) {
-      double d[8];
+      Key d[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) d[i] = key_of(x[q + i], Lay::expert(lane, q + i));
+      for (int i = 0; i < 8; ++i) to_key(x[q + i], Lay::expert(lane, q + i), &d[i]);
       sort8(d);
       if (q == 0) {
 #pragma unroll
@@ -375,7 +405,7 @@ __global__ __launch_bounds__(kRoute8Threads) void route_topk8_kernel(RouteArgs a
 #pragma unroll
     for (int q = 0; q < S; ++q) {
       const int k = lane + q * L;
-      double d = 0.0;
+      Key d = 0;
 #pragma unroll
       for (int i = q * L; i < 8 && i < (q + 1) * L; ++i) d = i == k ? best[i] : d;
       float xk;
@@ -420,7 +450,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_topk_kernel(RouteArgs a) 
       for (int v = 0; v < V; ++v) top = fmaxf(top, x[v]);
       top = group_max<L>(top);
 #pragma unroll
-      for (int v = 0; v < V; ++v) Z += exp_below(x[v] - top);
+      for (int v = 0; v < V; ++v) Z += exp_term(x[v] - top);
       Z = group_sum<L>(Z);
     }
     // slot k: the largest value left, and the lowest index that has it
@@ -470,39 +500,79 @@ __global__ __launch_bounds__(kRouteThreads) void route_topk_kernel(RouteArgs a) 
   blk.finish(a);
 }
 
-// One block per chunk: sums all rows of counts itself (they are in L2), which saves a launch that scans
-// them. Thread: eight experts, every stripes-th row.
-__global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs a, int log_q) {
+// Rows of counts up to which every placing block sums them itself; above, a launch scans them first.
+constexpr int kOwnRows = 32;
+constexpr int kScanExperts = 32;
+
+// Block: 32 experts, the rows in 64 runs. prefix[r][e] = tokens in the rows before r; total[e].
+__global__ __launch_bounds__(kRouteThreads) void route_scan_kernel(RouteArgs a) {
+  __shared__ int part[kScanExperts][kWave + 1];  // [expert][run]
+  const int tid = threadIdx.x, E8 = (a.E + 7) & ~7, p = tid & 15, run = tid >> 4, lane = tid & (kWave - 1);
+  const int e = blockIdx.x * kScanExperts + 2 * p, len = (a.rows + kWave - 1) / kWave;
+  const int r0 = min(run * len, a.rows), r1 = min(r0 + len, a.rows);
+  const uint32_t* h = (const uint32_t*)a.hist + e / 2;
+  int s0 = 0, s1 = 0;
+  if (e < E8) {
+#pragma unroll 8
+    for (int r = r0; r < r1; ++r) {
+      const uint32_t v = h[(int64_t)r * (E8 / 2)];
+      s0 += (int)(v & 0xFFFFu), s1 += (int)(v >> 16);
+    }
+  }
+  part[2 * p][run] = s0;
+  part[2 * p + 1][run] = s1;
+  __syncthreads();
+  for (int q = tid / kWave; q < kScanExperts; q += kRouteThreads / kWave) {  // a wavefront scans one expert's runs
+    const int mine = part[q][lane];
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+      const int up = __shfl_up(inc, o, kWave);
+      if (lane >= o) inc += up;
+    }
+    part[q][lane] = inc - mine;
+    const int x = blockIdx.x * kScanExperts + q;
+    if (lane == kWave - 1 && x < E8) a.total[x] = inc;
+  }
+  __syncthreads();
+  if (e < E8) {
+    s0 = part[2 * p][run], s1 = part[2 * p + 1][run];
+#pragma unroll 8
+    for (int r = r0; r < r1; ++r) {
+      const uint32_t v = h[(int64_t)r * (E8 / 2)];
+      *(int2*)(a.prefix + (int64_t)r * E8 + e) = make_int2(s0, s1);
+      s0 += (int)(v & 0xFFFFu), s1 += (int)(v >> 16);
+    }
+  }
+}
+
+// One block per chunk. Its experts' tokens in all and in earlier chunks come from the scan, or for few
+// rows from the rows themselves. (Every block summing all rows, at 256 rows of 128 experts, took
+// 5 us of 10; the scan takes SCAN_US.)
+__global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs a) {
   __shared__ int total[1024], before[1024];
   extern __shared__ uint32_t bits[];  // [C / 32][local]
-  const int tid = threadIdx.x, c = blockIdx.x;
+  const int tid = threadIdx.x, c = blockIdx.x, E8 = (a.E + 7) & ~7;
   const int64_t i0 = (int64_t)c * a.C * a.K;
   const int n = (int)(min((int64_t)(c + 1) * a.C, (int64_t)a.T) * a.K - i0);
-  const int e0 = tid < n ? a.idx[i0 + tid] : -1;  // on its way while the rows are summed
+  const int e0 = tid < n ? a.idx[i0 + tid] : -1;  // on its way meanwhile
   const float w0 = tid < n ? a.w[i0 + tid] : 0.0f;
-  total[tid] = before[tid] = 0;
   for (int i = tid; i < a.C / 32 * a.local; i += kRouteThreads) bits[i] = 0;
-  __syncthreads();
-  const int E8 = (a.E + 7) & ~7, e = 8 * (tid & ((1 << log_q) - 1)), stripes = kRouteThreads >> log_q;
-  if (e < E8) {
-    int sum[8] = {0, 0, 0, 0, 0, 0, 0, 0}, low[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 4
-    for (int r = tid >> log_q; r < a.rows; r += stripes) {
-      const uint4 h = *(const uint4*)(a.hist + (int64_t)r * E8 + e);
-      const uint32_t w[4] = {h.x, h.y, h.z, h.w};
-      const int m = r < c ? -1 : 0;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int lo = (int)(w[q] & 0xFFFFu), hi = (int)(w[q] >> 16);
-        sum[2 * q] += lo, sum[2 * q + 1] += hi;
-        low[2 * q] += lo & m, low[2 * q + 1] += hi & m;
+  if (tid < a.E) {
+    int sum = 0, low = 0;
+    if (a.prefix) {
+      sum = a.total[tid];
+      low = a.prefix[(int64_t)c * E8 + tid];
+    } else {
+#pragma unroll 8
+      for (int r = 0; r < a.rows; ++r) {
+        const int h = a.hist[(int64_t)r * E8 + tid];
+        sum += h;
+        low += r < c ? h : 0;
       }
     }
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      if (sum[q]) atomicAdd(&total[e + q], sum[q]);
-      if (low[q]) atomicAdd(&before[e + q], low[q]);
-    }
+    total[tid] = sum;
+    before[tid] = low;
   }
   __syncthreads();
   place_chunk<kRouteThreads>(
@@ -898,58 +968,58 @@ __global__ __launch_bounds__(kAlphaThreads) void alpha_grad_kernel(int T, int K,
 
 // Calls f with the layout for E experts and the logits' type: sixteen lanes to a token up to 512
 // experts, so that a wavefront takes four tokens and reduces them together, with as few values to a
-// lane as hold E (257 experts in bf16: 73 us with 32 lanes of 16, 41 us with 16 lanes of 20).
-template <bool BF16, bool VEC, class F>
+// lane as hold E.
+template <bool BF16, class F>
 void by_experts(int E, F&& f) {
-  if (E <= 16) f(Layout<16, 1, BF16, false>());
-  else if (E <= 64) f(Layout<16, 4, BF16, VEC>());
-  else if (E <= 128) f(Layout<16, 8, BF16, VEC>());
-  else if (E <= 192) f(Layout<16, 12, BF16, VEC>());
-  else if (E <= 256) f(Layout<16, 16, BF16, VEC>());
-  else if (E <= 320) f(Layout<16, 20, BF16, VEC>());
-  else if (E <= 384) f(Layout<16, 24, BF16, VEC>());
-  else if (E <= 512) f(Layout<16, 32, BF16, VEC>());
-  else f(Layout<64, 16, BF16, VEC>());
+  if (E <= 64) f(Layout<16, 4, BF16>());
+  else if (E <= 128) f(Layout<16, 8, BF16>());
+  else if (E <= 192) f(Layout<16, 12, BF16>());
+  else if (E <= 256) f(Layout<16, 16, BF16>());
+  else if (E <= 320) f(Layout<16, 20, BF16>());
+  else if (E <= 384) f(Layout<16, 24, BF16>());
+  else if (E <= 512) f(Layout<16, 32, BF16>());
+  else f(Layout<64, 16, BF16>());
 }
 // The same for lists of eight: values by the eight, and as few lanes as hold them in 40 values each.
-template <bool BF16, bool VEC, class F>
+template <bool BF16, class F>
 void by_experts8(int E, F&& f) {
-  if (E <= 32) f(Layout<4, 8, BF16, VEC>());
-  else if (E <= 64) f(Layout<4, 16, BF16, VEC>());
-  else if (E <= 128) f(Layout<4, 32, BF16, VEC>());
-  else if (E <= 192) f(Layout<8, 24, BF16, VEC>());
-  else if (E <= 256) f(Layout<8, 32, BF16, VEC>());
-  else if (E <= 320) f(Layout<8, 40, BF16, VEC>());
-  else if (E <= 512) f(Layout<16, 32, BF16, VEC>());
-  else f(Layout<32, 32, BF16, VEC>());
-}
-template <class F>
-lrmoe_status by_layout8(const lrmoe_router* r, F&& f) {
-  const bool vec = r->E % 4 == 0;
-  if (r->dtype == LRMOE_BF16) vec ? by_experts8<true, true>(r->E, f) : by_experts8<true, false>(r->E, f);
-  else vec ? by_experts8<false, true>(r->E, f) : by_experts8<false, false>(r->E, f);
-  return launch_status();
+  if (E <= 32) f(Layout<4, 8, BF16>());
+  else if (E <= 64) f(Layout<4, 16, BF16>());
+  else if (E <= 128) f(Layout<4, 32, BF16>());
+  else if (E <= 192) f(Layout<8, 24, BF16>());
+  else if (E <= 256) f(Layout<8, 32, BF16>());
+  else if (E <= 320) f(Layout<8, 40, BF16>());
+  else if (E <= 512) f(Layout<16, 32, BF16>());
+  else f(Layout<32, 32, BF16>());
 }
 template <class F>
 lrmoe_status by_layout(const lrmoe_router* r, F&& f) {
-  const bool vec = r->E % 4 == 0;
-  if (r->dtype == LRMOE_BF16) vec ? by_experts<true, true>(r->E, f) : by_experts<true, false>(r->E, f);
-  else vec ? by_experts<false, true>(r->E, f) : by_experts<false, false>(r->E, f);
+  r->dtype == LRMOE_BF16 ? by_experts<true>(r->E, f) : by_experts<false>(r->E, f);
+  return launch_status();
+}
+template <class F>
+lrmoe_status by_layout8(const lrmoe_router* r, F&& f) {
+  r->dtype == LRMOE_BF16 ? by_experts8<true>(r->E, f) : by_experts8<false>(r->E, f);
   return launch_status();
 }
 
 }  // namespace
 
 size_t route_ws_bytes(const lrmoe_router* r) {
-  return align_up(std::max<size_t>(16, (size_t)ceil_div(r->T, route_chunk(r)) * align_up(r->E, 8) * 2), 256);
+  const size_t rows = (size_t)ceil_div(r->T, route_chunk(r)), E8 = align_up(r->E, 8);
+  const size_t hist = align_up(rows * E8 * 2, 256);
+  return std::max<size_t>(256, rows > kOwnRows ? hist + align_up((rows + 1) * E8 * 4, 256) : hist);
 }
 
 lrmoe_status launch_route(const lrmoe_router* r, const void* logits, const uint8_t* mask, int32_t* idx, float* w,
                           int32_t* counts, int64_t* seg_off, int32_t* tok, int32_t* slot, float* alpha,
                           int32_t* pmap, void* ws, hipStream_t s) {
   const int C = route_chunk(r), rows = (int)ceil_div(r->T, C);
+  const size_t E8 = align_up(r->E, 8);
+  int* prefix = rows > kOwnRows ? (int*)((char*)ws + align_up((size_t)rows * E8 * 2, 256)) : nullptr;
   const RouteArgs a{r->T, r->E, r->K, C, rows, r->first, r->local, r->renorm, r->scale, logits, mask,
-                    (uint16_t*)ws, idx, counts, tok, slot, pmap, w, alpha, seg_off};
+                    prefix, prefix ? prefix + (size_t)rows * E8 : nullptr, (uint16_t*)ws,
+                    idx, counts, tok, slot, pmap, w, alpha, seg_off};
   const size_t bits = (size_t)C / 8 * r->local, cnt = (size_t)r->E * 4;
   if (rows > 0) {
     const size_t lds = rows == 1 ? 2 * cnt + (size_t)C * r->K * 8 + bits : cnt;
@@ -959,9 +1029,11 @@ lrmoe_status launch_route(const lrmoe_router* r, const void* logits, const uint8
             : by_layout(r, [&](auto lay) { route_topk_kernel<decltype(lay)><<<rows, kRouteThreads, lds, s>>>(a); });
     if (st != LRMOE_OK || rows == 1) return st;
   }
-  int log_q = 0;
-  while ((8 << log_q) < r->E) ++log_q;
-  route_place_kernel<<<(unsigned)std::max(1, rows), kRouteThreads, bits, s>>>(a, log_q);
+  if (prefix) {
+    route_scan_kernel<<<(unsigned)ceil_div(r->E, kScanExperts), kRouteThreads, 0, s>>>(a);
+    if (launch_status() != LRMOE_OK) return LRMOE_ERR_HIP;
+  }
+  route_place_kernel<<<(unsigned)std::max(1, rows), kRouteThreads, bits, s>>>(a);
   return launch_status();
 }
 
