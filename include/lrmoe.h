@@ -503,9 +503,19 @@ lrmoe_status lrmoe_adamw_step_scalars(const lrmoe_adamw_config* c, lrmoe_adamw_s
  * not 0 would make a step of m / eps). What is not finite becomes the NaN code.
  * scalars_d (may be NULL: computed from the config here): the scalars in device memory, read when
  * the kernel runs, for calls captured into a graph; step, lr, weight_decay, grad_scale and seed of
- * the config are then not used. No workspace. Several launches for more than 48 tensors. */
+ * the config are then not used.
+ * plan_d (may be NULL: the tensors travel in the launch's arguments, 48 to a launch): what
+ * lrmoe_adamw_plan wrote for these tensors, in device memory, 16-byte aligned, for one launch
+ * however many there are. It has to be the plan of this very array: the kernel reads the pointers
+ * from it. No workspace. */
 lrmoe_status lrmoe_adamw(const lrmoe_adamw_tensor* tensors, int32_t n_tensors, const lrmoe_adamw_config* c,
-                         const lrmoe_adamw_scalars* scalars_d, lrmoe_stream_t stream);
+                         const void* plan_d, const lrmoe_adamw_scalars* scalars_d, lrmoe_stream_t stream);
+
+/* Host-only. Writes the plan of lrmoe_adamw into plan (host memory of *bytes bytes; NULL: only its
+ * size is wanted), which the caller copies to the device, and its size into *bytes. Fewer bytes
+ * than that are LRMOE_ERR_WORKSPACE. The checks are those of lrmoe_adamw. */
+lrmoe_status lrmoe_adamw_plan(const lrmoe_adamw_tensor* tensors, int32_t n_tensors, const lrmoe_adamw_config* c,
+                              void* plan, size_t* bytes);
 
 #ifdef __cplusplus
 }

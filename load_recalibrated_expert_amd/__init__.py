@@ -660,7 +660,7 @@ class AdamW:
             e.m, e.v, e.n, e.first = _ptr(self.m[i]), _ptr(self.v[i]), k, int(first[i])
             if bits == 8:
                 e.m_scale, e.v_scale = _ptr(self.m_scale[i]), _ptr(self.v_scale[i])
-        self._scalars = None
+        self._scalars = self._plan = None
         self.grads = None
         if grads is not None:
             self.bind(grads)
@@ -677,7 +677,24 @@ class AdamW:
         for e, g in zip(self._table, grads):
             e.grad = _ptr(g)
         self.c.grad_dtype = BF16 if dt == torch.bfloat16 else F32
-        self.grads = grads
+        self.grads, self._plan = grads, None
+
+    def _plan_ptr(self):
+        """The plan in device memory for more tensors than one launch's arguments take. It is made at
+        the second step with the same gradient buffers: a copy of it to the device would cost a
+        program that binds new ones at every step more than the launches it saves."""
+        if len(self.w) <= 48:
+            return None
+        if self._plan is None:
+            self._plan = False
+        elif self._plan is False and not torch.cuda.is_current_stream_capturing():
+            n, lib = ctypes.c_size_t(0), library()
+            args = (self._table, len(self.w), ctypes.byref(self.c))
+            _lib.check(lib.lrmoe_adamw_plan(*args, None, ctypes.byref(n)), "lrmoe_adamw_plan")
+            host = torch.empty(n.value, dtype=torch.uint8)
+            _lib.check(lib.lrmoe_adamw_plan(*args, host.data_ptr(), ctypes.byref(n)), "lrmoe_adamw_plan")
+            self._plan = host.to(self.w[0].device)
+        return self._plan.data_ptr() if self._plan is not False else None
 
     def _config(self, grad_scale):
         self.c.step, self.c.lr, self.c.weight_decay, self.c.grad_scale = self.t, self.lr, self.weight_decay, grad_scale
@@ -696,8 +713,8 @@ class AdamW:
         self.t += 1
         self._config(grad_scale)
         try:
-            _lib.check(library().lrmoe_adamw(self._table, len(self.w), ctypes.byref(self.c), None, _stream(stream)),
-                       "lrmoe_adamw")
+            _lib.check(library().lrmoe_adamw(self._table, len(self.w), ctypes.byref(self.c), self._plan_ptr(), None,
+                                             _stream(stream)), "lrmoe_adamw")
         except LrmoeError:
             self.t -= 1
             raise
@@ -720,5 +737,5 @@ class AdamW:
         if self._scalars is None or self.grads is None:
             raise ValueError("call advance (and bind the gradient buffers) before step_captured")
         self._check_place()
-        _lib.check(library().lrmoe_adamw(self._table, len(self.w), ctypes.byref(self.c), _ptr(self._scalars),
-                                         _stream(stream)), "lrmoe_adamw")
+        _lib.check(library().lrmoe_adamw(self._table, len(self.w), ctypes.byref(self.c), self._plan_ptr(),
+                                         _ptr(self._scalars), _stream(stream)), "lrmoe_adamw")

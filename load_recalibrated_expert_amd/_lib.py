@@ -25,7 +25,7 @@ EXPORTS = ("lrmoe_status_string", "lrmoe_version", "lrmoe_validate", "lrmoe_work
            "lrmoe_compact", "lrmoe_grouped_gemm_bwd", "lrmoe_scatter", "lrmoe_expert_forward",
            "lrmoe_select_noalloc", "lrmoe_compact_weighted", "lrmoe_grouped_gemm_bwd_gathered",
            "lrmoe_router_workspace_size", "lrmoe_route", "lrmoe_balance_loss", "lrmoe_route_bwd", "lrmoe_alpha_grad",
-           "lrmoe_adamw_step_scalars", "lrmoe_adamw")
+           "lrmoe_adamw_step_scalars", "lrmoe_adamw_plan", "lrmoe_adamw")
 
 
 class LrmoeError(RuntimeError):
@@ -110,7 +110,8 @@ def load() -> ctypes.CDLL:
         "lrmoe_route_bwd": [ctypes.POINTER(CRouter), vp, vp, vp, vp, vp, i64, vp, i32, vp, vp, vp, vp, vp],
         "lrmoe_alpha_grad": [P, vp, vp, vp, vp, vp, vp, vp],
         "lrmoe_adamw_step_scalars": [ctypes.POINTER(CAdamwConfig), ctypes.POINTER(CAdamwScalars)],
-        "lrmoe_adamw": [ctypes.POINTER(CAdamwTensor), i32, ctypes.POINTER(CAdamwConfig), vp, vp],
+        "lrmoe_adamw": [ctypes.POINTER(CAdamwTensor), i32, ctypes.POINTER(CAdamwConfig), vp, vp, vp],
+        "lrmoe_adamw_plan": [ctypes.POINTER(CAdamwTensor), i32, ctypes.POINTER(CAdamwConfig), vp, ctypes.POINTER(sz)],
     }
     for name, args in sigs.items():
         f = getattr(lib, name)

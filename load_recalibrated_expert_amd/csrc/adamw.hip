@@ -1,8 +1,9 @@
 // AdamW over many tensors in one launch, first and second moments in 32 or in 8 bits.
 //
-// Elementwise over [n]: HBM-bound, every array read and written once. A launch takes the tensors
-// from a table in its arguments (nothing is copied to the device), cut into chunks of kChunk
-// elements; a block finds its chunk's tensor by bisection of the chunk counts.
+// Elementwise over [n]: HBM-bound, every array read and written once. The tensors come in a table,
+// cut into chunks of kChunk elements: in the launch's arguments, 48 to a launch, or all of them
+// in device memory (a plan). A wavefront finds its chunk's tensor by comparing with 64 first chunks
+// at a time.
 #include <algorithm>
 
 #include "common.h"
@@ -14,12 +15,22 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBlock = 256;   // elements that share a scale: four to a lane of one wavefront
-constexpr int kChunk = 4096;  // elements of one thread block
+constexpr int kChunk = 1024;  // elements of one thread block: four to a thread
 
-struct AdamwTable {
+// The tensors that have elements, and the first chunk of each.
+struct ArgTable {
   lrmoe_adamw_tensor t[kAdamwTensors];
-  uint32_t chunk[kAdamwTensors + 1];  // first chunk of each tensor
+  uint32_t chunk[kAdamwTensors];
   int32_t n;
+  __device__ __forceinline__ const lrmoe_adamw_tensor& tensor(int i) const { return t[i]; }
+  __device__ __forceinline__ uint32_t first(int i) const { return chunk[i]; }
+};
+struct PlanTable {
+  const lrmoe_adamw_tensor* t;
+  const uint32_t* chunk;
+  int32_t n;
+  __device__ __forceinline__ const lrmoe_adamw_tensor& tensor(int i) const { return t[i]; }
+  __device__ __forceinline__ uint32_t first(int i) const { return chunk[i]; }
 };
 
 struct AdamwArgs {
@@ -147,17 +158,17 @@ __device__ __forceinline__ void store_codes(void* __restrict__ p, float* __restr
   if ((threadIdx.x & (kWave - 1)) == 0 && left > 0) scales[i / kBlock] = pow2(k);
 }
 
-template <bool Q8, bool W16, bool G16, bool MASTER>
-__global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwTable tab, AdamwArgs a) {
-  int lo = 0, hi = tab.n - 1;
-  while (lo < hi) {  // the last tensor whose first chunk is at or before this one
-    const int m = (lo + hi + 1) / 2;
-    if (tab.chunk[m] <= blockIdx.x) lo = m;
-    else hi = m - 1;
+template <bool Q8, bool W16, bool G16, bool MASTER, class Table>
+__global__ __launch_bounds__(kThreads) void adamw_kernel(Table tab, AdamwArgs a) {
+  int at = -1;  // the last tensor whose first chunk is at or before this one
+  for (int i = 0; i < tab.n; i += kWave) {
+    const int q = i + (int)(threadIdx.x & (kWave - 1));
+    at += __popcll(__ballot(q < tab.n && tab.first(q) <= blockIdx.x));
   }
-  const lrmoe_adamw_tensor t = tab.t[lo];
+  at = __builtin_amdgcn_readfirstlane(at);
+  const lrmoe_adamw_tensor t = tab.tensor(at);
   const lrmoe_adamw_scalars s = a.dyn ? *a.dyn : a.s;
-  const int64_t i0 = (int64_t)(blockIdx.x - tab.chunk[lo]) * kChunk;
+  const int64_t i0 = (int64_t)(blockIdx.x - tab.first(at)) * kChunk;
   for (int u = 0; u < kChunk / (4 * kThreads); ++u) {
     const int64_t i = i0 + (int64_t)u * 4 * kThreads + threadIdx.x * 4;
     const int left = (int)max((int64_t)0, min((int64_t)4, t.n - i));
@@ -205,15 +216,56 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwTable tab, AdamwAr
   }
 }
 
-template <bool Q8, bool W16, bool G16, bool MASTER>
-void run(unsigned grid, const AdamwTable& tab, const AdamwArgs& a, hipStream_t s) {
-  adamw_kernel<Q8, W16, G16, MASTER><<<grid, kThreads, 0, s>>>(tab, a);
+template <class Table>
+lrmoe_status run(const lrmoe_adamw_config* c, unsigned grid, const Table& tab, const AdamwArgs& a, hipStream_t s) {
+  const int kind = (c->state_bits == 8 ? 8 : 0) + (c->w_dtype == LRMOE_BF16 ? 4 : 0) +
+                   (c->grad_dtype == LRMOE_BF16 ? 2 : 0) + (c->master ? 1 : 0);
+  switch (kind) {
+    case 0: adamw_kernel<false, false, false, false><<<grid, kThreads, 0, s>>>(tab, a); break;
+    case 2: adamw_kernel<false, false, true, false><<<grid, kThreads, 0, s>>>(tab, a); break;
+    case 4: adamw_kernel<false, true, false, false><<<grid, kThreads, 0, s>>>(tab, a); break;
+    case 5: adamw_kernel<false, true, false, true><<<grid, kThreads, 0, s>>>(tab, a); break;
+    case 6: adamw_kernel<false, true, true, false><<<grid, kThreads, 0, s>>>(tab, a); break;
+    case 7: adamw_kernel<false, true, true, true><<<grid, kThreads, 0, s>>>(tab, a); break;
+    case 8: adamw_kernel<true, false, false, false><<<grid, kThreads, 0, s>>>(tab, a); break;
+    case 10: adamw_kernel<true, false, true, false><<<grid, kThreads, 0, s>>>(tab, a); break;
+    case 12: adamw_kernel<true, true, false, false><<<grid, kThreads, 0, s>>>(tab, a); break;
+    case 13: adamw_kernel<true, true, false, true><<<grid, kThreads, 0, s>>>(tab, a); break;
+    case 14: adamw_kernel<true, true, true, false><<<grid, kThreads, 0, s>>>(tab, a); break;
+    case 15: adamw_kernel<true, true, true, true><<<grid, kThreads, 0, s>>>(tab, a); break;
+    default: return LRMOE_ERR_UNSUPPORTED;
+  }
+  return launch_status();
+}
+
+// Tables as a plan holds them: the tensors that have elements, then their first chunks.
+int live_tensors(const lrmoe_adamw_tensor* t, int32_t n) {
+  int k = 0;
+  for (int32_t i = 0; i < n; ++i) k += t[i].n > 0;
+  return k;
 }
 
 }  // namespace
 
+size_t adamw_plan_bytes(int32_t n_tensors) {
+  return std::max<size_t>(256, align_up((size_t)n_tensors * (sizeof(lrmoe_adamw_tensor) + sizeof(uint32_t)), 256));
+}
+
+void adamw_plan(const lrmoe_adamw_tensor* tensors, int32_t n_tensors, void* plan) {
+  lrmoe_adamw_tensor* t = (lrmoe_adamw_tensor*)plan;
+  uint32_t* first = (uint32_t*)(t + live_tensors(tensors, n_tensors));
+  uint32_t chunks = 0;
+  for (int32_t i = 0; i < n_tensors; ++i) {
+    if (tensors[i].n == 0) continue;
+    *t++ = tensors[i];
+    *first++ = chunks;
+    chunks += (uint32_t)ceil_div(tensors[i].n, kChunk);
+  }
+}
+
 lrmoe_status launch_adamw(const lrmoe_adamw_tensor* tensors, int32_t n_tensors, const lrmoe_adamw_config* c,
-                          const lrmoe_adamw_scalars& host, const lrmoe_adamw_scalars* scalars_d, hipStream_t s) {
+                          const lrmoe_adamw_scalars& host, const void* plan_d, const lrmoe_adamw_scalars* scalars_d,
+                          hipStream_t s) {
   AdamwArgs a;
   a.b1 = (float)c->beta1;
   a.a1 = (float)(1.0 - c->beta1);
@@ -222,37 +274,31 @@ lrmoe_status launch_adamw(const lrmoe_adamw_tensor* tensors, int32_t n_tensors, 
   a.eps = (float)c->eps;
   a.s = host;
   a.dyn = scalars_d;
-  const bool q = c->state_bits == 8, w16 = c->w_dtype == LRMOE_BF16, g16 = c->grad_dtype == LRMOE_BF16;
+  if (plan_d) {
+    const int n = live_tensors(tensors, n_tensors);
+    uint64_t chunks = 0;
+    for (int32_t i = 0; i < n_tensors; ++i) chunks += (uint64_t)ceil_div(tensors[i].n, kChunk);
+    if (n == 0) return LRMOE_OK;
+    if (chunks >> 31) return LRMOE_ERR_UNSUPPORTED;
+    const lrmoe_adamw_tensor* t = (const lrmoe_adamw_tensor*)plan_d;
+    return run(c, (unsigned)chunks, PlanTable{t, (const uint32_t*)(t + n), n}, a, s);
+  }
   int32_t i = 0;
   while (i < n_tensors) {
-    AdamwTable tab;
+    ArgTable tab;
     tab.n = 0;
-    uint32_t chunks = 0;
+    uint64_t chunks = 0;
     for (; i < n_tensors && tab.n < kAdamwTensors; ++i) {
-      if (tensors[i].n == 0) continue;
+      const uint64_t more = (uint64_t)ceil_div(tensors[i].n, kChunk);
+      if (more == 0) continue;
+      if ((chunks + more) >> 31) break;  // the next launch takes it
       tab.t[tab.n] = tensors[i];
-      tab.chunk[tab.n++] = chunks;
-      chunks += (uint32_t)ceil_div(tensors[i].n, kChunk);
+      tab.chunk[tab.n++] = (uint32_t)chunks;
+      chunks += more;
     }
     if (tab.n == 0) break;
-    tab.chunk[tab.n] = chunks;
-    const int kind = (q ? 8 : 0) + (w16 ? 4 : 0) + (g16 ? 2 : 0) + (c->master ? 1 : 0);
-    switch (kind) {
-      case 0: run<false, false, false, false>(chunks, tab, a, s); break;
-      case 2: run<false, false, true, false>(chunks, tab, a, s); break;
-      case 4: run<false, true, false, false>(chunks, tab, a, s); break;
-      case 5: run<false, true, false, true>(chunks, tab, a, s); break;
-      case 6: run<false, true, true, false>(chunks, tab, a, s); break;
-      case 7: run<false, true, true, true>(chunks, tab, a, s); break;
-      case 8: run<true, false, false, false>(chunks, tab, a, s); break;
-      case 10: run<true, false, true, false>(chunks, tab, a, s); break;
-      case 12: run<true, true, false, false>(chunks, tab, a, s); break;
-      case 13: run<true, true, false, true>(chunks, tab, a, s); break;
-      case 14: run<true, true, true, false>(chunks, tab, a, s); break;
-      case 15: run<true, true, true, true>(chunks, tab, a, s); break;
-      default: return LRMOE_ERR_UNSUPPORTED;
-    }
-    if (launch_status() != LRMOE_OK) return LRMOE_ERR_HIP;
+    const lrmoe_status st = run(c, (unsigned)chunks, tab, a, s);
+    if (st != LRMOE_OK) return st;
   }
   return LRMOE_OK;
 }

@@ -160,6 +160,9 @@ lrmoe_status launch_alpha_grad(const lrmoe_problem* p, const void* G, const void
 
 constexpr int kAdamwTensors = 48;  // tensors of one launch: their table travels in the kernel arguments
 lrmoe_status launch_adamw(const lrmoe_adamw_tensor* tensors, int32_t n_tensors, const lrmoe_adamw_config* c,
-                          const lrmoe_adamw_scalars& host, const lrmoe_adamw_scalars* scalars_d, hipStream_t s);
+                          const lrmoe_adamw_scalars& host, const void* plan_d, const lrmoe_adamw_scalars* scalars_d,
+                          hipStream_t s);
+size_t adamw_plan_bytes(int32_t n_tensors);
+void adamw_plan(const lrmoe_adamw_tensor* tensors, int32_t n_tensors, void* plan);
 
 }  // namespace lrmoe

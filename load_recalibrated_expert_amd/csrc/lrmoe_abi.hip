@@ -117,6 +117,24 @@ lrmoe_status check_adamw(const lrmoe_adamw_config* c) {
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
+lrmoe_status check_adamw_tensors(const lrmoe_adamw_tensor* tensors, int32_t n_tensors, const lrmoe_adamw_config* c) {
+  if (n_tensors < 0 || (n_tensors > 0 && !tensors)) return LRMOE_ERR_INVALID_ARG;
+  const bool q = c->state_bits == 8;
+  for (int32_t i = 0; i < n_tensors; ++i) {
+    const lrmoe_adamw_tensor& t = tensors[i];
+    if (t.n < 0 || t.first < 0 || (q && t.first % 256 != 0)) return LRMOE_ERR_INVALID_ARG;
+    if (t.n > ((int64_t)1 << 36)) return LRMOE_ERR_UNSUPPORTED;
+    if (t.n == 0) continue;
+    if (!t.w || !t.grad || !t.m || !t.v || (c->master != 0) != (t.master != nullptr)) return LRMOE_ERR_INVALID_ARG;
+    if (q != (t.m_scale != nullptr) || q != (t.v_scale != nullptr)) return LRMOE_ERR_INVALID_ARG;
+    const uintptr_t a = q ? 4 : 16;
+    if (!aligned(t.w, 16) || !aligned(t.master, 16) || !aligned(t.grad, 16) || !aligned(t.m, a) || !aligned(t.v, a) ||
+        !aligned(t.m_scale, 4) || !aligned(t.v_scale, 4))
+      return LRMOE_ERR_INVALID_ARG;
+  }
+  return LRMOE_OK;
+}
+
 #define LRMOE_TRY(x)                      \
   do {                                    \
     const lrmoe_status st_ = (x);         \
@@ -455,25 +473,27 @@ lrmoe_status lrmoe_adamw_step_scalars(const lrmoe_adamw_config* c, lrmoe_adamw_s
   return LRMOE_OK;
 }
 
+lrmoe_status lrmoe_adamw_plan(const lrmoe_adamw_tensor* tensors, int32_t n_tensors, const lrmoe_adamw_config* c,
+                              void* plan, size_t* bytes) {
+  LRMOE_TRY(check_adamw(c));
+  LRMOE_TRY(check_adamw_tensors(tensors, n_tensors, c));
+  if (!bytes) return LRMOE_ERR_INVALID_ARG;
+  const size_t need = adamw_plan_bytes(n_tensors);
+  if (plan) {
+    if (*bytes < need) return LRMOE_ERR_WORKSPACE;
+    adamw_plan(tensors, n_tensors, plan);
+  }
+  *bytes = need;
+  return LRMOE_OK;
+}
+
 lrmoe_status lrmoe_adamw(const lrmoe_adamw_tensor* tensors, int32_t n_tensors, const lrmoe_adamw_config* c,
-                         const lrmoe_adamw_scalars* scalars_d, lrmoe_stream_t stream) {
+                         const void* plan_d, const lrmoe_adamw_scalars* scalars_d, lrmoe_stream_t stream) {
   lrmoe_adamw_scalars host;
   LRMOE_TRY(lrmoe_adamw_step_scalars(c, &host));
-  if (n_tensors < 0 || (n_tensors > 0 && !tensors)) return LRMOE_ERR_INVALID_ARG;
-  const bool q = c->state_bits == 8;
-  for (int32_t i = 0; i < n_tensors; ++i) {
-    const lrmoe_adamw_tensor& t = tensors[i];
-    if (t.n < 0 || t.first < 0 || (q && t.first % 256 != 0)) return LRMOE_ERR_INVALID_ARG;
-    if (t.n > ((int64_t)1 << 36)) return LRMOE_ERR_UNSUPPORTED;
-    if (t.n == 0) continue;
-    if (!t.w || !t.grad || !t.m || !t.v || (c->master != 0) != (t.master != nullptr)) return LRMOE_ERR_INVALID_ARG;
-    if (q != (t.m_scale != nullptr) || q != (t.v_scale != nullptr)) return LRMOE_ERR_INVALID_ARG;
-    const uintptr_t a = q ? 4 : 16;
-    if (!aligned(t.w, 16) || !aligned(t.master, 16) || !aligned(t.grad, 16) || !aligned(t.m, a) || !aligned(t.v, a) ||
-        !aligned(t.m_scale, 4) || !aligned(t.v_scale, 4))
-      return LRMOE_ERR_INVALID_ARG;
-  }
-  return launch_adamw(tensors, n_tensors, c, host, scalars_d, (hipStream_t)stream);
+  LRMOE_TRY(check_adamw_tensors(tensors, n_tensors, c));
+  if (!aligned(plan_d, 16) || !aligned(scalars_d, 4)) return LRMOE_ERR_INVALID_ARG;
+  return launch_adamw(tensors, n_tensors, c, host, plan_d, scalars_d, (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -127,7 +127,7 @@ def _config(**kw):
 def test_adamw_config_checks(kw, expect):
     lib, s = _lib.load(), _lib.CAdamwScalars()
     assert lib.lrmoe_adamw_step_scalars(ctypes.byref(_config(**kw)), ctypes.byref(s)) == expect
-    assert lib.lrmoe_adamw(None, 0, ctypes.byref(_config(**kw)), None, None) == expect  # no tensors: nothing to launch
+    assert lib.lrmoe_adamw(None, 0, ctypes.byref(_config(**kw)), None, None, None) == expect  # no tensors: nothing to launch
 
 
 def test_adamw_scalars():
@@ -147,7 +147,7 @@ def test_adamw_tensor_refusals():
 
     def call(cfg=None, **kw):
         t = (_lib.CAdamwTensor * 2)(_lib.CAdamwTensor(n=0), _lib.CAdamwTensor(**{**good, **kw}))
-        return lib.lrmoe_adamw(t, 2, ctypes.byref(cfg or _config()), None, None)
+        return lib.lrmoe_adamw(t, 2, ctypes.byref(cfg or _config()), None, None, None)
 
     for kw in (dict(w=None), dict(master=None), dict(grad=None), dict(m=None), dict(v=None), dict(m_scale=None),
                dict(v_scale=None), dict(n=-1), dict(first=-256), dict(first=100), dict(w=0x1008), dict(master=0x2004),
@@ -157,8 +157,38 @@ def test_adamw_tensor_refusals():
     c32 = _config(state_bits=32)
     assert call(c32) == _lib.ERR_INVALID_ARG  # scales given to 32-bit states
     assert call(c32, m_scale=None, v_scale=None, m=0x4004) == _lib.ERR_INVALID_ARG  # 32-bit states: 16 bytes
-    assert lib.lrmoe_adamw(None, 1, ctypes.byref(_config()), None, None) == _lib.ERR_INVALID_ARG
-    assert lib.lrmoe_adamw(None, -1, ctypes.byref(_config()), None, None) == _lib.ERR_INVALID_ARG
+    assert lib.lrmoe_adamw(None, 1, ctypes.byref(_config()), None, None, None) == _lib.ERR_INVALID_ARG
+    assert lib.lrmoe_adamw(None, -1, ctypes.byref(_config()), None, None, None) == _lib.ERR_INVALID_ARG
+
+
+def test_adamw_plan():
+    """The plan's size, its refusals, and its contents: the tensors that have elements and their first
+    chunks of a whole number of elements each."""
+    lib = _lib.load()
+    c = _config(state_bits=32)
+    sizes = [5, 0, 100000, 4096, 1]
+    t = (_lib.CAdamwTensor * 5)(*[_lib.CAdamwTensor(w=0x1000 * (i + 1), master=0x90000, grad=0x90000, m=0x90000, v=0x90000,
+                                                   n=n) for i, n in enumerate(sizes)])
+    n = ctypes.c_size_t(0)
+    assert lib.lrmoe_adamw_plan(t, 5, ctypes.byref(c), None, None) == _lib.ERR_INVALID_ARG
+    assert lib.lrmoe_adamw_plan(t, 5, None, None, ctypes.byref(n)) == _lib.ERR_INVALID_ARG
+    assert lib.lrmoe_adamw_plan(None, 5, ctypes.byref(c), None, ctypes.byref(n)) == _lib.ERR_INVALID_ARG
+    assert lib.lrmoe_adamw_plan(t, 5, ctypes.byref(c), None, ctypes.byref(n)) == _lib.OK
+    need = n.value
+    buf = (ctypes.c_uint8 * need)()
+    n.value = need - 1
+    assert lib.lrmoe_adamw_plan(t, 5, ctypes.byref(c), buf, ctypes.byref(n)) == _lib.ERR_WORKSPACE
+    n.value = need
+    assert lib.lrmoe_adamw_plan(t, 5, ctypes.byref(c), buf, ctypes.byref(n)) == _lib.OK and n.value == need
+    size = ctypes.sizeof(_lib.CAdamwTensor)
+    live = (_lib.CAdamwTensor * 4).from_buffer(buf)
+    assert [e.n for e in live] == [5, 100000, 4096, 1] and [e.w for e in live] == [0x1000, 0x3000, 0x4000, 0x5000]
+    first = np.frombuffer(buf, np.uint32, 4, 4 * size).tolist()
+    assert first[0] == 0 and first[1] == 1  # five elements are one chunk
+    chunk = 4096 // (first[3] - first[2])
+    assert first[2] == 1 + -(-100000 // chunk)
+    assert lib.lrmoe_adamw(t, 5, ctypes.byref(c), ctypes.c_void_p(0x1008), None, None) == _lib.ERR_INVALID_ARG
+    assert lib.lrmoe_adamw(t, 5, ctypes.byref(c), None, ctypes.c_void_p(0x1002), None) == _lib.ERR_INVALID_ARG
 
 
 def test_python_refusals():
