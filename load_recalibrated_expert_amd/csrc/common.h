@@ -90,6 +90,22 @@ __device__ __forceinline__ double sumsq_f32x4(uint4 v) {
   return a * a + b * b + c * c + d * d;
 }
 
+// Reductions over groups of L lanes (4 to 64); every lane gets the result, the same bits in each, as
+// both lanes of a pair compute the same sum. Up to sixteen lanes the partner's value comes by DPP,
+// at register speed, instead of a cross-lane permute through LDS. lane_swap<S> exchanges lanes S
+// apart, or mirrored in 2 S lanes, which is the same once S lanes agree.
+template <int S>
+__device__ __forceinline__ int lane_swap(int v) {
+  constexpr int ctrl = S == 1 ? 0xB1 : S == 2 ? 0x4E : S == 4 ? 0x141 : 0x140;
+  if (S <= 8) return __builtin_amdgcn_update_dpp(0, v, ctrl, 0xF, 0xF, true);
+  return __shfl_xor(v, S, kWave);
+}
+template <int L, int S = 1, class Op>
+__device__ __forceinline__ int group_reduce(int v, Op op) {
+  if constexpr (S < L) return group_reduce<L, 2 * S>(op(v, lane_swap<S>(v)), op);
+  else return v;
+}
+
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 

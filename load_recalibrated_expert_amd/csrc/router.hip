@@ -35,21 +35,6 @@ __device__ __forceinline__ float exp_below(float d) {
 // so a whole sum over E values is off by less than 2 ln(E) 2^-24 more. NaN if the token is not live.
 __device__ __forceinline__ float exp_term(float d) { return __builtin_amdgcn_exp2f(d * 1.44269502f); }
 
-// Reductions over the L lanes of a token's group (4 to 64); every lane gets the result, the same bits
-// in each, as both lanes of a pair compute the same sum. Up to sixteen lanes the partner's value
-// comes by DPP, at register speed, instead of a cross-lane permute through LDS. swap<S> exchanges
-// lanes S apart, or mirrored in 2 S lanes, which is the same once S lanes agree.
-template <int S>
-__device__ __forceinline__ int swap(int v) {
-  constexpr int ctrl = S == 1 ? 0xB1 : S == 2 ? 0x4E : S == 4 ? 0x141 : 0x140;
-  if (S <= 8) return __builtin_amdgcn_update_dpp(0, v, ctrl, 0xF, 0xF, true);
-  return __shfl_xor(v, S, kWave);
-}
-template <int L, int S = 1, class Op>
-__device__ __forceinline__ int group_reduce(int v, Op op) {
-  if constexpr (S < L) return group_reduce<L, 2 * S>(op(v, swap<S>(v)), op);
-  else return v;
-}
 template <int L>
 __device__ __forceinline__ float group_max(float v) {
   return __int_as_float(group_reduce<L>(__float_as_int(v), [](int a, int b) {
@@ -289,10 +274,8 @@ struct RouteBlock {
 // reversed are the eight largest of both, sorted by 12 more exchanges. With four lanes to a token
 // (up to 128 experts) that is a fifth of the instructions of taking the largest K times over:
 // 32768 x 128 f32 takes 8.2 us here and 13.4 us that way.
-#pragma float_control(precise, off, push)  // maxima without NaN handling: there are none among the keys
 __device__ __forceinline__ double key_max(double a, double b) { return __builtin_fmax(a, b); }
 __device__ __forceinline__ double key_min(double a, double b) { return __builtin_fmin(a, b); }
-#pragma float_control(pop)
 __device__ __forceinline__ uint32_t key_max(uint32_t a, uint32_t b) { return a > b ? a : b; }
 __device__ __forceinline__ uint32_t key_min(uint32_t a, uint32_t b) { return a < b ? a : b; }
 template <class Key>
@@ -320,19 +303,19 @@ __device__ __forceinline__ void merge8(Key* a, const Key* b) {
   exchange(a[0], a[1]), exchange(a[2], a[3]), exchange(a[4], a[5]), exchange(a[6], a[7]);
 }
 template <int S>
-__device__ __forceinline__ double swap(double v) {
-  return __hiloint2double(swap<S>(__double2hiint(v)), swap<S>(__double2loint(v)));
+__device__ __forceinline__ double key_swap(double v) {
+  return __hiloint2double(lane_swap<S>(__double2hiint(v)), lane_swap<S>(__double2loint(v)));
 }
 template <int S>
-__device__ __forceinline__ uint32_t swap(uint32_t v) {
-  return (uint32_t)swap<S>((int)v);
+__device__ __forceinline__ uint32_t key_swap(uint32_t v) {
+  return (uint32_t)lane_swap<S>((int)v);
 }
 template <int L, int S = 1, class Key>
 __device__ __forceinline__ void merge_lanes(Key* a) {
   if constexpr (S < L) {
     Key b[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = swap<S>(a[i]);
+    for (int i = 0; i < 8; ++i) b[i] = key_swap<S>(a[i]);
     merge8(a, b);
     merge_lanes<L, 2 * S>(a);
   }
