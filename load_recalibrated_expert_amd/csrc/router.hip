@@ -531,7 +531,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_scan_kernel(RouteArgs a) 
 
 // One block per chunk. Its experts' tokens in all and in earlier chunks come from the scan, or for few
 // rows from the rows themselves. (Every block summing all rows, at 256 rows of 128 experts, took
-// 5 us of 10; the scan takes SCAN_US.)
+// 5 us of 10; the scan takes 4.1 us.)
 __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs a) {
   __shared__ int total[1024], before[1024];
   extern __shared__ uint32_t bits[];  // [C / 32][local]
@@ -566,7 +566,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs a)
 // ---------------------------------------------------------------- balance loss
 
 constexpr int kBalThreads = 1024;
-constexpr int kBalTile = 64;  // tokens of one tile
+constexpr int kBalTile = 64;      // tokens of one tile
+constexpr int kJoinExperts = 64;  // experts of one joining block, one to a lane
 
 // Sequence s, clamped into [0, T] whatever the offsets hold.
 __device__ __forceinline__ void seq_range(const int64_t* __restrict__ off, int s, int T, int64_t* lo, int64_t* hi) {
@@ -600,7 +601,7 @@ struct BalanceWs {
   float* psum;     // [tiles][E] sums of probabilities
   int32_t* count;  // [tiles][E]
   int32_t* live;   // [tiles]
-  double* dot;     // [n_seq][parts] sum_e counts psum over 64 experts
+  double* dot;     // [n_seq][parts] sum_e counts psum over a joining block's experts
   int32_t* n;      // [n_seq] live tokens
   uint32_t* done;  // join blocks that are through
 };
@@ -608,7 +609,7 @@ struct BalanceWs {
 int64_t balance_tiles(const lrmoe_router* r, int32_t n_seq) { return r->T / kBalTile + n_seq; }
 
 size_t balance_layout(const lrmoe_router* r, int32_t n_seq, char* base, BalanceWs* out) {
-  const size_t tiles = (size_t)balance_tiles(r, n_seq), parts = (size_t)ceil_div(r->E, kWave);
+  const size_t tiles = (size_t)balance_tiles(r, n_seq), parts = (size_t)ceil_div(r->E, kJoinExperts);
   size_t at = 0;
   auto take = [&](size_t b) {
     char* p = base + at;
@@ -710,20 +711,23 @@ __device__ __forceinline__ double block_sum(double v, double* sh) {  // kJoinThr
   return a;
 }
 
-// Grid (sequence, 64 experts): the sequence's tiles joined, wavefront by wavefront and then over
+// Grid (sequence, 64 experts): the sequence's tiles joined, every 16th by one wavefront and those over
 // the wavefronts, always in the same order. The block that finishes last sums the loss; it reads
 // what the others wrote behind their release, in a fixed order, so the result does not depend on
-// which block it is.
+// which block it is. 8.4 us for 512 tiles of 128 experts, 2.5 of them the last block's part, most
+// of the rest latency: 16 experts to a block took 7.9 us there, but 9.1 instead of 7.0 us for 37
+// sequences of 60 experts, whose releases are then four times as many.
 __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(int T, int E, int K, int n_seq, float coef,
                                                                     const int64_t* __restrict__ off, BalanceWs ws,
                                                                     int32_t* __restrict__ counts,
                                                                     float* __restrict__ psum, float* __restrict__ norm,
                                                                     float* __restrict__ loss) {
-  __shared__ double sh[kJoinWaves], sum_of[kJoinWaves][kWave];
-  __shared__ int n_of[kJoinWaves][kWave];
+  __shared__ double sh[kJoinWaves], sum_of[kJoinWaves][kJoinExperts];
+  __shared__ int n_of[kJoinWaves][kJoinExperts];
   __shared__ bool last;
   const int s = blockIdx.x, part = blockIdx.y, parts = gridDim.y;
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, e = part * kWave + lane;
+  const int wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1);
+  const int e = part * kJoinExperts + lane;
   int64_t lo, hi;
   seq_range(off, s, T, &lo, &hi);
   const int64_t b0 = first_tile(lo, s);
@@ -731,17 +735,17 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(int T, int E
   double a = 0.0;
   int n = 0;
   if (e < E) {
-#pragma unroll 16
+#pragma unroll 8
     for (int i = wave; i < tiles; i += kJoinWaves) {
       a += (double)ws.psum[(b0 + i) * E + e];
       n += ws.count[(b0 + i) * E + e];
     }
   }
-  sum_of[wave][lane] = a;
-  n_of[wave][lane] = n;
   int live = 0;
   if (part == 0)
     for (int i = threadIdx.x; i < tiles; i += kJoinThreads) live += ws.live[b0 + i];
+  sum_of[wave][lane] = a;
+  n_of[wave][lane] = n;
   __syncthreads();
   double dot = 0.0;
   if (wave == 0 && e < E) {
@@ -909,9 +913,37 @@ __global__ __launch_bounds__(kGradThreads) void route_bwd_kernel(
 // ---------------------------------------------------------------- gradient of the routing weights
 
 constexpr int kAlphaThreads = 256;
+constexpr int kAlphaRows = 8;  // pairs whose rows a wavefront reads at once
 
-// One wavefront per token: its gradient row against the rows of its K pairs. Products and sums in
-// fp64, as the score's norms.
+// Sum over the wavefront, the same bits in every lane.
+template <int S = 1>
+__device__ __forceinline__ double lanes_sum(double v) {
+  if constexpr (S < kWave)
+    return lanes_sum<2 * S>(v + __hiloint2double(lane_swap<S>(__double2hiint(v)), lane_swap<S>(__double2loint(v))));
+  else return v;
+}
+
+// Products of 16 bytes of two rows, added to s in fp64 (as the score's norms; products of bf16 values are
+// exact in f32).
+template <bool BF16>
+__device__ __forceinline__ double dot16(uint4 g, uint4 y, double s) {
+  const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (BF16) {
+      s += (double)(bf16_lo(gw[i]) * bf16_lo(yw[i]));
+      s += (double)(bf16_hi(gw[i]) * bf16_hi(yw[i]));
+    } else {
+      s += (double)__uint_as_float(gw[i]) * (double)__uint_as_float(yw[i]);
+    }
+  }
+  return s;
+}
+
+// One wavefront per token: its gradient row is read once against the rows of up to eight of its
+// pairs, whose loads are all in flight before the first product (one row after the other: 256 us for
+// 32768 tokens, top-8, 2048 bf16; so: 190 us, 6.4 TB/s, with one or two column blocks at a time;
+// four: 207 us). Bound by HBM on the [N x D] rows.
 template <bool BF16>
 __global__ __launch_bounds__(kAlphaThreads) void alpha_grad_kernel(int T, int K, int D, int64_t N,
                                                                    const uint4* __restrict__ G,
@@ -924,28 +956,34 @@ __global__ __launch_bounds__(kAlphaThreads) void alpha_grad_kernel(int T, int K,
   const int64_t t = (int64_t)blockIdx.x * (kAlphaThreads / kWave) + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   if (t >= T) return;
   const int words = BF16 ? D / 8 : D / 4;
-  for (int k = 0; k < K; ++k) {
-    const int64_t j = pmap[t * K + k];
-    if (j < 0 || j >= N) continue;
-    double s = 0.0;
-    const float a = alpha[j];
-    if (a != 0.0f && (!keep || keep[j])) {
-      for (int c = lane; c < words; c += kWave) {
-        const uint4 g = G[t * words + c], y = ld_stream(Y + j * words + c);
-        const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, yw[4] = {y.x, y.y, y.z, y.w};
+  for (int k0 = 0; k0 < K; k0 += kAlphaRows) {
+    // lane k has slot k0 + k: its pair row, whether that row is read, and its weight
+    int j = lane < kAlphaRows && k0 + lane < K ? pmap[t * K + k0 + lane] : -1;
+    if (j >= N) j = -1;
+    const bool read = j >= 0 && (!keep || keep[j] != 0);
+    const float a = j >= 0 ? alpha[j] : 0.0f;
+    int row[kAlphaRows];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (BF16) {
-            s += (double)(bf16_lo(gw[i]) * bf16_lo(yw[i]));  // exact in f32
-            s += (double)(bf16_hi(gw[i]) * bf16_hi(yw[i]));
-          } else {
-            s += (double)__uint_as_float(gw[i]) * (double)__uint_as_float(yw[i]);
-          }
-        }
-      }
-      s = wave_sum(s) / (double)a;
+    for (int k = 0; k < kAlphaRows; ++k) row[k] = __builtin_amdgcn_readlane(read ? j : -1, k);
+    double s[kAlphaRows] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int c = lane; c < words; c += kWave) {
+      uint4 y[kAlphaRows];
+      const uint4 g = G[t * words + c];
+#pragma unroll
+      for (int k = 0; k < kAlphaRows; ++k)
+        y[k] = row[k] >= 0 ? ld_stream(Y + (int64_t)row[k] * words + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int k = 0; k < kAlphaRows; ++k)
+        if (row[k] >= 0) s[k] = dot16<BF16>(g, y[k], s[k]);
     }
-    if (lane == 0) dalpha[j] = (float)s;
+    double mine = 0.0;
+#pragma unroll
+    for (int k = 0; k < kAlphaRows; ++k) {
+      if (row[k] < 0) continue;
+      const double v = lanes_sum(s[k]);
+      mine = lane == k ? v : mine;
+    }
+    if (j >= 0) dalpha[j] = read && a != 0.0f ? (float)(mine / (double)a) : 0.0f;
   }
 }
 
@@ -1032,7 +1070,7 @@ lrmoe_status launch_balance_loss(const lrmoe_router* r, const void* logits, cons
             r->T, r->E, r->K, n_seq, logits, mask, idx, seq_off_d, b);
       }) != LRMOE_OK)
     return LRMOE_ERR_HIP;
-  balance_join_kernel<<<dim3((unsigned)n_seq, (unsigned)ceil_div(r->E, kWave)), kJoinThreads, 0, s>>>(
+  balance_join_kernel<<<dim3((unsigned)n_seq, (unsigned)ceil_div(r->E, kJoinExperts)), kJoinThreads, 0, s>>>(
       r->T, r->E, r->K, n_seq, coef, seq_off_d, b, counts, psum, norm, loss);
   return launch_status();
 }
