@@ -577,18 +577,19 @@ def route_bwd(r: Router, logits, idx, dalpha=None, pmap=None, balance=None, glos
 def alpha_grad(p: Problem, G, Y, alpha, pmap, keep=None, out=None, stream=None):
     """Gradient of the N pairs' routing weights from expert_forward's rows Y and the output's
     gradient G (lrmoe_alpha_grad); ``pmap`` [T, K] from route, ``keep`` [N] uint8 from select."""
-    here = torch._C._cuda_getDevice()
+    here, f32, dt, N = torch._C._cuda_getDevice(), torch.float32, p.torch_dtype, p.N
     if out is None:
-        out = torch.empty(p.N, dtype=torch.float32, device=p.device)
-    for name, t in (("alpha", alpha), ("out", out)):
-        if t.dtype != torch.float32 or t.numel() < p.N or t.get_device() != here:
-            raise ValueError(f"{name}: expected f32 of at least N elements on the current device")
-    for name, t, rows in (("G", G, p.T), ("Y", Y, p.N)):
-        if t.dtype != p.torch_dtype or t.dim() != 2 or t.shape[0] < rows or t.shape[1] != p.D or t.get_device() != here:
-            raise ValueError(f"{name}: expected {p.torch_dtype} of {rows} rows of {p.D} on the current device")
+        out = torch.empty(N, dtype=f32, device=p.device)
+    if alpha.dtype != f32 or out.dtype != f32 or alpha.numel() < N or out.numel() < N:
+        raise ValueError("alpha and out: expected f32 of at least N elements")
+    if G.dtype != dt or Y.dtype != dt or G.dim() != 2 or Y.dim() != 2 or G.shape[1] != p.D or Y.shape[1] != p.D or (
+            G.shape[0] < p.T or Y.shape[0] < N):
+        raise ValueError(f"G and Y: expected {dt} of T and N rows of {p.D}")
+    if not alpha.get_device() == out.get_device() == G.get_device() == Y.get_device() == here:
+        raise ValueError("alpha, out, G and Y must be on the current device")
     _lib.check(library().lrmoe_alpha_grad(ctypes.byref(p.c), _ptr(G), _ptr(Y), _ptr(alpha),
                                           _want(pmap, "pmap", (p.T, p.K), torch.int32, here),
-                                          _flags(keep, "keep", p.N, here), _ptr(out), _stream(stream)),
+                                          _flags(keep, "keep", N, here), _ptr(out), _stream(stream)),
                "lrmoe_alpha_grad")
     return out
 

@@ -17,7 +17,7 @@ constexpr float kFltMax = 3.402823466e+38f;
 constexpr float kNegInf = -__builtin_huge_valf();
 
 __device__ __forceinline__ float clean(float x) {  // NaN -> -inf, +inf -> FLT_MAX
-  return x != x ? kNegInf : fminf(x, kFltMax);
+  return fminf(fmaxf(x, kNegInf), kFltMax);  // the maximum of a NaN and a number is the number
 }
 
 // exp(d) for d = x - max: d is at most 0, or NaN where both are -inf (a token that is not live). h + l is
@@ -140,15 +140,19 @@ __device__ __forceinline__ bool unmasked(const uint8_t* __restrict__ mask, int64
 
 // ---------------------------------------------------------------- routing
 
-constexpr int kRouteThreads = 1024;   // placing blocks, and the top-K blocks of more than 8 slots
-constexpr int kRoute8Threads = 512;   // the top-K blocks of up to 8 slots
-constexpr int kOneChunk = 128;        // up to so many tokens one block does the whole call
+constexpr int kRouteThreads = 1024;  // scanning and placing blocks
+constexpr int kOneChunk = 128;       // up to so many tokens one block does the whole call
 
-// Tokens of one top-K block and of one placing block. Each top-K block writes a row of counts, and a
-// placing block reads all rows and holds a bit per (token, local expert) in 48 KB of LDS: chunks
-// grow until there are at most 512, as far as those bits let them.
+// Tokens of one top-K block and of one placing block: 128, or 64 where eight or more lanes to a token make
+// two passes of that and the blocks are fewer than the 256 compute units (16384 x 512: top-K 19 us
+// in chunks of 128, 13 us in chunks of 64; 50021 x 257: 24 us either way, but 4 us more for the
+// scan and the placing). Each block writes a row of counts, and a placing block holds a bit per
+// (token, local expert) in 48 KB of LDS: chunks grow until there are at most 512 rows, as far as
+// those bits let them.
 int route_chunk(const lrmoe_router* r) {
-  int c = kOneChunk;
+  if (r->T <= kOneChunk) return kOneChunk;
+  if (r->E > 128 && r->T <= 256 * 128) return 64;
+  int c = 128;
   while (c < 1024 && ceil_div(r->T, c) > 512 && (int64_t)r->local * c * 2 / 8 <= 48 * 1024) c *= 2;
   return c;
 }
@@ -226,7 +230,7 @@ __device__ __forceinline__ void place_chunk(const RouteArgs& a, int c, int n, co
   }
 }
 
-// What the two top-K kernels have in common: the block's LDS, one slot's outputs, and the end.
+// A top-K block's LDS, one slot's outputs, and the end.
 template <int NT>
 struct RouteBlock {
   // [E] counts; with one block for all tokens also [E] zeros, [C K] experts, [C K] weights, [C / 32][local] bits
@@ -266,14 +270,15 @@ struct RouteBlock {
   }
 };
 
-// Up to 8 slots. A logit and its expert make one key: the logit's bits, mapped so that they order as
-// unsigned numbers, above 1023 - e, so one maximum compares both and ties go to the lower index.
-// f32 logits take 63 bits as a positive double (f64 maxima run at full rate), bf16 logits 32. Lanes
-// sort their keys in eights (19 exchanges of a maximum and a minimum), and lists of eight are
-// merged, in a lane and then over the token's lanes: the larger of one list against the other
-// reversed are the eight largest of both, sorted by 12 more exchanges. With four lanes to a token
-// (up to 128 experts) that is a fifth of the instructions of taking the largest K times over:
-// 32768 x 128 f32 takes 8.2 us here and 13.4 us that way.
+// A logit and its expert make one key: the logit's bits, mapped so that they order as unsigned numbers,
+// above 1023 - e, so one maximum compares both and ties go to the lower index. f32 logits take 63
+// bits as a positive double (f64 maxima run at full rate), bf16 logits 32. Lanes sort their keys in
+// lists of N = 8, 16 or 32, as many as there are slots or more (odd-even merge sort: 19, 63 or 191
+// exchanges of a maximum and a minimum), and the lists are merged, in a lane and then over the
+// token's lanes: the larger of one list against the other reversed are the N largest of both,
+// sorted by N / 2 log2 N more exchanges. With four lanes to a token (up to 128 experts) and 8 slots
+// that is a fifth of the instructions of taking the largest K times over: 32768 x 128 f32 takes
+// 8.2 us here and 13.4 us that way.
 __device__ __forceinline__ double key_max(double a, double b) { return __builtin_fmax(a, b); }
 __device__ __forceinline__ double key_min(double a, double b) { return __builtin_fmin(a, b); }
 __device__ __forceinline__ uint32_t key_max(uint32_t a, uint32_t b) { return a > b ? a : b; }
@@ -284,23 +289,41 @@ __device__ __forceinline__ void exchange(Key& a, Key& b) {
   a = hi;
   b = lo;
 }
-template <class Key>
-__device__ __forceinline__ void sort8(Key* a) {
-  exchange(a[0], a[1]), exchange(a[2], a[3]), exchange(a[4], a[5]), exchange(a[6], a[7]);
-  exchange(a[0], a[2]), exchange(a[1], a[3]), exchange(a[4], a[6]), exchange(a[5], a[7]);
-  exchange(a[1], a[2]), exchange(a[5], a[6]);
-  exchange(a[0], a[4]), exchange(a[1], a[5]), exchange(a[2], a[6]), exchange(a[3], a[7]);
-  exchange(a[2], a[4]), exchange(a[3], a[5]);
-  exchange(a[1], a[2]), exchange(a[3], a[4]), exchange(a[5], a[6]);
-}
-// a = the eight largest of a and b, both sorted
-template <class Key>
-__device__ __forceinline__ void merge8(Key* a, const Key* b) {
+// Two sorted lists, interleaved at distance R from LO on, become one.
+template <int LO, int N, int R, class Key>
+__device__ __forceinline__ void merge_odd_even(Key* a) {
+  if constexpr (2 * R < N) {
+    merge_odd_even<LO, N, 2 * R>(a);
+    merge_odd_even<LO + R, N, 2 * R>(a);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a[i] = key_max(a[i], b[7 - i]);
-  exchange(a[0], a[4]), exchange(a[1], a[5]), exchange(a[2], a[6]), exchange(a[3], a[7]);
-  exchange(a[0], a[2]), exchange(a[1], a[3]), exchange(a[4], a[6]), exchange(a[5], a[7]);
-  exchange(a[0], a[1]), exchange(a[2], a[3]), exchange(a[4], a[5]), exchange(a[6], a[7]);
+    for (int i = LO + R; i + R < LO + N; i += 2 * R) exchange(a[i], a[i + R]);
+  } else {
+    exchange(a[LO], a[LO + R]);
+  }
+}
+template <int LO, int N, class Key>
+__device__ __forceinline__ void sort_list(Key* a) {
+  if constexpr (N > 1) {
+    sort_list<LO, N / 2>(a);
+    sort_list<LO + N / 2, N / 2>(a);
+    merge_odd_even<LO, N, 1>(a);
+  }
+}
+template <int N, int D, class Key>
+__device__ __forceinline__ void sort_bitonic(Key* a) {
+  if constexpr (D > 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (!(i & D)) exchange(a[i], a[i + D]);
+    sort_bitonic<N, D / 2>(a);
+  }
+}
+// a = the N largest of a and b, both sorted
+template <int N, class Key>
+__device__ __forceinline__ void merge_lists(Key* a, const Key* b) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) a[i] = key_max(a[i], b[N - 1 - i]);
+  sort_bitonic<N, N / 2>(a);
 }
 template <int S>
 __device__ __forceinline__ double key_swap(double v) {
@@ -310,14 +333,14 @@ template <int S>
 __device__ __forceinline__ uint32_t key_swap(uint32_t v) {
   return (uint32_t)lane_swap<S>((int)v);
 }
-template <int L, int S = 1, class Key>
+template <int N, int L, int S = 1, class Key>
 __device__ __forceinline__ void merge_lanes(Key* a) {
   if constexpr (S < L) {
-    Key b[8];
+    Key b[N];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = key_swap<S>(a[i]);
-    merge8(a, b);
-    merge_lanes<L, 2 * S>(a);
+    for (int i = 0; i < N; ++i) b[i] = key_swap<S>(a[i]);
+    merge_lists<N>(a, b);
+    merge_lanes<N, L, 2 * S>(a);
   }
 }
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -343,12 +366,20 @@ __device__ __forceinline__ void of_key(uint32_t k, float* x, int* e) {
   *e = u > 0x007FFFFFu ? 1023 - (int)(k & 1023u) : -1;
 }
 
-template <class Lay>
-__global__ __launch_bounds__(kRoute8Threads) void route_topk8_kernel(RouteArgs a) {
-  constexpr int L = Lay::L, V = Lay::V, kGroups = kRoute8Threads / L;
-  constexpr int S = (8 + L - 1) / L;  // slots of a lane: k = lane, lane + L
+// Threads of a top-K block: 128 tokens in one pass up to eight lanes to a token, if 1024 threads have the
+// registers (lists of 32 do not).
+constexpr int topk_threads(int L, int N) { return L >= 8 && N <= 16 ? 1024 : 512; }
+
+// One block per chunk of tokens: the K largest logits of each, their weights, and how often the chunk
+// chose each expert. With few tokens (rows = 1) the block places the pairs itself.
+template <class Lay, int N>
+__global__ __launch_bounds__(topk_threads(Lay::L, N)) void route_topk_kernel(RouteArgs a) {
+  constexpr int kTopkThreads = topk_threads(Lay::L, N);
+  constexpr int L = Lay::L, V = Lay::V, kGroups = kTopkThreads / L;
+  constexpr int S = (N + L - 1) / L;  // slots of a lane: k = lane, lane + L, ...
+  static_assert(V % N == 0, "whole lists");
   extern __shared__ uint32_t lds[];
-  RouteBlock<kRoute8Threads> blk(a, lds);
+  RouteBlock<kTopkThreads> blk(a, lds);
   const int lane = threadIdx.x & (L - 1), group = threadIdx.x / L;
   const int64_t t0 = (int64_t)blockIdx.x * a.C, t1 = min(t0 + a.C, (int64_t)a.T);
   __syncthreads();
@@ -367,21 +398,21 @@ __global__ __launch_bounds__(kRoute8Threads) void route_topk8_kernel(RouteArgs a
       Z = group_sum<L>(Z);
     }
     using Key = std::conditional_t<Lay::BF16, uint32_t, double>;
-    Key best[8];
+    Key best[N];
 #pragma unroll
-    for (int q = 0; q < V; q += 8) {
-      Key d[8];
+    for (int q = 0; q < V; q += N) {
+      Key d[N];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) to_key(x[q + i], Lay::expert(lane, q + i), &d[i]);
-      sort8(d);
+      for (int i = 0; i < N; ++i) to_key(x[q + i], Lay::expert(lane, q + i), &d[i]);
+      sort_list<0, N>(d);
       if (q == 0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) best[i] = d[i];
+        for (int i = 0; i < N; ++i) best[i] = d[i];
       } else {
-        merge8(best, d);
+        merge_lists<N>(best, d);
       }
     }
-    merge_lanes<L>(best);
+    merge_lanes<N, L>(best);
     int e[S], top_e;
     float p[S], sum = 0.0f;
     of_key(best[0], &top, &top_e);
@@ -390,7 +421,7 @@ __global__ __launch_bounds__(kRoute8Threads) void route_topk8_kernel(RouteArgs a
       const int k = lane + q * L;
       Key d = 0;
 #pragma unroll
-      for (int i = q * L; i < 8 && i < (q + 1) * L; ++i) d = i == k ? best[i] : d;
+      for (int i = q * L; i < N && i < (q + 1) * L; ++i) d = i == k ? best[i] : d;
       float xk;
       of_key(d, &xk, &e[q]);
       if (k >= a.K) e[q] = -1;
@@ -402,82 +433,6 @@ __global__ __launch_bounds__(kRoute8Threads) void route_topk8_kernel(RouteArgs a
     for (int q = 0; q < S; ++q) {
       const int k = lane + q * L;
       if (in && k < a.K) blk.put(a, t, k, e[q], e[q] >= 0 ? a.scale * (p[q] / Z) : 0.0f);
-    }
-  }
-  blk.finish(a);
-}
-
-// More than 8 slots: the largest value left, K times.
-template <class Lay>
-__global__ __launch_bounds__(kRouteThreads) void route_topk_kernel(RouteArgs a) {
-  constexpr int L = Lay::L, V = Lay::V, kGroups = kRouteThreads / L;
-  constexpr int S = (32 + L - 1) / L;  // slots that a lane keeps: k = lane, lane + L
-  extern __shared__ uint32_t lds[];
-  RouteBlock<kRouteThreads> blk(a, lds);
-  const int lane = threadIdx.x & (L - 1), group = threadIdx.x / L;
-  const int64_t t0 = (int64_t)blockIdx.x * a.C, t1 = min(t0 + a.C, (int64_t)a.T);
-  float next[V];
-  Lay::load(a.logits, t0 + group, a.E, t0 + group < t1 && unmasked(a.mask, t0 + group), lane, next);
-  __syncthreads();
-  for (int64_t tb = t0; tb < t1; tb += kGroups) {
-    const int64_t t = tb + group;
-    const bool in = t < t1;
-    float x[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) x[v] = next[v];
-    if (tb + kGroups < t1)  // the next pass's row, while this one is ranked
-      Lay::load(a.logits, t + kGroups, a.E, t + kGroups < t1 && unmasked(a.mask, t + kGroups), lane, next);
-    float top = kNegInf, Z = 0.0f;
-    if (!a.renorm) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) top = fmaxf(top, x[v]);
-      top = group_max<L>(top);
-#pragma unroll
-      for (int v = 0; v < V; ++v) Z += exp_term(x[v] - top);
-      Z = group_sum<L>(Z);
-    }
-    // slot k: the largest value left, and the lowest index that has it
-    int my_e[S];
-    float my_x[S];
-#pragma unroll
-    for (int q = 0; q < S; ++q) my_e[q] = -1, my_x[q] = kNegInf;
-    for (int k = 0; k < a.K; ++k) {
-      float best = kNegInf;
-#pragma unroll
-      for (int v = 0; v < V; ++v) best = fmaxf(best, x[v]);
-      best = group_max<L>(best);
-      if (k == 0) top = best;
-      int at = 1 << 30;
-      bool hit[V], found = false;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {  // the lane's first value that is the best
-        const bool eq = x[v] == best;
-        hit[v] = eq && !found;
-        found = found || eq;
-        at = hit[v] ? Lay::expert(lane, v) : at;
-      }
-      const int win = group_min<L>(at);
-      const bool mine = at == win;
-#pragma unroll
-      for (int v = 0; v < V; ++v) x[v] = hit[v] && mine ? kNegInf : x[v];
-#pragma unroll
-      for (int q = 0; q < S; ++q)
-        if (lane + q * L == k) {
-          my_e[q] = best > kNegInf ? win : -1;
-          my_x[q] = best;
-        }
-    }
-    float p[S], sum = 0.0f;
-#pragma unroll
-    for (int q = 0; q < S; ++q) {
-      p[q] = my_e[q] >= 0 ? exp_below(my_x[q] - top) : 0.0f;
-      sum += p[q];
-    }
-    if (a.renorm) Z = group_sum<L>(sum);
-#pragma unroll
-    for (int q = 0; q < S; ++q) {
-      const int k = lane + q * L;
-      if (in && k < a.K) blk.put(a, t, k, my_e[q], my_e[q] >= 0 ? a.scale * (p[q] / Z) : 0.0f);
     }
   }
   blk.finish(a);
@@ -1001,17 +956,34 @@ void by_experts(int E, F&& f) {
   else if (E <= 512) f(Layout<16, 32, BF16>());
   else f(Layout<64, 16, BF16>());
 }
-// The same for lists of eight: values by the eight, and as few lanes as hold them in 40 values each.
+// The same for lists of N = 8, 16 or 32 slots: whole lists to a lane, and few lanes to a token.
 template <bool BF16, class F>
-void by_experts8(int E, F&& f) {
-  if (E <= 32) f(Layout<4, 8, BF16>());
-  else if (E <= 64) f(Layout<4, 16, BF16>());
-  else if (E <= 128) f(Layout<4, 32, BF16>());
-  else if (E <= 192) f(Layout<8, 24, BF16>());
-  else if (E <= 256) f(Layout<8, 32, BF16>());
-  else if (E <= 320) f(Layout<8, 40, BF16>());
-  else if (E <= 512) f(Layout<16, 32, BF16>());
-  else f(Layout<32, 32, BF16>());
+void by_lists(int E, int K, F&& f) {
+  using std::integral_constant;
+  if (K <= 8) {
+    integral_constant<int, 8> n;
+    if (E <= 32) f(Layout<4, 8, BF16>(), n);
+    else if (E <= 64) f(Layout<4, 16, BF16>(), n);
+    else if (E <= 128) f(Layout<4, 32, BF16>(), n);
+    else if (E <= 192) f(Layout<8, 24, BF16>(), n);
+    else if (E <= 256) f(Layout<8, 32, BF16>(), n);
+    else if (E <= 320) f(Layout<8, 40, BF16>(), n);
+    else if (E <= 512) f(Layout<16, 32, BF16>(), n);
+    else f(Layout<32, 32, BF16>(), n);
+  } else if (K <= 16) {
+    integral_constant<int, 16> n;
+    if (E <= 64) f(Layout<4, 16, BF16>(), n);
+    else if (E <= 128) f(Layout<4, 32, BF16>(), n);
+    else if (E <= 256) f(Layout<8, 32, BF16>(), n);
+    else if (E <= 512) f(Layout<16, 32, BF16>(), n);
+    else f(Layout<32, 32, BF16>(), n);
+  } else {
+    integral_constant<int, 32> n;
+    if (E <= 128) f(Layout<4, 32, BF16>(), n);
+    else if (E <= 256) f(Layout<8, 32, BF16>(), n);
+    else if (E <= 512) f(Layout<16, 32, BF16>(), n);
+    else f(Layout<32, 32, BF16>(), n);
+  }
 }
 template <class F>
 lrmoe_status by_layout(const lrmoe_router* r, F&& f) {
@@ -1019,8 +991,8 @@ lrmoe_status by_layout(const lrmoe_router* r, F&& f) {
   return launch_status();
 }
 template <class F>
-lrmoe_status by_layout8(const lrmoe_router* r, F&& f) {
-  r->dtype == LRMOE_BF16 ? by_experts8<true>(r->E, f) : by_experts8<false>(r->E, f);
+lrmoe_status by_slots(const lrmoe_router* r, F&& f) {
+  r->dtype == LRMOE_BF16 ? by_lists<true>(r->E, r->K, f) : by_lists<false>(r->E, r->K, f);
   return launch_status();
 }
 
@@ -1044,10 +1016,11 @@ lrmoe_status launch_route(const lrmoe_router* r, const void* logits, const uint8
   const size_t bits = (size_t)C / 8 * r->local, cnt = (size_t)r->E * 4;
   if (rows > 0) {
     const size_t lds = rows == 1 ? 2 * cnt + (size_t)C * r->K * 8 + bits : cnt;
-    const lrmoe_status st =
-        r->K <= 8
-            ? by_layout8(r, [&](auto lay) { route_topk8_kernel<decltype(lay)><<<rows, kRoute8Threads, lds, s>>>(a); })
-            : by_layout(r, [&](auto lay) { route_topk_kernel<decltype(lay)><<<rows, kRouteThreads, lds, s>>>(a); });
+    const lrmoe_status st = by_slots(r, [&](auto lay, auto n) {
+      using Lay = decltype(lay);
+      constexpr int N = decltype(n)::value;
+      route_topk_kernel<Lay, N><<<rows, topk_threads(Lay::L, N), lds, s>>>(a);
+    });
     if (st != LRMOE_OK || rows == 1) return st;
   }
   if (prefix) {

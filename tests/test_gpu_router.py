@@ -23,6 +23,13 @@ CASES = {
     "odd_f32": (515, 257, 6, 200, 57, "f32", False, 0.1, "normal"),
     "two_groups": (130, 66, 32, 0, 66, "f32", False, 0.0, "normal"),
     "wide": (129, 600, 16, 3, 590, "bf16", False, 0.0, "normal"),
+    "ten_bf16": (200, 128, 10, 0, 128, "bf16", True, 0.1, "ties"),
+    "sixteen": (311, 200, 16, 40, 100, "f32", False, 0.0, "bad"),
+    "sixteen_small": (140, 33, 16, 0, 33, "bf16", True, 0.0, "normal"),
+    "thirty_two": (150, 300, 32, 0, 300, "bf16", True, 0.0, "few"),
+    "eight_of_300": (150, 300, 8, 0, 300, "f32", True, 0.0, "bad"),
+    "eight_of_400": (150, 400, 8, 0, 400, "bf16", False, 0.0, "normal"),
+    "eight_of_180": (150, 180, 8, 0, 180, "f32", False, 0.0, "ties"),
     "widest": (77, 1024, 32, 0, 1024, "f32", True, 0.1, "normal"),
     "ties": (400, 48, 6, 0, 48, "bf16", True, 0.0, "ties"),
     "constant": (70, 16, 4, 2, 9, "f32", False, 0.0, "constant"),
