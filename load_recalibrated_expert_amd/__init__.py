@@ -441,7 +441,7 @@ class Router:
         self._route_out = (("idx", (T, K), i32), ("w", (T, K), f32), ("counts", (E,), i32),
                            ("seg_off", (self.local + 1,), torch.int64), ("tok", (T * K,), i32),
                            ("slot", (T * K,), i32), ("alpha", (T * K,), f32), ("pmap", (T, K), i32))
-        self._ws, self._ws_size = None, {}
+        self._ws, self._ws_size, self._grown = None, {}, []
         self.workspace_size()  # checks the router
 
     def workspace_size(self, n_seq=1) -> int:
@@ -455,11 +455,23 @@ class Router:
 
     def workspace(self, n_seq=1) -> torch.Tensor:
         """The router's scratch buffer. Calls that overlap on several streams, or graphs that
-        may replay at the same time, need a Router each."""
+        may replay at the same time, need a Router each. A buffer that has become too small is
+        kept: a captured graph may still use it."""
         n = self.workspace_size(n_seq)
         if self._ws is None or self._ws.numel() < n:
+            if self._ws is not None:
+                self._grown.append(self._ws)
             self._ws = torch.empty(n, dtype=torch.uint8, device=self.device)
         return self._ws
+
+
+def _empty(shape, dtype, device, stream):
+    """An output of a call on `stream` (None: the current one), allocated there: memory that other
+    work of the current stream gave back is not written before that work is done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _want(t, name, shape, dtype, here):
@@ -482,14 +494,14 @@ def _flags(t, name, n, here):
     return _ptr(t)
 
 
-def _outputs(given, wanted, device, here):
+def _outputs(given, wanted, device, here, stream):
     """(dict of outputs, their pointers): the given ones checked, the others allocated."""
     o = dict(given) if given else {}
     ptrs = []
     for name, shape, dt in wanted:
         t = o.get(name)
         if t is None:
-            t = o[name] = torch.empty(shape, dtype=dt, device=device)
+            t = o[name] = _empty(shape, dt, device, stream)
             ptrs.append(t.data_ptr())
         else:
             ptrs.append(_want(t, name, shape, dt, here))
@@ -502,7 +514,7 @@ def route(r: Router, logits, mask=None, out=None, stream=None):
     at and after seg_off[local] are not written) and pmap [T, K]. ``mask`` [T] uint8 or bool: 0
     leaves a token out. ``out`` reuses buffers."""
     here = torch._C._cuda_getDevice()
-    o, ptrs = _outputs(out, r._route_out, r.device, here)
+    o, ptrs = _outputs(out, r._route_out, r.device, here, stream)
     ws = r.workspace()
     _lib.check(library().lrmoe_route(r.ref, _want(logits, "logits", (r.T, r.E), r.torch_dtype, here),
                                      _flags(mask, "mask", r.T, here), *ptrs, ws.data_ptr(), ws.numel(),
@@ -510,7 +522,7 @@ def route(r: Router, logits, mask=None, out=None, stream=None):
     return o
 
 
-def _sequences(r, seq_off, here):
+def _sequences(r, seq_off, here, stream):
     """(device offsets or None, number of sequences). Offsets on the host are checked and copied."""
     if seq_off is None:
         return None, 1
@@ -523,6 +535,8 @@ def _sequences(r, seq_off, here):
         if a[0] < 0 or a[-1] > r.T or any(x > y for x, y in zip(a, a[1:])):
             raise ValueError("seq_off must not decrease and stay inside [0, T]")
         seq_off = seq_off.to(r.device)
+        if stream is not None:
+            seq_off.record_stream(stream)
     elif seq_off.get_device() != here:
         raise ValueError("seq_off must be on the current device")
     return seq_off, seq_off.numel() - 1
@@ -533,9 +547,9 @@ def balance_loss(r: Router, logits, idx, coef=1.0, mask=None, seq_off=None, out=
     [1], counts, psum [n_seq, E] and norm [n_seq]. ``seq_off`` (int64 [n_seq + 1], host or device;
     None: one sequence of all tokens). ``route_bwd`` takes the result as ``balance``."""
     here = torch._C._cuda_getDevice()
-    off, S = _sequences(r, seq_off, here)
+    off, S = _sequences(r, seq_off, here, stream)
     o, ptrs = _outputs(out, (("counts", (S, r.E), torch.int32), ("psum", (S, r.E), torch.float32),
-                             ("norm", (S,), torch.float32), ("loss", (1,), torch.float32)), r.device, here)
+                             ("norm", (S,), torch.float32), ("loss", (1,), torch.float32)), r.device, here, stream)
     ws = r.workspace(S)
     _lib.check(library().lrmoe_balance_loss(r.ref, _want(logits, "logits", (r.T, r.E), r.torch_dtype, here),
                                             _flags(mask, "mask", r.T, here),
@@ -553,9 +567,11 @@ def route_bwd(r: Router, logits, idx, dalpha=None, pmap=None, balance=None, glos
     f32 [1] or None = 1): the gradient of its loss. Either part may be None."""
     here = torch._C._cuda_getDevice()
     shape = (r.T, r.E)
-    off, S = _sequences(r, seq_off, here) if balance is not None else (None, 1)
+    off, S = _sequences(r, seq_off, here, stream) if balance is not None else (None, 1)
     if out is None:
-        out = torch.empty(shape, dtype=r.torch_dtype, device=r.device)
+        out = _empty(shape, r.torch_dtype, r.device, stream)
+    elif out.data_ptr() == logits.data_ptr() and out.numel():
+        raise ValueError("out must not be the logits")
     n_pairs, d = 0, None
     if dalpha is not None:
         n_pairs = dalpha.numel()
@@ -579,7 +595,7 @@ def alpha_grad(p: Problem, G, Y, alpha, pmap, keep=None, out=None, stream=None):
     gradient G (lrmoe_alpha_grad); ``pmap`` [T, K] from route, ``keep`` [N] uint8 from select."""
     here, f32, dt, N = torch._C._cuda_getDevice(), torch.float32, p.torch_dtype, p.N
     if out is None:
-        out = torch.empty(N, dtype=f32, device=p.device)
+        out = _empty(N, f32, p.device, stream)
     if alpha.dtype != f32 or out.dtype != f32 or alpha.numel() < N or out.numel() < N:
         raise ValueError("alpha and out: expected f32 of at least N elements")
     if G.dtype != dt or Y.dtype != dt or G.dim() != 2 or Y.dim() != 2 or G.shape[1] != p.D or Y.shape[1] != p.D or (
@@ -662,6 +678,7 @@ class AdamW:
             if bits == 8:
                 e.m_scale, e.v_scale = _ptr(self.m_scale[i]), _ptr(self.v_scale[i])
         self._scalars = self._plan = None
+        self._captured = []
         self.grads = None
         if grads is not None:
             self.bind(grads)
@@ -711,12 +728,14 @@ class AdamW:
         if self.grads is None:
             raise ValueError("AdamW has no gradient buffers: pass grads")
         self._check_place()
+        if torch.cuda.is_current_stream_capturing():
+            raise ValueError("a graph would repeat this very step: capture step_captured")
         self.t += 1
         self._config(grad_scale)
         try:
             _lib.check(library().lrmoe_adamw(self._table, len(self.w), ctypes.byref(self.c), self._plan_ptr(), None,
                                              _stream(stream)), "lrmoe_adamw")
-        except LrmoeError:
+        except Exception:
             self.t -= 1
             raise
 
@@ -734,9 +753,13 @@ class AdamW:
         self._scalars.copy_(values)
 
     def step_captured(self, stream=None):
-        """The update with the scalars of the last ``advance``, for capture into a graph."""
+        """The update with the scalars of the last ``advance``, for capture into a graph. What a graph
+        reads stays alive with this object: the plan and the gradient buffers bound now."""
         if self._scalars is None or self.grads is None:
             raise ValueError("call advance (and bind the gradient buffers) before step_captured")
         self._check_place()
-        _lib.check(library().lrmoe_adamw(self._table, len(self.w), ctypes.byref(self.c), self._plan_ptr(),
+        plan = self._plan_ptr()
+        if torch.cuda.is_current_stream_capturing():
+            self._captured.append((self._plan, self.grads))
+        _lib.check(library().lrmoe_adamw(self._table, len(self.w), ctypes.byref(self.c), plan,
                                          _ptr(self._scalars), _stream(stream)), "lrmoe_adamw")

@@ -416,7 +416,7 @@ lrmoe_status lrmoe_route(const lrmoe_router* r, const void* logits, const uint8_
   LRMOE_TRY(check_router(r));
   if (!counts || !seg_off) return LRMOE_ERR_INVALID_ARG;
   if (r->T > 0 && (!logits || !idx || !w || !tok || !slot || !alpha || !pmap)) return LRMOE_ERR_INVALID_ARG;
-  if (!aligned(logits, 16)) return LRMOE_ERR_INVALID_ARG;
+  if (!aligned(logits, 16) || !aligned(ws, 16)) return LRMOE_ERR_INVALID_ARG;
   if (!ws || ws_bytes < route_ws_bytes(r)) return LRMOE_ERR_WORKSPACE;
   return launch_route(r, logits, mask, idx, w, counts, seg_off, tok, slot, alpha, pmap, ws, (hipStream_t)stream);
 }
@@ -428,7 +428,7 @@ lrmoe_status lrmoe_balance_loss(const lrmoe_router* r, const void* logits, const
   LRMOE_TRY(check_sequences(r, seq_off_d, n_seq));
   if (!std::isfinite(coef)) return LRMOE_ERR_INVALID_ARG;
   if (!counts || !psum || !norm || !loss || (r->T > 0 && (!logits || !idx))) return LRMOE_ERR_INVALID_ARG;
-  if (!aligned(logits, 16)) return LRMOE_ERR_INVALID_ARG;
+  if (!aligned(logits, 16) || !aligned(ws, 16)) return LRMOE_ERR_INVALID_ARG;
   if (!ws || ws_bytes < balance_ws_bytes(r, n_seq)) return LRMOE_ERR_WORKSPACE;
   return launch_balance_loss(r, logits, mask, idx, seq_off_d, n_seq, coef, counts, psum, norm, loss, ws,
                              (hipStream_t)stream);

@@ -158,7 +158,7 @@ int route_chunk(const lrmoe_router* r) {
 }
 
 struct RouteArgs {
-  int T, E, K, C, rows, first, local, renorm;
+  int T, E, K, C, rows, first, local, renorm, sorted;
   float scale;
   const void* logits;
   const uint8_t* mask;
@@ -468,7 +468,7 @@ __global__ __launch_bounds__(topk_threads(Lay::L, N)) void route_topk_kernel(Rou
 
 // Rows of counts up to which every placing block sums them itself; above, a launch scans them first.
 constexpr int kOwnRows = 32;
-constexpr int kSortedPairs = 4096;  // slots of a chunk whose pairs are sorted in LDS: 32 KB
+constexpr size_t kPlaceLds = 48 * 1024;  // of a placing block, beside its 8 KB of sums
 constexpr int kScanExperts = 32;
 
 // Block: 32 experts, the rows in 64 runs. prefix[r][e] = tokens in the rows before r; total[e].
@@ -520,8 +520,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs a)
   __shared__ int total[1024], before[1024];
   extern __shared__ uint32_t lds[];  // [C / 32][local] bits (C is at least 64: an even number of words); [2 C K] pairs
   uint32_t* bits = lds;
-  // without tokens there is no row of counts to sort by
-  uint32_t* sorted = a.rows > 0 && a.C * a.K <= kSortedPairs ? lds + a.C / 32 * a.local : nullptr;
+  uint32_t* sorted = a.sorted ? lds + a.C / 32 * a.local : nullptr;
   const int tid = threadIdx.x, c = blockIdx.x, E8 = (a.E + 7) & ~7;
   const int64_t i0 = (int64_t)c * a.C * a.K;
   const int n = (int)(min((int64_t)(c + 1) * a.C, (int64_t)a.T) * a.K - i0);
@@ -1042,10 +1041,12 @@ lrmoe_status launch_route(const lrmoe_router* r, const void* logits, const uint8
   const int C = route_chunk(r), rows = (int)ceil_div(r->T, C);
   const size_t E8 = align_up(r->E, 8);
   int* prefix = rows > kOwnRows ? (int*)((char*)ws + align_up((size_t)rows * E8 * 2, 256)) : nullptr;
-  const RouteArgs a{r->T, r->E, r->K, C, rows, r->first, r->local, r->renorm, r->scale, logits, mask,
+  const size_t bits = (size_t)C / 8 * r->local, cnt = (size_t)r->E * 4, pairs = (size_t)C * r->K * 8;
+  // a chunk's pairs are sorted where they fit beside its bits; without tokens there are no counts to sort by
+  const int sorted = rows > 0 && bits + pairs <= kPlaceLds;
+  const RouteArgs a{r->T, r->E, r->K, C, rows, r->first, r->local, r->renorm, sorted, r->scale, logits, mask,
                     prefix, prefix ? prefix + (size_t)rows * E8 : nullptr, (uint16_t*)ws,
                     idx, counts, tok, slot, pmap, w, alpha, seg_off};
-  const size_t bits = (size_t)C / 8 * r->local, cnt = (size_t)r->E * 4;
   if (rows > 0) {
     const size_t lds = rows == 1 ? 2 * cnt + (size_t)C * r->K * 8 + bits : cnt;
     const lrmoe_status st = by_slots(r, [&](auto lay, auto n) {
@@ -1059,8 +1060,7 @@ lrmoe_status launch_route(const lrmoe_router* r, const void* logits, const uint8
     route_scan_kernel<<<(unsigned)ceil_div(r->E, kScanExperts), kRouteThreads, 0, s>>>(a);
     if (launch_status() != LRMOE_OK) return LRMOE_ERR_HIP;
   }
-  const size_t pairs = C * r->K <= kSortedPairs ? (size_t)C * r->K * 8 : 0;
-  route_place_kernel<<<(unsigned)std::max(1, rows), kRouteThreads, bits + pairs, s>>>(a);
+  route_place_kernel<<<(unsigned)std::max(1, rows), kRouteThreads, bits + (sorted ? pairs : 0), s>>>(a);
   return launch_status();
 }
 

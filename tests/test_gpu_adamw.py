@@ -244,3 +244,56 @@ def test_replayed_graph(bits):
         for a, b in zip(opt.w + opt.m + opt.v, twin.w + twin.m + twin.v):
             assert torch.equal(a.view(torch.uint8) if a.dtype != torch.float32 else a,
                                b.view(torch.uint8) if b.dtype != torch.float32 else b), rep
+
+
+def test_rebinding_keeps_a_captured_graph():
+    """A graph of more tensors than one launch's arguments take reads its plan: binding other gradient
+    buffers afterwards leaves the graph, which still uses those it was captured with."""
+    rng = np.random.default_rng(8)
+    sizes = [300] * 60
+    w = _tensors(sizes, torch.float32, rng, 0.05)
+    g = _tensors(sizes, torch.float32, rng, 0.01)
+    opt = lr.AdamW(w, grads=g, **HYPER)
+    twin = lr.AdamW([t.clone() for t in w], grads=g, **HYPER)
+    for o in (opt, twin):
+        o.step()
+        o.step()  # the second step makes the plan
+    opt.advance()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(ValueError):
+            opt.step()
+        opt.step_captured()
+    opt.bind(_tensors(sizes, torch.float32, rng, 0.5))
+    trash = [torch.full((100000,), 77, dtype=torch.uint8, device=DEV) for _ in range(50)]  # what bind freed
+    log(f"replay after binding others, {len(trash)} buffers written")
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    twin.step()
+    for a, b in zip(opt.w + opt.m + opt.v, twin.w + twin.m + twin.v):
+        assert torch.equal(a, b)
+
+
+def test_other_stream():
+    """Steps on a side stream, the gradients written there: equal to steps on the current one."""
+    rng = np.random.default_rng(12)
+    w = _tensors([5000, 70001], torch.float32, rng, 0.05)
+    g = _tensors([5000, 70001], torch.float32, rng, 0.01)
+    twin = lr.AdamW([t.clone() for t in w], grads=[t.clone() for t in g], bits=8, **HYPER)
+    opt = lr.AdamW(w, grads=g, bits=8, **HYPER)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    log("side stream")
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            for t in g:
+                t.mul_(0.5)
+        opt.step(stream=side)
+        for t in twin.grads:
+            t.mul_(0.5)
+        twin.step()
+    torch.cuda.synchronize()
+    for a, b in zip(opt.w, twin.w):
+        assert torch.equal(a, b)

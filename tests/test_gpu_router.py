@@ -282,6 +282,7 @@ def test_python_checks():
                  lambda: lr.route_bwd(r, x, idx, dalpha=b["psum"]), lambda: lr.route_bwd(r, x, idx, dalpha=x.double()),
                  lambda: lr.route_bwd(r, x, idx, balance=b, seq_off=[0, 4, 9]),
                  lambda: lr.route_bwd(r, x, idx, balance=b, gloss=torch.ones((), device=DEV)),
+                 lambda: lr.route_bwd(r, x, idx, balance=b, out=x),
                  lambda: lr.route_bwd(r, x, idx, balance=b, out=x.bfloat16())):
         with pytest.raises(ValueError):
             call()
@@ -321,3 +322,66 @@ def test_replayed_graph_and_other_stream():
         for k in want:
             a, b = (t[k][:n] if k in ("tok", "slot", "alpha") else t[k] for t in (got, want))
             assert torch.equal(a, b), (rep, k)
+
+
+def test_side_stream_argument():
+    """Calls on a stream that is not the current one, outputs allocated by them: the logits are written there
+    just before, so a call on the current stream would not see them."""
+    r, x, mask, rng = _inputs("share")
+    want = lr.route(r, x)
+    wb = lr.balance_loss(r, x, want["idx"], seq_off=[0, 100, r.T])
+    wg = lr.route_bwd(r, x, want["idx"], balance=wb, seq_off=[0, 100, r.T])
+    side = torch.cuda.Stream()
+    late = torch.zeros_like(x)
+    torch.cuda.synchronize()
+    big = torch.zeros(1 << 28, device=DEV)
+    log("side stream")
+    with torch.cuda.stream(side):
+        for _ in range(4):
+            big.add_(1.0)
+        late.copy_(x)
+    o = lr.route(r, late, stream=side)
+    b = lr.balance_loss(r, late, o["idx"], seq_off=[0, 100, r.T], stream=side)
+    g = lr.route_bwd(r, late, o["idx"], balance=b, seq_off=[0, 100, r.T], stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    for k in ("idx", "w", "counts", "seg_off", "tok", "alpha", "pmap"):
+        assert torch.equal(o[k], want[k]), k
+    assert torch.equal(b["loss"], wb["loss"]) and torch.equal(b["psum"], wb["psum"]) and torch.equal(g, wg)
+
+
+def test_a_grown_workspace_leaves_a_captured_graph():
+    """A graph captured with one sequence keeps its workspace when a later call with many needs a larger one."""
+    r, x, mask, rng = _inputs("share")
+    idx = lr.route(r, x)["idx"]
+    want = lr.balance_loss(r, x, idx)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = lr.balance_loss(r, x, idx)
+    log("workspace grows")
+    lr.balance_loss(r, x, idx, seq_off=list(range(r.T + 1)))
+    trash = [torch.full((r.workspace_size(1),), 99, dtype=torch.uint8, device=DEV) for _ in range(8)]
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[k], want[k]) for k in want)
+    assert all(bool(torch.all(t == 99)) for t in trash)
+
+
+def test_wide_local_share_with_many_slots():
+    """Bits and pairs of a placing block that do not fit its LDS together: the pairs are stored directly."""
+    T, E, K = 70001, 1024, 16
+    x = torch.randn(T, E, generator=torch.Generator(device=DEV).manual_seed(1), device=DEV).bfloat16()
+    r = lr.Router(T=T, E=E, K=K, dtype=lr.BF16, device=DEV)
+    log("wide local share")
+    o = lr.route(r, x)
+    top, order = torch.sort(x.float(), dim=1, descending=True, stable=True)
+    assert torch.equal(o["idx"].long(), order[:, :K])
+    flat = o["idx"].reshape(-1).long()
+    by = torch.argsort(flat, stable=True)
+    assert torch.equal(o["tok"].long(), by // K) and torch.equal(o["slot"].long(), by % K)
+    assert torch.equal(o["alpha"], o["w"].reshape(-1)[by])
+    assert torch.equal(o["counts"].long(), torch.bincount(flat, minlength=E))
+    back = torch.empty_like(by)
+    back[by] = torch.arange(T * K, device=DEV)
+    assert torch.equal(o["pmap"].reshape(-1).long(), back)
