@@ -119,10 +119,11 @@ struct Layout {
       const int e = expert(lane, q);
       if (e + 4 <= E) {
         if (BF16) {
-          *(bf16x4u_t*)((uint16_t*)out + t * E + e) =
-              bf16x4u_t{pack_bf16x2(x[q], x[q + 1]), pack_bf16x2(x[q + 2], x[q + 3])};
+          __builtin_nontemporal_store(bf16x4u_t{pack_bf16x2(x[q], x[q + 1]), pack_bf16x2(x[q + 2], x[q + 3])},
+                                      (bf16x4u_t*)((uint16_t*)out + t * E + e));
         } else {
-          *(f32x4u_t*)((float*)out + t * E + e) = f32x4u_t{x[q], x[q + 1], x[q + 2], x[q + 3]};
+          __builtin_nontemporal_store(f32x4u_t{x[q], x[q + 1], x[q + 2], x[q + 3]},
+                                      (f32x4u_t*)((float*)out + t * E + e));
         }
       } else if (e < E) {
 #pragma unroll
@@ -796,22 +797,20 @@ __global__ __launch_bounds__(kGradThreads) void route_bwd_kernel(
   const int lane = threadIdx.x & (L - 1);
   const int64_t t = (int64_t)blockIdx.x * (kGradThreads / L) + threadIdx.x / L;
   const bool in = t < T, on = in && unmasked(mask, t);
-  // the slots' loads start first: three of them depend on each other
+  // the slots' loads start first: dalpha's depends on pmap's
   int e[S];
-  float xe[S], y[S];
+  float y[S];
   if (dalpha) {
+    int64_t j[S];
 #pragma unroll
     for (int q = 0; q < S; ++q) {
       const int k = lane + q * L;
-      e[q] = on && k < K ? idx[t * K + k] : -1;
-      y[q] = 0.0f;
-      xe[q] = kNegInf;
-      if (e[q] >= 0 && e[q] < E) {
-        const int64_t j = pmap ? pmap[t * K + k] : t * K + k;
-        if (!pmap || (j >= 0 && j < n_pairs)) y[q] = scale * dalpha[j];
-        xe[q] = Lay::load_one(logits, t * E + e[q]);
-      }
+      const bool slot = on && k < K;
+      e[q] = slot ? idx[t * K + k] : -1;
+      j[q] = !slot ? -1 : pmap ? pmap[t * K + k] : t * K + k;
     }
+#pragma unroll
+    for (int q = 0; q < S; ++q) y[q] = j[q] >= 0 && (!pmap || j[q] < n_pairs) ? scale * dalpha[j[q]] : 0.0f;
   }
   float x[V], p[V], dx[V], top = kNegInf, Z = 0.0f;
   Lay::load(logits, t, E, on, lane, x);
@@ -830,10 +829,17 @@ __global__ __launch_bounds__(kGradThreads) void route_bwd_kernel(
 #pragma unroll
   for (int v = 0; v < V; ++v) p[v] *= rz;
   if (dalpha) {
+    // the row passes the logits of the chosen experts to their slots, then the slots' results back
     float* row = rows[threadIdx.x / L];
+    float xe[S], ref = top, r = rz, q_of[S], s = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) row[Lay::expert(lane, v)] = x[v];
+    wave_sync();
+#pragma unroll
+    for (int q = 0; q < S; ++q) xe[q] = e[q] >= 0 && e[q] < E ? row[e[q]] : kNegInf;
+    wave_sync();
 #pragma unroll
     for (int v = 0; v < V; ++v) row[Lay::expert(lane, v)] = 0.0f;
-    float ref = top, r = rz, q_of[S], s = 0.0f;
     if (renorm) {  // softmax over the chosen experts
       ref = kNegInf;
 #pragma unroll
