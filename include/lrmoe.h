@@ -490,7 +490,8 @@ lrmoe_status lrmoe_adamw_step_scalars(const lrmoe_adamw_config* c, lrmoe_adamw_s
 /* One AdamW step over n_tensors tensors (a host array; nothing of it is read after the call):
  *   g = grad_scale * grad;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
  *   w = w * decay - lr * (m c1) / (sqrt(v) c2 + eps)
- * in f32 with a rounding at each operation (eps = 0 divides by zero where v is 0); w of bf16 without a master is rounded to nearest
+ * in f32 with a rounding at each operation (with 8-bit states the quotient is a product with the
+ * reciprocal to 1 ulp; eps = 0 divides by zero where v is 0); w of bf16 without a master is rounded to nearest
  * even, with a master the master takes the f32 result and w its rounded copy.
  * 8-bit states: m and r = sqrt(v) are e4m3 codes times one power of two per 256 elements,
  * 2^(floor(log2(0.8164966 a)) - 7) with a the block's largest finite magnitude (1 where a = 0).
