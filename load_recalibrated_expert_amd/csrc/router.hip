@@ -145,15 +145,14 @@ constexpr int kRouteThreads = 1024;  // scanning and placing blocks
 constexpr int kFewTokens = 64;        // one pass of 1024 threads at sixteen lanes to a token
 constexpr int kOneChunk = 128;       // up to so many tokens one block does the whole call
 
-// Tokens of one top-K block and of one placing block: 128, or 64 where eight or more lanes to a token make
-// two passes of that and the blocks are fewer than the 256 compute units (16384 x 512: top-K 19 us
-// in chunks of 128, 13 us in chunks of 64; 50021 x 257: 24 us either way, but 4 us more for the
-// scan and the placing). Each block writes a row of counts, and a placing block holds a bit per
-// (token, local expert) in 48 KB of LDS: chunks grow until there are at most 512 rows, as far as
-// those bits let them.
+// Tokens of one top-K block and of one placing block: 128, or 64 where sixteen or more lanes to a token
+// make two passes of that and the blocks are fewer than the 256 compute units (16384 x 512: top-K 22
+// us in chunks of 128, 14.5 us in chunks of 64). Each block writes a row of counts, and a placing
+// block holds a bit per (token, local expert) in 48 KB of LDS: chunks grow until there are at most
+// 512 rows, as far as those bits let them.
 int route_chunk(const lrmoe_router* r) {
   if (r->T <= kOneChunk) return kOneChunk;
-  if (r->E > 128 && r->T <= 256 * 128) return 64;
+  if (r->E > 320 && r->T <= 256 * 128) return 64;
   int c = 128;
   while (c < 1024 && ceil_div(r->T, c) > 512 && (int64_t)r->local * c * 2 / 8 <= 48 * 1024) c *= 2;
   return c;
@@ -396,9 +395,10 @@ __device__ __forceinline__ void of_key(uint32_t k, float* x, int* e) {
   *e = u > 0x007FFFFFu ? 1023 - (int)(k & 1023u) : -1;
 }
 
-// Threads of a top-K block: 128 tokens in one pass up to eight lanes to a token, if 1024 threads have the
-// registers (lists of 32 do not).
-constexpr int topk_threads(int L, int N) { return L >= 8 && N <= 16 ? 1024 : 512; }
+// Threads of a top-K block: 64 tokens in one pass with sixteen lanes to a token, if 1024 threads have the
+// registers (lists of 32 do not). 16384 x 512: 15.5 us with 512 threads, 14.5 us with 1024; with
+// eight lanes to a token 50021 x 257 takes 22.9 us with 512 and 24.5 us with 1024.
+constexpr int topk_threads(int L, int N) { return L >= 16 && N <= 16 ? 1024 : 512; }
 
 // One block per chunk of tokens: the K largest logits of each, their weights, and how often the chunk
 // chose each expert. With few tokens (rows = 1) the block places the pairs itself.
