@@ -497,7 +497,7 @@ lrmoe_status lrmoe_adamw_step_scalars(const lrmoe_adamw_config* c, lrmoe_adamw_s
  * 2^(floor(log2(0.8164966 a)) - 7) with a the block's largest finite magnitude (1 where a = 0).
  * The update uses m and v before they are rounded. Magnitudes are rounded at random,
  * floor(x / u + (b + 0.5) / 65536) * u with u the spacing of e4m3 at x: rounding to nearest
- * would keep v where it is, as a step changes it by less than half a spacing. b are the low (m)
+ * would never let v fall, as a step lowers it by less than half a spacing. b are the low (m)
  * and high (r) 16 bits of mix(lo + mix(key + hi * 0x9E3779B1)) with hi, lo the 32-bit halves of
  * first + i and mix(x): x ^= x >> 16; x *= 0x9E3779B1; x ^= x >> 15; x *= 0x85EBCA77;
  * x ^= x >> 13. A positive r is never rounded to 0 (a root of 0 beside a first moment that is

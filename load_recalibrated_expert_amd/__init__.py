@@ -692,8 +692,9 @@ class AdamW:
         if len(grads) != len(self.w) or dt not in (torch.float32, torch.bfloat16) or any(
                 g.dtype != dt or g.numel() != w.numel() or g.device != w.device for g, w in zip(grads, self.w)):
             raise ValueError("grads: one f32 or bf16 tensor per weight, of its size, all of one type")
-        for e, g in zip(self._table, grads):
-            e.grad = _ptr(g)
+        ptrs = [_ptr(g) for g in grads]  # all of them first: a tensor that is refused leaves the old ones bound
+        for e, at in zip(self._table, ptrs):
+            e.grad = at
         self.c.grad_dtype = BF16 if dt == torch.bfloat16 else F32
         self.grads, self._plan = grads, None
 

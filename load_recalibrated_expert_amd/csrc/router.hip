@@ -16,9 +16,8 @@ namespace {
 constexpr float kFltMax = 3.402823466e+38f;
 constexpr float kNegInf = -__builtin_huge_valf();
 
-__device__ __forceinline__ float clean(float x) {  // NaN -> -inf, +inf -> FLT_MAX
-  return fminf(fmaxf(x, kNegInf), kFltMax);  // the maximum of a NaN and a number is the number
-}
+__device__ __forceinline__ float not_nan(float x) { return fmaxf(x, kNegInf); }  // NaN -> -inf: the maximum is the number
+__device__ __forceinline__ float clean(float x) { return fminf(not_nan(x), kFltMax); }  // and +inf -> FLT_MAX
 
 // exp(d) for d = x - max: d is at most 0, or NaN where both are -inf (a token that is not live). h + l is
 // d log2(e) to about 2^-48, so the error is that of the 2^h instruction and of d itself; below
@@ -67,9 +66,10 @@ struct Layout {
   static constexpr bool BF16 = BF16_;
   static __device__ __forceinline__ int expert(int lane, int v) { return (v >> 2) * (4 * L) + lane * 4 + (v & 3); }
   static __device__ __forceinline__ float load_one(const void* __restrict__ logits, int64_t i) {
-    return clean(BF16 ? __uint_as_float((uint32_t)((const uint16_t*)logits)[i] << 16) : ((const float*)logits)[i]);
+    return BF16 ? __uint_as_float((uint32_t)((const uint16_t*)logits)[i] << 16) : ((const float*)logits)[i];
   }
-  // Token t by the rules of the header; -inf beyond E, and everywhere if `on` is false.
+  // Token t by the rules of the header; -inf beyond E, and everywhere if `on` is false. INF: +inf stays.
+  template <bool INF = false>
   static __device__ __forceinline__ void load(const void* __restrict__ logits, int64_t t, int E, bool on, int lane,
                                               float x[V]) {
 #pragma unroll
@@ -92,7 +92,7 @@ struct Layout {
       x[q] = a, x[q + 1] = b, x[q + 2] = c, x[q + 3] = d;
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) x[v] = clean(x[v]);
+    for (int v = 0; v < V; ++v) x[v] = INF ? not_nan(x[v]) : clean(x[v]);
   }
   // Row s of the [n_seq x E] counts, zeros beyond E and where `on` is false.
   static __device__ __forceinline__ void load_counts(const int32_t* __restrict__ counts, int64_t s, int E, bool on,
@@ -391,7 +391,7 @@ __device__ __forceinline__ void of_key(double d, float* x, int* e) {  // e = -1 
 }
 __device__ __forceinline__ void of_key(uint32_t k, float* x, int* e) {
   const uint32_t u = k >> 31 ? k & 0xFFFF0000u : k | 0xFFFFu;
-  *x = unordered(u);
+  *x = fminf(unordered(u), kFltMax);
   *e = u > 0x007FFFFFu ? 1023 - (int)(k & 1023u) : -1;
 }
 
@@ -417,14 +417,16 @@ __global__ __launch_bounds__(topk_threads(Lay::L, N)) void route_topk_kernel(Rou
     const int64_t t = tb + group;
     const bool in = t < t1;
     float x[V];
-    Lay::load(a.logits, t, a.E, in && unmasked(a.mask, t), lane, x);
+    // the keys of bf16 logits hold +inf itself: the largest finite f32 that it stands for is no bf16
+    // value, and is above the largest that is
+    Lay::template load<Lay::BF16>(a.logits, t, a.E, in && unmasked(a.mask, t), lane, x);
     float top = kNegInf, Z = 0.0f;
     if (!a.renorm) {
 #pragma unroll
       for (int v = 0; v < V; ++v) top = fmaxf(top, x[v]);
-      top = group_max<L>(top);
+      top = fminf(group_max<L>(top), kFltMax);
 #pragma unroll
-      for (int v = 0; v < V; ++v) Z += exp_term(x[v] - top);
+      for (int v = 0; v < V; ++v) Z += exp_term((Lay::BF16 ? fminf(x[v], kFltMax) : x[v]) - top);
       Z = group_sum<L>(Z);
     }
     using Key = std::conditional_t<Lay::BF16, uint32_t, double>;

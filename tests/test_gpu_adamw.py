@@ -204,6 +204,12 @@ def test_python_checks():
         opt.step([g[0].half()])
     with pytest.raises(ValueError):
         lr.AdamW([torch.zeros(64, 2, device=DEV)[:, 0]])  # strided
+    good = torch.ones(64, device=DEV)
+    two = lr.AdamW([torch.zeros(64, device=DEV) for _ in range(2)], grads=[good, good])
+    table = [e.grad for e in two._table]
+    with pytest.raises(ValueError):  # the second is strided: the first is not taken either
+        two.step([torch.ones(64, device=DEV), torch.ones(64, 2, device=DEV)[:, 0]])
+    assert [e.grad for e in two._table] == table and two.t == 0
     odd = lr.AdamW([torch.zeros(65, device=DEV)[1:]], grads=g)
     with pytest.raises(lr.LrmoeError):  # not 16-byte aligned
         odd.step()

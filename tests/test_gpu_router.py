@@ -35,6 +35,9 @@ CASES = {
     "constant": (70, 16, 4, 2, 9, "f32", False, 0.0, "constant"),
     "bad_values": (333, 40, 6, 0, 40, "f32", False, 0.1, "bad"),
     "bad_values_bf16": (333, 40, 6, 0, 40, "bf16", True, 0.1, "bad"),
+    "infinite_bf16": (257, 40, 6, 0, 40, "bf16", True, 0.0, "infinite"),
+    "infinite_bf16_all": (257, 40, 6, 0, 40, "bf16", False, 0.0, "infinite"),
+    "infinite_f32": (257, 40, 12, 0, 40, "f32", True, 0.0, "infinite"),
     "all_masked": (90, 12, 3, 0, 12, "f32", True, 1.0, "normal"),
     "few_left": (64, 24, 8, 4, 16, "f32", True, 0.0, "few"),
     "lowest": (64, 24, 8, 0, 24, "f32", True, 0.0, "lowest"),
@@ -58,6 +61,9 @@ def _inputs(name):
             x[rng.random((T, E)) < share] = v
         x[5], x[6], x[7] = np.nan, -np.inf, np.inf
         x[8] = -3.3e38
+    elif kind == "infinite":  # beside the largest and lowest finite values of either type
+        for v in (np.inf, 3.3895314e38, np.finfo(np.float32).max, -3.3895314e38, np.finfo(np.float32).min, -np.inf):
+            x[rng.random((T, E)) < 0.08] = v
     elif kind == "few":
         x[rng.random((T, E)) < 0.85] = -np.inf
     elif kind == "lowest":  # masked by the type's lowest value instead of -inf
