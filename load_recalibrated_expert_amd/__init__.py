@@ -468,10 +468,11 @@ class Router:
 def _empty(shape, dtype, device, stream):
     """An output of a call on `stream` (None: the current one), allocated there: memory that other
     work of the current stream gave back is not written before that work is done."""
+    strides = (1,) if len(shape) == 1 else (shape[1], 1)  # given, they save a third of torch.empty's host time
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
 
 
 def _want(t, name, shape, dtype, here):
@@ -595,7 +596,7 @@ def alpha_grad(p: Problem, G, Y, alpha, pmap, keep=None, out=None, stream=None):
     gradient G (lrmoe_alpha_grad); ``pmap`` [T, K] from route, ``keep`` [N] uint8 from select."""
     here, f32, dt, N = torch._C._cuda_getDevice(), torch.float32, p.torch_dtype, p.N
     if out is None:
-        out = _empty(N, f32, p.device, stream)
+        out = _empty((N,), f32, p.device, stream)
     if alpha.dtype != f32 or out.dtype != f32 or alpha.numel() < N or out.numel() < N:
         raise ValueError("alpha and out: expected f32 of at least N elements")
     if G.dtype != dt or Y.dtype != dt or G.dim() != 2 or Y.dim() != 2 or G.shape[1] != p.D or Y.shape[1] != p.D or (

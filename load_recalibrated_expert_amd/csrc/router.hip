@@ -474,6 +474,7 @@ __global__ __launch_bounds__(topk_threads(Lay::L, N)) void route_topk_kernel(Rou
 constexpr int kOwnRows = 32;
 constexpr size_t kPlaceLds = 48 * 1024;  // of a placing block, beside its 8 KB of sums
 constexpr int kScanExperts = 32;
+constexpr int kScanKept = 8;  // rows of a run: all of them up to 512 chunks
 
 // Block: 32 experts, the rows in 64 runs. prefix[r][e] = tokens in the rows before r; total[e].
 __global__ __launch_bounds__(kRouteThreads) void route_scan_kernel(RouteArgs a) {
@@ -482,10 +483,14 @@ __global__ __launch_bounds__(kRouteThreads) void route_scan_kernel(RouteArgs a) 
   const int e = blockIdx.x * kScanExperts + 2 * p, len = (a.rows + kWave - 1) / kWave;
   const int r0 = min(run * len, a.rows), r1 = min(r0 + len, a.rows);
   const uint32_t* h = (const uint32_t*)a.hist + e / 2;
+  uint32_t kept[kScanKept];  // a run's first rows stay in registers for the second pass
   int s0 = 0, s1 = 0;
   if (e < E8) {
-#pragma unroll 8
-    for (int r = r0; r < r1; ++r) {
+#pragma unroll
+    for (int q = 0; q < kScanKept; ++q) kept[q] = r0 + q < r1 ? h[(int64_t)(r0 + q) * (E8 / 2)] : 0;
+#pragma unroll
+    for (int q = 0; q < kScanKept; ++q) s0 += (int)(kept[q] & 0xFFFFu), s1 += (int)(kept[q] >> 16);
+    for (int r = r0 + kScanKept; r < r1; ++r) {
       const uint32_t v = h[(int64_t)r * (E8 / 2)];
       s0 += (int)(v & 0xFFFFu), s1 += (int)(v >> 16);
     }
@@ -508,10 +513,15 @@ __global__ __launch_bounds__(kRouteThreads) void route_scan_kernel(RouteArgs a) 
   __syncthreads();
   if (e < E8) {
     s0 = part[2 * p][run], s1 = part[2 * p + 1][run];
-#pragma unroll 8
-    for (int r = r0; r < r1; ++r) {
+    int* out = a.prefix + e;
+#pragma unroll
+    for (int q = 0; q < kScanKept; ++q) {
+      if (r0 + q < r1) *(int2*)(out + (int64_t)(r0 + q) * E8) = make_int2(s0, s1);
+      s0 += (int)(kept[q] & 0xFFFFu), s1 += (int)(kept[q] >> 16);
+    }
+    for (int r = r0 + kScanKept; r < r1; ++r) {
       const uint32_t v = h[(int64_t)r * (E8 / 2)];
-      *(int2*)(a.prefix + (int64_t)r * E8 + e) = make_int2(s0, s1);
+      *(int2*)(out + (int64_t)r * E8) = make_int2(s0, s1);
       s0 += (int)(v & 0xFFFFu), s1 += (int)(v >> 16);
     }
   }
