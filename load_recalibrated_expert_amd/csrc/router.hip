@@ -701,14 +701,12 @@ __global__ __launch_bounds__(kBalThreads) void balance_tile_kernel(int T, int E,
 
 constexpr int kJoinThreads = 1024, kJoinWaves = kJoinThreads / kWave;
 
-__device__ __forceinline__ double block_sum(double v, double* sh) {  // kJoinThreads threads, all get the sum
-  v = wave_sum(v);
-  if ((threadIdx.x & (kWave - 1)) == 0) sh[threadIdx.x / kWave] = v;
-  __syncthreads();
-  double a = 0.0;
-  for (int i = 0; i < kJoinWaves; ++i) a += sh[i];
-  __syncthreads();
-  return a;
+// Sum over the wavefront, the same bits in every lane.
+template <int S = 1>
+__device__ __forceinline__ double lanes_sum(double v) {
+  if constexpr (S < kWave)
+    return lanes_sum<2 * S>(v + __hiloint2double(lane_swap<S>(__double2hiint(v)), lane_swap<S>(__double2loint(v))));
+  else return v;
 }
 
 // Grid (sequence, 64 experts): the sequence's tiles joined, every 16th by one wavefront and those over
@@ -722,9 +720,8 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(int T, int E
                                                                     int32_t* __restrict__ counts,
                                                                     float* __restrict__ psum, float* __restrict__ norm,
                                                                     float* __restrict__ loss) {
-  __shared__ double sh[kJoinWaves], sum_of[kJoinWaves][kJoinExperts];
-  __shared__ int n_of[kJoinWaves][kJoinExperts];
-  __shared__ bool last;
+  __shared__ double sum_of[kJoinWaves][kWave];
+  __shared__ int n_of[kJoinWaves][kWave], live_of;
   const int s = blockIdx.x, part = blockIdx.y, parts = gridDim.y;
   const int wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1);
   const int e = part * kJoinExperts + lane;
@@ -741,14 +738,18 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(int T, int E
       n += ws.count[(b0 + i) * E + e];
     }
   }
-  int live = 0;
-  if (part == 0)
-    for (int i = threadIdx.x; i < tiles; i += kJoinThreads) live += ws.live[b0 + i];
   sum_of[wave][lane] = a;
   n_of[wave][lane] = n;
+  if (part == 0 && wave == kJoinWaves - 1) {
+    int live = 0;
+    for (int i = lane; i < tiles; i += kWave) live += ws.live[b0 + i];
+    live = group_reduce<kWave>(live, [](int p, int q) { return p + q; });
+    if (lane == 0) live_of = live;
+  }
   __syncthreads();
+  if (wave != 0) return;  // the rest is one wavefront's
   double dot = 0.0;
-  if (wave == 0 && e < E) {
+  if (e < E) {
     a = 0.0;
     n = 0;
     for (int q = 0; q < kJoinWaves; ++q) {
@@ -759,31 +760,31 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(int T, int E
     counts[(int64_t)s * E + e] = n;
     dot = a * n;
   }
-  dot = wave_sum(dot);
-  const double alive_tokens = block_sum((double)live, sh);  // exact: whole numbers
-  if (threadIdx.x == 0) {
+  dot = lanes_sum(dot);
+  uint32_t before = 0;
+  if (lane == 0) {
     __hip_atomic_store(&ws.dot[(int64_t)s * parts + part], dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (part == 0) __hip_atomic_store(&ws.n[s], (int)alive_tokens, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    const uint32_t before = __hip_atomic_fetch_add(ws.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-    last = before == gridDim.x * gridDim.y - 1;
+    if (part == 0) __hip_atomic_store(&ws.n[s], live_of, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    before = __hip_atomic_fetch_add(ws.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
   }
-  __syncthreads();
-  if (!last) return;
-  double alive = 0.0, sum = 0.0;
-  for (int i = threadIdx.x; i < n_seq; i += kJoinThreads)
-    alive += __hip_atomic_load(&ws.n[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) > 0 ? 1.0 : 0.0;
-  alive = block_sum(alive, sh);
-  for (int i = threadIdx.x; i < n_seq; i += kJoinThreads) {
+  if (__builtin_amdgcn_readfirstlane(before) != gridDim.x * gridDim.y - 1) return;
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");  // lane 0's acquire, for the whole wavefront
+  int alive = 0;
+  for (int i = lane; i < n_seq; i += kWave)
+    alive += __hip_atomic_load(&ws.n[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) > 0 ? 1 : 0;
+  alive = group_reduce<kWave>(alive, [](int p, int q) { return p + q; });
+  double sum = 0.0;
+  for (int i = lane; i < n_seq; i += kWave) {
     const double m = __hip_atomic_load(&ws.n[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    const double f = m > 0 ? (double)coef * E / (alive * K * m * m) : 0.0;
+    const double f = m > 0 ? (double)coef * E / ((double)alive * K * m * m) : 0.0;
     norm[i] = (float)f;
     double d = 0.0;
     for (int q = 0; q < parts; ++q)
       d += __hip_atomic_load(&ws.dot[(int64_t)i * parts + q], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     sum += f * d;
   }
-  sum = block_sum(sum, sh);
-  if (threadIdx.x == 0) loss[0] = (float)sum;
+  sum = lanes_sum(sum);
+  if (lane == 0) loss[0] = (float)sum;
 }
 
 // ---------------------------------------------------------------- gradient of the logits
@@ -919,14 +920,6 @@ __global__ __launch_bounds__(kGradThreads) void route_bwd_kernel(
 
 constexpr int kAlphaThreads = 256;
 constexpr int kAlphaRows = 8;  // pairs whose rows a wavefront reads at once
-
-// Sum over the wavefront, the same bits in every lane.
-template <int S = 1>
-__device__ __forceinline__ double lanes_sum(double v) {
-  if constexpr (S < kWave)
-    return lanes_sum<2 * S>(v + __hiloint2double(lane_swap<S>(__double2hiint(v)), lane_swap<S>(__double2loint(v))));
-  else return v;
-}
 
 // Products of 16 bytes of two rows, added to s in fp64 (as the score's norms; products of bf16 values are
 // exact in f32).
