@@ -566,7 +566,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs a)
 // ---------------------------------------------------------------- balance loss
 
 constexpr int kBalThreads = 1024;
-constexpr int kBalTile = 64;      // tokens of one tile
+constexpr int kMaxTile = 8192;    // its tokens that are live take one byte of LDS each
 constexpr int kJoinExperts = 64;  // experts of one joining block, one to a lane
 
 // Sequence s, clamped into [0, T] whatever the offsets hold.
@@ -581,17 +581,28 @@ __device__ __forceinline__ void seq_range(const int64_t* __restrict__ off, int s
   *hi = b < *lo ? *lo : (b > T ? T : b);
 }
 
+// Tokens of one tile: one pass of a block, or more where the tiles of one sequence would be more than 512,
+// which the join takes one after the other (a million tokens of 64 experts: 216 us in tiles of 64,
+// 65 us in tiles of 2048). Up to 128 values of a lane are summed in fp32: above 512 experts, where a
+// pass takes 16 tokens, tiles end at 2048.
+int balance_log_tile(const lrmoe_router* r) {
+  int log = 6;
+  while ((1 << log) < (r->E > 512 ? kMaxTile / 4 : kMaxTile) && (r->T >> log) > 512) ++log;
+  return log;
+}
+
 // Sequence s has the tile slots from floor(off[s] / tile) + s on, which are at least as many as it
 // has tiles, so tiles need no table: floor(T / tile) + n_seq slots in all.
-__device__ __forceinline__ int64_t first_tile(int64_t lo, int s) { return lo / kBalTile + s; }
+__device__ __forceinline__ int64_t first_tile(int64_t lo, int s, int log_tile) { return (lo >> log_tile) + s; }
 
-__device__ __forceinline__ int seq_of_tile(const int64_t* __restrict__ off, int n_seq, int T, int64_t b) {
+__device__ __forceinline__ int seq_of_tile(const int64_t* __restrict__ off, int n_seq, int T, int log_tile,
+                                           int64_t b) {
   int a = 0, z = n_seq - 1;  // the last sequence whose first slot is at or before b
   while (a < z) {
     const int m = (a + z + 1) / 2;
     int64_t lo, hi;
     seq_range(off, m, T, &lo, &hi);
-    if (first_tile(lo, m) <= b) a = m;
+    if (first_tile(lo, m, log_tile) <= b) a = m;
     else z = m - 1;
   }
   return a;
@@ -606,7 +617,7 @@ struct BalanceWs {
   uint32_t* done;  // join blocks that are through
 };
 
-int64_t balance_tiles(const lrmoe_router* r, int32_t n_seq) { return r->T / kBalTile + n_seq; }
+int64_t balance_tiles(const lrmoe_router* r, int32_t n_seq) { return (r->T >> balance_log_tile(r)) + n_seq; }
 
 size_t balance_layout(const lrmoe_router* r, int32_t n_seq, char* base, BalanceWs* out) {
   const size_t tiles = (size_t)balance_tiles(r, n_seq), parts = (size_t)ceil_div(r->E, kJoinExperts);
@@ -627,9 +638,11 @@ size_t balance_layout(const lrmoe_router* r, int32_t n_seq, char* base, BalanceW
   return at;
 }
 
-// One block per tile slot; up to 512 experts every group of lanes has one token.
-template <class Lay>
-__global__ __launch_bounds__(kBalThreads) void balance_tile_kernel(int T, int E, int K, int n_seq,
+// One block per tile slot; up to 512 experts a pass takes 64 tokens, one to a group of lanes. LONG: tiles of
+// more than 64 tokens. (Without its own code for 64, whose loop is one pass, 32768 x 128 took 9.3
+// instead of 7.3 us.)
+template <class Lay, bool LONG>
+__global__ __launch_bounds__(kBalThreads) void balance_tile_kernel(int T, int E, int K, int n_seq, int log_long,
                                                                    const void* __restrict__ logits,
                                                                    const uint8_t* __restrict__ mask,
                                                                    const int32_t* __restrict__ idx,
@@ -637,16 +650,20 @@ __global__ __launch_bounds__(kBalThreads) void balance_tile_kernel(int T, int E,
   constexpr int L = Lay::L, V = Lay::V, kGroups = kBalThreads / L, kWaves = kBalThreads / kWave;
   __shared__ int cnt[1024];
   __shared__ float part[kWaves][L * V];
-  __shared__ int live_of[kBalTile];
+  __shared__ uint8_t live_of[LONG ? kMaxTile : 64];
+  __shared__ int live_n;
+  const int log_tile = LONG ? log_long : 6;
   const int64_t b = blockIdx.x;
   if (b == 0 && threadIdx.x == 0) *ws.done = 0;
-  const int s = off ? seq_of_tile(off, n_seq, T, b) : 0;
+  const int s = off ? seq_of_tile(off, n_seq, T, log_tile, b) : 0;
   int64_t lo, hi;
   seq_range(off, s, T, &lo, &hi);
-  lo += (b - first_tile(lo, s)) * kBalTile;
-  hi = min(hi, lo + kBalTile);
+  lo += (b - first_tile(lo, s, log_tile)) << log_tile;
+  hi = min(hi, lo + (1 << log_tile));
   if (lo >= hi) return;  // a slot that no tile uses: the whole block leaves
+  if (!LONG) hi = min(hi, lo + 64);  // what the compiler is to know
   for (int e = threadIdx.x; e < E; e += kBalThreads) cnt[e] = 0;
+  if (threadIdx.x == 0) live_n = 0;
   const int lane = threadIdx.x & (L - 1), group = threadIdx.x / L, n = (int)(hi - lo) * K;
   const int e0 = (int)threadIdx.x < n ? idx[lo * K + threadIdx.x] : -1;  // on its way meanwhile
   float acc[V];
@@ -681,6 +698,14 @@ __global__ __launch_bounds__(kBalThreads) void balance_tile_kernel(int T, int E,
 #pragma unroll
     for (int v = 0; v < V; ++v) part[threadIdx.x / kWave][Lay::expert(lane, v)] = acc[v];
   __syncthreads();
+  if (LONG) {
+    int mine = 0;
+    for (int i = threadIdx.x; i < (int)(hi - lo); i += kBalThreads) mine += live_of[i];
+    if (mine) atomicAdd(&live_n, mine);
+  } else if (threadIdx.x < kWave) {
+    const unsigned long long on = __ballot(threadIdx.x < hi - lo && live_of[threadIdx.x] != 0);
+    if (threadIdx.x == 0) live_n = __popcll(on);
+  }
   for (int i = threadIdx.x; i < n; i += kBalThreads) {
     const int e = i < kBalThreads ? e0 : idx[lo * K + i];
     if (e >= 0 && e < E && live_of[i / K]) atomicAdd(&cnt[e], 1);
@@ -693,10 +718,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_tile_kernel(int T, int E,
     ws.psum[b * E + e] = a;
     ws.count[b * E + e] = cnt[e];
   }
-  if (threadIdx.x < kBalTile) {
-    const unsigned long long on = __ballot(threadIdx.x < hi - lo && live_of[threadIdx.x] != 0);
-    if (threadIdx.x == 0) ws.live[b] = __popcll(on);
-  }
+  if (threadIdx.x == 0) ws.live[b] = live_n;
 }
 
 constexpr int kJoinThreads = 1024, kJoinWaves = kJoinThreads / kWave;
@@ -715,7 +737,7 @@ __device__ __forceinline__ double lanes_sum(double v) {
 // which block it is. 8.4 us for 512 tiles of 128 experts, 2.5 of them the last block's part, most
 // of the rest latency: 16 experts to a block took 7.9 us there, but 9.1 instead of 7.0 us for 37
 // sequences of 60 experts, whose releases are then four times as many.
-__global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(int T, int E, int K, int n_seq, float coef,
+__global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(int T, int E, int K, int n_seq, int log_tile, float coef,
                                                                     const int64_t* __restrict__ off, BalanceWs ws,
                                                                     int32_t* __restrict__ counts,
                                                                     float* __restrict__ psum, float* __restrict__ norm,
@@ -727,8 +749,8 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(int T, int E
   const int e = part * kJoinExperts + lane;
   int64_t lo, hi;
   seq_range(off, s, T, &lo, &hi);
-  const int64_t b0 = first_tile(lo, s);
-  const int tiles = (int)((hi - lo + kBalTile - 1) / kBalTile);
+  const int64_t b0 = first_tile(lo, s, log_tile);
+  const int tiles = (int)((hi - lo + (1 << log_tile) - 1) >> log_tile);
   double a = 0.0;
   int n = 0;
   if (e < E) {
@@ -1090,13 +1112,20 @@ lrmoe_status launch_balance_loss(const lrmoe_router* r, const void* logits, cons
                                  float* norm, float* loss, void* ws, hipStream_t s) {
   BalanceWs b;
   balance_layout(r, n_seq, (char*)ws, &b);
+  const int log_tile = balance_log_tile(r);
   if (by_layout(r, [&](auto lay) {
-        balance_tile_kernel<decltype(lay)><<<(unsigned)balance_tiles(r, n_seq), kBalThreads, 0, s>>>(
-            r->T, r->E, r->K, n_seq, logits, mask, idx, seq_off_d, b);
+        using Lay = decltype(lay);
+        const unsigned g = (unsigned)balance_tiles(r, n_seq);
+        if (log_tile > 6)
+          balance_tile_kernel<Lay, true><<<g, kBalThreads, 0, s>>>(r->T, r->E, r->K, n_seq, log_tile, logits, mask, idx,
+                                                                   seq_off_d, b);
+        else
+          balance_tile_kernel<Lay, false><<<g, kBalThreads, 0, s>>>(r->T, r->E, r->K, n_seq, log_tile, logits, mask,
+                                                                    idx, seq_off_d, b);
       }) != LRMOE_OK)
     return LRMOE_ERR_HIP;
   balance_join_kernel<<<dim3((unsigned)n_seq, (unsigned)ceil_div(r->E, kJoinExperts)), kJoinThreads, 0, s>>>(
-      r->T, r->E, r->K, n_seq, coef, seq_off_d, b, counts, psum, norm, loss);
+      r->T, r->E, r->K, n_seq, log_tile, coef, seq_off_d, b, counts, psum, norm, loss);
   return launch_status();
 }
 

@@ -391,3 +391,33 @@ def test_wide_local_share_with_many_slots():
     back = torch.empty_like(by)
     back[by] = torch.arange(T * K, device=DEV)
     assert torch.equal(o["pmap"].reshape(-1).long(), back)
+
+
+@pytest.mark.parametrize("off", [None, [0, 30000, 30001, 100000]])
+def test_balance_of_long_sequences(off):
+    """Tiles of more than one pass: counts and sums against torch in fp64."""
+    T, E, K = 100003, 24, 3
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.randn(T, E, generator=gen, device=DEV)
+    mask = (torch.rand(T, generator=gen, device=DEV) < 0.7).to(torch.uint8)
+    r = lr.Router(T=T, E=E, K=K, device=DEV)
+    idx = lr.route(r, x, mask=mask)["idx"]
+    log("long sequences")
+    b = lr.balance_loss(r, x, idx, coef=0.5, mask=mask, seq_off=off)
+    again = lr.balance_loss(r, x, idx, coef=0.5, mask=mask, seq_off=off)
+    assert all(torch.equal(b[k], again[k]) for k in b)
+    p, on = torch.softmax(x.double(), 1), mask.bool()
+    ends = [0, T] if off is None else off
+    loss, S = 0.0, len(ends) - 1
+    for s, (lo, hi) in enumerate(zip(ends, ends[1:])):
+        rows = on[lo:hi]
+        want = p[lo:hi][rows].sum(0)
+        count = torch.bincount(idx[lo:hi][rows].reshape(-1).long(), minlength=E)
+        assert torch.equal(b["counts"][s].long(), count)
+        # each p to 60 x 2^-24 (|x - max| is under 12), 128 sums of a lane and 80 over lanes in fp32
+        assert torch.all((b["psum"][s].double() - want).abs() <= want * 270 * 2.0 ** -24)
+        n = int(rows.sum())
+        if n:
+            loss += 0.5 * E / (K * n * n) * float((count.double() * want).sum()) / sum(
+                int(on[a:c].sum()) > 0 for a, c in zip(ends, ends[1:]))
+    assert abs(float(b["loss"]) - loss) <= 280 * 2.0 ** -24 * loss
