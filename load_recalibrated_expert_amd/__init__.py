@@ -453,7 +453,7 @@ class Router:
             self._ws_size[n_seq] = int(n.value)
         return self._ws_size[n_seq]
 
-    def workspace(self, n_seq=1) -> torch.Tensor:
+    def workspace(self, n_seq=1, stream=None) -> torch.Tensor:
         """The router's scratch buffer. Calls that overlap on several streams, or graphs that
         may replay at the same time, need a Router each. A buffer that has become too small is
         kept: a captured graph may still use it."""
@@ -461,7 +461,7 @@ class Router:
         if self._ws is None or self._ws.numel() < n:
             if self._ws is not None:
                 self._grown.append(self._ws)
-            self._ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+            self._ws = _empty((n,), torch.uint8, self.device, stream)
         return self._ws
 
 
@@ -516,7 +516,7 @@ def route(r: Router, logits, mask=None, out=None, stream=None):
     leaves a token out. ``out`` reuses buffers."""
     here = torch._C._cuda_getDevice()
     o, ptrs = _outputs(out, r._route_out, r.device, here, stream)
-    ws = r.workspace()
+    ws = r.workspace(1, stream)
     _lib.check(library().lrmoe_route(r.ref, _want(logits, "logits", (r.T, r.E), r.torch_dtype, here),
                                      _flags(mask, "mask", r.T, here), *ptrs, ws.data_ptr(), ws.numel(),
                                      _stream(stream)), "lrmoe_route")
@@ -546,12 +546,13 @@ def _sequences(r, seq_off, here, stream):
 def balance_loss(r: Router, logits, idx, coef=1.0, mask=None, seq_off=None, out=None, stream=None):
     """Per-expert counts and the balance loss of every sequence (lrmoe_balance_loss): a dict of loss
     [1], counts, psum [n_seq, E] and norm [n_seq]. ``seq_off`` (int64 [n_seq + 1], host or device;
-    None: one sequence of all tokens). ``route_bwd`` takes the result as ``balance``."""
+    None: one sequence of all tokens): host offsets are checked and copied, which a capture into a
+    graph does not allow. ``route_bwd`` takes the result as ``balance``."""
     here = torch._C._cuda_getDevice()
     off, S = _sequences(r, seq_off, here, stream)
     o, ptrs = _outputs(out, (("counts", (S, r.E), torch.int32), ("psum", (S, r.E), torch.float32),
                              ("norm", (S,), torch.float32), ("loss", (1,), torch.float32)), r.device, here, stream)
-    ws = r.workspace(S)
+    ws = r.workspace(S, stream)
     _lib.check(library().lrmoe_balance_loss(r.ref, _want(logits, "logits", (r.T, r.E), r.torch_dtype, here),
                                             _flags(mask, "mask", r.T, here),
                                             _want(idx, "idx", (r.T, r.K), torch.int32, here), _ptr(off), S,

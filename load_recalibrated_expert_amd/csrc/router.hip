@@ -46,10 +46,6 @@ __device__ __forceinline__ float group_sum(float v) {
     return __float_as_int(__int_as_float(a) + __int_as_float(b));
   }));
 }
-template <int L>
-__device__ __forceinline__ int group_min(int v) {
-  return group_reduce<L>(v, [](int a, int b) { return min(a, b); });
-}
 
 // Four logits from or to any element of a row: rows of an odd number of experts are aligned to their
 // elements only, which vector loads and stores of global memory take.
@@ -142,7 +138,7 @@ __device__ __forceinline__ bool unmasked(const uint8_t* __restrict__ mask, int64
 // ---------------------------------------------------------------- routing
 
 constexpr int kRouteThreads = 1024;  // scanning and placing blocks
-constexpr int kFewTokens = 64;        // one pass of 1024 threads at sixteen lanes to a token
+constexpr int kFewTokens = 64;       // one pass of 1024 threads at sixteen lanes to a token
 constexpr int kOneChunk = 128;       // up to so many tokens one block does the whole call
 
 // Tokens of one top-K block and of one placing block: 128, or 64 where sixteen or more lanes to a token
@@ -659,9 +655,10 @@ __global__ __launch_bounds__(kBalThreads) void balance_tile_kernel(int T, int E,
   const int s = off ? seq_of_tile(off, n_seq, T, log_tile, b) : 0;
   int64_t lo, hi;
   seq_range(off, s, T, &lo, &hi);
-  lo += (b - first_tile(lo, s, log_tile)) << log_tile;
+  const int64_t tile = b - first_tile(lo, s, log_tile);  // negative in slots before the first sequence's
+  lo += tile << log_tile;
   hi = min(hi, lo + (1 << log_tile));
-  if (lo >= hi) return;  // a slot that no tile uses: the whole block leaves
+  if (tile < 0 || lo >= hi) return;  // a slot that no tile uses: the whole block leaves
   if (!LONG) hi = min(hi, lo + 64);  // what the compiler is to know
   for (int e = threadIdx.x; e < E; e += kBalThreads) cnt[e] = 0;
   if (threadIdx.x == 0) live_n = 0;

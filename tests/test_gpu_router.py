@@ -136,6 +136,7 @@ def _sequences(name, T, rng):
     yield sorted([0, 0, T, T] + rng.integers(0, T + 1, size=9).tolist())
     if T > 3:
         yield [1, T // 2, T - 1]  # tokens before the first and behind the last sequence
+        yield [2 * T // 3, 3 * T // 4, T]
 
 
 @pytest.mark.parametrize("name", sorted(CASES))
