@@ -369,7 +369,7 @@ lrmoe_status lrmoe_scatter(const lrmoe_problem* p, lrmoe_scatter_mode mode, int6
  * cover. Logits are [T x E] of `dtype` (f32 or bf16), and are read by these rules everywhere:
  * a NaN counts as -inf, +inf as the largest finite f32. mask [T] uint8 (NULL: all ones) leaves
  * the tokens with a zero out. A token is live if it is not masked and has a logit over -inf.
- * T * K must be under 2^31, E at most 1024, K at most min(E, 32). */
+ * T must be under 2^26, T * K under 2^31, E at most 1024, K at most min(E, 32). */
 typedef struct lrmoe_router {
   int32_t T;        /* tokens                                                        */
   int32_t E;        /* experts of the layer                                          */
@@ -401,8 +401,8 @@ lrmoe_status lrmoe_route(const lrmoe_router* r, const void* logits, const uint8_
                          int32_t* pmap, void* ws, size_t ws_bytes, lrmoe_stream_t stream);
 
 /* Balance loss and per-expert counts. Sequence s holds the tokens [seq_off[s], seq_off[s+1])
- * (seq_off_d: device int64 [n_seq + 1], not decreasing, inside [0, T]; NULL with n_seq = 1: all
- * T tokens). Over the n_s live tokens of sequence s, with p = softmax of a token's logits:
+ * (seq_off_d: device int64 [n_seq + 1], not decreasing, inside [0, T], n_seq under 2^21 and n_seq * E
+ * under 2^31; NULL with n_seq = 1: all T tokens). Over the n_s live tokens of sequence s, with p = softmax of a token's logits:
  *   counts[s, e] = slots idx[t, k] = e        int32 [n_seq x E]
  *   psum[s, e]   = sum of p[t, e]             f32 [n_seq x E]
  *   norm[s]      = coef * E / (S' K n_s^2)    f32 [n_seq], 0 where n_s = 0; S' = sequences with
@@ -440,7 +440,7 @@ lrmoe_status lrmoe_route_bwd(const lrmoe_router* r, const void* logits, const ui
  * kept; the selection's keep gives the gradient of the retained pairs). G [T x D], Y [N x D] of
  * the storage dtype. pmap [T x K]: the pair row of each (token, slot) position, as lrmoe_route
  * wrote it; each pair has one position. An entry outside [0, N) is none, and pairs without a
- * position keep what dalpha held. Products and sums in fp64. No workspace. */
+ * position keep what dalpha held. Products and sums in fp64. T must be under 2^26. No workspace. */
 lrmoe_status lrmoe_alpha_grad(const lrmoe_problem* p, const void* G, const void* Y, const float* alpha,
                               const int32_t* pmap, const uint8_t* keep, float* dalpha, lrmoe_stream_t stream);
 

@@ -114,6 +114,10 @@ inline lrmoe_status launch_status() {
   return e == hipSuccess ? LRMOE_OK : LRMOE_ERR_HIP;
 }
 
+// A launch has fewer than 2^32 threads along a dimension, a limit of the runtime's own. One wavefront to
+// a token, and a block of 1024 threads to a tile of tokens and to a sequence, stay below it under these:
+constexpr int64_t kMaxTokens = (int64_t)1 << 26, kMaxSequences = (int64_t)1 << 21;
+
 // ---------------------------------------------------------------- launchers (one per .hip file)
 
 lrmoe_status launch_score(const lrmoe_problem* p, const void* G, const void* Phi, const float* alpha,

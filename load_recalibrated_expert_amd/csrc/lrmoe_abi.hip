@@ -83,15 +83,20 @@ lrmoe_status check_router(const lrmoe_router* r) {
   if ((r->renorm != 0 && r->renorm != 1) || !std::isfinite(r->scale)) return LRMOE_ERR_INVALID_ARG;
   if (r->dtype != LRMOE_F32 && r->dtype != LRMOE_BF16) return LRMOE_ERR_UNSUPPORTED;
   if (r->E > 1024 || r->K > 32) return LRMOE_ERR_UNSUPPORTED;
-  if ((int64_t)r->T * r->K >= ((int64_t)1 << 31)) return LRMOE_ERR_UNSUPPORTED;
+  if (r->T >= kMaxTokens || (int64_t)r->T * r->K >= ((int64_t)1 << 31)) return LRMOE_ERR_UNSUPPORTED;
   return LRMOE_OK;
 }
 
 // Sequences of the balance loss: without offsets there is one, of all tokens.
-lrmoe_status check_sequences(const lrmoe_router* r, const int64_t* seq_off_d, int32_t n_seq) {
-  if (n_seq < 1 || (!seq_off_d && n_seq != 1)) return LRMOE_ERR_INVALID_ARG;
-  if ((int64_t)n_seq * r->E >= ((int64_t)1 << 31)) return LRMOE_ERR_UNSUPPORTED;
+lrmoe_status check_sequences(int32_t n_seq, int32_t E) {
+  if (n_seq < 1) return LRMOE_ERR_INVALID_ARG;
+  if (n_seq >= kMaxSequences || (int64_t)n_seq * E >= ((int64_t)1 << 31)) return LRMOE_ERR_UNSUPPORTED;
   return LRMOE_OK;
+}
+
+lrmoe_status check_sequences(const lrmoe_router* r, const int64_t* seq_off_d, int32_t n_seq) {
+  if (!seq_off_d && n_seq != 1) return LRMOE_ERR_INVALID_ARG;
+  return check_sequences(n_seq, r->E);
 }
 
 uint32_t mix32(uint32_t x) {
@@ -404,8 +409,7 @@ lrmoe_status lrmoe_scatter(const lrmoe_problem* p, lrmoe_scatter_mode mode, int6
 lrmoe_status lrmoe_router_workspace_size(const lrmoe_router* r, int32_t n_seq, size_t* bytes) {
   if (!bytes) return LRMOE_ERR_INVALID_ARG;
   LRMOE_TRY(check_router(r));
-  if (n_seq < 1) return LRMOE_ERR_INVALID_ARG;
-  if ((int64_t)n_seq * r->E >= ((int64_t)1 << 31)) return LRMOE_ERR_UNSUPPORTED;
+  LRMOE_TRY(check_sequences(n_seq, r->E));
   *bytes = std::max<size_t>(256, std::max(route_ws_bytes(r), balance_ws_bytes(r, n_seq)));
   return LRMOE_OK;
 }
@@ -454,6 +458,7 @@ lrmoe_status lrmoe_route_bwd(const lrmoe_router* r, const void* logits, const ui
 lrmoe_status lrmoe_alpha_grad(const lrmoe_problem* p, const void* G, const void* Y, const float* alpha,
                               const int32_t* pmap, const uint8_t* keep, float* dalpha, lrmoe_stream_t stream) {
   LRMOE_TRY(check_problem(p, nullptr, nullptr));
+  if (p->T >= kMaxTokens) return LRMOE_ERR_UNSUPPORTED;
   if (p->N == 0) return LRMOE_OK;
   if (!G || !Y || !alpha || !pmap || !dalpha) return LRMOE_ERR_INVALID_ARG;
   if (!aligned(G, 16) || !aligned(Y, 16)) return LRMOE_ERR_INVALID_ARG;

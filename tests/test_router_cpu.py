@@ -46,6 +46,22 @@ def test_sequence_counts_are_checked():
     assert _size(_router(), 1000)[1] > _size(_router(), 1)[1]
 
 
+def test_sizes_past_one_launch_are_refused():
+    """A launch takes fewer than 2^32 threads along a dimension: T < 2^26 tokens, n_seq < 2^21."""
+    lib, few = _lib.load(), dict(E=2, K=1, local=2)
+    assert _size(_router(T=2 ** 26 - 1, **few))[0] == _lib.OK
+    assert _size(_router(T=2 ** 26, **few))[0] == _lib.ERR_UNSUPPORTED
+    assert _size(_router(**few), 2 ** 21 - 1)[0] == _lib.OK
+    assert _size(_router(**few), 2 ** 21)[0] == _lib.ERR_UNSUPPORTED
+    r = _router(**few)
+    assert lib.lrmoe_balance_loss(ctypes.byref(r), FAKE, None, FAKE, FAKE, 2 ** 21, 0.1, *([FAKE] * 5), 2 ** 40,
+                                  None) == _lib.ERR_UNSUPPORTED
+    assert lib.lrmoe_route_bwd(ctypes.byref(r), FAKE, None, FAKE, None, None, 0, FAKE, 2 ** 21, FAKE, FAKE, None, FAKE,
+                               None) == _lib.ERR_UNSUPPORTED
+    p, keep = _lib.make_problem_struct(2, 2 ** 26, 2, 8, 8, True, _lib.BF16, [0, 5, 9], [5, 4])
+    assert lib.lrmoe_alpha_grad(ctypes.byref(p), *([FAKE] * 4), None, FAKE, None) == _lib.ERR_UNSUPPORTED
+
+
 def test_route_refusals():
     lib, r = _lib.load(), _router()
     n = _size(r)[1]
