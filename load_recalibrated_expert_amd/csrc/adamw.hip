@@ -15,6 +15,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBlock = 256;   // elements that share a scale: four to a lane of one wavefront
+constexpr uint32_t kLaunchChunks = (1u << 24) - 1;  // a launch has fewer than 2^32 threads
 constexpr int kChunk = 4 * kThreads;  // elements of one thread block (four times as many: 3 % slower on
                                       // 75 M elements, 7.5 instead of 4.4 us on a small tensor)
 
@@ -38,6 +39,7 @@ struct AdamwArgs {
   float b1, a1, b2, a2, eps;  // beta, 1 - beta
   lrmoe_adamw_scalars s;
   const lrmoe_adamw_scalars* dyn;
+  uint32_t chunk0;  // this launch's first chunk
 };
 
 __device__ __forceinline__ uint32_t mix(uint32_t x) {
@@ -234,15 +236,16 @@ __device__ __forceinline__ void step4(const lrmoe_adamw_tensor& t, const AdamwAr
 
 template <bool Q8, bool W16, bool G16, bool MASTER, class Table>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(Table tab, AdamwArgs a) {
+  const uint32_t chunk = a.chunk0 + blockIdx.x;
   int at = -1;  // the last tensor whose first chunk is at or before this one
   for (int i = 0; i < tab.n; i += kWave) {
     const int q = i + (int)(threadIdx.x & (kWave - 1));
-    at += __popcll(__ballot(q < tab.n && tab.first(q) <= blockIdx.x));
+    at += __popcll(__ballot(q < tab.n && tab.first(q) <= chunk));
   }
   at = __builtin_amdgcn_readfirstlane(at);
   const lrmoe_adamw_tensor t = tab.tensor(at);
   const lrmoe_adamw_scalars s = a.dyn ? *a.dyn : a.s;
-  const int64_t i0 = (int64_t)(blockIdx.x - tab.first(at)) * kChunk, i = i0 + threadIdx.x * 4;
+  const int64_t i0 = (int64_t)(chunk - tab.first(at)) * kChunk, i = i0 + threadIdx.x * 4;
   // without the bounds' instructions a whole chunk of 8-bit states, which is bound by them, takes 252
   // instead of 276 us for 75 M elements; with 32-bit states it takes 415 instead of 403 us
   if (Q8 && i0 + kChunk <= t.n) step4<Q8, W16, G16, MASTER, true>(t, a, s, i);
@@ -250,7 +253,8 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Table tab, AdamwArgs a)
 }
 
 template <class Table>
-lrmoe_status run(const lrmoe_adamw_config* c, unsigned grid, const Table& tab, const AdamwArgs& a, hipStream_t s) {
+lrmoe_status run_launch(const lrmoe_adamw_config* c, unsigned grid, const Table& tab, const AdamwArgs& a,
+                        hipStream_t s) {
   const int kind = (c->state_bits == 8 ? 8 : 0) + (c->w_dtype == LRMOE_BF16 ? 4 : 0) +
                    (c->grad_dtype == LRMOE_BF16 ? 2 : 0) + (c->master ? 1 : 0);
   switch (kind) {
@@ -269,6 +273,15 @@ lrmoe_status run(const lrmoe_adamw_config* c, unsigned grid, const Table& tab, c
     default: return LRMOE_ERR_UNSUPPORTED;
   }
   return launch_status();
+}
+
+template <class Table>
+lrmoe_status run(const lrmoe_adamw_config* c, uint32_t chunks, const Table& tab, AdamwArgs a, hipStream_t s) {
+  for (a.chunk0 = 0; a.chunk0 < chunks; a.chunk0 += kLaunchChunks) {
+    const lrmoe_status st = run_launch(c, std::min(chunks - a.chunk0, kLaunchChunks), tab, a, s);
+    if (st != LRMOE_OK) return st;
+  }
+  return LRMOE_OK;
 }
 
 // Tables as a plan holds them: the tensors that have elements, then their first chunks.
@@ -314,7 +327,7 @@ lrmoe_status launch_adamw(const lrmoe_adamw_tensor* tensors, int32_t n_tensors, 
     if (n == 0) return LRMOE_OK;
     if (chunks >> 31) return LRMOE_ERR_UNSUPPORTED;
     const lrmoe_adamw_tensor* t = (const lrmoe_adamw_tensor*)plan_d;
-    return run(c, (unsigned)chunks, PlanTable{t, (const uint32_t*)(t + n), n}, a, s);
+    return run(c, (uint32_t)chunks, PlanTable{t, (const uint32_t*)(t + n), n}, a, s);
   }
   int32_t i = 0;
   while (i < n_tensors) {
@@ -330,7 +343,7 @@ lrmoe_status launch_adamw(const lrmoe_adamw_tensor* tensors, int32_t n_tensors, 
       chunks += more;
     }
     if (tab.n == 0) break;
-    const lrmoe_status st = run(c, (unsigned)chunks, tab, a, s);
+    const lrmoe_status st = run(c, (uint32_t)chunks, tab, a, s);
     if (st != LRMOE_OK) return st;
   }
   return LRMOE_OK;

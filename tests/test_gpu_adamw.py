@@ -128,6 +128,35 @@ def test_views_leave_their_neighbours():
         assert torch.all(flat[i * step:i * step + n] != 9.0)
 
 
+@pytest.mark.parametrize("plan", [False, True])
+def test_more_elements_than_one_launch_takes(plan):
+    """18.3e9 elements, 8-bit states: more chunks than a launch has blocks, so that the update takes two,
+    with the second one's start inside a tensor. The first step from zero states does the same to
+    every element of a tensor, and what it does is checked on a small one."""
+    if torch.cuda.mem_get_info()[0] < 96 << 30:
+        pytest.skip("needs 96 GB of device memory")
+    n, tensors = (1 << 30) + 256, 17
+    sizes = [n] * tensors + [1000] * (40 if plan else 1)
+    w = [torch.full((k,), 0.5 + i / 64, dtype=torch.bfloat16, device=DEV) for i, k in enumerate(sizes)]
+    g = torch.full((n,), 0.25, dtype=torch.bfloat16, device=DEV)
+    small = torch.full((1024,), 0.25, dtype=torch.bfloat16, device=DEV)
+    opt = lr.AdamW(w, grads=[g] * tensors + [small[:1000]] * (len(sizes) - tensors), bits=8, **HYPER)
+    small_w = [torch.full((64,), 0.5 + i / 64, dtype=torch.bfloat16, device=DEV) for i in range(len(sizes))]
+    log(f"{sum(sizes)} elements in {len(sizes)} tensors, plan: {plan}")
+    if plan:
+        opt._plan = False  # as after a first step
+    opt.step()
+    assert isinstance(opt._plan, torch.Tensor) == plan
+    torch.cuda.synchronize()
+    twin = lr.AdamW(small_w, grads=[small[:64]] * len(sizes), bits=8, **HYPER)
+    twin.step()
+    for i, (a, b) in enumerate(zip(opt.w, twin.w)):
+        lo, hi = a.aminmax()
+        assert lo == hi == b[0] and b[0] != 0.5 + i / 64, i
+        assert opt.v_scale[i].min() == opt.v_scale[i].max() == twin.v_scale[i][0], i
+        assert opt.m_scale[i].min() == opt.m_scale[i].max() == twin.m_scale[i][0], i
+
+
 def test_not_finite_gradients():
     """An infinite or NaN gradient spoils its own element only: the block's scale comes from the rest."""
     n = 700
