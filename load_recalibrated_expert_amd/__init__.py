@@ -441,7 +441,7 @@ class Router:
         self._route_out = (("idx", (T, K), i32), ("w", (T, K), f32), ("counts", (E,), i32),
                            ("seg_off", (self.local + 1,), torch.int64), ("tok", (T * K,), i32),
                            ("slot", (T * K,), i32), ("alpha", (T * K,), f32), ("pmap", (T, K), i32))
-        self._ws, self._ws_size, self._grown = None, {}, []
+        self._ws, self._ws_bytes, self._ws_size, self._grown, self._streams = None, 0, {}, [], set()
         self.workspace_size()  # checks the router
 
     def workspace_size(self, n_seq=1) -> int:
@@ -457,12 +457,19 @@ class Router:
         """The router's scratch buffer. Calls that overlap on several streams, or graphs that
         may replay at the same time, need a Router each. A buffer that has become too small is
         kept: a captured graph may still use it."""
-        n = self.workspace_size(n_seq)
-        if self._ws is None or self._ws.numel() < n:
+        return self._scratch(n_seq, stream)[0]
+
+    def _scratch(self, n_seq, stream):
+        """(workspace, its bytes, raw handle of the stream)"""
+        n, raw = self.workspace_size(n_seq), _stream(stream)
+        if self._ws_bytes < n:
             if self._ws is not None:
                 self._grown.append(self._ws)
-            self._ws = _empty((n,), torch.uint8, self.device, stream)
-        return self._ws
+            self._ws, self._ws_bytes = _empty((n,), torch.uint8, self.device, stream), n
+            self._streams.clear()
+        if raw not in self._streams:
+            _used_on(raw, stream, self._streams, (self._ws,))
+        return self._ws, self._ws_bytes, raw
 
 
 def _empty(shape, dtype, device, stream):
@@ -473,6 +480,14 @@ def _empty(shape, dtype, device, stream):
         return torch.empty_strided(shape, strides, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+
+
+def _used_on(raw, stream, seen, tensors):
+    """Notes, once per stream (its handle: raw), that work there uses `tensors`: memory that is freed
+    meanwhile is given out again only behind that work. `seen`: the streams noted since they were allocated."""
+    seen.add(raw)
+    for t in tensors:
+        t.record_stream(stream if stream is not None else torch.cuda.current_stream())
 
 
 def _want(t, name, shape, dtype, here):
@@ -516,10 +531,9 @@ def route(r: Router, logits, mask=None, out=None, stream=None):
     leaves a token out. ``out`` reuses buffers."""
     here = torch._C._cuda_getDevice()
     o, ptrs = _outputs(out, r._route_out, r.device, here, stream)
-    ws = r.workspace(1, stream)
+    ws, n, raw = r._scratch(1, stream)
     _lib.check(library().lrmoe_route(r.ref, _want(logits, "logits", (r.T, r.E), r.torch_dtype, here),
-                                     _flags(mask, "mask", r.T, here), *ptrs, ws.data_ptr(), ws.numel(),
-                                     _stream(stream)), "lrmoe_route")
+                                     _flags(mask, "mask", r.T, here), *ptrs, ws.data_ptr(), n, raw), "lrmoe_route")
     return o
 
 
@@ -552,12 +566,11 @@ def balance_loss(r: Router, logits, idx, coef=1.0, mask=None, seq_off=None, out=
     off, S = _sequences(r, seq_off, here, stream)
     o, ptrs = _outputs(out, (("counts", (S, r.E), torch.int32), ("psum", (S, r.E), torch.float32),
                              ("norm", (S,), torch.float32), ("loss", (1,), torch.float32)), r.device, here, stream)
-    ws = r.workspace(S, stream)
+    ws, n, raw = r._scratch(S, stream)
     _lib.check(library().lrmoe_balance_loss(r.ref, _want(logits, "logits", (r.T, r.E), r.torch_dtype, here),
                                             _flags(mask, "mask", r.T, here),
                                             _want(idx, "idx", (r.T, r.K), torch.int32, here), _ptr(off), S,
-                                            float(coef), *ptrs, ws.data_ptr(), ws.numel(), _stream(stream)),
-               "lrmoe_balance_loss")
+                                            float(coef), *ptrs, ws.data_ptr(), n, raw), "lrmoe_balance_loss")
     return o
 
 
@@ -680,7 +693,7 @@ class AdamW:
             if bits == 8:
                 e.m_scale, e.v_scale = _ptr(self.m_scale[i]), _ptr(self.v_scale[i])
         self._scalars = self._plan = None
-        self._captured = []
+        self._captured, self._streams = [], set()
         self.grads = None
         if grads is not None:
             self.bind(grads)
@@ -715,7 +728,18 @@ class AdamW:
             host = torch.empty(n.value, dtype=torch.uint8)
             _lib.check(lib.lrmoe_adamw_plan(*args, host.data_ptr(), ctypes.byref(n)), "lrmoe_adamw_plan")
             self._plan = host.to(self.w[0].device)
+            self._streams.clear()
         return self._plan.data_ptr() if self._plan is not False else None
+
+    def _used_on(self, stream):
+        """Raw handle of `stream`, on which work uses what this object allocated."""
+        raw = _stream(stream)
+        if raw in self._streams:
+            return raw
+        own = [t for ts in (self.m, self.v, self.m_scale or (), self.v_scale or ()) for t in ts]
+        own += [t for t in (self._plan, self._scalars) if isinstance(t, torch.Tensor)]
+        _used_on(raw, stream, self._streams, own)
+        return raw
 
     def _config(self, grad_scale):
         self.c.step, self.c.lr, self.c.weight_decay, self.c.grad_scale = self.t, self.lr, self.weight_decay, grad_scale
@@ -736,8 +760,9 @@ class AdamW:
         self.t += 1
         self._config(grad_scale)
         try:
-            _lib.check(library().lrmoe_adamw(self._table, len(self.w), ctypes.byref(self.c), self._plan_ptr(), None,
-                                             _stream(stream)), "lrmoe_adamw")
+            plan = self._plan_ptr()
+            _lib.check(library().lrmoe_adamw(self._table, len(self.w), ctypes.byref(self.c), plan, None,
+                                             self._used_on(stream)), "lrmoe_adamw")
         except Exception:
             self.t -= 1
             raise
@@ -753,6 +778,7 @@ class AdamW:
         values = torch.frombuffer(bytearray(host), dtype=torch.int32)
         if self._scalars is None:
             self._scalars = torch.empty(8, dtype=torch.int32, device=self.w[0].device)
+            self._streams.clear()
         self._scalars.copy_(values)
 
     def step_captured(self, stream=None):
@@ -765,4 +791,4 @@ class AdamW:
         if torch.cuda.is_current_stream_capturing():
             self._captured.append((self._plan, self.grads))
         _lib.check(library().lrmoe_adamw(self._table, len(self.w), ctypes.byref(self.c), plan,
-                                         _ptr(self._scalars), _stream(stream)), "lrmoe_adamw")
+                                         _ptr(self._scalars), self._used_on(stream)), "lrmoe_adamw")

@@ -332,3 +332,36 @@ def test_other_stream():
     torch.cuda.synchronize()
     for a, b in zip(opt.w, twin.w):
         assert torch.equal(a, b)
+
+
+def test_plan_and_states_freed_while_a_side_stream_uses_them():
+    """Work queued on a side stream still reads the plan that bind drops and the states of an object that
+    is gone: their memory is not given out before that work is done."""
+    rng = np.random.default_rng(13)
+    sizes = [300] * 60
+    w = _tensors(sizes, torch.float32, rng, 0.05)
+    g = _tensors(sizes, torch.float32, rng, 0.01)
+    twin = lr.AdamW([t.clone() for t in w], grads=g, **HYPER)
+    opt = lr.AdamW(w, grads=g, **HYPER)
+    side = torch.cuda.Stream()
+    for o in (opt, twin):
+        o.step()
+        o.step()  # makes the plan
+    torch.cuda.synchronize()
+    log("two steps behind a wait on the side stream")
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)  # well over the host's time for what follows
+        opt.step()
+    opt.step(stream=side)
+    held = {t.data_ptr() for t in [opt._plan] + opt.m + opt.v}
+    bytes_ = [t.numel() * t.element_size() for t in [opt._plan, opt.m[0]]]
+    opt.bind([t.clone() for t in g])
+    del opt
+    trash = [torch.full((n,), 255, dtype=torch.uint8, device=DEV) for n in bytes_ for _ in range(200)]
+    assert not side.query(), "the side stream ended before the buffers were asked for"
+    assert held.isdisjoint(t.data_ptr() for t in trash)
+    torch.cuda.synchronize()
+    twin.step()
+    twin.step()
+    for a, b in zip(w, twin.w):
+        assert torch.equal(a, b)

@@ -422,3 +422,27 @@ def test_balance_of_long_sequences(off):
             loss += 0.5 * E / (K * n * n) * float((count.double() * want).sum()) / sum(
                 int(on[a:c].sum()) > 0 for a, c in zip(ends, ends[1:]))
     assert abs(float(b["loss"]) - loss) <= 280 * 2.0 ** -24 * loss
+
+
+def test_workspace_freed_while_a_side_stream_uses_it():
+    """A router that is gone while a call of it waits on a side stream: its workspace, allocated on the current
+    stream, is not given out before that call is done."""
+    r = lr.Router(T=9000, E=64, K=4, dtype=lr.BF16)
+    x = torch.randn(r.T, r.E, device=DEV).bfloat16()
+    want = lr.route(r, x)
+    n, at = r.workspace().numel(), r.workspace().data_ptr()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    log("a call behind a wait on the side stream")
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)  # well over the host's time for what follows
+    got = lr.route(r, x, stream=side)
+    del r
+    trash = [torch.full((n,), 255, dtype=torch.uint8, device=DEV) for _ in range(50)]
+    assert not side.query(), "the side stream ended before the buffers were asked for"
+    assert at not in {t.data_ptr() for t in trash}
+    torch.cuda.synchronize()
+    pairs = int(want["seg_off"][-1])
+    for name in want:
+        a, b = (o[name][:pairs] if name in ("tok", "slot", "alpha") else o[name] for o in (got, want))
+        assert torch.equal(a, b), name
