@@ -758,8 +758,8 @@ class AdamW:
         if torch.cuda.is_current_stream_capturing():
             raise ValueError("a graph would repeat this very step: capture step_captured")
         self.t += 1
-        self._config(grad_scale)
         try:
+            self._config(grad_scale)
             plan = self._plan_ptr()
             _lib.check(library().lrmoe_adamw(self._table, len(self.w), ctypes.byref(self.c), plan, None,
                                              self._used_on(stream)), "lrmoe_adamw")
@@ -772,9 +772,13 @@ class AdamW:
         the current stream. Call it before each replay of a graph that holds ``step_captured``."""
         host = _lib.CAdamwScalars()
         self.t += 1
-        self._config(grad_scale)
-        _lib.check(library().lrmoe_adamw_step_scalars(ctypes.byref(self.c), ctypes.byref(host)),
-                   "lrmoe_adamw_step_scalars")
+        try:
+            self._config(grad_scale)
+            _lib.check(library().lrmoe_adamw_step_scalars(ctypes.byref(self.c), ctypes.byref(host)),
+                       "lrmoe_adamw_step_scalars")
+        except Exception:
+            self.t -= 1
+            raise
         values = torch.frombuffer(bytearray(host), dtype=torch.int32)
         if self._scalars is None:
             self._scalars = torch.empty(8, dtype=torch.int32, device=self.w[0].device)

@@ -232,6 +232,21 @@ def test_python_refusals():
         lr.AdamW(w, grads=g).step_captured()
 
 
+def test_a_refused_advance_counts_no_step():
+    opt = lr.AdamW([torch.zeros(40)], grads=[torch.zeros(40)], step=6)
+    for bad in (float("nan"), float("inf"), None):
+        with pytest.raises((lr.LrmoeError, TypeError)):
+            opt.advance(grad_scale=bad)
+        assert opt.t == 6
+    opt.lr = float("nan")
+    with pytest.raises(lr.LrmoeError):
+        opt.advance()
+    assert opt.t == 6
+    opt.lr = 1e-3
+    opt.advance()
+    assert opt.t == 7
+
+
 # ----------------------------------------------------------------------- the definitions themselves
 
 def _logits(rng, T, E):
