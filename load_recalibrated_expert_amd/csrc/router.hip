@@ -141,17 +141,24 @@ constexpr int kRouteThreads = 1024;  // scanning and placing blocks
 constexpr int kFewTokens = 64;       // one pass of 1024 threads at sixteen lanes to a token
 constexpr int kOneChunk = 128;       // up to so many tokens one block does the whole call
 
-// Tokens of one top-K block and of one placing block: 128, or 64 where sixteen or more lanes to a token
-// make two passes of that and the blocks are fewer than the 256 compute units (16384 x 512: top-K 22
-// us in chunks of 128, 14.5 us in chunks of 64). Each block writes a row of counts, and a placing
-// block holds a bit per (token, local expert) in 48 KB of LDS: chunks grow until there are at most
-// 512 rows, as far as those bits let them.
+constexpr size_t kPlaceLds = 48 * 1024;  // of a placing block, beside its 8 KB of sums
+
+// Words of a placing block's bits, one per (token, local expert); an even number.
+__host__ __device__ constexpr int bit_words(int C, int local) { return ((C + 31) / 32 * local + 1) & ~1; }
+
+// Tokens of one top-K block and of one placing block, so that the 256 compute units have about as many
+// each: 256 chunks of up to 128 tokens, then 512 (top-K and placing of 300000 x 64 in chunks of 1024
+// 27.2 + 16.8 us, of 592 19.3 + 12.7 us; 70000 x 1024 bf16 in chunks of 256 121 us, of 144 70 us). Each
+// writes a row of counts, so chunks have at least 128 tokens, or 64 where the top-K gains more by
+// smaller ones than the scan loses by more rows (sixteen or more lanes to a token: 16384 x 512 in
+// chunks of 128 22 us, of 64 14.5 us; more than 256 chunks: 50021 x 257 in chunks of 128 23.6 us, of
+// 104 21.8 us).
 int route_chunk(const lrmoe_router* r) {
   if (r->T <= kOneChunk) return kOneChunk;
-  if (r->E > 320 && r->T <= 256 * 128) return 64;
-  int c = 128;
-  while (c < 1024 && ceil_div(r->T, c) > 512 && (int64_t)r->local * c * 2 / 8 <= 48 * 1024) c *= 2;
-  return c;
+  const int64_t even = align_up((size_t)ceil_div(r->T, r->T <= 256 * 128 ? 256 : 512), 8);
+  const int64_t room = (int64_t)kPlaceLds / 4 / r->local * 32;  // whose bits fit
+  return (int)std::min(std::max(even, (int64_t)(r->E > 320 || r->T > 256 * 128 ? 64 : 128)),
+                       std::min<int64_t>(room, 1024));
 }
 
 struct RouteArgs {
@@ -406,11 +413,12 @@ __global__ __launch_bounds__(topk_threads(Lay::L, N)) void route_topk_kernel(Rou
   static_assert(V % N == 0, "whole lists");
   extern __shared__ uint32_t lds[];
   RouteBlock<kTopkThreads> blk(a, lds);
-  const int lane = threadIdx.x & (L - 1), group = threadIdx.x / L;
+  const int lane = threadIdx.x & (L - 1);
   const int64_t t0 = (int64_t)blockIdx.x * a.C, t1 = min(t0 + a.C, (int64_t)a.T);
   __syncthreads();
-  for (int64_t tb = t0; tb < t1; tb += kGroups) {
-    const int64_t t = tb + group;
+  // each wavefront for itself: one that has no tokens left leaves the others the units
+  for (int64_t tb = t0 + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) * (kWave / L); tb < t1; tb += kGroups) {
+    const int64_t t = tb + (threadIdx.x & (kWave - 1)) / L;
     const bool in = t < t1;
     float x[V];
     // the keys of bf16 logits hold +inf itself: the largest finite f32 that it stands for is no bf16
@@ -470,7 +478,6 @@ __global__ __launch_bounds__(topk_threads(Lay::L, N)) void route_topk_kernel(Rou
 // 128 experts: 7.3 us of placing against 3.2 us of scan and 5.7 us of placing; 128 rows: 9.9 against
 // 3.1 and 6.1 us.
 constexpr int kOwnRows = 64;
-constexpr size_t kPlaceLds = 48 * 1024;  // of a placing block, beside its 8 KB of sums
 constexpr int kScanExperts = 32;
 constexpr int kScanKept = 8;  // rows of a run: all of them up to 512 chunks
 
@@ -529,15 +536,16 @@ __global__ __launch_bounds__(kRouteThreads) void route_scan_kernel(RouteArgs a) 
 // rows from the rows themselves.
 __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs a) {
   __shared__ int total[1024], before[1024];
-  extern __shared__ uint32_t lds[];  // [C / 32][local] bits (C is at least 64: an even number of words); [2 C K] pairs
+  extern __shared__ uint32_t lds[];  // [C / 32, rounded up][local] bits; [2 C K] pairs
   uint32_t* bits = lds;
-  uint32_t* sorted = a.sorted ? lds + a.C / 32 * a.local : nullptr;
+  const int words = bit_words(a.C, a.local);
+  uint32_t* sorted = a.sorted ? lds + words : nullptr;
   const int tid = threadIdx.x, c = blockIdx.x, E8 = (a.E + 7) & ~7;
   const int64_t i0 = (int64_t)c * a.C * a.K;
   const int n = (int)(min((int64_t)(c + 1) * a.C, (int64_t)a.T) * a.K - i0);
   const int e0 = tid < n ? a.idx[i0 + tid] : -1;  // on its way meanwhile
   const float w0 = tid < n ? a.w[i0 + tid] : 0.0f;
-  for (int i = tid; i < a.C / 32 * a.local; i += kRouteThreads) bits[i] = 0;
+  for (int i = tid; i < words; i += kRouteThreads) bits[i] = 0;
   if (tid < a.E) {
     int sum = 0, low = 0;
     if (a.prefix) {
@@ -1080,7 +1088,7 @@ lrmoe_status launch_route(const lrmoe_router* r, const void* logits, const uint8
   const int C = route_chunk(r), rows = (int)ceil_div(r->T, C);
   const size_t E8 = align_up(r->E, 8);
   int* prefix = rows > kOwnRows ? (int*)((char*)ws + align_up((size_t)rows * E8 * 2, 256)) : nullptr;
-  const size_t bits = (size_t)C / 8 * r->local, cnt = (size_t)r->E * 4, pairs = (size_t)C * r->K * 8;
+  const size_t bits = 4 * (size_t)bit_words(C, r->local), cnt = (size_t)r->E * 4, pairs = (size_t)C * r->K * 8;
   // a chunk's pairs are sorted where they fit beside its bits; without tokens there are no counts to sort by
   const int sorted = rows > 0 && bits + pairs <= kPlaceLds;
   const RouteArgs a{r->T, r->E, r->K, C, rows, r->first, r->local, r->renorm, sorted, r->scale, logits, mask,

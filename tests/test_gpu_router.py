@@ -120,6 +120,23 @@ def test_route(name):
         assert torch.equal(o[k], again[k]), k
 
 
+@pytest.mark.parametrize("T,E,K,first,local,dt", [
+    (32769, 9, 3, 2, 5, "bf16"), (33000, 9, 3, 0, 9, "f32"), (70001, 6, 2, 1, 1, "f32"), (20000, 330, 2, 5, 33, "bf16"),
+    (140001, 3, 1, 0, 3, "f32"), (600007, 2, 1, 1, 1, "bf16")])
+def test_route_chunk_sizes(T, E, K, first, local, dt):
+    """Lengths whose chunks are no power of two (72 to 1024 tokens), with last ones that are nearly empty."""
+    rng = np.random.default_rng(T)
+    x = torch.from_numpy((rng.standard_normal((T, E)) * 2).astype(np.float32))
+    x = (x.bfloat16() if dt == "bf16" else x).to(DEV)
+    mask = torch.from_numpy(rng.random(T) >= 0.2).to(DEV)
+    r = lr.Router(T=T, E=E, K=K, dtype=lr.BF16 if dt == "bf16" else lr.F32, first=first, local=local, renorm=True,
+                  device=DEV)
+    log(f"route {T} x {E}")
+    o = lr.route(r, x, mask=mask, out=_outs(r))
+    torch.cuda.synchronize()
+    _check_route(r, o, ro.route(_host(x), K, mask.cpu().numpy(), first, local, True, 1.0))
+
+
 def test_route_no_tokens():
     r = lr.Router(T=0, E=9, K=2, first=3, local=4, device=DEV)
     log("route without tokens")
