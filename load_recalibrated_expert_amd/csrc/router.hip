@@ -727,7 +727,12 @@ __global__ __launch_bounds__(kBalThreads) void balance_tile_kernel(int T, int E,
   if (threadIdx.x == 0) ws.live[b] = live_n;
 }
 
-constexpr int kJoinThreads = 1024, kJoinWaves = kJoinThreads / kWave;
+constexpr int kJoinWaves = 16, kJoinWavesMany = 4;  // of a joining block
+constexpr int kLossThreads = 1024;
+// Joining blocks up to which the last one sums the loss. Their releases follow one another at some 30 ns
+// each; above, a launch of its own does it. 131072 x 128: 32 sequences (64 blocks) 28.8 us so and
+// 30.2 us with the launch, 64 sequences 29.7 and 28.7, 1024 sequences 79 and 35, 16384 994 and 240.
+constexpr int64_t kJoinLast = 64;
 
 // Sum over the wavefront, the same bits in every lane.
 template <int S = 1>
@@ -737,19 +742,25 @@ __device__ __forceinline__ double lanes_sum(double v) {
   else return v;
 }
 
-// Grid (sequence, 64 experts): the sequence's tiles joined, every 16th by one wavefront and those over
-// the wavefronts, always in the same order. The block that finishes last sums the loss; it reads
+// What of its loss a sequence of m live tokens has beside its own sums, with `alive` sequences that have any.
+__device__ __forceinline__ double loss_factor(float coef, int E, int K, int alive, double m) {
+  return m > 0 ? (double)coef * E / ((double)alive * K * m * m) : 0.0;
+}
+
+// Grid (sequence, 64 experts): the sequence's tiles joined, every WAVES-th by one wavefront and those over
+// the wavefronts, always in the same order. LAST: the block that finishes last sums the loss; it reads
 // what the others wrote behind their release, in a fixed order, so the result does not depend on
 // which block it is. 8.4 us for 512 tiles of 128 experts, 2.5 of them the last block's part, most
 // of the rest latency: 16 experts to a block took 7.9 us there, but 9.1 instead of 7.0 us for 37
-// sequences of 60 experts, whose releases are then four times as many.
-__global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(int T, int E, int K, int n_seq, int log_tile, float coef,
-                                                                    const int64_t* __restrict__ off, BalanceWs ws,
-                                                                    int32_t* __restrict__ counts,
+// sequences of 60 experts, whose releases are then four times as many. Else balance_loss_kernel follows.
+template <int WAVES, bool LAST>
+__global__ __launch_bounds__(WAVES* kWave) void balance_join_kernel(int T, int E, int K, int n_seq, int log_tile,
+                                                                    float coef, const int64_t* __restrict__ off,
+                                                                    BalanceWs ws, int32_t* __restrict__ counts,
                                                                     float* __restrict__ psum, float* __restrict__ norm,
                                                                     float* __restrict__ loss) {
-  __shared__ double sum_of[kJoinWaves][kWave];
-  __shared__ int n_of[kJoinWaves][kWave], live_of;
+  __shared__ double sum_of[WAVES][kWave];
+  __shared__ int n_of[WAVES][kWave], live_of;
   const int s = blockIdx.x, part = blockIdx.y, parts = gridDim.y;
   const int wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1);
   const int e = part * kJoinExperts + lane;
@@ -761,14 +772,14 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(int T, int E
   int n = 0;
   if (e < E) {
 #pragma unroll 8
-    for (int i = wave; i < tiles; i += kJoinWaves) {
+    for (int i = wave; i < tiles; i += WAVES) {
       a += (double)ws.psum[(b0 + i) * E + e];
       n += ws.count[(b0 + i) * E + e];
     }
   }
   sum_of[wave][lane] = a;
   n_of[wave][lane] = n;
-  if (part == 0 && wave == kJoinWaves - 1) {
+  if (part == 0 && wave == WAVES - 1) {
     int live = 0;
     for (int i = lane; i < tiles; i += kWave) live += ws.live[b0 + i];
     live = group_reduce<kWave>(live, [](int p, int q) { return p + q; });
@@ -780,7 +791,7 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(int T, int E
   if (e < E) {
     a = 0.0;
     n = 0;
-    for (int q = 0; q < kJoinWaves; ++q) {
+    for (int q = 0; q < WAVES; ++q) {
       a += sum_of[q][lane];
       n += n_of[q][lane];
     }
@@ -789,6 +800,13 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(int T, int E
     dot = a * n;
   }
   dot = lanes_sum(dot);
+  if (!LAST) {
+    if (lane == 0) {
+      ws.dot[(int64_t)s * parts + part] = dot;
+      if (part == 0) ws.n[s] = live_of;
+    }
+    return;
+  }
   uint32_t before = 0;
   if (lane == 0) {
     __hip_atomic_store(&ws.dot[(int64_t)s * parts + part], dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -804,7 +822,7 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(int T, int E
   double sum = 0.0;
   for (int i = lane; i < n_seq; i += kWave) {
     const double m = __hip_atomic_load(&ws.n[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    const double f = m > 0 ? (double)coef * E / ((double)alive * K * m * m) : 0.0;
+    const double f = loss_factor(coef, E, K, alive, m);
     norm[i] = (float)f;
     double d = 0.0;
     for (int q = 0; q < parts; ++q)
@@ -813,6 +831,41 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(int T, int E
   }
   sum = lanes_sum(sum);
   if (lane == 0) loss[0] = (float)sum;
+}
+
+// One block: every sequence's factor, and the loss.
+__global__ __launch_bounds__(kLossThreads) void balance_loss_kernel(int E, int K, int n_seq, float coef, BalanceWs ws,
+                                                                    float* __restrict__ norm,
+                                                                    float* __restrict__ loss) {
+  constexpr int kWaves = kLossThreads / kWave;
+  __shared__ int alive_of[kWaves];
+  __shared__ double sum_of[kWaves];
+  const int wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1), parts = (E + kJoinExperts - 1) / kJoinExperts;
+  int alive = 0;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < n_seq; i += kLossThreads) alive += ws.n[i] > 0 ? 1 : 0;
+  alive = group_reduce<kWave>(alive, [](int p, int q) { return p + q; });
+  if (lane == 0) alive_of[wave] = alive;
+  __syncthreads();
+  alive = 0;
+#pragma unroll
+  for (int q = 0; q < kWaves; ++q) alive += alive_of[q];
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < n_seq; i += kLossThreads) {
+    const double f = loss_factor(coef, E, K, alive, ws.n[i]);
+    norm[i] = (float)f;
+    double d = 0.0;
+    for (int q = 0; q < parts; ++q) d += ws.dot[(int64_t)i * parts + q];
+    sum += f * d;
+  }
+  sum = lanes_sum(sum);
+  if (lane == 0) sum_of[wave] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    sum = 0.0;
+    for (int q = 0; q < kWaves; ++q) sum += sum_of[q];
+    loss[0] = (float)sum;
+  }
 }
 
 // ---------------------------------------------------------------- gradient of the logits
@@ -1130,8 +1183,15 @@ lrmoe_status launch_balance_loss(const lrmoe_router* r, const void* logits, cons
                                                                     idx, seq_off_d, b);
       }) != LRMOE_OK)
     return LRMOE_ERR_HIP;
-  balance_join_kernel<<<dim3((unsigned)n_seq, (unsigned)ceil_div(r->E, kJoinExperts)), kJoinThreads, 0, s>>>(
+  const dim3 g((unsigned)n_seq, (unsigned)ceil_div(r->E, kJoinExperts));
+  if ((int64_t)g.x * g.y <= kJoinLast) {
+    balance_join_kernel<kJoinWaves, true><<<g, kJoinWaves * kWave, 0, s>>>(r->T, r->E, r->K, n_seq, log_tile, coef,
+                                                                           seq_off_d, b, counts, psum, norm, loss);
+    return launch_status();
+  }
+  balance_join_kernel<kJoinWavesMany, false><<<g, kJoinWavesMany * kWave, 0, s>>>(
       r->T, r->E, r->K, n_seq, log_tile, coef, seq_off_d, b, counts, psum, norm, loss);
+  balance_loss_kernel<<<1, kLossThreads, 0, s>>>(r->E, r->K, n_seq, coef, b, norm, loss);
   return launch_status();
 }
 

@@ -463,3 +463,31 @@ def test_workspace_freed_while_a_side_stream_uses_it():
     for name in want:
         a, b = (o[name][:pairs] if name in ("tok", "slot", "alpha") else o[name] for o in (got, want))
         assert torch.equal(a, b), name
+
+
+@pytest.mark.parametrize("E,S,masked", [(9, 64, 0.2), (9, 65, 0.2), (130, 22, 0.0), (130, 700, 0.3), (64, 3000, 0.9),
+                                        (20, 100, 1.0)])
+def test_balance_of_many_sequences(E, S, masked):
+    """On both sides of the number of sequences whose loss has a launch of its own, empty and long ones
+    among them."""
+    rng = np.random.default_rng(E + S)
+    T, K = 6001, 3
+    x = torch.from_numpy((rng.standard_normal((T, E)) * 2).astype(np.float32)).to(DEV)
+    mask = torch.from_numpy(rng.random(T) >= masked).to(DEV)
+    off = np.sort(np.concatenate([[0], rng.integers(0, T // 3, size=S - 1), [T]])).tolist()
+    r = lr.Router(T=T, E=E, K=K, device=DEV)
+    idx = lr.route(r, x, mask=mask)["idx"]
+    log(f"{S} sequences of {E} experts")
+    b = lr.balance_loss(r, x, idx, coef=0.3, mask=mask, seq_off=off)
+    again = lr.balance_loss(r, x, idx, coef=0.3, mask=mask, seq_off=off)
+    assert all(torch.equal(b[k], again[k]) for k in b)
+    M = mask.cpu().numpy()
+    ref = ro.balance(_host(x), idx.cpu().numpy(), float(np.float32(0.3)), M, off)
+    assert np.array_equal(b["counts"].cpu().numpy(), ref["counts"])
+    assert np.all(np.abs(as_f64(b["psum"]) - ref["psum"]) <= ref["psum_err"])
+    assert np.all(np.abs(as_f64(b["norm"]) - ref["norm"]) <= 2 * ro.U * ref["norm"])
+    assert abs(float(b["loss"]) - ref["loss"]) <= ref["loss_err"] + 1e-37
+    dx, err = ro.route_bwd(_host(x), idx.cpu().numpy(), counts=ref["counts"], norm=as_f64(b["norm"]), mask=M,
+                           seq_off=off)
+    got = lr.route_bwd(r, x, idx, balance=b, mask=mask, seq_off=off)
+    assert np.all(np.abs(as_f64(got) - dx) <= err)
