@@ -880,14 +880,13 @@ __device__ __forceinline__ void wave_sync() {
 
 // The K slots of a token are worked on in K lanes of its group, whose results reach the lanes that
 // hold their experts through a row of LDS.
-template <class Lay>
+template <class Lay, int S>  // S: slots of a lane, k = lane, lane + L, ...
 __global__ __launch_bounds__(kGradThreads) void route_bwd_kernel(
     int T, int E, int K, int renorm, float scale, const void* __restrict__ logits, const uint8_t* __restrict__ mask,
     const int32_t* __restrict__ idx, const float* __restrict__ dalpha, const int32_t* __restrict__ pmap,
     int64_t n_pairs, const int64_t* __restrict__ off, int n_seq, const int32_t* __restrict__ counts,
     const float* __restrict__ norm, const float* __restrict__ gloss, void* __restrict__ dlogits) {
   constexpr int L = Lay::L, V = Lay::V;
-  constexpr int S = (32 + L - 1) / L;  // slots of a lane: k = lane, lane + L
   __shared__ float rows[kGradThreads / L][L * V];
   const int lane = threadIdx.x & (L - 1);
   const int64_t t = (int64_t)blockIdx.x * (kGradThreads / L) + threadIdx.x / L;
@@ -1068,10 +1067,15 @@ __global__ __launch_bounds__(kAlphaThreads) void alpha_grad_kernel(int T, int K,
 
 // Calls f with the layout for E experts and the logits' type: sixteen lanes to a token up to 512
 // experts, so that a wavefront takes four tokens and reduces them together, with as few values to a
-// lane as hold E.
+// lane as hold E. `narrow`: four or eight lanes for up to 64 experts, for callers whose blocks have tokens
+// enough to use them all (gradient of 200000 x 16 19.5 -> 7.9 us, of 500000 x 64 bf16 44.9 -> 35.7 us;
+// balance loss of 1000000 x 8 60.2 -> 29.6 us; with 128 experts eight lanes gain nothing).
 template <bool BF16, class F>
-void by_experts(int E, F&& f) {
-  if (E <= 64) f(Layout<16, 4, BF16>());
+void by_experts(int E, bool narrow, F&& f) {
+  if (narrow && E <= 16) f(Layout<4, 4, BF16>());
+  else if (narrow && E <= 32) f(Layout<8, 4, BF16>());
+  else if (narrow && E <= 64) f(Layout<8, 8, BF16>());
+  else if (E <= 64) f(Layout<16, 4, BF16>());
   else if (E <= 128) f(Layout<16, 8, BF16>());
   else if (E <= 192) f(Layout<16, 12, BF16>());
   else if (E <= 256) f(Layout<16, 16, BF16>());
@@ -1083,7 +1087,8 @@ void by_experts(int E, F&& f) {
 // The same for lists of N = 8, 16 or 32 slots: whole lists to a lane, and few lanes to a token. Where one
 // pass takes all tokens anyway, more lanes shorten its chain of instructions (16 tokens of 128
 // experts: 6.1 us with four lanes to a token, 5.6 us with sixteen; one token of 200: 7.8 and 5.9 us;
-// 120 tokens of 128, two passes: 7.6 and 9.4 us).
+// 120 tokens of 128, two passes: 7.6 and 9.4 us). Two lanes for up to 16 experts: 1000000 x 8 60 us with
+// four, 44 us with two.
 template <bool BF16, class F>
 void by_lists(int T, int E, int K, F&& f) {
   using std::integral_constant;
@@ -1093,7 +1098,8 @@ void by_lists(int T, int E, int K, F&& f) {
       if (E <= 64) f(Layout<8, 8, BF16>(), n);
       else if (E <= 128) f(Layout<16, 8, BF16>(), n);
       else f(Layout<16, 16, BF16>(), n);
-    } else if (E <= 32) f(Layout<4, 8, BF16>(), n);
+    } else if (E <= 16) f(Layout<2, 8, BF16>(), n);
+    else if (E <= 32) f(Layout<4, 8, BF16>(), n);
     else if (E <= 64) f(Layout<4, 16, BF16>(), n);
     else if (E <= 128) f(Layout<4, 32, BF16>(), n);
     else if (E <= 192) f(Layout<8, 24, BF16>(), n);
@@ -1117,8 +1123,8 @@ void by_lists(int T, int E, int K, F&& f) {
   }
 }
 template <class F>
-lrmoe_status by_layout(const lrmoe_router* r, F&& f) {
-  r->dtype == LRMOE_BF16 ? by_experts<true>(r->E, f) : by_experts<false>(r->E, f);
+lrmoe_status by_layout(const lrmoe_router* r, bool narrow, F&& f) {
+  r->dtype == LRMOE_BF16 ? by_experts<true>(r->E, narrow, f) : by_experts<false>(r->E, narrow, f);
   return launch_status();
 }
 template <class F>
@@ -1172,13 +1178,14 @@ lrmoe_status launch_balance_loss(const lrmoe_router* r, const void* logits, cons
   BalanceWs b;
   balance_layout(r, n_seq, (char*)ws, &b);
   const int log_tile = balance_log_tile(r);
-  if (by_layout(r, [&](auto lay) {
+  // a tile of 64 tokens fills its block with sixteen lanes to each (32768 x 60: 13.7 us, with eight 15.7 us)
+  if (by_layout(r, log_tile > 6, [&](auto lay) {
         using Lay = decltype(lay);
         const unsigned g = (unsigned)balance_tiles(r, n_seq);
         if (log_tile > 6)
           balance_tile_kernel<Lay, true><<<g, kBalThreads, 0, s>>>(r->T, r->E, r->K, n_seq, log_tile, logits, mask, idx,
                                                                    seq_off_d, b);
-        else
+        else if constexpr (Lay::L >= 16)
           balance_tile_kernel<Lay, false><<<g, kBalThreads, 0, s>>>(r->T, r->E, r->K, n_seq, log_tile, logits, mask,
                                                                     idx, seq_off_d, b);
       }) != LRMOE_OK)
@@ -1199,11 +1206,17 @@ lrmoe_status launch_route_bwd(const lrmoe_router* r, const void* logits, const u
                               const float* dalpha, const int32_t* pmap, int64_t n_pairs, const int64_t* seq_off_d,
                               int32_t n_seq, const int32_t* counts, const float* norm, const float* gloss,
                               void* dlogits, hipStream_t s) {
-  return by_layout(r, [&](auto lay) {
+  return by_layout(r, true, [&](auto lay) {
     using Lay = decltype(lay);
-    route_bwd_kernel<Lay><<<(unsigned)ceil_div(r->T, kGradThreads / Lay::L), kGradThreads, 0, s>>>(
-        r->T, r->E, r->K, r->renorm, r->scale, logits, mask, idx, dalpha, pmap, n_pairs, seq_off_d, n_seq, counts, norm,
-        gloss, dlogits);
+    constexpr int L = Lay::L, most = std::min(32, L * Lay::V);  // slots: no more than experts
+    auto run = [&](auto slots) {
+      route_bwd_kernel<Lay, decltype(slots)::value>
+          <<<(unsigned)ceil_div(r->T, kGradThreads / L), kGradThreads, 0, s>>>(
+              r->T, r->E, r->K, r->renorm, r->scale, logits, mask, idx, dalpha, pmap, n_pairs, seq_off_d, n_seq, counts,
+              norm, gloss, dlogits);
+    };
+    if (L >= most || r->K <= L) run(std::integral_constant<int, 1>());
+    else run(std::integral_constant<int, (most + L - 1) / L>());
   });
 }
 

@@ -411,10 +411,11 @@ def test_wide_local_share_with_many_slots():
     assert torch.equal(o["pmap"].reshape(-1).long(), back)
 
 
+@pytest.mark.parametrize("E", [6, 24, 60, 100])
 @pytest.mark.parametrize("off", [None, [0, 30000, 30001, 100000]])
-def test_balance_of_long_sequences(off):
+def test_balance_of_long_sequences(off, E):
     """Tiles of more than one pass: counts and sums against torch in fp64."""
-    T, E, K = 100003, 24, 3
+    T, K = 100003, 3
     gen = torch.Generator(device=DEV).manual_seed(3)
     x = torch.randn(T, E, generator=gen, device=DEV)
     mask = (torch.rand(T, generator=gen, device=DEV) < 0.7).to(torch.uint8)
@@ -432,7 +433,8 @@ def test_balance_of_long_sequences(off):
         want = p[lo:hi][rows].sum(0)
         count = torch.bincount(idx[lo:hi][rows].reshape(-1).long(), minlength=E)
         assert torch.equal(b["counts"][s].long(), count)
-        # each p to 60 x 2^-24 (|x - max| is under 12), 128 sums of a lane and 80 over lanes in fp32
+        # each p to 60 x 2^-24 (|x - max| is under 12), 128 sums of a lane and 80 over lanes in fp32,
+        # at the most: fewer of a lane with four or eight lanes to a token
         assert torch.all((b["psum"][s].double() - want).abs() <= want * 270 * 2.0 ** -24)
         n = int(rows.sum())
         if n:
