@@ -1000,6 +1000,8 @@ __global__ __launch_bounds__(kGradThreads) void route_bwd_kernel(
 
 constexpr int kAlphaThreads = 256;
 constexpr int kAlphaRows = 8;  // pairs whose rows a wavefront reads at once
+// Tokens up to which a block shares one: any, or those of rows of 4 KB and more (a word to a thread).
+constexpr int kAlphaSplit = 1024, kAlphaSplitWide = 8192;
 
 // Products of 16 bytes of two rows, added to s in fp64 (as the score's norms; products of bf16 values are
 // exact in f32).
@@ -1021,8 +1023,11 @@ __device__ __forceinline__ double dot16(uint4 g, uint4 y, double s) {
 // One wavefront per token: its gradient row is read once against the rows of up to eight of its
 // pairs, whose loads are all in flight before the first product (one row after the other: 256 us for
 // 32768 tokens, top-8, 2048 bf16; so: 190 us, 6.4 TB/s, with one or two column blocks at a time;
-// four: 207 us). Bound by HBM on the [N x D] rows.
-template <bool BF16>
+// four: 207 us). Bound by HBM on the [N x D] rows. SPLIT: the block's four wavefronts share a token's
+// columns, which fills the compute units with few tokens and shortens their chains: 8 tokens of 4096 f32
+// 18.0 -> 7.6 us, 1024 of 2048 f32 15.6 -> 12.7 us, 8192 of 2048 bf16 53 -> 50 us. With many tokens the
+// wavefronts' joins cost more than that: 32768 of 2048 bf16 188 -> 200 us, 65536 of 512 100 -> 211 us.
+template <bool BF16, bool SPLIT>
 __global__ __launch_bounds__(kAlphaThreads) void alpha_grad_kernel(int T, int K, int D, int64_t N,
                                                                    const uint4* __restrict__ G,
                                                                    const uint4* __restrict__ Y,
@@ -1030,8 +1035,10 @@ __global__ __launch_bounds__(kAlphaThreads) void alpha_grad_kernel(int T, int K,
                                                                    const int32_t* __restrict__ pmap,
                                                                    const uint8_t* __restrict__ keep,
                                                                    float* __restrict__ dalpha) {
-  const int lane = threadIdx.x & (kWave - 1);
-  const int64_t t = (int64_t)blockIdx.x * (kAlphaThreads / kWave) + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  constexpr int kWaves = kAlphaThreads / kWave;
+  __shared__ double part[SPLIT ? kWaves : 1][kAlphaRows];
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int64_t t = SPLIT ? blockIdx.x : (int64_t)blockIdx.x * kWaves + wave;
   if (t >= T) return;
   const int words = BF16 ? D / 8 : D / 4;
   for (int k0 = 0; k0 < K; k0 += kAlphaRows) {
@@ -1044,7 +1051,7 @@ __global__ __launch_bounds__(kAlphaThreads) void alpha_grad_kernel(int T, int K,
 #pragma unroll
     for (int k = 0; k < kAlphaRows; ++k) row[k] = __builtin_amdgcn_readlane(read ? j : -1, k);
     double s[kAlphaRows] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int c = lane; c < words; c += kWave) {
+    for (int c = SPLIT ? threadIdx.x : lane; c < words; c += SPLIT ? kAlphaThreads : kWave) {
       uint4 y[kAlphaRows];
       const uint4 g = G[t * words + c];
 #pragma unroll
@@ -1060,6 +1067,16 @@ __global__ __launch_bounds__(kAlphaThreads) void alpha_grad_kernel(int T, int K,
       if (row[k] < 0) continue;
       const double v = lanes_sum(s[k]);
       mine = lane == k ? v : mine;
+    }
+    if (SPLIT) {
+      if (k0 > 0) __syncthreads();  // the last eight's sums are read
+      if (lane < kAlphaRows) part[wave][lane] = mine;
+      __syncthreads();
+      if (wave != 0) continue;
+      mine = 0.0;
+      if (lane < kAlphaRows)
+#pragma unroll
+        for (int q = 0; q < kWaves; ++q) mine += part[q][lane];
     }
     if (j >= 0) dalpha[j] = read && a != 0.0f ? (float)(mine / (double)a) : 0.0f;
   }
@@ -1222,13 +1239,15 @@ lrmoe_status launch_route_bwd(const lrmoe_router* r, const void* logits, const u
 
 lrmoe_status launch_alpha_grad(const lrmoe_problem* p, const void* G, const void* Y, const float* alpha,
                                const int32_t* pmap, const uint8_t* keep, float* dalpha, hipStream_t s) {
-  const unsigned g = (unsigned)ceil_div(p->T, kAlphaThreads / kWave);
-  if (p->dtype == LRMOE_BF16)
-    alpha_grad_kernel<true><<<g, kAlphaThreads, 0, s>>>(p->T, p->K, p->D, p->N, (const uint4*)G, (const uint4*)Y,
-                                                        alpha, pmap, keep, dalpha);
-  else
-    alpha_grad_kernel<false><<<g, kAlphaThreads, 0, s>>>(p->T, p->K, p->D, p->N, (const uint4*)G, (const uint4*)Y,
-                                                         alpha, pmap, keep, dalpha);
+  const int64_t row = (int64_t)p->D * (p->dtype == LRMOE_BF16 ? 2 : 4);
+  const bool split = p->T <= (row >= 16 * kAlphaThreads ? kAlphaSplitWide : kAlphaSplit);
+  const unsigned g = (unsigned)(split ? p->T : ceil_div(p->T, kAlphaThreads / kWave));
+  auto run = [&](auto kernel) {
+    kernel<<<g, kAlphaThreads, 0, s>>>(p->T, p->K, p->D, p->N, (const uint4*)G, (const uint4*)Y, alpha, pmap, keep,
+                                       dalpha);
+  };
+  if (p->dtype == LRMOE_BF16) split ? run(alpha_grad_kernel<true, true>) : run(alpha_grad_kernel<true, false>);
+  else split ? run(alpha_grad_kernel<false, true>) : run(alpha_grad_kernel<false, false>);
   return launch_status();
 }
 

@@ -283,6 +283,14 @@ def test_alpha_grad(T, K, D, dt, keep):
     assert torch.all(out[N:] == -7)
 
 
+@pytest.mark.parametrize("T,K,D,dt", [(1024, 2, 24, "f32"), (1025, 2, 24, "f32"), (1030, 9, 1024, "f32"),
+                                      (1030, 17, 2056, "bf16"), (8192, 1, 2048, "bf16"), (8193, 1, 2048, "bf16")])
+def test_alpha_grad_of_few_and_many_tokens(T, K, D, dt):
+    """On both sides of the sizes up to which a block shares a token's columns, more than eight slots among
+    them."""
+    test_alpha_grad(T, K, D, dt, 0.7)
+
+
 def test_alpha_grad_leaves_pairs_without_a_position():
     p = lr.Problem(E=1, T=2, K=2, D=8, F=8, swiglu=True, dtype=lr.F32, seg_off=[0, 4], quota=[4], device=DEV)
     one = torch.ones(4, 8, device=DEV)
