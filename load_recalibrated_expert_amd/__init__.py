@@ -426,7 +426,8 @@ def backward(p: Problem, *, G, Phi, alpha, tok, slot, W2, X=None, H=None, W1=Non
 class Router:
     """The router of one layer: T tokens, E experts of the whole layer, K slots per token, and the
     experts [first, first + local) that this GPU's pair lists cover (local=None: all from first).
-    ``dtype``: F32 or BF16 logits. ``renorm``: a token's weights sum to ``scale``."""
+    ``dtype``: F32 or BF16 logits. ``renorm``: a token's weights sum to ``scale``. ``device``:
+    the one that is current when the calls are made."""
 
     def __init__(self, *, T, E, K, dtype=F32, first=0, local=None, renorm=False, scale=1.0, device="cuda"):
         self.T, self.E, self.K, self.dtype = int(T), int(E), int(K), int(dtype)
@@ -467,6 +468,8 @@ class Router:
                 self._grown.append(self._ws)
             self._ws, self._ws_bytes = _empty((n,), torch.uint8, self.device, stream), n
             self._streams.clear()
+        if self._ws.get_device() != torch._C._cuda_getDevice():  # the outputs allocated for it are there too
+            raise ValueError(f"the router's workspace is on {self._ws.device}, which is not the current device")
         if raw not in self._streams:
             _used_on(raw, stream, self._streams, (self._ws,))
         return self._ws, self._ws_bytes, raw

@@ -1,0 +1,100 @@
+"""The binding of the router's operators and of AdamW without a GPU: what has to be refused before the
+library is called. Tensors, streams and the library are stand-ins, so that a call that is wrongly let
+through is seen and not run."""
+import types
+
+import pytest
+import torch
+
+import load_recalibrated_expert_amd as lr
+
+
+class Tensor:
+    """What the binding asks of a device tensor."""
+
+    def __init__(self, shape, dtype, dev, at=1 << 20):
+        self.shape, self.dtype, self.at = torch.Size(shape), dtype, at
+        self.device = torch.device("cpu" if dev < 0 else f"cuda:{dev}")
+
+    def get_device(self):
+        return -1 if self.device.type == "cpu" else self.device.index
+
+    def numel(self):
+        return self.shape.numel()
+
+    def element_size(self):
+        return torch.empty(0, dtype=self.dtype).element_size()
+
+    def dim(self):
+        return len(self.shape)
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return self.at
+
+    def record_stream(self, stream):
+        pass
+
+
+class Library:
+    """Counts the calls that would launch; the host-only ones are the real library's."""
+
+    def __init__(self, real):
+        self.real, self.launched = real, []
+
+    def __getattr__(self, name):
+        if name.endswith("_size") or name in ("lrmoe_adamw_step_scalars", "lrmoe_adamw_plan"):
+            return getattr(self.real, name)
+        return lambda *a: self.launched.append(name) or 0
+
+
+@pytest.fixture
+def gpu(monkeypatch):
+    """A current device (gpu.here) with stand-ins behind the binding; gpu.lib.launched lists the launches."""
+    g = types.SimpleNamespace(here=0, lib=Library(lr.library()))
+    monkeypatch.setattr(lr, "library", lambda: g.lib)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: g.here, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 7000 + d, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: None)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+
+    def empty(shape, dtype, device, stream):
+        d = torch.device(device)
+        return Tensor(shape, dtype, -1 if d.type == "cpu" else g.here if d.index is None else d.index)
+
+    monkeypatch.setattr(lr, "_empty", empty)
+    return g
+
+
+def _calls(r, dev=0):
+    x, idx = Tensor((r.T, r.E), torch.float32, dev), Tensor((r.T, r.K), torch.int32, dev)
+    bal = {"counts": Tensor((1, r.E), torch.int32, dev), "norm": Tensor((1,), torch.float32, dev)}
+    return (lambda **kw: lr.route(r, x, **kw), lambda **kw: lr.balance_loss(r, x, idx, **kw),
+            lambda **kw: lr.route_bwd(r, x, idx, balance=bal, **kw))
+
+
+@pytest.mark.parametrize("device", ["cuda:1", "cpu"])
+def test_a_router_of_another_device_is_refused(gpu, device):
+    """Its workspace and the outputs it allocates are not on the device that the kernels run on."""
+    for call in _calls(lr.Router(T=8, E=4, K=2, device=device)):
+        with pytest.raises(ValueError):
+            call()
+    assert gpu.lib.launched == []
+    for call in _calls(lr.Router(T=8, E=4, K=2, device="cuda:0")):
+        call()
+    assert gpu.lib.launched == ["lrmoe_route", "lrmoe_balance_loss", "lrmoe_route_bwd"]
+
+
+def test_a_router_stays_on_the_device_of_its_workspace(gpu):
+    """device="cuda" is the current one: a workspace of device 0 is not used by a call on device 1."""
+    r = lr.Router(T=8, E=4, K=2, device="cuda")
+    route, balance, _ = _calls(r, 0)
+    route()
+    gpu.here = 1
+    route, balance, _ = _calls(r, 1)
+    for call in (route, balance):
+        with pytest.raises(ValueError):
+            call()
+    assert gpu.lib.launched == ["lrmoe_route"]
