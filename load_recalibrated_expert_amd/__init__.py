@@ -45,10 +45,13 @@ def _ptr(t):
 
 
 def _stream(stream=None):
+    here = torch._C._cuda_getDevice()
     if stream is not None:
+        if stream.device_index != here:
+            raise ValueError(f"stream: of cuda:{stream.device_index}, which is not the current device")
         return stream.cuda_stream
     # the handle alone: a torch.cuda.Stream object costs 3 us of host time per call
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return torch._C._cuda_getCurrentRawStream(here)
 
 
 def _event(ev, stream=None):

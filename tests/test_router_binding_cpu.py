@@ -98,3 +98,26 @@ def test_a_router_stays_on_the_device_of_its_workspace(gpu):
         with pytest.raises(ValueError):
             call()
     assert gpu.lib.launched == ["lrmoe_route"]
+
+
+class Stream:
+    def __init__(self, dev, raw):
+        self.device_index, self.cuda_stream = dev, raw
+        self.device = torch.device("cuda", dev)
+
+
+def test_a_stream_of_another_device_is_refused(gpu):
+    """A kernel launched there would run on that device, with this one's buffers."""
+    p = types.SimpleNamespace(T=8, K=2, D=8, N=9, torch_dtype=torch.bfloat16, device="cuda:0",
+                              c=lr._lib.CProblem())
+    rows, alpha = Tensor((9, 8), torch.bfloat16, 0), Tensor((9,), torch.float32, 0)
+    opt = lr.AdamW([torch.zeros(64)], grads=[torch.zeros(64)])
+    opt._check_place = lambda: None
+    opt.m[0] = opt.v[0] = Tensor((64,), torch.float32, 0)
+    calls = _calls(lr.Router(T=8, E=4, K=2, device="cuda:0")) + (
+        lambda **kw: lr.alpha_grad(p, rows, rows, alpha, Tensor((8, 2), torch.int32, 0), **kw),
+        lambda **kw: opt.step(**kw))
+    for call in calls:
+        with pytest.raises(ValueError):
+            call(stream=Stream(1, 7001))
+    assert gpu.lib.launched == [] and opt.t == 0
