@@ -478,6 +478,16 @@ class Router:
         return self._ws, self._ws_bytes, raw
 
 
+def _capturing(stream):
+    """Whether the current stream, or `stream`, records into a graph."""
+    if torch.cuda.is_current_stream_capturing():
+        return True
+    if stream is None or stream.cuda_stream == _stream():
+        return False
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _empty(shape, dtype, device, stream):
     """An output of a call on `stream` (None: the current one), allocated there: memory that other
     work of the current stream gave back is not written before that work is done."""
@@ -719,7 +729,7 @@ class AdamW:
         self.c.grad_dtype = BF16 if dt == torch.bfloat16 else F32
         self.grads, self._plan = grads, None
 
-    def _plan_ptr(self):
+    def _plan_ptr(self, stream):
         """The plan in device memory for more tensors than one launch's arguments take. It is made at
         the second step with the same gradient buffers: a copy of it to the device would cost a
         program that binds new ones at every step more than the launches it saves."""
@@ -727,7 +737,7 @@ class AdamW:
             return None
         if self._plan is None:
             self._plan = False
-        elif self._plan is False and not torch.cuda.is_current_stream_capturing():
+        elif self._plan is False and not _capturing(stream):
             n, lib = ctypes.c_size_t(0), library()
             args = (self._table, len(self.w), ctypes.byref(self.c))
             _lib.check(lib.lrmoe_adamw_plan(*args, None, ctypes.byref(n)), "lrmoe_adamw_plan")
@@ -761,12 +771,12 @@ class AdamW:
         if self.grads is None:
             raise ValueError("AdamW has no gradient buffers: pass grads")
         self._check_place()
-        if torch.cuda.is_current_stream_capturing():
+        if _capturing(stream):
             raise ValueError("a graph would repeat this very step: capture step_captured")
         self.t += 1
         try:
             self._config(grad_scale)
-            plan = self._plan_ptr()
+            plan = self._plan_ptr(stream)
             _lib.check(library().lrmoe_adamw(self._table, len(self.w), ctypes.byref(self.c), plan, None,
                                              self._used_on(stream)), "lrmoe_adamw")
         except Exception:
@@ -797,8 +807,8 @@ class AdamW:
         if self._scalars is None or self.grads is None:
             raise ValueError("call advance (and bind the gradient buffers) before step_captured")
         self._check_place()
-        plan = self._plan_ptr()
-        if torch.cuda.is_current_stream_capturing():
+        plan = self._plan_ptr(stream)
+        if _capturing(stream):
             self._captured.append((self._plan, self.grads))
         _lib.check(library().lrmoe_adamw(self._table, len(self.w), ctypes.byref(self.c), plan,
                                          _ptr(self._scalars), self._used_on(stream)), "lrmoe_adamw")

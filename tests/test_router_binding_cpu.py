@@ -121,3 +121,68 @@ def test_a_stream_of_another_device_is_refused(gpu):
         with pytest.raises(ValueError):
             call(stream=Stream(1, 7001))
     assert gpu.lib.launched == [] and opt.t == 0
+
+
+@pytest.fixture
+def capture(gpu, monkeypatch):
+    """gpu with a set of streams (None: the current one) that record into a graph."""
+    gpu.capturing, at = set(), [None]
+
+    class on:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            self.before, at[0] = at[0], self.stream
+
+        def __exit__(self, *a):
+            at[0] = self.before
+
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: at[0] in gpu.capturing)
+    return gpu
+
+
+def _adamw(n=1):
+    opt = lr.AdamW([torch.zeros(64) for _ in range(n)], grads=[torch.zeros(64) for _ in range(n)])
+    opt._check_place = lambda: None
+    opt._used_on = lr._stream
+    return opt
+
+
+def test_a_step_on_a_capturing_stream_is_refused(capture):
+    """step(stream=s) while s, which is not the current stream, records a graph that would repeat this step."""
+    opt, side = _adamw(), Stream(0, 7100)
+    capture.capturing = {side}
+    with pytest.raises(ValueError):
+        opt.step(stream=side)
+    assert opt.t == 0 and capture.lib.launched == []
+    opt.step()
+    opt.step(stream=Stream(0, 7200))
+    assert opt.t == 2
+    capture.capturing = {None}
+    for s in (None, side):
+        with pytest.raises(ValueError):
+            opt.step(stream=s)
+    assert opt.t == 2
+
+
+def test_a_graph_of_a_side_stream_keeps_what_it_reads(capture):
+    """step_captured(stream=s) while s records: the gradient buffers stay with the object when others are bound."""
+    opt, side = _adamw(), Stream(0, 7100)
+    opt.advance()
+    grads = opt.grads
+    capture.capturing = {side}
+    opt.step_captured(stream=side)
+    opt.bind([torch.zeros(64)])
+    assert any(g is grads for _, g in opt._captured)
+
+
+def test_a_plan_is_not_copied_while_its_stream_records(capture):
+    """A copy to the device would be an error inside the capture, and would end it."""
+    opt, side = _adamw(49), Stream(0, 7100)
+    opt.advance()
+    opt._plan = False  # as after a first step
+    capture.capturing = {side}
+    opt.step_captured(stream=side)
+    assert opt._plan is False and capture.lib.launched == ["lrmoe_adamw"]
