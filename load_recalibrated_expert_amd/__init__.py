@@ -783,23 +783,32 @@ class AdamW:
             self.t -= 1
             raise
 
-    def advance(self, grad_scale=1.0):
+    def advance(self, grad_scale=1.0, stream=None):
         """Counts one step and copies its scalars (step, lr, weight_decay, grad_scale) to the device, on
-        the current stream. Call it before each replay of a graph that holds ``step_captured``."""
+        `stream` (None: the current one), without waiting for it. Call it before each replay of a graph
+        that holds ``step_captured``, on the stream of the replays: the copy then follows those before
+        it, which read their own step's scalars from the same place."""
+        gpu = self.w[0].is_cuda
+        if gpu and _capturing(stream):
+            raise ValueError("advance belongs before a replay, not into the graph")
         host = _lib.CAdamwScalars()
         self.t += 1
         try:
             self._config(grad_scale)
             _lib.check(library().lrmoe_adamw_step_scalars(ctypes.byref(self.c), ctypes.byref(host)),
                        "lrmoe_adamw_step_scalars")
+            values = torch.frombuffer(bytearray(host), dtype=torch.int32)
+            if self._scalars is None:
+                self._scalars = _empty((8,), torch.int32, self.w[0].device, stream)
+                self._streams.clear()
+            if gpu:
+                self._used_on(stream)
+                values = values.pin_memory()  # torch gives it out again only behind the copy
+            with torch.cuda.stream(stream):
+                self._scalars.copy_(values, non_blocking=True)
         except Exception:
             self.t -= 1
             raise
-        values = torch.frombuffer(bytearray(host), dtype=torch.int32)
-        if self._scalars is None:
-            self._scalars = torch.empty(8, dtype=torch.int32, device=self.w[0].device)
-            self._streams.clear()
-        self._scalars.copy_(values)
 
     def step_captured(self, stream=None):
         """The update with the scalars of the last ``advance``, for capture into a graph. What a graph

@@ -37,6 +37,13 @@ class Tensor:
     def record_stream(self, stream):
         pass
 
+    def copy_(self, values, non_blocking=False):
+        pass
+
+    @property
+    def is_cuda(self):
+        return self.device.type == "cuda"
+
 
 class Library:
     """Counts the calls that would launch; the host-only ones are the real library's."""
@@ -138,6 +145,7 @@ def capture(gpu, monkeypatch):
         def __exit__(self, *a):
             at[0] = self.before
 
+    gpu.current = lambda: at[0]
     monkeypatch.setattr(torch.cuda, "stream", on)
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: at[0] in gpu.capturing)
     return gpu
@@ -186,3 +194,50 @@ def test_a_plan_is_not_copied_while_its_stream_records(capture):
     capture.capturing = {side}
     opt.step_captured(stream=side)
     assert opt._plan is False and capture.lib.launched == ["lrmoe_adamw"]
+
+
+class Scalars(Tensor):
+    """AdamW's scalars on the device: the stream of every copy into them."""
+
+    def __init__(self, gpu, fails=False):
+        super().__init__((8,), torch.int32, 0)
+        self.gpu, self.fails, self.copies = gpu, fails, []
+
+    def copy_(self, values, non_blocking=False):
+        if self.fails:
+            raise RuntimeError("no copy")
+        self.copies.append(self.gpu.current())
+
+
+def _on_device(opt, scalars, monkeypatch):
+    monkeypatch.setattr(torch.Tensor, "pin_memory", lambda t: t)
+    opt.w = [Tensor((64,), torch.float32, 0)]
+    opt._scalars = scalars
+    return opt
+
+
+def test_advance_copies_on_the_stream_of_the_replays(capture, monkeypatch):
+    """Elsewhere the copy could overtake a replay that still reads the step before."""
+    opt, side = _on_device(_adamw(), Scalars(capture), monkeypatch), Stream(0, 7100)
+    opt.advance(stream=side)
+    opt.advance()
+    assert opt._scalars.copies == [side, None] and opt.t == 2
+    with pytest.raises(ValueError):
+        opt.advance(stream=Stream(1, 7001))
+    assert opt._scalars.copies == [side, None] and opt.t == 2
+
+
+def test_advance_inside_a_capture_counts_no_step(capture, monkeypatch):
+    opt, side = _on_device(_adamw(), Scalars(capture), monkeypatch), Stream(0, 7100)
+    for capturing, stream in ((None, None), (side, side), (None, side)):
+        capture.capturing = {capturing}
+        with pytest.raises(ValueError):
+            opt.advance(stream=stream)
+    assert opt.t == 0 and opt._scalars.copies == []
+
+
+def test_an_advance_whose_copy_fails_counts_no_step(capture, monkeypatch):
+    opt = _on_device(_adamw(), Scalars(capture, fails=True), monkeypatch)
+    with pytest.raises(RuntimeError):
+        opt.advance()
+    assert opt.t == 0
