@@ -16,6 +16,7 @@ raises ImportError.
 """
 from __future__ import annotations
 
+import bisect
 import ctypes
 
 import numpy as np
@@ -650,7 +651,7 @@ class AdamW:
     states ``m``, ``v`` (8 bits: e4m3 codes, v's of its square root, with ``m_scale``, ``v_scale`` per 256
     elements) start at zero unless given. ``first``: 8 bits, the counter of each tensor's first
     element for the random rounding (multiples of 256; None: one tensor behind the other).
-    ``t`` counts the steps taken. Buffers must not overlap."""
+    ``t`` counts the steps taken. Buffers must not overlap; gradients, which are only read, may share one."""
 
     def __init__(self, weights, grads=None, masters=None, m=None, v=None, m_scale=None, v_scale=None, *, lr=1e-3,
                  betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, bits=32, first=None, step=0, seed=0):
@@ -697,6 +698,7 @@ class AdamW:
                        if ts is not None for t in ts if t.numel())
         if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
             raise ValueError("AdamW's buffers overlap")
+        self._sizes, self._starts, self._ends = sizes, [a for a, _ in spans], [b for _, b in spans]
         self.c = _lib.CAdamwConfig(w_dtype=BF16 if wt == torch.bfloat16 else F32, grad_dtype=F32,
                                    master=int(masters is not None), state_bits=bits, lr=lr, beta1=betas[0],
                                    beta2=betas[1], eps=eps, weight_decay=weight_decay, grad_scale=1.0, step=1,
@@ -708,6 +710,8 @@ class AdamW:
             e.m, e.v, e.n, e.first = _ptr(self.m[i]), _ptr(self.v[i]), k, int(first[i])
             if bits == 8:
                 e.m_scale, e.v_scale = _ptr(self.m_scale[i]), _ptr(self.v_scale[i])
+        words = np.frombuffer(self._table, np.uint64).reshape(len(sizes), -1)  # the table's fields are 8 bytes each
+        self._table_grads = words[:, _lib.CAdamwTensor.grad.offset // 8]
         self._scalars = self._plan = None
         self._captured, self._streams = [], set()
         self.grads = None
@@ -719,13 +723,17 @@ class AdamW:
     def bind(self, grads):
         """Takes these tensors as the gradient buffers from now on."""
         grads = list(grads)
-        dt = grads[0].dtype if grads else None
+        dt, dev = grads[0].dtype if grads else None, self.w[0].device
         if len(grads) != len(self.w) or dt not in (torch.float32, torch.bfloat16) or any(
-                g.dtype != dt or g.numel() != w.numel() or g.device != w.device for g, w in zip(grads, self.w)):
+                g.dtype != dt or g.numel() != n or g.device != dev for g, n in zip(grads, self._sizes)):
             raise ValueError("grads: one f32 or bf16 tensor per weight, of its size, all of one type")
         ptrs = [_ptr(g) for g in grads]  # all of them first: a tensor that is refused leaves the old ones bound
-        for e, at in zip(self._table, ptrs):
-            e.grad = at
+        size = grads[0].element_size()
+        for at, n in zip(ptrs, self._sizes):
+            i = bisect.bisect_left(self._starts, at + n * size) - 1  # the last buffer that starts before its end
+            if n and i >= 0 and self._ends[i] > at:
+                raise ValueError("grads: a gradient overlaps the weights, their masters or the states")
+        self._table_grads[:] = ptrs
         self.c.grad_dtype = BF16 if dt == torch.bfloat16 else F32
         self.grads, self._plan = grads, None
 

@@ -327,3 +327,23 @@ def test_root_never_rounds_to_zero():
 def test_counter_has_64_bits():
     a, b = ro.random_bits(600, 2 ** 32 - 256, 5, 9), ro.random_bits(344, 2 ** 32, 5, 9)
     assert np.array_equal(a[0][256:], b[0]) and not np.array_equal(a[0][256:], ro.random_bits(344, 0, 5, 9)[0])
+
+
+def test_gradients_that_overlap_what_adamw_writes_are_refused():
+    """A gradient inside the weights, the masters or the states would be read while it is overwritten."""
+    flat, g = torch.zeros(1000), [torch.zeros(300), torch.zeros(40)]
+    w = [flat[:300], flat[400:440]]
+    for grads in (w, [g[0], w[1]], [flat[100:400], g[1]], [g[0], flat[401:441]], [g[0], flat[361:401]]):
+        with pytest.raises(ValueError):
+            lr.AdamW(w, grads=grads)
+    m = torch.zeros(300)
+    with pytest.raises(ValueError):
+        lr.AdamW([w[0]], grads=[m], m=[m])
+    half = [t.bfloat16() for t in w]
+    opt = lr.AdamW(half, masters=w, grads=g)
+    with pytest.raises(ValueError):
+        opt.bind(w)
+    assert opt.grads == g
+    lr.AdamW(w, grads=[flat[440:740], flat[300:340]])  # beside them
+    lr.AdamW([w[0], torch.zeros(300)], grads=[g[0], g[0]])  # one gradient for two weights is only read
+    lr.AdamW([flat[:0], w[1]], grads=[flat[400:400], g[1]])  # without elements nothing overlaps
