@@ -415,7 +415,7 @@ lrmoe_status lrmoe_balance_loss(const lrmoe_router* r, const void* logits, const
                                 const int64_t* seq_off_d, int32_t n_seq, float coef, int32_t* counts, float* psum,
                                 float* norm, float* loss, void* ws, size_t ws_bytes, lrmoe_stream_t stream);
 
-/* Gradient of the logits, dlogits [T x E] of r->dtype (not the logits' own buffer), every element
+/* Gradient of the logits, dlogits [T x E] of r->dtype (no part of the logits' buffer), every element
  * written (0 for tokens that are not live). Two parts, either of which may be left out:
  * - routing weights, if dalpha is not NULL: with pmap, dalpha is [n_pairs] by pair row (as
  *   lrmoe_alpha_grad gives it) and a slot whose pmap is outside [0, n_pairs) has gradient 0;

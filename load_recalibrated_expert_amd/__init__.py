@@ -602,8 +602,8 @@ def route_bwd(r: Router, logits, idx, dalpha=None, pmap=None, balance=None, glos
     off, S = _sequences(r, seq_off, here, stream) if balance is not None else (None, 1)
     if out is None:
         out = _empty(shape, r.torch_dtype, r.device, stream)
-    elif out.data_ptr() == logits.data_ptr() and out.numel():
-        raise ValueError("out must not be the logits")
+    elif abs(out.data_ptr() - logits.data_ptr()) < r.T * r.E * logits.element_size():
+        raise ValueError("out must not overlap the logits")
     n_pairs, d = 0, None
     if dalpha is not None:
         n_pairs = dalpha.numel()

@@ -241,3 +241,18 @@ def test_an_advance_whose_copy_fails_counts_no_step(capture, monkeypatch):
     with pytest.raises(RuntimeError):
         opt.advance()
     assert opt.t == 0
+
+
+def test_a_gradient_over_the_logits_is_refused(gpu):
+    """Rows of the logits that other tokens still read would be overwritten."""
+    r = lr.Router(T=8, E=5, K=2, device="cuda:0")
+    idx = Tensor((8, 2), torch.int32, 0)
+    at = 1 << 20
+    x = Tensor((8, 5), torch.float32, 0, at)
+    for shift in (0, 20, 159, -20, -159):
+        with pytest.raises(ValueError):
+            lr.route_bwd(r, x, idx, dalpha=Tensor((8, 2), torch.float32, 0), out=Tensor((8, 5), torch.float32, 0, at + shift))
+    assert gpu.lib.launched == []
+    for shift in (160, -160):
+        lr.route_bwd(r, x, idx, dalpha=Tensor((8, 2), torch.float32, 0), out=Tensor((8, 5), torch.float32, 0, at + shift))
+    assert gpu.lib.launched == ["lrmoe_route_bwd"] * 2
