@@ -426,7 +426,8 @@ lrmoe_status lrmoe_balance_loss(const lrmoe_router* r, const void* logits, const
  * - balance loss, if norm is not NULL (counts, norm, seq_off_d and n_seq as in
  *   lrmoe_balance_loss; tokens outside every sequence get none):
  *     dx_e += gloss[0] * norm[s] * p_e (counts[s, e] - sum_e' counts[s, e'] p_e')
- *   with gloss a device f32 (NULL: 1), the gradient of the loss value.
+ *   with gloss a device f32 (NULL: 1), the gradient of the loss value. The counts' differences are
+ *     taken as whole numbers before anything is rounded, so nearly equal counts lose nothing.
  * A token's idx entries have to be different; an entry outside [0, E) is an empty slot. */
 lrmoe_status lrmoe_route_bwd(const lrmoe_router* r, const void* logits, const uint8_t* mask, const int32_t* idx,
                              const float* dalpha, const int32_t* pmap, int64_t n_pairs, const int64_t* seq_off_d,
