@@ -441,7 +441,8 @@ lrmoe_status lrmoe_route_bwd(const lrmoe_router* r, const void* logits, const ui
  * kept; the selection's keep gives the gradient of the retained pairs). G [T x D], Y [N x D] of
  * the storage dtype. pmap [T x K]: the pair row of each (token, slot) position, as lrmoe_route
  * wrote it; each pair has one position. An entry outside [0, N) is none, and pairs without a
- * position keep what dalpha held. Products and sums in fp64. T must be under 2^26. No workspace. */
+ * position keep what dalpha held. Products and sums in fp64; what Y lost to subnormal values of the
+ * storage dtype (alpha near 2^-126) cannot be had back. T must be under 2^26. No workspace. */
 lrmoe_status lrmoe_alpha_grad(const lrmoe_problem* p, const void* G, const void* Y, const float* alpha,
                               const int32_t* pmap, const uint8_t* keep, float* dalpha, lrmoe_stream_t stream);
 

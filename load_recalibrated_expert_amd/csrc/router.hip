@@ -1012,16 +1012,16 @@ constexpr int kAlphaRows = 8;  // pairs whose rows a wavefront reads at once
 // Tokens up to which a block shares one: any, or those of rows of 4 KB and more (a word to a thread).
 constexpr int kAlphaSplit = 1024, kAlphaSplitWide = 8192;
 
-// Products of 16 bytes of two rows, added to s in fp64 (as the score's norms; products of bf16 values are
-// exact in f32).
+// Products of 16 bytes of two rows, added to s: both in fp64, which holds every product of two f32 or bf16
+// values exactly (f32 holds those of bf16 values between 2^-126 and 2^128 only; the time is the same).
 template <bool BF16>
 __device__ __forceinline__ double dot16(uint4 g, uint4 y, double s) {
   const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (BF16) {
-      s += (double)(bf16_lo(gw[i]) * bf16_lo(yw[i]));
-      s += (double)(bf16_hi(gw[i]) * bf16_hi(yw[i]));
+      s += (double)bf16_lo(gw[i]) * (double)bf16_lo(yw[i]);
+      s += (double)bf16_hi(gw[i]) * (double)bf16_hi(yw[i]);
     } else {
       s += (double)__uint_as_float(gw[i]) * (double)__uint_as_float(yw[i]);
     }

@@ -60,3 +60,29 @@ def test_balance_gradient_of_nearly_equal_counts(E, dt, spread):
     assert np.all(got[~live] == 0)
     worst = float(np.max((np.abs(got - want) / err)[live]))
     assert worst <= 1
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("g,y,a", [(1e-7, 1e-36, 1e-36), (1e-25, 1e-20, 1e-20), (1e-30, 1e-30, 1e-38), (1e25, 1e20, 1e20),
+                                   (1e30, 1e-38, 1e-38), (1e-39, 1e-3, 1e-3), (1.0, 1e-39, 1e-39), (1e30, 1e30, 3e38)])
+@pytest.mark.parametrize("T,D", [(5, 264), (1100, 64)])
+def test_alpha_grad_products_that_f32_does_not_hold(T, D, g, y, a, dt):
+    """G, Y and alpha of ordinary and subnormal values whose products vanish in f32 or pass its largest value,
+    and whose quotients do neither. The bound is the definition's for products and sums in fp64, the f32
+    result's own rounding below 2^-126 added."""
+    rng = np.random.default_rng(T + D)
+    K = 3
+    N = T * K
+    td, code = DTYPES[dt]
+    G = torch.from_numpy((rng.standard_normal((T, D)) * g).astype(np.float32)).to(DEV).to(td)
+    Y = torch.from_numpy((rng.standard_normal((N, D)) * y).astype(np.float32)).to(DEV).to(td)
+    alpha = torch.from_numpy(((rng.random(N) * 0.5 + 0.5) * a).astype(np.float32)).to(DEV)
+    pmap = torch.from_numpy(rng.permutation(N).astype(np.int32).reshape(T, K)).to(DEV)
+    p = lr.Problem(E=1, T=T, K=K, D=D, F=8, swiglu=True, dtype=code, seg_off=[0, N], quota=[0], device=DEV)
+    log(f"alpha gradient T={T} {dt} G {g:g} Y {y:g} alpha {a:g}")
+    got = as_f64(lr.alpha_grad(p, G, Y, alpha, pmap))
+    tok = np.empty(N, np.int64)
+    tok[pmap.cpu().numpy().reshape(-1)] = np.repeat(np.arange(T), K)
+    want, err = ro.alpha_grad(as_f64(G), as_f64(Y), as_f64(alpha), tok)
+    worst = float(np.max(np.abs(got - want) / (err + 2.0 ** -149)))
+    assert worst <= 1 and np.abs(want).max() > 0
