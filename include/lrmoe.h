@@ -390,7 +390,7 @@ lrmoe_status lrmoe_router_workspace_size(const lrmoe_router* r, int32_t n_seq, s
  * -inf, in decreasing order, among equal ones the lower index first; -1 in slots without one.
  *   w[t, k] = scale * exp(x_k - max) / Z      f32, Z = the sum of exp(x - max) over all experts,
  *                                             or over the token's chosen ones (renorm)
- * and 0 in empty slots. counts [E] int32: tokens per expert over the whole layer.
+ * (subnormal values too) and 0 in empty slots. counts [E] int32: tokens per expert over the whole layer.
  * Pair lists of the local experts in the order every other call uses: expert-major, by token
  * inside an expert. seg_off [local + 1] int64 (device; its host copy goes into lrmoe_problem),
  * tok, slot [T*K] int32, alpha [T*K] f32 = w of the pair; rows at and after seg_off[local] are
@@ -427,7 +427,8 @@ lrmoe_status lrmoe_balance_loss(const lrmoe_router* r, const void* logits, const
  *   lrmoe_balance_loss; tokens outside every sequence get none):
  *     dx_e += gloss[0] * norm[s] * p_e (counts[s, e] - sum_e' counts[s, e'] p_e')
  *   with gloss a device f32 (NULL: 1), the gradient of the loss value. The counts' differences are
- *     taken as whole numbers before anything is rounded, so nearly equal counts lose nothing.
+ *   taken as whole numbers before anything is rounded, so nearly equal counts lose nothing.
+ * The probability p_e of an expert that is not chosen counts as 0 below 2^-126.
  * A token's idx entries have to be different; an entry outside [0, E) is an empty slot. */
 lrmoe_status lrmoe_route_bwd(const lrmoe_router* r, const void* logits, const uint8_t* mask, const int32_t* idx,
                              const float* dalpha, const int32_t* pmap, int64_t n_pairs, const int64_t* seq_off_d,

@@ -86,3 +86,56 @@ def test_alpha_grad_products_that_f32_does_not_hold(T, D, g, y, a, dt):
     want, err = ro.alpha_grad(as_f64(G), as_f64(Y), as_f64(alpha), tok)
     worst = float(np.max(np.abs(got - want) / (err + 2.0 ** -149)))
     assert worst <= 1 and np.abs(want).max() > 0
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("T,E,K", [(1, 8, 3), (50, 16, 4), (333, 60, 8), (200, 128, 8), (40, 300, 16), (33, 1024, 32),
+                                   (5000, 24, 4)])
+@pytest.mark.parametrize("least", [80, 92])
+def test_chosen_logits_far_below_the_largest(least, T, E, K, renorm, dt):
+    """Chosen experts 80 to 104 below the maximum: weights from 2^-115 to the smallest subnormal number, and
+    their share of the logits' gradient. The bounds are the definition's; below 2^-126 the exponential,
+    the quotient and the product with scale are each off by up to half of 2^-149 more. What is not
+    chosen counts as 0 below 2^-126, so scale * sum_k p_k y_k reaches a slot within that."""
+    rng = np.random.default_rng(T + E)
+    td, code = DTYPES[dt]
+    x = -least - (104 - least) * rng.random((T, E))
+    x[np.arange(T), rng.integers(0, E, T)] = rng.standard_normal(T)
+    x = torch.from_numpy(x.astype(np.float32)).to(DEV).to(td)
+    r = lr.Router(T=T, E=E, K=K, dtype=code, renorm=renorm, scale=1.5, device=DEV)
+    log(f"route {T} x {E} {dt} with far logits")
+    ref = ro.route(as_f64(x), K, renorm=renorm, scale=1.5)
+    o = lr.route(r, x)
+    assert np.array_equal(o["idx"].cpu().numpy(), ref["idx"])
+    w, tiny = as_f64(o["w"]), 2.0 ** -149
+    rel = (ref["w_err"] - 1e-37) / ref["w"]
+    worst = float(np.max(np.abs(w - ref["w"]) / (ref["w"] * rel + 3 * tiny)))
+    assert worst <= 1
+    assert np.all(w[ref["w"] > 4 * tiny] > 0)
+    y = torch.from_numpy((rng.standard_normal((T, K)) * 1e30).astype(np.float32)).to(DEV)
+    y[:, 0] *= 1e-30  # the largest's is ordinary, so that the others' part is seen
+    got = as_f64(lr.route_bwd(r, x, o["idx"], dalpha=y))
+    want, err = ro.route_bwd(as_f64(x), ref["idx"], y=as_f64(y), renorm=renorm, scale=1.5)
+    d = np.zeros((T, E))
+    np.put_along_axis(d, ref["idx"], np.abs(1.5 * as_f64(y)), 1)
+    # q to 2 tiny at each slot and in the sum; the sum times what counts as 0
+    err = err + 2 * tiny * d + ref_p(as_f64(x), ref["idx"], renorm) * 2 * tiny * d.sum(1, keepdims=True)
+    err = err + 2.0 ** -126 * np.abs(ref_sum(as_f64(x), ref["idx"], as_f64(y), renorm))
+    if dt == "bf16":
+        err = err + np.abs(want) * 2.0 ** -8
+    worst = float(np.max(np.abs(got - want) / err))
+    assert worst <= 1
+
+
+def ref_p(x, idx, renorm):
+    """fp64 softmax over all experts, or over the chosen ones."""
+    if renorm:
+        chosen = np.zeros(x.shape, bool)
+        np.put_along_axis(chosen, idx, True, 1)
+        x = np.where(chosen, x, -np.inf)
+    return ro.softmax(x)[0]
+
+
+def ref_sum(x, idx, y, renorm):
+    return 1.5 * (np.take_along_axis(ref_p(x, idx, renorm), idx, 1) * y).sum(1, keepdims=True)
