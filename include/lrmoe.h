@@ -369,7 +369,9 @@ lrmoe_status lrmoe_scatter(const lrmoe_problem* p, lrmoe_scatter_mode mode, int6
  * cover. Logits are [T x E] of `dtype` (f32 or bf16), and are read by these rules everywhere:
  * a NaN counts as -inf, +inf as the largest finite f32. mask [T] uint8 (NULL: all ones) leaves
  * the tokens with a zero out. A token is live if it is not masked and has a logit over -inf.
- * T must be under 2^26, T * K under 2^31, E at most 1024, K at most min(E, 32). */
+ * Logits and their gradient may start at any row of a 16-byte aligned buffer: rows are read at the
+ * alignment that their length leaves. T must be under 2^26, T * K under 2^31, E at most 1024, K at
+ * most min(E, 32). */
 typedef struct lrmoe_router {
   int32_t T;        /* tokens                                                        */
   int32_t E;        /* experts of the layer                                          */

@@ -122,6 +122,12 @@ lrmoe_status check_adamw(const lrmoe_adamw_config* c) {
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
+// Logits or their gradient from any row of a 16-byte aligned buffer on.
+bool aligned_rows(const void* p, const lrmoe_router* r) {
+  const uintptr_t row = (uintptr_t)r->E * (r->dtype == LRMOE_BF16 ? 2 : 4);
+  return aligned(p, std::min<uintptr_t>(16, row & (0 - row)));
+}
+
 lrmoe_status check_adamw_tensors(const lrmoe_adamw_tensor* tensors, int32_t n_tensors, const lrmoe_adamw_config* c) {
   if (n_tensors < 0 || (n_tensors > 0 && !tensors)) return LRMOE_ERR_INVALID_ARG;
   const bool q = c->state_bits == 8;
@@ -420,7 +426,7 @@ lrmoe_status lrmoe_route(const lrmoe_router* r, const void* logits, const uint8_
   LRMOE_TRY(check_router(r));
   if (!counts || !seg_off) return LRMOE_ERR_INVALID_ARG;
   if (r->T > 0 && (!logits || !idx || !w || !tok || !slot || !alpha || !pmap)) return LRMOE_ERR_INVALID_ARG;
-  if (!aligned(logits, 16) || !aligned(ws, 16)) return LRMOE_ERR_INVALID_ARG;
+  if (!aligned_rows(logits, r) || !aligned(ws, 16)) return LRMOE_ERR_INVALID_ARG;
   if (!ws || ws_bytes < route_ws_bytes(r)) return LRMOE_ERR_WORKSPACE;
   return launch_route(r, logits, mask, idx, w, counts, seg_off, tok, slot, alpha, pmap, ws, (hipStream_t)stream);
 }
@@ -432,7 +438,7 @@ lrmoe_status lrmoe_balance_loss(const lrmoe_router* r, const void* logits, const
   LRMOE_TRY(check_sequences(r, seq_off_d, n_seq));
   if (!std::isfinite(coef)) return LRMOE_ERR_INVALID_ARG;
   if (!counts || !psum || !norm || !loss || (r->T > 0 && (!logits || !idx))) return LRMOE_ERR_INVALID_ARG;
-  if (!aligned(logits, 16) || !aligned(ws, 16)) return LRMOE_ERR_INVALID_ARG;
+  if (!aligned_rows(logits, r) || !aligned(ws, 16)) return LRMOE_ERR_INVALID_ARG;
   if (!ws || ws_bytes < balance_ws_bytes(r, n_seq)) return LRMOE_ERR_WORKSPACE;
   return launch_balance_loss(r, logits, mask, idx, seq_off_d, n_seq, coef, counts, psum, norm, loss, ws,
                              (hipStream_t)stream);
@@ -450,7 +456,7 @@ lrmoe_status lrmoe_route_bwd(const lrmoe_router* r, const void* logits, const ui
   if (dalpha && pmap && n_pairs < 0) return LRMOE_ERR_INVALID_ARG;
   if (r->T == 0) return LRMOE_OK;
   if (!logits || !dlogits || (dalpha && !idx)) return LRMOE_ERR_INVALID_ARG;
-  if (!aligned(logits, 16) || !aligned(dlogits, 16)) return LRMOE_ERR_INVALID_ARG;
+  if (!aligned_rows(logits, r) || !aligned_rows(dlogits, r)) return LRMOE_ERR_INVALID_ARG;
   return launch_route_bwd(r, logits, mask, idx, dalpha, pmap, n_pairs, seq_off_d, n_seq, counts, norm, gloss, dlogits,
                           (hipStream_t)stream);
 }

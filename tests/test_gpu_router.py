@@ -501,3 +501,25 @@ def test_balance_of_many_sequences(E, S, masked):
                            seq_off=off)
     got = lr.route_bwd(r, x, idx, balance=b, mask=mask, seq_off=off)
     assert np.all(np.abs(as_f64(got) - dx) <= err)
+
+
+@pytest.mark.parametrize("E,dt", [(17, "f32"), (61, "bf16"), (130, "f32"), (257, "bf16"), (601, "f32")])
+def test_logits_from_a_later_row(E, dt):
+    """Logits and their gradient as views that start at rows 1 to 3 of a buffer: as a copy of them gives."""
+    rng = np.random.default_rng(E)
+    T, K = 400, 3
+    t = torch.bfloat16 if dt == "bf16" else torch.float32
+    whole = torch.from_numpy((rng.standard_normal((T + 3, E)) * 2).astype(np.float32)).to(DEV).to(t)
+    r = lr.Router(T=T, E=E, K=K, dtype=lr.BF16 if dt == "bf16" else lr.F32, device=DEV)
+    y = torch.from_numpy(rng.standard_normal((T, K)).astype(np.float32)).to(DEV)
+    for row in (1, 2, 3):
+        x = whole[row:row + T]
+        log(f"logits of {E} {dt} from row {row}")
+        got, want = [], []
+        grad = torch.full((T + 6, E), 5.0, dtype=t, device=DEV)
+        for to, logits, out in ((got, x, grad[row:row + T]), (want, x.clone(), None)):
+            o = lr.route(r, logits)
+            b = lr.balance_loss(r, logits, o["idx"])
+            to += [*o.values(), *b.values(), lr.route_bwd(r, logits, o["idx"], dalpha=y, balance=b, out=out)]
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert torch.all(grad[:row] == 5.0) and torch.all(grad[row + T:] == 5.0)

@@ -347,3 +347,21 @@ def test_gradients_that_overlap_what_adamw_writes_are_refused():
     lr.AdamW(w, grads=[flat[440:740], flat[300:340]])  # beside them
     lr.AdamW([w[0], torch.zeros(300)], grads=[g[0], g[0]])  # one gradient for two weights is only read
     lr.AdamW([flat[:0], w[1]], grads=[flat[400:400], g[1]])  # without elements nothing overlaps
+
+
+@pytest.mark.parametrize("E,dtype,off,ok", [
+    (17, _lib.F32, 4, True), (17, _lib.F32, 2, False), (18, _lib.F32, 8, True), (18, _lib.F32, 4, False),
+    (20, _lib.F32, 16, True), (20, _lib.F32, 8, False), (17, _lib.BF16, 2, True), (17, _lib.BF16, 1, False),
+    (20, _lib.BF16, 8, True), (20, _lib.BF16, 4, False), (1, _lib.BF16, 2, True), (1024, _lib.F32, 8, False)])
+def test_logits_may_start_at_any_row(E, dtype, off, ok):
+    """A view that starts at a later row of an aligned buffer is as aligned as a row is long. What is taken
+    goes on to the workspace's check."""
+    lib, r = _lib.load(), _router(E=E, local=E, K=1, dtype=dtype)
+    at = ctypes.c_void_p(0x1000 + off)
+    want = _lib.ERR_WORKSPACE if ok else _lib.ERR_INVALID_ARG
+    assert lib.lrmoe_route(ctypes.byref(r), at, None, *([FAKE] * 8), None, 0, None) == want
+    assert lib.lrmoe_balance_loss(ctypes.byref(r), at, None, FAKE, None, 1, 0.1, *([FAKE] * 4), None, 0, None) == want
+    if not ok:
+        for pair in ((at, FAKE), (FAKE, at)):
+            assert lib.lrmoe_route_bwd(ctypes.byref(r), pair[0], None, FAKE, FAKE, None, 0, None, 1, None, None, None,
+                                       pair[1], None) == want
