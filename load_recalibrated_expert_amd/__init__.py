@@ -446,7 +446,8 @@ class Router:
         self._route_out = (("idx", (T, K), i32), ("w", (T, K), f32), ("counts", (E,), i32),
                            ("seg_off", (self.local + 1,), torch.int64), ("tok", (T * K,), i32),
                            ("slot", (T * K,), i32), ("alpha", (T * K,), f32), ("pmap", (T, K), i32))
-        self._ws, self._ws_bytes, self._ws_size, self._grown, self._streams = None, 0, {}, [], set()
+        self._ws, self._ws_bytes, self._ws_size, self._streams = None, 0, {}, set()
+        self._ws_captured, self._grown = False, []
         self.workspace_size()  # checks the router
 
     def workspace_size(self, n_seq=1) -> int:
@@ -461,19 +462,23 @@ class Router:
     def workspace(self, n_seq=1, stream=None) -> torch.Tensor:
         """The router's scratch buffer. Calls that overlap on several streams, or graphs that
         may replay at the same time, need a Router each. A buffer that has become too small is
-        kept: a captured graph may still use it."""
+        kept if a call was captured with it: that graph may still use it."""
         return self._scratch(n_seq, stream)[0]
 
     def _scratch(self, n_seq, stream):
         """(workspace, its bytes, raw handle of the stream)"""
         n, raw = self.workspace_size(n_seq), _stream(stream)
         if self._ws_bytes < n:
-            if self._ws is not None:
+            if self._ws_captured:
                 self._grown.append(self._ws)
+            self._ws_captured = False
             self._ws, self._ws_bytes = _empty((n,), torch.uint8, self.device, stream), n
+            self._ws_device = self._ws.get_device()
             self._streams.clear()
-        if self._ws.get_device() != torch._C._cuda_getDevice():  # the outputs allocated for it are there too
+        if self._ws_device != torch._C._cuda_getDevice():  # the outputs allocated for it are there too
             raise ValueError(f"the router's workspace is on {self._ws.device}, which is not the current device")
+        if raw and not self._ws_captured and _capturing(stream):  # the null stream, 0, is never captured
+            self._ws_captured = True
         if raw not in self._streams:
             _used_on(raw, stream, self._streams, (self._ws,))
         return self._ws, self._ws_bytes, raw

@@ -523,3 +523,25 @@ def test_logits_from_a_later_row(E, dt):
             to += [*o.values(), *b.values(), lr.route_bwd(r, logits, o["idx"], dalpha=y, balance=b, out=out)]
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert torch.all(grad[:row] == 5.0) and torch.all(grad[row + T:] == 5.0)
+
+
+def test_a_workspace_outgrown_while_a_side_stream_uses_it():
+    """A call that waits on a side stream keeps its workspace when a call on the current stream needs a larger
+    one; afterwards the smaller one is given back."""
+    r = lr.Router(T=9000, E=64, K=4, dtype=lr.BF16, device=DEV)
+    x = torch.randn(r.T, r.E, device=DEV).bfloat16()
+    want = lr.route(r, x)
+    n = r.workspace().numel()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    log("a call behind a wait on the side stream")
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)
+    got = lr.route(r, x, stream=side)
+    lr.balance_loss(r, x, want["idx"], seq_off=list(range(r.T + 1)))
+    assert r.workspace().numel() > n and r._grown == []
+    trash = [torch.full((n,), 255, dtype=torch.uint8, device=DEV) for _ in range(50)]
+    torch.cuda.synchronize()
+    for name in want:
+        assert torch.equal(got[name], want[name]), name
+    assert all(bool(torch.all(t == 255)) for t in trash)

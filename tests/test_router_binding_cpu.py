@@ -256,3 +256,24 @@ def test_a_gradient_over_the_logits_is_refused(gpu):
     for shift in (160, -160):
         lr.route_bwd(r, x, idx, dalpha=Tensor((8, 2), torch.float32, 0), out=Tensor((8, 5), torch.float32, 0, at + shift))
     assert gpu.lib.launched == ["lrmoe_route_bwd"] * 2
+
+
+def test_an_outgrown_workspace_is_kept_for_graphs_alone(capture):
+    """One that no captured call has used is given back; one that a graph may replay with is not."""
+    r, side = lr.Router(T=8, E=4, K=2, device="cuda:0"), Stream(0, 7100)
+    for n_seq in range(1, 3000, 97):
+        r.workspace(n_seq)
+    assert r._grown == []
+    kept = []
+    for n_seq, stream in ((4000, None), (6000, side)):
+        capture.capturing = {stream}
+        kept.append(r.workspace(1, stream))  # large enough already
+        capture.capturing = set()
+        for more in (0, 500, 1000):
+            assert r.workspace(n_seq + more) is not kept[-1]
+        assert all(a is b for a, b in zip(r._grown, kept)) and len(r._grown) == len(kept)
+    capture.capturing = {side}
+    kept.append(r.workspace(9000, side))  # allocated inside a capture; the one before it was never in one
+    capture.capturing = set()
+    r.workspace(10000)
+    assert all(a is b for a, b in zip(r._grown, kept)) and len(r._grown) == 3
