@@ -652,7 +652,9 @@ class AdamW:
 
     ``weights``: f32 or bf16 tensors, all of one type; ``masters``: their f32 masters (bf16 weights
     only), or None; ``grads``: the gradient buffers the backward writes (f32 or bf16, all of one
-    type; they can also be given to each ``step``). ``bits``: 32 or 8 bits of state per moment. The
+    type), if they are the same at every step. Others are given to each ``step``: new ones are checked
+    one by one (about 1 us of host time each), and more than 48 tensors then take a launch for every
+    48 instead of one. ``bits``: 32 or 8 bits of state per moment. The
     states ``m``, ``v`` (8 bits: e4m3 codes, v's of its square root, with ``m_scale``, ``v_scale`` per 256
     elements) start at zero unless given. ``first``: 8 bits, the counter of each tensor's first
     element for the random rounding (multiples of 256; None: one tensor behind the other).
