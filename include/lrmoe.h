@@ -471,6 +471,7 @@ typedef struct lrmoe_adamw_config {
   int32_t grad_dtype;  /* lrmoe_dtype of grad                                              */
   int32_t master;      /* 1: every tensor has f32 master weights                           */
   int32_t state_bits;  /* 32 or 8                                                          */
+  /* lr, eps, grad_scale and 1 - lr * weight_decay have to be finite in f32, which they are used in */
   double lr, beta1, beta2, eps, weight_decay;
   double grad_scale;   /* factor of every gradient (1 / loss scale, or a clipping factor)  */
   int64_t step;        /* number of this step, from 1                                      */

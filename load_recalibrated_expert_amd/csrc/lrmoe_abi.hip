@@ -113,8 +113,9 @@ lrmoe_status check_adamw(const lrmoe_adamw_config* c) {
     if (t != LRMOE_F32 && t != LRMOE_BF16) return LRMOE_ERR_UNSUPPORTED;
   if (c->state_bits != 32 && c->state_bits != 8) return LRMOE_ERR_UNSUPPORTED;
   if (c->master && c->w_dtype != LRMOE_BF16) return LRMOE_ERR_UNSUPPORTED;  // an f32 w is its own master
-  for (double x : {c->lr, c->eps, c->weight_decay, c->grad_scale})
-    if (!std::isfinite(x)) return LRMOE_ERR_INVALID_ARG;
+  // weight_decay is used as a part of decay only
+  for (double x : {c->lr, c->eps, c->grad_scale, 1.0 - c->lr * c->weight_decay})
+    if (!std::isfinite((float)x)) return LRMOE_ERR_INVALID_ARG;
   if (!(c->beta1 >= 0 && c->beta1 < 1) || !(c->beta2 >= 0 && c->beta2 < 1) || c->eps < 0) return LRMOE_ERR_INVALID_ARG;
   if (c->step < 1) return LRMOE_ERR_INVALID_ARG;
   return LRMOE_OK;

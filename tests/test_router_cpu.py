@@ -365,3 +365,14 @@ def test_logits_may_start_at_any_row(E, dtype, off, ok):
         for pair in ((at, FAKE), (FAKE, at)):
             assert lib.lrmoe_route_bwd(ctypes.byref(r), pair[0], None, FAKE, FAKE, None, 0, None, 1, None, None, None,
                                        pair[1], None) == want
+
+
+@pytest.mark.parametrize("kw", [dict(lr=1e39), dict(lr=-1e39), dict(weight_decay=1e300, lr=1e300), dict(eps=1e39),
+                                dict(grad_scale=1e39), dict(lr=1e20, weight_decay=1e20)])
+def test_adamw_values_that_f32_does_not_hold_are_refused(kw):
+    """The kernel takes them in f32, where they would be infinite and end every weight."""
+    lib, s = _lib.load(), _lib.CAdamwScalars()
+    c = _config(**kw)
+    assert lib.lrmoe_adamw_step_scalars(ctypes.byref(c), ctypes.byref(s)) == _lib.ERR_INVALID_ARG
+    assert lib.lrmoe_adamw(None, 0, ctypes.byref(c), None, None, None) == _lib.ERR_INVALID_ARG
+    assert lib.lrmoe_adamw_plan(None, 0, ctypes.byref(c), None, ctypes.byref(ctypes.c_size_t(0))) == _lib.ERR_INVALID_ARG
