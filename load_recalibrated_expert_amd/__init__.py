@@ -479,8 +479,9 @@ class Router:
             raise ValueError(f"the router's workspace is on {self._ws.device}, which is not the current device")
         if raw and not self._ws_captured and _capturing(stream):  # the null stream, 0, is never captured
             self._ws_captured = True
-        if raw not in self._streams:
-            _used_on(raw, stream, self._streams, (self._ws,))
+        if raw not in self._streams:  # noted once per stream
+            self._streams.add(raw)
+            _used_on(stream, (self._ws,))
         return self._ws, self._ws_bytes, raw
 
 
@@ -504,12 +505,13 @@ def _empty(shape, dtype, device, stream):
         return torch.empty_strided(shape, strides, dtype=dtype, device=device)
 
 
-def _used_on(raw, stream, seen, tensors):
-    """Notes, once per stream (its handle: raw), that work there uses `tensors`: memory that is freed
-    meanwhile is given out again only behind that work. `seen`: the streams noted since they were allocated."""
-    seen.add(raw)
+def _used_on(stream, tensors):
+    """Notes that work on `stream` uses `tensors`: memory that is freed meanwhile is given out again only behind
+    that work."""
+    if stream is None:
+        stream = torch.cuda.current_stream()
     for t in tensors:
-        t.record_stream(stream if stream is not None else torch.cuda.current_stream())
+        t.record_stream(stream)
 
 
 def _want(t, name, shape, dtype, here):
@@ -671,11 +673,15 @@ class AdamW:
             raise ValueError("bits must be 32 or 8")
         st = torch.float8_e4m3fn if bits == 8 else torch.float32
 
+        self._own = []  # what is allocated here; the caller looks after the rest
+
         def states(given, dt, n, fill=0):
             if given is not None:
                 return list(given)
-            return [torch.full((k,), fill, dtype=torch.uint8 if dt == torch.float8_e4m3fn else dt,
-                               device=dev).view(dt) for k in n]
+            new = [torch.full((k,), fill, dtype=torch.uint8 if dt == torch.float8_e4m3fn else dt,
+                              device=dev).view(dt) for k in n]
+            self._own += new
+            return new
 
         blocks = [(k + 255) // 256 for k in sizes]
         self.m, self.v = states(m, st, sizes), states(v, st, sizes)
@@ -720,7 +726,7 @@ class AdamW:
         words = np.frombuffer(self._table, np.uint64).reshape(len(sizes), -1)  # the table's fields are 8 bytes each
         self._table_grads = words[:, _lib.CAdamwTensor.grad.offset // 8]
         self._scalars = self._plan = None
-        self._captured, self._streams = [], set()
+        self._captured, self._plans, self._noted = [], 0, {}
         self.grads = None
         if grads is not None:
             self.bind(grads)
@@ -759,17 +765,22 @@ class AdamW:
             host = torch.empty(n.value, dtype=torch.uint8)
             _lib.check(lib.lrmoe_adamw_plan(*args, host.data_ptr(), ctypes.byref(n)), "lrmoe_adamw_plan")
             self._plan = host.to(self.w[0].device)
-            self._streams.clear()
+            self._plans += 1
         return self._plan.data_ptr() if self._plan is not False else None
 
     def _used_on(self, stream):
         """Raw handle of `stream`, on which work uses what this object allocated."""
         raw = _stream(stream)
-        if raw in self._streams:
-            return raw
-        own = [t for ts in (self.m, self.v, self.m_scale or (), self.v_scale or ()) for t in ts]
-        own += [t for t in (self._plan, self._scalars) if isinstance(t, torch.Tensor)]
-        _used_on(raw, stream, self._streams, own)
+        now = self._plans, self._scalars is not None
+        seen = self._noted.get(raw)
+        if seen != now:  # noted once per stream
+            own = [] if seen else list(self._own)
+            if isinstance(self._plan, torch.Tensor) and (not seen or seen[0] != now[0]):
+                own.append(self._plan)
+            if now[1] and not (seen and seen[1]):
+                own.append(self._scalars)
+            _used_on(stream, own)
+            self._noted[raw] = now
         return raw
 
     def _config(self, grad_scale):
@@ -815,7 +826,6 @@ class AdamW:
             values = torch.frombuffer(bytearray(host), dtype=torch.int32)
             if self._scalars is None:
                 self._scalars = _empty((8,), torch.int32, self.w[0].device, stream)
-                self._streams.clear()
             if gpu:
                 self._used_on(stream)
                 values = values.pin_memory()  # torch gives it out again only behind the copy

@@ -277,3 +277,29 @@ def test_an_outgrown_workspace_is_kept_for_graphs_alone(capture):
     capture.capturing = set()
     r.workspace(10000)
     assert all(a is b for a, b in zip(r._grown, kept)) and len(r._grown) == 3
+
+
+def test_adamw_notes_its_own_buffers_once_per_stream(capture, monkeypatch):
+    """record_stream, once for each stream, of what the object allocated: not of moments that the caller gave,
+    and not of everything again when a plan or the scalars are new."""
+    noted = []
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: noted.append((t.data_ptr(), s)))
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True, raising=False)
+    n, current = 60, Stream(0, 7000)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: current)
+    w, g = ([torch.zeros(64) for _ in range(n)] for _ in range(2))
+    given = [torch.zeros(64) for _ in range(n)]
+    opt = lr.AdamW(w, grads=g, m=given)
+    opt._check_place = lambda: None
+    side = Stream(0, 7100)
+    for _ in range(4):  # the second one makes the plan
+        opt.step()
+    opt.step(stream=side)
+    opt.step(stream=side)
+    own = {t.data_ptr() for t in opt.v}
+    plan = opt._plan.data_ptr()
+    assert sorted(noted, key=str) == sorted([(p, s) for p in own | {plan} for s in (current, side)], key=str)
+    opt.bind([t.clone() for t in g])
+    opt.step()
+    opt.step()  # another plan
+    assert noted[-1] == (opt._plan.data_ptr(), current) and len(noted) == 2 * (n + 1) + 1
