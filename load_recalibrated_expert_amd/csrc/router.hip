@@ -1001,14 +1001,10 @@ __global__ __launch_bounds__(kGradThreads) void route_bwd_kernel(
     }
     dot = group_sum<L>(dot);
     const float f = inside ? norm[s] * (gloss ? gloss[0] : 1.0f) : 0.0f;
-    if (inside) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) dx[v] += f * (p[v] * (c[v] - dot));
-    }
+    for (int v = 0; v < V; ++v) dx[v] += f * (p[v] * (c[v] - dot));  // zeros where f or, not live, p is 0
   }
   if (!in) return;
-#pragma unroll
-  for (int v = 0; v < V; ++v) dx[v] = live ? dx[v] : 0.0f;
   Lay::store(dlogits, t, E, lane, dx);
 }
 
