@@ -412,7 +412,8 @@ lrmoe_status lrmoe_route(const lrmoe_router* r, const void* logits, const uint8_
  *   loss[0]      = sum_s norm[s] sum_e counts[s, e] psum[s, e]
  * i.e. coef times the mean over the sequences of E * sum_e f_e P_e, with f_e the share of the
  * slots and P_e the mean probability of expert e. idx [T x K] as lrmoe_route wrote it; an entry
- * outside [0, E) counts nowhere. Sums of probabilities are joined in fp64. Deterministic. */
+ * outside [0, E) counts nowhere. A p below 2^-126 counts as 0. Sums of probabilities are joined in
+ * fp64. Deterministic. */
 lrmoe_status lrmoe_balance_loss(const lrmoe_router* r, const void* logits, const uint8_t* mask, const int32_t* idx,
                                 const int64_t* seq_off_d, int32_t n_seq, float coef, int32_t* counts, float* psum,
                                 float* norm, float* loss, void* ws, size_t ws_bytes, lrmoe_stream_t stream);
@@ -497,8 +498,9 @@ lrmoe_status lrmoe_adamw_step_scalars(const lrmoe_adamw_config* c, lrmoe_adamw_s
  *   g = grad_scale * grad;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
  *   w = w * decay - lr * (m c1) / (sqrt(v) c2 + eps)
  * in f32 with a rounding at each operation (with 8-bit states the quotient is a product with the
- * reciprocal to 1 ulp; eps = 0 divides by zero where v is 0); w of bf16 without a master is rounded to nearest
- * even, with a master the master takes the f32 result and w its rounded copy.
+ * reciprocal to 1 ulp; eps = 0, with 8-bit states any eps below 2^-126, divides by zero where v is
+ * 0); w of bf16 without a master is rounded to nearest even, with a master the master takes the f32
+ * result and w its rounded copy.
  * 8-bit states: m and r = sqrt(v) are e4m3 codes times one power of two per 256 elements,
  * 2^(floor(log2(0.8164966 a)) - 7) with a the block's largest finite magnitude (1 where a = 0).
  * The update uses m and v before they are rounded. Magnitudes are rounded at random,

@@ -24,8 +24,7 @@ __device__ __forceinline__ float clean(float x) { return fminf(not_nan(x), kFltM
 // gives 0 below 2^-126, so the result is 0 from d of -87.34 down. Half the instructions of expf, whose
 // range checks are not needed here. ALL: subnormal results too, to d of -104, for the K slots of a
 // token: a chosen expert's weight is not 0 while f32 has a value for it (routing of 32768 x 128: 17.7 us
-// without, 17.9 us with it). Probabilities that are summed over experts or tokens do without: their sum
-// holds nothing that small.
+// without, 17.9 us with it). The probabilities of all experts do without: below 2^-126 they count as 0.
 template <bool ALL = false>
 __device__ __forceinline__ float exp_below(float d) {
   d = fmaxf(d, -104.0f);
@@ -156,9 +155,10 @@ __host__ __device__ constexpr int bit_words(int C, int local) { return ((C + 31)
 // each: 256 chunks of up to 128 tokens, then 512 (top-K and placing of 300000 x 64 in chunks of 1024
 // 27.2 + 16.8 us, of 592 19.3 + 12.7 us; 70000 x 1024 bf16 in chunks of 256 121 us, of 144 70 us). Each
 // writes a row of counts, so chunks have at least 128 tokens, or 64 where the top-K gains more by
-// smaller ones than the scan loses by more rows (sixteen or more lanes to a token: 16384 x 512 in
-// chunks of 128 22 us, of 64 14.5 us; more than 256 chunks: 50021 x 257 in chunks of 128 23.6 us, of
-// 104 21.8 us).
+// smaller ones than the scan loses by more rows: above 320 experts, where a token has sixteen or more
+// lanes whatever K (16384 x 512 in chunks of 128 22 us, of 64 14.5 us), and with more than 256 chunks
+// (50021 x 257 in chunks of 128 23.6 us, of 104 21.8 us). With 9 to 32 slots sixteen lanes begin at 257
+// experts; chunks of 64 there were not measured.
 int route_chunk(const lrmoe_router* r) {
   if (r->T <= kOneChunk) return kOneChunk;
   const int64_t even = align_up((size_t)ceil_div(r->T, r->T <= 256 * 128 ? 256 : 512), 8);
@@ -480,9 +480,10 @@ __global__ __launch_bounds__(topk_threads(Lay::L, N)) void route_topk_kernel(Rou
   blk.finish(a);
 }
 
-// Rows of counts up to which every placing block sums them itself; above, a launch scans them first. 64 rows of
-// 128 experts: 7.3 us of placing against 3.2 us of scan and 5.7 us of placing; 128 rows: 9.9 against
-// 3.1 and 6.1 us.
+// Rows of counts up to which every placing block sums them itself, a thread to an expert and one row
+// after the other; above, a launch scans them first. 64 rows of 128 experts: 7.3 us of placing against
+// 3.2 us of scan and 5.7 us of placing; 128 rows: 9.9 against 3.1 and 6.1 us. (With 128 experts that
+// loop leaves seven eighths of the block's threads idle; sums by all of them were not measured.)
 constexpr int kOwnRows = 64;
 constexpr int kScanExperts = 32;
 constexpr int kScanKept = 8;  // rows of a run: all of them up to 512 chunks
@@ -987,7 +988,8 @@ __global__ __launch_bounds__(kGradThreads) void route_bwd_kernel(
     }
     // The counts relative to the most probable expert's, as whole numbers: sum_e p_e = 1, so that changes
     // nothing in c - dot, and near balance, where counts in the millions differ by a few, the common part
-    // would leave its rounding there (counts of 2^17 +- 1, 64 experts: an error of 1.6e-2, so 1.1e-7; 32768 x 128: 7.5 and 7.9 us).
+    // would leave its rounding there. Counts of 2^17 +- 1 over 64 experts: an error of 1.6e-2 of the
+    // gradient without, 1.1e-7 with it; 32768 x 128 takes 7.5 and 7.85 us.
     int32_t n[V], ref = INT32_MIN;
     Lay::load_counts(counts, s, E, inside, lane, n);
 #pragma unroll
