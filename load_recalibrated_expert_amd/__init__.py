@@ -569,15 +569,16 @@ def _sequences(r, seq_off, here, stream):
         seq_off = torch.as_tensor(seq_off, dtype=torch.int64)
     if seq_off.dtype != torch.int64 or seq_off.dim() != 1 or seq_off.numel() < 2:
         raise ValueError("seq_off must be int64 [n_seq + 1]")
-    if not seq_off.is_cuda:
+    host = not seq_off.is_cuda
+    if host:
         a = seq_off.tolist()
         if a[0] < 0 or a[-1] > r.T or any(x > y for x, y in zip(a, a[1:])):
             raise ValueError("seq_off must not decrease and stay inside [0, T]")
         seq_off = seq_off.to(r.device)
-        if stream is not None:
-            seq_off.record_stream(stream)
-    elif seq_off.get_device() != here:
-        raise ValueError("seq_off must be on the current device")
+    if seq_off.get_device() != here:
+        raise ValueError("seq_off must be on the current device, or on the host with the router on that device")
+    if host and stream is not None:
+        seq_off.record_stream(stream)
     return seq_off, seq_off.numel() - 1
 
 

@@ -303,3 +303,14 @@ def test_adamw_notes_its_own_buffers_once_per_stream(capture, monkeypatch):
     opt.step()
     opt.step()  # another plan
     assert noted[-1] == (opt._plan.data_ptr(), current) and len(noted) == 2 * (n + 1) + 1
+
+
+def test_offsets_copied_to_another_device_are_refused(gpu):
+    """Host offsets go to the router's device: route_bwd with a given output uses nothing else that is there."""
+    r = lr.Router(T=8, E=4, K=2, device="cpu")
+    x, idx = Tensor((8, 4), torch.float32, 0), Tensor((8, 2), torch.int32, 0)
+    bal = {"counts": Tensor((2, 4), torch.int32, 0), "norm": Tensor((2,), torch.float32, 0)}
+    for off in ([0, 3, 8], torch.tensor([0, 3, 8])):
+        with pytest.raises(ValueError):
+            lr.route_bwd(r, x, idx, balance=bal, seq_off=off, out=Tensor((8, 4), torch.float32, 0, 1 << 30))
+    assert gpu.lib.launched == []
