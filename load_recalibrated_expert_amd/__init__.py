@@ -816,8 +816,10 @@ class AdamW:
         that holds ``step_captured``, on the stream of the replays: the copy then follows those before
         it, which read their own step's scalars from the same place."""
         gpu = self.w[0].is_cuda
-        if gpu and _capturing(stream):
-            raise ValueError("advance belongs before a replay, not into the graph")
+        if gpu:
+            self._check_place()
+            if _capturing(stream):
+                raise ValueError("advance belongs before a replay, not into the graph")
         host = _lib.CAdamwScalars()
         self.t += 1
         try:

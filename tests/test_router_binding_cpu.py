@@ -314,3 +314,15 @@ def test_offsets_copied_to_another_device_are_refused(gpu):
         with pytest.raises(ValueError):
             lr.route_bwd(r, x, idx, balance=bal, seq_off=off, out=Tensor((8, 4), torch.float32, 0, 1 << 30))
     assert gpu.lib.launched == []
+
+
+def test_advance_on_another_device_is_refused(capture, monkeypatch):
+    """Its stream, like step_captured's, is one of the current device."""
+    opt = _on_device(_adamw(), Scalars(capture), monkeypatch)
+    del opt._check_place
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: capture.here)
+    opt.advance()
+    capture.here = 1
+    with pytest.raises(ValueError):
+        opt.advance()
+    assert opt.t == 1 and len(opt._scalars.copies) == 1
