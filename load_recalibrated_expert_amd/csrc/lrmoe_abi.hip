@@ -3,6 +3,7 @@
 // synchronises or keeps state.
 #include <algorithm>
 #include <cmath>
+#include <limits>
 #include <vector>
 
 #include "common.h"
@@ -115,7 +116,7 @@ lrmoe_status check_adamw(const lrmoe_adamw_config* c) {
   if (c->master && c->w_dtype != LRMOE_BF16) return LRMOE_ERR_UNSUPPORTED;  // an f32 w is its own master
   // weight_decay is used as a part of decay only
   for (double x : {c->lr, c->eps, c->grad_scale, 1.0 - c->lr * c->weight_decay})
-    if (!std::isfinite((float)x)) return LRMOE_ERR_INVALID_ARG;
+    if (!(std::fabs(x) <= std::numeric_limits<float>::max())) return LRMOE_ERR_INVALID_ARG;
   if (!(c->beta1 >= 0 && c->beta1 < 1) || !(c->beta2 >= 0 && c->beta2 < 1) || c->eps < 0) return LRMOE_ERR_INVALID_ARG;
   if (c->step < 1) return LRMOE_ERR_INVALID_ARG;
   return LRMOE_OK;
