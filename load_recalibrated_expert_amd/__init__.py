@@ -462,7 +462,7 @@ class Router:
     def workspace(self, n_seq=1, stream=None) -> torch.Tensor:
         """The router's scratch buffer. Calls that overlap on several streams, or graphs that
         may replay at the same time, need a Router each. A buffer that has become too small is
-        kept if a call was captured with it: that graph may still use it."""
+        kept if a call was captured with it: that graph may still use it, and needs the Router alive."""
         return self._scratch(n_seq, stream)[0]
 
     def _scratch(self, n_seq, stream):
