@@ -30,6 +30,10 @@
  *   lrmoe_balance_loss     per-expert counts and the balance loss of every sequence
  *   lrmoe_alpha_grad       gradient of the routing weights from the saved output rows
  *   lrmoe_route_bwd        gradient of the logits: routing weights and balance loss
+ *   lrmoe_route_scored,    the same with softmax or sigmoid scores, a bias per expert in the choice,
+ *   lrmoe_balance_loss_scored,   and groups of experts
+ *   lrmoe_route_bwd_scored
+ *   lrmoe_bias_update      a step of that bias towards equal loads
  *   lrmoe_adamw            AdamW step over many tensors, states in 32 or 8 bits
  *
  * Conventions shared by every entry point
@@ -437,6 +441,59 @@ lrmoe_status lrmoe_route_bwd(const lrmoe_router* r, const void* logits, const ui
                              const float* dalpha, const int32_t* pmap, int64_t n_pairs, const int64_t* seq_off_d,
                              int32_t n_seq, const int32_t* counts, const float* norm, const float* gloss,
                              void* dlogits, lrmoe_stream_t stream);
+
+/* How scores decide. score: s_e of expert e is softmax of the token's logits, or 1 / (1 + exp(-x_e)) of its own.
+ * groups: the experts are that many runs of E / groups; a token keeps the top_groups of them whose group_best (1 or 2)
+ * largest choice scores have the largest sum. groups = top_groups = 1: no groups. At most 64 groups; the kept ones hold at
+ * least K experts. */
+typedef enum lrmoe_score_kind { LRMOE_SCORE_SOFTMAX = 0, LRMOE_SCORE_SIGMOID = 1 } lrmoe_score_kind;
+typedef struct lrmoe_scoring {
+  int32_t score;      /* lrmoe_score_kind            */
+  int32_t groups;     /* a divisor of E, at most 64  */
+  int32_t top_groups; /* 1 to groups                 */
+  int32_t group_best; /* 1 or 2                      */
+} lrmoe_scoring;
+
+/* Host-only. Checks the router and its scoring. */
+lrmoe_status lrmoe_scoring_check(const lrmoe_router* r, const lrmoe_scoring* c);
+
+/* lrmoe_route with c's scores, under the same rules for logits and mask and with the same outputs and workspace.
+ * Choice scores are s_e + bias_e (bias [E] f32, NULL: zeros; a NaN counts as -inf, +inf as the largest finite f32).
+ * Experts with a logit or a bias of -inf are no candidates. A group's score is the sum of its group_best largest choice
+ * scores (fewer if it has fewer candidates); groups with equal scores: the lower index first.
+ * idx[t, 0..K) = the candidates of the kept groups with the largest choice scores, in decreasing order, among equal ones
+ * the lower index first; -1 in slots without one.
+ *   w[t, k] = scale * s_k                     renorm = 0
+ *             scale * s_k / sum_j s_idx_j     renorm = 1, over the token's chosen experts; no sum underflows
+ * The bias is no part of w. Choice scores are f64 and compared to 42 bits (scores that differ by less, relative,
+ * may count as equal); sigmoid scores without bias and groups are chosen by the logits, exactly. A sigmoid logit below
+ * -700 counts as -700 in the choice. Deterministic. */
+lrmoe_status lrmoe_route_scored(const lrmoe_router* r, const lrmoe_scoring* c, const void* logits, const float* bias,
+                                const uint8_t* mask, int32_t* idx, float* w, int32_t* counts, int64_t* seg_off,
+                                int32_t* tok, int32_t* slot, float* alpha, int32_t* pmap, void* ws, size_t ws_bytes,
+                                lrmoe_stream_t stream);
+
+/* lrmoe_balance_loss with p_e = s_e / sum of the token's s (for softmax scores that is p itself). */
+lrmoe_status lrmoe_balance_loss_scored(const lrmoe_router* r, const lrmoe_scoring* c, const void* logits,
+                                       const uint8_t* mask, const int32_t* idx, const int64_t* seq_off_d, int32_t n_seq,
+                                       float coef, int32_t* counts, float* psum, float* norm, float* loss, void* ws,
+                                       size_t ws_bytes, lrmoe_stream_t stream);
+
+/* lrmoe_route_bwd for lrmoe_route_scored's weights and lrmoe_balance_loss_scored's loss. The choice has no gradient,
+ * and neither has the bias. Softmax: as lrmoe_route_bwd. Sigmoid, with y = scale * dalpha:
+ *   renorm = 0: dx_idx_k = s_k (1 - s_k) y_k
+ *   renorm = 1: dx_idx_k = q_k (1 - s_k) (y_k - sum_j q_j y_j), q = s over its sum over the token's chosen experts
+ *   balance:    dx_e += gloss[0] * norm[s] * p_e (1 - s_e) (counts[s, e] - sum_e' counts[s, e'] p_e')
+ * 1 - s_e counts as 0 below 2^-126. An expert with a logit of -inf has gradient 0. */
+lrmoe_status lrmoe_route_bwd_scored(const lrmoe_router* r, const lrmoe_scoring* c, const void* logits,
+                                    const uint8_t* mask, const int32_t* idx, const float* dalpha, const int32_t* pmap,
+                                    int64_t n_pairs, const int64_t* seq_off_d, int32_t n_seq, const int32_t* counts,
+                                    const float* norm, const float* gloss, void* dlogits, lrmoe_stream_t stream);
+
+/* out[e] = bias[e] + rate * sign(mean of counts - counts[e])   f32 [E]; counts [E] int32 as lrmoe_route_scored gives
+ * them (summed over the GPUs, where each routes tokens of its own), compared as whole numbers. out may be bias. */
+lrmoe_status lrmoe_bias_update(const lrmoe_router* r, const int32_t* counts, float rate, const float* bias, float* out,
+                               lrmoe_stream_t stream);
 
 /* Gradient of the routing weights of the N pairs: the layer output is the token sum of the saved
  * rows Y[j] = alpha[j] * u_j (lrmoe_expert_forward), so with G the output's gradient

@@ -29,7 +29,7 @@ from ._lib import (BF16, COMPACT_PHYSICAL, COMPACT_ZERO_MASKED, F32, SCATTER_SLO
 
 __all__ = ["Problem", "score", "select", "select_noalloc", "compact", "compact_weighted", "grouped_gemm_bwd",
            "grouped_gemm_bwd_gathered", "expert_forward", "scatter", "backward", "backward_bytes", "plan_quotas",
-           "Router", "route", "balance_loss", "route_bwd", "alpha_grad", "AdamW", "library", "BF16", "F32", "COMPACT_PHYSICAL", "COMPACT_ZERO_MASKED", "SCATTER_TOKEN",
+           "Router", "route", "bias_update", "balance_loss", "route_bwd", "alpha_grad", "AdamW", "library", "BF16", "F32", "COMPACT_PHYSICAL", "COMPACT_ZERO_MASKED", "SCATTER_TOKEN",
            "SCATTER_SLOT", "SCATTER_TOKEN_BESIDE", "LrmoeError", "InfeasibleQuotaError"]
 
 
@@ -431,15 +431,28 @@ class Router:
     """The router of one layer: T tokens, E experts of the whole layer, K slots per token, and the
     experts [first, first + local) that this GPU's pair lists cover (local=None: all from first).
     ``dtype``: F32 or BF16 logits. ``renorm``: a token's weights sum to ``scale``. ``device``:
-    the one that is current when the calls are made."""
+    the one that is current when the calls are made.
+    ``score``: "softmax" or "sigmoid" scores. ``groups``: the experts are that many equal runs, of which a token keeps
+    the ``top_groups`` whose ``group_best`` (1 or 2) largest choice scores have the largest sum. A bias that
+    enters the choice but not the weights is given to each ``route``."""
 
-    def __init__(self, *, T, E, K, dtype=F32, first=0, local=None, renorm=False, scale=1.0, device="cuda"):
+    def __init__(self, *, T, E, K, dtype=F32, first=0, local=None, renorm=False, scale=1.0, device="cuda",
+                 score="softmax", groups=1, top_groups=1, group_best=1):
         self.T, self.E, self.K, self.dtype = int(T), int(E), int(K), int(dtype)
         self.first, self.local = int(first), int(E) - int(first) if local is None else int(local)
         self.renorm, self.scale = bool(renorm), float(scale)
         self.c = _lib.CRouter(T=self.T, E=self.E, K=self.K, first=self.first, local=self.local, dtype=self.dtype,
                               renorm=int(self.renorm), reserved=0, scale=self.scale)
         self.ref = ctypes.byref(self.c)
+        if score not in _lib.SCORES:
+            raise ValueError(f"unknown score {score!r}; expected one of {sorted(_lib.SCORES)}")
+        self.score, self.groups, self.top_groups = score, int(groups), int(top_groups)
+        self.group_best = int(group_best)
+        self.scoring = _lib.CScoring(score=_lib.SCORES[score], groups=self.groups, top_groups=self.top_groups,
+                                     group_best=self.group_best)
+        self._scoring_ref = ctypes.byref(self.scoring)
+        # softmax without groups: the calls without _scored, unless there is a bias
+        self._plain = score == "softmax" and self.groups == self.top_groups == self.group_best == 1
         self.device = torch.device(device)
         self.torch_dtype = torch.bfloat16 if self.dtype == BF16 else torch.float32
         T, E, K, i32, f32 = self.T, self.E, self.K, torch.int32, torch.float32
@@ -449,6 +462,8 @@ class Router:
         self._ws, self._ws_bytes, self._ws_size, self._streams = None, 0, {}, set()
         self._ws_captured, self._grown = False, []
         self.workspace_size()  # checks the router
+        if not self._plain:
+            _lib.check(library().lrmoe_scoring_check(self.ref, self._scoring_ref), "lrmoe_scoring_check")
 
     def workspace_size(self, n_seq=1) -> int:
         """lrmoe_router_workspace_size, asked once per number of sequences."""
@@ -548,17 +563,36 @@ def _outputs(given, wanted, device, here, stream):
     return o, ptrs
 
 
-def route(r: Router, logits, mask=None, out=None, stream=None):
-    """Top-K routing of ``logits`` [T, E] (lrmoe_route): a dict of idx, w [T, K], counts [E],
+def route(r: Router, logits, mask=None, out=None, stream=None, bias=None):
+    """Top-K routing of ``logits`` [T, E] (lrmoe_route, lrmoe_route_scored): a dict of idx, w [T, K], counts [E],
     seg_off [local + 1] (device; ``.cpu()`` of it is Problem's seg_off), tok, slot, alpha [T*K] (rows
     at and after seg_off[local] are not written) and pmap [T, K]. ``mask`` [T] uint8 or bool: 0
-    leaves a token out. ``out`` reuses buffers."""
+    leaves a token out. ``bias`` f32 [E]: added to the scores in the choice, not in the weights. ``out``
+    reuses buffers."""
     here = torch._C._cuda_getDevice()
     o, ptrs = _outputs(out, r._route_out, r.device, here, stream)
     ws, n, raw = r._scratch(1, stream)
-    _lib.check(library().lrmoe_route(r.ref, _want(logits, "logits", (r.T, r.E), r.torch_dtype, here),
-                                     _flags(mask, "mask", r.T, here), *ptrs, ws.data_ptr(), n, raw), "lrmoe_route")
+    x, m = _want(logits, "logits", (r.T, r.E), r.torch_dtype, here), _flags(mask, "mask", r.T, here)
+    if r._plain and bias is None:
+        _lib.check(library().lrmoe_route(r.ref, x, m, *ptrs, ws.data_ptr(), n, raw), "lrmoe_route")
+    else:
+        _lib.check(library().lrmoe_route_scored(r.ref, r._scoring_ref, x,
+                                                _want(bias, "bias", (r.E,), torch.float32, here), m, *ptrs,
+                                                ws.data_ptr(), n, raw), "lrmoe_route_scored")
     return o
+
+
+def bias_update(r: Router, bias, counts, rate, out=None, stream=None):
+    """One step of the routing bias towards equal loads (lrmoe_bias_update): bias + rate * sign(mean(counts) - counts),
+    f32 [E]. ``counts`` int32 [E]: route's, or their sum over the GPUs. ``out`` may be ``bias``."""
+    here = torch._C._cuda_getDevice()
+    if out is None:
+        out = _empty((r.E,), torch.float32, r.device, stream)
+    _lib.check(library().lrmoe_bias_update(r.ref, _want(counts, "counts", (r.E,), torch.int32, here), float(rate),
+                                           _want(bias, "bias", (r.E,), torch.float32, here),
+                                           _want(out, "out", (r.E,), torch.float32, here), _stream(stream)),
+               "lrmoe_bias_update")
+    return out
 
 
 def _sequences(r, seq_off, here, stream):
@@ -592,10 +626,12 @@ def balance_loss(r: Router, logits, idx, coef=1.0, mask=None, seq_off=None, out=
     o, ptrs = _outputs(out, (("counts", (S, r.E), torch.int32), ("psum", (S, r.E), torch.float32),
                              ("norm", (S,), torch.float32), ("loss", (1,), torch.float32)), r.device, here, stream)
     ws, n, raw = r._scratch(S, stream)
-    _lib.check(library().lrmoe_balance_loss(r.ref, _want(logits, "logits", (r.T, r.E), r.torch_dtype, here),
-                                            _flags(mask, "mask", r.T, here),
-                                            _want(idx, "idx", (r.T, r.K), torch.int32, here), _ptr(off), S,
-                                            float(coef), *ptrs, ws.data_ptr(), n, raw), "lrmoe_balance_loss")
+    args = (_want(logits, "logits", (r.T, r.E), r.torch_dtype, here), _flags(mask, "mask", r.T, here),
+            _want(idx, "idx", (r.T, r.K), torch.int32, here), _ptr(off), S, float(coef), *ptrs, ws.data_ptr(), n, raw)
+    if r._plain:
+        _lib.check(library().lrmoe_balance_loss(r.ref, *args), "lrmoe_balance_loss")
+    else:
+        _lib.check(library().lrmoe_balance_loss_scored(r.ref, r._scoring_ref, *args), "lrmoe_balance_loss_scored")
     return o
 
 
@@ -620,13 +656,14 @@ def route_bwd(r: Router, logits, idx, dalpha=None, pmap=None, balance=None, glos
     if balance is not None:
         counts = _want(balance["counts"], "counts", (S, r.E), torch.int32, here)
         norm = _want(balance["norm"], "norm", (S,), torch.float32, here)
-    _lib.check(library().lrmoe_route_bwd(r.ref, _want(logits, "logits", shape, r.torch_dtype, here),
-                                         _flags(mask, "mask", r.T, here),
-                                         _want(idx, "idx", (r.T, r.K), torch.int32, here), d,
-                                         _want(pmap, "pmap", (r.T, r.K), torch.int32, here), n_pairs, _ptr(off), S,
-                                         counts, norm, _want(gloss, "gloss", (1,), torch.float32, here),
-                                         _want(out, "out", shape, r.torch_dtype, here), _stream(stream)),
-               "lrmoe_route_bwd")
+    args = (_want(logits, "logits", shape, r.torch_dtype, here), _flags(mask, "mask", r.T, here),
+            _want(idx, "idx", (r.T, r.K), torch.int32, here), d, _want(pmap, "pmap", (r.T, r.K), torch.int32, here),
+            n_pairs, _ptr(off), S, counts, norm, _want(gloss, "gloss", (1,), torch.float32, here),
+            _want(out, "out", shape, r.torch_dtype, here), _stream(stream))
+    if r._plain:
+        _lib.check(library().lrmoe_route_bwd(r.ref, *args), "lrmoe_route_bwd")
+    else:
+        _lib.check(library().lrmoe_route_bwd_scored(r.ref, r._scoring_ref, *args), "lrmoe_route_bwd_scored")
     return out
 
 

@@ -17,6 +17,7 @@ LIB_PATH = os.path.join(_HERE, "liblrmoe.so")
 
 OK, ERR_INVALID_ARG, ERR_INFEASIBLE_QUOTA, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_HIP = range(6)
 F32, BF16 = 0, 1
+SCORES = {"softmax": 0, "sigmoid": 1}
 COMPACT_PHYSICAL, COMPACT_ZERO_MASKED = 0, 1
 SCATTER_TOKEN, SCATTER_SLOT, SCATTER_TOKEN_BESIDE = 0, 1, 2
 
@@ -25,7 +26,8 @@ EXPORTS = ("lrmoe_status_string", "lrmoe_version", "lrmoe_validate", "lrmoe_work
            "lrmoe_compact", "lrmoe_grouped_gemm_bwd", "lrmoe_scatter", "lrmoe_expert_forward",
            "lrmoe_select_noalloc", "lrmoe_compact_weighted", "lrmoe_grouped_gemm_bwd_gathered",
            "lrmoe_router_workspace_size", "lrmoe_route", "lrmoe_balance_loss", "lrmoe_route_bwd", "lrmoe_alpha_grad",
-           "lrmoe_adamw_step_scalars", "lrmoe_adamw_plan", "lrmoe_adamw")
+           "lrmoe_adamw_step_scalars", "lrmoe_adamw_plan", "lrmoe_adamw", "lrmoe_scoring_check", "lrmoe_route_scored",
+           "lrmoe_balance_loss_scored", "lrmoe_route_bwd_scored", "lrmoe_bias_update")
 
 
 class LrmoeError(RuntimeError):
@@ -49,6 +51,10 @@ class CRouter(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("K", ctypes.c_int32), ("first", ctypes.c_int32),
                 ("local", ctypes.c_int32), ("dtype", ctypes.c_int32), ("renorm", ctypes.c_int32),
                 ("reserved", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class CScoring(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("score", "groups", "top_groups", "group_best")]
 
 
 class CAdamwTensor(ctypes.Structure):
@@ -108,6 +114,13 @@ def load() -> ctypes.CDLL:
         "lrmoe_balance_loss": [ctypes.POINTER(CRouter), vp, vp, vp, vp, i32, ctypes.c_float, vp, vp, vp, vp, vp, sz,
                                vp],
         "lrmoe_route_bwd": [ctypes.POINTER(CRouter), vp, vp, vp, vp, vp, i64, vp, i32, vp, vp, vp, vp, vp],
+        "lrmoe_scoring_check": [ctypes.POINTER(CRouter), ctypes.POINTER(CScoring)],
+        "lrmoe_route_scored": [ctypes.POINTER(CRouter), ctypes.POINTER(CScoring)] + [vp] * 12 + [sz, vp],
+        "lrmoe_balance_loss_scored": [ctypes.POINTER(CRouter), ctypes.POINTER(CScoring), vp, vp, vp, vp, i32,
+                                      ctypes.c_float, vp, vp, vp, vp, vp, sz, vp],
+        "lrmoe_route_bwd_scored": [ctypes.POINTER(CRouter), ctypes.POINTER(CScoring), vp, vp, vp, vp, vp, i64, vp, i32,
+                                   vp, vp, vp, vp, vp],
+        "lrmoe_bias_update": [ctypes.POINTER(CRouter), vp, ctypes.c_float, vp, vp, vp],
         "lrmoe_alpha_grad": [P, vp, vp, vp, vp, vp, vp, vp],
         "lrmoe_adamw_step_scalars": [ctypes.POINTER(CAdamwConfig), ctypes.POINTER(CAdamwScalars)],
         "lrmoe_adamw": [ctypes.POINTER(CAdamwTensor), i32, ctypes.POINTER(CAdamwConfig), vp, vp, vp],

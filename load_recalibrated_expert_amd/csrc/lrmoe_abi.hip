@@ -12,6 +12,12 @@ using namespace lrmoe;
 
 namespace {
 
+#define LRMOE_TRY(x)                      \
+  do {                                    \
+    const lrmoe_status st_ = (x);         \
+    if (st_ != LRMOE_OK) return st_;      \
+  } while (0)
+
 lrmoe_status check_problem(const lrmoe_problem* p, int64_t* K_tot, std::vector<int64_t>* cseg) {
   if (!p || !p->seg_off || !p->quota) return LRMOE_ERR_INVALID_ARG;
   if (p->reserved != 0) return LRMOE_ERR_INVALID_ARG;
@@ -88,6 +94,16 @@ lrmoe_status check_router(const lrmoe_router* r) {
   return LRMOE_OK;
 }
 
+lrmoe_status check_scoring(const lrmoe_router* r, const lrmoe_scoring* c) {
+  LRMOE_TRY(check_router(r));
+  if (!c || (c->score != LRMOE_SCORE_SOFTMAX && c->score != LRMOE_SCORE_SIGMOID)) return LRMOE_ERR_INVALID_ARG;
+  if (c->groups < 1 || r->E % c->groups != 0) return LRMOE_ERR_INVALID_ARG;
+  if (c->top_groups < 1 || c->top_groups > c->groups) return LRMOE_ERR_INVALID_ARG;
+  if (c->group_best != 1 && c->group_best != 2) return LRMOE_ERR_INVALID_ARG;
+  if (c->top_groups * (r->E / c->groups) < r->K) return LRMOE_ERR_INVALID_ARG;
+  return c->groups > max_groups() ? LRMOE_ERR_UNSUPPORTED : LRMOE_OK;
+}
+
 // Sequences of the balance loss: without offsets there is one, of all tokens.
 lrmoe_status check_sequences(int32_t n_seq, int32_t E) {
   if (n_seq < 1) return LRMOE_ERR_INVALID_ARG;
@@ -147,12 +163,6 @@ lrmoe_status check_adamw_tensors(const lrmoe_adamw_tensor* tensors, int32_t n_te
   }
   return LRMOE_OK;
 }
-
-#define LRMOE_TRY(x)                      \
-  do {                                    \
-    const lrmoe_status st_ = (x);         \
-    if (st_ != LRMOE_OK) return st_;      \
-  } while (0)
 
 }  // namespace
 
@@ -422,35 +432,79 @@ lrmoe_status lrmoe_router_workspace_size(const lrmoe_router* r, int32_t n_seq, s
   return LRMOE_OK;
 }
 
+static lrmoe_status route_checked(const lrmoe_router* r, const lrmoe_scoring* c, const void* logits, const float* bias,
+                                  const uint8_t* mask, int32_t* idx, float* w, int32_t* counts, int64_t* seg_off,
+                                  int32_t* tok, int32_t* slot, float* alpha, int32_t* pmap, void* ws, size_t ws_bytes,
+                                  lrmoe_stream_t stream) {
+  if (!counts || !seg_off) return LRMOE_ERR_INVALID_ARG;
+  if (r->T > 0 && (!logits || !idx || !w || !tok || !slot || !alpha || !pmap)) return LRMOE_ERR_INVALID_ARG;
+  if (!aligned_rows(logits, r) || !aligned(bias, 4) || !aligned(ws, 16)) return LRMOE_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < route_ws_bytes(r)) return LRMOE_ERR_WORKSPACE;
+  if (c && c->score == LRMOE_SCORE_SOFTMAX && !bias && c->groups == c->top_groups) c = nullptr;  // by logits
+  return launch_route(r, c, logits, bias, mask, idx, w, counts, seg_off, tok, slot, alpha, pmap, ws,
+                      (hipStream_t)stream);
+}
+
 lrmoe_status lrmoe_route(const lrmoe_router* r, const void* logits, const uint8_t* mask, int32_t* idx, float* w,
                          int32_t* counts, int64_t* seg_off, int32_t* tok, int32_t* slot, float* alpha,
                          int32_t* pmap, void* ws, size_t ws_bytes, lrmoe_stream_t stream) {
   LRMOE_TRY(check_router(r));
-  if (!counts || !seg_off) return LRMOE_ERR_INVALID_ARG;
-  if (r->T > 0 && (!logits || !idx || !w || !tok || !slot || !alpha || !pmap)) return LRMOE_ERR_INVALID_ARG;
+  return route_checked(r, nullptr, logits, nullptr, mask, idx, w, counts, seg_off, tok, slot, alpha, pmap, ws, ws_bytes,
+                       stream);
+}
+
+lrmoe_status lrmoe_scoring_check(const lrmoe_router* r, const lrmoe_scoring* c) { return check_scoring(r, c); }
+
+lrmoe_status lrmoe_route_scored(const lrmoe_router* r, const lrmoe_scoring* c, const void* logits, const float* bias,
+                                const uint8_t* mask, int32_t* idx, float* w, int32_t* counts, int64_t* seg_off,
+                                int32_t* tok, int32_t* slot, float* alpha, int32_t* pmap, void* ws, size_t ws_bytes,
+                                lrmoe_stream_t stream) {
+  LRMOE_TRY(check_scoring(r, c));
+  return route_checked(r, c, logits, bias, mask, idx, w, counts, seg_off, tok, slot, alpha, pmap, ws, ws_bytes, stream);
+}
+
+lrmoe_status lrmoe_bias_update(const lrmoe_router* r, const int32_t* counts, float rate, const float* bias, float* out,
+                               lrmoe_stream_t stream) {
+  LRMOE_TRY(check_router(r));
+  if (!std::isfinite(rate) || !counts || !bias || !out) return LRMOE_ERR_INVALID_ARG;
+  if (!aligned(counts, 4) || !aligned(bias, 4) || !aligned(out, 4)) return LRMOE_ERR_INVALID_ARG;
+  return launch_bias_update(r->E, counts, rate, bias, out, (hipStream_t)stream);
+}
+
+static lrmoe_status balance_checked(const lrmoe_router* r, bool sigmoid, const void* logits, const uint8_t* mask,
+                                    const int32_t* idx, const int64_t* seq_off_d, int32_t n_seq, float coef,
+                                    int32_t* counts, float* psum, float* norm, float* loss, void* ws, size_t ws_bytes,
+                                    lrmoe_stream_t stream) {
+  LRMOE_TRY(check_sequences(r, seq_off_d, n_seq));
+  if (!std::isfinite(coef)) return LRMOE_ERR_INVALID_ARG;
+  if (!counts || !psum || !norm || !loss || (r->T > 0 && (!logits || !idx))) return LRMOE_ERR_INVALID_ARG;
   if (!aligned_rows(logits, r) || !aligned(ws, 16)) return LRMOE_ERR_INVALID_ARG;
-  if (!ws || ws_bytes < route_ws_bytes(r)) return LRMOE_ERR_WORKSPACE;
-  return launch_route(r, logits, mask, idx, w, counts, seg_off, tok, slot, alpha, pmap, ws, (hipStream_t)stream);
+  if (!ws || ws_bytes < balance_ws_bytes(r, n_seq)) return LRMOE_ERR_WORKSPACE;
+  return launch_balance_loss(r, sigmoid, logits, mask, idx, seq_off_d, n_seq, coef, counts, psum, norm, loss, ws,
+                             (hipStream_t)stream);
 }
 
 lrmoe_status lrmoe_balance_loss(const lrmoe_router* r, const void* logits, const uint8_t* mask, const int32_t* idx,
                                 const int64_t* seq_off_d, int32_t n_seq, float coef, int32_t* counts, float* psum,
                                 float* norm, float* loss, void* ws, size_t ws_bytes, lrmoe_stream_t stream) {
   LRMOE_TRY(check_router(r));
-  LRMOE_TRY(check_sequences(r, seq_off_d, n_seq));
-  if (!std::isfinite(coef)) return LRMOE_ERR_INVALID_ARG;
-  if (!counts || !psum || !norm || !loss || (r->T > 0 && (!logits || !idx))) return LRMOE_ERR_INVALID_ARG;
-  if (!aligned_rows(logits, r) || !aligned(ws, 16)) return LRMOE_ERR_INVALID_ARG;
-  if (!ws || ws_bytes < balance_ws_bytes(r, n_seq)) return LRMOE_ERR_WORKSPACE;
-  return launch_balance_loss(r, logits, mask, idx, seq_off_d, n_seq, coef, counts, psum, norm, loss, ws,
-                             (hipStream_t)stream);
+  return balance_checked(r, false, logits, mask, idx, seq_off_d, n_seq, coef, counts, psum, norm, loss, ws, ws_bytes,
+                         stream);
 }
 
-lrmoe_status lrmoe_route_bwd(const lrmoe_router* r, const void* logits, const uint8_t* mask, const int32_t* idx,
-                             const float* dalpha, const int32_t* pmap, int64_t n_pairs, const int64_t* seq_off_d,
-                             int32_t n_seq, const int32_t* counts, const float* norm, const float* gloss,
-                             void* dlogits, lrmoe_stream_t stream) {
-  LRMOE_TRY(check_router(r));
+lrmoe_status lrmoe_balance_loss_scored(const lrmoe_router* r, const lrmoe_scoring* c, const void* logits,
+                                       const uint8_t* mask, const int32_t* idx, const int64_t* seq_off_d, int32_t n_seq,
+                                       float coef, int32_t* counts, float* psum, float* norm, float* loss, void* ws,
+                                       size_t ws_bytes, lrmoe_stream_t stream) {
+  LRMOE_TRY(check_scoring(r, c));
+  return balance_checked(r, c->score == LRMOE_SCORE_SIGMOID, logits, mask, idx, seq_off_d, n_seq, coef, counts, psum,
+                         norm, loss, ws, ws_bytes, stream);
+}
+
+static lrmoe_status route_bwd_checked(const lrmoe_router* r, bool sigmoid, const void* logits, const uint8_t* mask,
+                                      const int32_t* idx, const float* dalpha, const int32_t* pmap, int64_t n_pairs,
+                                      const int64_t* seq_off_d, int32_t n_seq, const int32_t* counts, const float* norm,
+                                      const float* gloss, void* dlogits, lrmoe_stream_t stream) {
   if (norm) {
     LRMOE_TRY(check_sequences(r, seq_off_d, n_seq));
     if (!counts) return LRMOE_ERR_INVALID_ARG;
@@ -459,8 +513,26 @@ lrmoe_status lrmoe_route_bwd(const lrmoe_router* r, const void* logits, const ui
   if (r->T == 0) return LRMOE_OK;
   if (!logits || !dlogits || (dalpha && !idx)) return LRMOE_ERR_INVALID_ARG;
   if (!aligned_rows(logits, r) || !aligned_rows(dlogits, r)) return LRMOE_ERR_INVALID_ARG;
-  return launch_route_bwd(r, logits, mask, idx, dalpha, pmap, n_pairs, seq_off_d, n_seq, counts, norm, gloss, dlogits,
-                          (hipStream_t)stream);
+  return launch_route_bwd(r, sigmoid, logits, mask, idx, dalpha, pmap, n_pairs, seq_off_d, n_seq, counts, norm, gloss,
+                          dlogits, (hipStream_t)stream);
+}
+
+lrmoe_status lrmoe_route_bwd(const lrmoe_router* r, const void* logits, const uint8_t* mask, const int32_t* idx,
+                             const float* dalpha, const int32_t* pmap, int64_t n_pairs, const int64_t* seq_off_d,
+                             int32_t n_seq, const int32_t* counts, const float* norm, const float* gloss,
+                             void* dlogits, lrmoe_stream_t stream) {
+  LRMOE_TRY(check_router(r));
+  return route_bwd_checked(r, false, logits, mask, idx, dalpha, pmap, n_pairs, seq_off_d, n_seq, counts, norm, gloss,
+                           dlogits, stream);
+}
+
+lrmoe_status lrmoe_route_bwd_scored(const lrmoe_router* r, const lrmoe_scoring* c, const void* logits,
+                                    const uint8_t* mask, const int32_t* idx, const float* dalpha, const int32_t* pmap,
+                                    int64_t n_pairs, const int64_t* seq_off_d, int32_t n_seq, const int32_t* counts,
+                                    const float* norm, const float* gloss, void* dlogits, lrmoe_stream_t stream) {
+  LRMOE_TRY(check_scoring(r, c));
+  return route_bwd_checked(r, c->score == LRMOE_SCORE_SIGMOID, logits, mask, idx, dalpha, pmap, n_pairs, seq_off_d,
+                           n_seq, counts, norm, gloss, dlogits, stream);
 }
 
 lrmoe_status lrmoe_alpha_grad(const lrmoe_problem* p, const void* G, const void* Y, const float* alpha,
