@@ -36,6 +36,14 @@
  *   lrmoe_bias_update      a step of that bias towards equal loads
  *   lrmoe_adamw            AdamW step over many tensors, states in 32 or 8 bits
  *
+ * Saved activations in 8 bits (beside the calls above that save and read them in the storage dtype):
+ *
+ *   lrmoe_checkpoint,      rows to codes with a scale per 128 columns, and back
+ *   lrmoe_restore
+ *   lrmoe_expert_forward_checkpoint     the forward that saves [gate | up] as codes
+ *   lrmoe_score_checkpoint, lrmoe_compact_checkpoint, lrmoe_grouped_gemm_bwd_checkpoint
+ *                          the backward's steps that read them
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  * - Pairs are stored expert-major: expert e owns pair rows [seg_off[e], seg_off[e+1]).
@@ -365,6 +373,50 @@ lrmoe_status lrmoe_expert_forward(const lrmoe_problem* p, const int64_t* seg_off
 lrmoe_status lrmoe_scatter(const lrmoe_problem* p, lrmoe_scatter_mode mode, int64_t n_rows, int32_t width,
                            int32_t rows_dtype, const void* rows, const int32_t* ctok, const int32_t* cslot,
                            const int32_t* pmap, float* out, void* ws, size_t ws_bytes, lrmoe_stream_t stream);
+
+/* ---------------------------------------------------------------- saved activations in 8 bits
+ *
+ * A row of parts * width values is held as int8 codes q [n x parts * width] and one bf16 scale for every 128 columns of
+ * each part (the last group of a part may be short), scale [n x parts x ceil(width / 128)]; the values are q * scale.
+ *   scale = the smallest bf16 number that is at least amax / 127 and at least 2^-126, amax = the group's largest magnitude
+ *   q     = x / scale rounded to the nearest whole number, ties to even (exactly; -127 to 127)
+ * so a value is off by at most half a scale. A group with an infinity or a NaN has the scale NaN and codes 0: all of it
+ * reads as NaN. 1.016 bytes a value instead of 2 or 4.
+ * Saved [gate | up] rows have two parts of F, which makes the saved Phi needless: a pair keeps 2 F bytes and its
+ * scales instead of 6 F bytes (bf16). FC2-only problems keep Phi itself, one part. */
+
+/* rows [n x parts * width] of dtype; width a multiple of 8; n * parts * ceil(width / 128) under 2^30. */
+lrmoe_status lrmoe_checkpoint(int64_t n, int32_t parts, int32_t width, lrmoe_dtype dtype, const void* rows, int8_t* q,
+                              uint16_t* scale, lrmoe_stream_t stream);
+
+/* rows = q * scale, rounded to dtype (f32: exact). Restored X rows are what lrmoe_grouped_gemm_bwd_checkpoint reads. */
+lrmoe_status lrmoe_restore(int64_t n, int32_t parts, int32_t width, const int8_t* q, const uint16_t* scale,
+                           lrmoe_dtype dtype, void* rows, lrmoe_stream_t stream);
+
+/* lrmoe_expert_forward with q, scale in the place of H: bit for bit what lrmoe_checkpoint gives for that H (two parts of
+ * F). Phi [N x F] is still written (FC2 reads it) and need not be kept. */
+lrmoe_status lrmoe_expert_forward_checkpoint(const lrmoe_problem* p, const int64_t* seg_off_d, const void* X,
+                                             const int32_t* tok, const float* alpha, const void* W1, const void* W2,
+                                             int8_t* q, uint16_t* scale, void* Phi, void* Y, lrmoe_stream_t stream);
+
+/* lrmoe_score with phi_j from the codes of pair j: silu(gate) * up (swiglu; in f32, not rounded to the storage dtype),
+ * or the value itself (q, scale of one part of F). */
+lrmoe_status lrmoe_score_checkpoint(const lrmoe_problem* p, const void* G, const int8_t* q, const uint16_t* scale,
+                                    const float* alpha, const int32_t* tok, float* R, void* ws, size_t ws_bytes,
+                                    lrmoe_stream_t stream);
+
+/* lrmoe_compact_weighted with the same phi_j: PhiW[c] = alpha[j] * phi_j, j = sel[c], rounded to the storage dtype. */
+lrmoe_status lrmoe_compact_checkpoint(const lrmoe_problem* p, const int32_t* sel, const int8_t* q,
+                                      const uint16_t* scale, const float* alpha, void* PhiW, lrmoe_stream_t stream);
+
+/* lrmoe_grouped_gemm_bwd_gathered with gate and up from the codes of pair j (swiglu problems only; the others read no
+ * saved rows there). q, scale [N x 2 x ...] are read in place. */
+lrmoe_status lrmoe_grouped_gemm_bwd_checkpoint(const lrmoe_problem* p, const int64_t* cseg_off_d, const void* G,
+                                               const float* alpha, const int32_t* sel, const int32_t* ctok,
+                                               const void* PhiW, const void* X, const int8_t* q, const uint16_t* scale,
+                                               const void* W2, const void* W1, float* dW2, float* dW1, void* dH,
+                                               void* dIn, int32_t accumulate, void* ws, size_t ws_bytes,
+                                               lrmoe_stream_t stream, lrmoe_event_t din_ready);
 
 /* ---------------------------------------------------------------- the router
  *

@@ -9,7 +9,8 @@ section 3.3) are calls into ``liblrmoe.so`` (hand-written HIP for gfx950):
 
 The functions here have the C entry points' names and only marshal arguments:
 torch tensors supply device memory and the current HIP stream. ``backward`` chains
-the five calls. Around the experts, ``Router`` with route, balance_loss, alpha_grad and
+the five calls. ``Checkpoint`` holds saved activations in 8 bits: expert_forward_checkpoint
+(or checkpoint) makes one, and backward takes it in the place of H and Phi, and of X. Around the experts, ``Router`` with route, balance_loss, alpha_grad and
 route_bwd makes the pair lists and trains the router, and ``AdamW`` applies the gradients.
 Nothing falls back to another implementation; if the library is not built, the first call
 raises ImportError.
@@ -29,7 +30,8 @@ from ._lib import (BF16, COMPACT_PHYSICAL, COMPACT_ZERO_MASKED, F32, SCATTER_SLO
 
 __all__ = ["Problem", "score", "select", "select_noalloc", "compact", "compact_weighted", "grouped_gemm_bwd",
            "grouped_gemm_bwd_gathered", "expert_forward", "scatter", "backward", "backward_bytes", "plan_quotas",
-           "Router", "route", "bias_update", "balance_loss", "route_bwd", "alpha_grad", "AdamW", "library", "BF16", "F32", "COMPACT_PHYSICAL", "COMPACT_ZERO_MASKED", "SCATTER_TOKEN",
+           "Checkpoint", "checkpoint", "restore", "expert_forward_checkpoint", "score_checkpoint", "compact_checkpoint",
+           "grouped_gemm_bwd_checkpoint", "Router", "route", "bias_update", "balance_loss", "route_bwd", "alpha_grad", "AdamW", "library", "BF16", "F32", "COMPACT_PHYSICAL", "COMPACT_ZERO_MASKED", "SCATTER_TOKEN",
            "SCATTER_SLOT", "SCATTER_TOKEN_BESIDE", "LrmoeError", "InfeasibleQuotaError"]
 
 
@@ -284,14 +286,9 @@ def compact_weighted(p: Problem, sel, Phi, alpha, out=None, stream=None):
     return PhiW[:p.K_tot]
 
 
-def grouped_gemm_bwd_gathered(p: Problem, G, alpha, sel, ctok, PhiW, W2, X=None, H=None, W1=None, out=None,
-                              accumulate=False, din_ready=None, stream=None):
-    """Step 4 without a packed Dlt (lrmoe_grouped_gemm_bwd_gathered): gradient rows G[ctok]
-    and X[ctok] read by token, H[sel] and alpha[sel] by pair, PhiW from compact_weighted.
-    Same outputs as grouped_gemm_bwd in physical mode."""
-    rows = p.K_tot
-    dt = p.torch_dtype
-    dev = p.device
+def _gemm_outputs(p, rows, out):
+    """The outputs of the gathered grouped GEMM, those that `out` does not give allocated."""
+    dt, dev = p.torch_dtype, p.device
     o = dict(out or {})
     o.setdefault("dW2", torch.empty(p.E, p.F, p.D, dtype=torch.float32, device=dev))
     if p.swiglu:
@@ -300,17 +297,30 @@ def grouped_gemm_bwd_gathered(p: Problem, G, alpha, sel, ctok, PhiW, W2, X=None,
         o.setdefault("dIn", torch.empty(max(rows, 1), p.D, dtype=dt, device=dev))
     else:
         o.setdefault("dIn", torch.empty(max(rows, 1), p.F, dtype=dt, device=dev))
+    return o
+
+
+def _gemm_results(p, rows, o):
+    res = dict(o)
+    res["dIn"] = o["dIn"][:rows]
+    if "dH" in o:
+        res["dH"] = o["dH"][:rows]
+    return res
+
+
+def grouped_gemm_bwd_gathered(p: Problem, G, alpha, sel, ctok, PhiW, W2, X=None, H=None, W1=None, out=None,
+                              accumulate=False, din_ready=None, stream=None):
+    """Step 4 without a packed Dlt (lrmoe_grouped_gemm_bwd_gathered): gradient rows G[ctok]
+    and X[ctok] read by token, H[sel] and alpha[sel] by pair, PhiW from compact_weighted.
+    Same outputs as grouped_gemm_bwd in physical mode."""
+    o = _gemm_outputs(p, p.K_tot, out)
     ws = p.workspace(COMPACT_PHYSICAL)
     _lib.check(library().lrmoe_grouped_gemm_bwd_gathered(
         ctypes.byref(p.c), _ptr(p.cseg_off_d), _ptr(G), _ptr(alpha), _ptr(sel), _ptr(ctok), _ptr(PhiW), _ptr(X),
         _ptr(H), _ptr(W2), _ptr(W1), _ptr(o["dW2"]), _ptr(o.get("dW1")), _ptr(o.get("dH")), _ptr(o["dIn"]),
         int(bool(accumulate)), _ptr(ws), ws.numel(), _stream(stream), _event(din_ready, stream)),
         "lrmoe_grouped_gemm_bwd_gathered")
-    res = dict(o)
-    res["dIn"] = o["dIn"][:rows]
-    if "dH" in o:
-        res["dH"] = o["dH"][:rows]
-    return res
+    return _gemm_results(p, p.K_tot, o)
 
 
 def expert_forward(p: Problem, X, tok, alpha, W1, W2, out=None, stream=None):
@@ -348,7 +358,22 @@ def scatter(p: Problem, rows_t, ctok, cslot, n_rows=None, mode=SCATTER_TOKEN, ou
     return out
 
 
-def backward(p: Problem, *, G, Phi, alpha, tok, slot, W2, X=None, H=None, W1=None, mode=COMPACT_PHYSICAL,
+def _saved_in_8_bits(p, Phi, H):
+    """The Checkpoint that phi comes from, or None."""
+    if isinstance(H, Checkpoint):
+        if not p.swiglu or Phi is not None:
+            raise ValueError("a checkpoint of [gate | up] is for SwiGLU problems, without Phi")
+        return H
+    if isinstance(Phi, Checkpoint):
+        if p.swiglu:
+            raise ValueError("a SwiGLU problem takes a checkpoint of [gate | up], not of Phi")
+        return Phi
+    if Phi is None:
+        raise ValueError("Phi is missing")
+    return None
+
+
+def backward(p: Problem, *, G, Phi=None, alpha, tok, slot, W2, X=None, H=None, W1=None, mode=COMPACT_PHYSICAL,
              scatter_mode=SCATTER_TOKEN, bufs=None, overlap_scatter=False, packed_dlt=False, stream=None):
     """The whole path: score -> select -> compact -> grouped GEMMs -> scatter.
 
@@ -357,6 +382,10 @@ def backward(p: Problem, *, G, Phi, alpha, tok, slot, W2, X=None, H=None, W1=Non
     [gate | up] rows H[sel] in place (compact_weighted, grouped_gemm_bwd_gathered). With
     ``packed_dlt`` (and always in zero-masked mode) compaction packs the weighted gradient
     rows Dlt instead and grouped_gemm_bwd reads them.
+
+    Saved activations in 8 bits: ``H`` may be a Checkpoint of the [gate | up] rows (``Phi`` is then left out), or
+    ``Phi`` one of the Phi rows of an FC2-only problem, and ``X`` one of the FC1 inputs, which are restored for the
+    call. Physical compaction without ``packed_dlt`` only.
 
     ``bufs`` (a dict, optional) carries preallocated outputs between calls; it is
     filled on first use. With ``overlap_scatter`` the scatter runs on a second stream as
@@ -367,8 +396,17 @@ def backward(p: Problem, *, G, Phi, alpha, tok, slot, W2, X=None, H=None, W1=Non
     bit). Returns a dict of every intermediate and output."""
     b = bufs if bufs is not None else {}
     main = stream if stream is not None else torch.cuda.current_stream()
-    b["R"] = score(p, G, Phi, alpha, tok, R=b.get("R"), stream=stream)
     phys = mode == COMPACT_PHYSICAL
+    saved = _saved_in_8_bits(p, Phi, H)
+    if isinstance(X, Checkpoint) or saved is not None:
+        if not phys or packed_dlt:
+            raise ValueError("checkpoints need physical compaction without packed_dlt")
+        if isinstance(X, Checkpoint):
+            X._ptrs("X", p.T, 1, p.D, torch._C._cuda_getDevice())
+    if saved is None:
+        b["R"] = score(p, G, Phi, alpha, tok, R=b.get("R"), stream=stream)
+    else:
+        b["R"] = score_checkpoint(p, G, saved, alpha, tok, R=b.get("R"), stream=stream)
     maps = None
     if phys:  # the selection also writes the (token, slot) map that compaction and the scatter use
         sel, keep, maps = select(p, b["R"], sel=b.get("sel_full"), keep=b.get("keep_full"), tok=tok, slot=slot,
@@ -380,7 +418,12 @@ def backward(p: Problem, *, G, Phi, alpha, tok, slot, W2, X=None, H=None, W1=Non
     b.setdefault("keep_full", keep)
     gathered = phys and not packed_dlt
     if gathered:  # the weighted saved rows only; G, X and H are read in place
-        PhiW = compact_weighted(p, sel, Phi, alpha, out=b.get("PhiW"), stream=stream)
+        if saved is None:
+            PhiW = compact_weighted(p, sel, Phi, alpha, out=b.get("PhiW"), stream=stream)
+        else:
+            PhiW = compact_checkpoint(p, sel, saved, alpha, out=b.get("PhiW"), stream=stream)
+        if isinstance(X, Checkpoint):
+            X = b["X"] = restore(X, dtype=p.torch_dtype, out=b.get("X"), stream=stream)
         b.setdefault("PhiW", PhiW)
         c = {"PhiW": PhiW, "ctok": maps["ctok"], "cslot": maps["cslot"]}
     else:  # the weighted gradient rows; the GEMMs read Phi, X and H in place through sel and ctok
@@ -405,7 +448,10 @@ def backward(p: Problem, *, G, Phi, alpha, tok, slot, W2, X=None, H=None, W1=Non
         if "out" not in b:
             nout = p.T if scatter_mode in (SCATTER_TOKEN, SCATTER_TOKEN_BESIDE) else p.T * p.K
             b["out"] = torch.empty(max(nout, 1), p.D if p.swiglu else p.F, dtype=torch.float32, device=p.device)
-    if gathered:
+    if gathered and isinstance(H, Checkpoint):
+        g = grouped_gemm_bwd_checkpoint(p, G, alpha, sel, ctok, PhiW, W2, X, H, W1, out=b.get("gemm"),
+                                        din_ready=b["din_ready"] if overlap_scatter else None, stream=main)
+    elif gathered:
         g = grouped_gemm_bwd_gathered(p, G, alpha, sel, ctok, PhiW, W2, X=X, H=H, W1=W1, out=b.get("gemm"),
                                       din_ready=b["din_ready"] if overlap_scatter else None, stream=main)
     else:
@@ -425,6 +471,122 @@ def backward(p: Problem, *, G, Phi, alpha, tok, slot, W2, X=None, H=None, W1=Non
                       pmap=pmap, stream=main)
     b.setdefault("out", out)
     return {"R": b["R"], "sel": sel, "keep": keep, **c, **g, "out": out}
+
+
+class Checkpoint:
+    """Activation rows in 8 bits (the header's section on saved activations): codes ``q`` int8 [n, width] and ``scale``
+    bf16 [n, parts, ceil(width / parts / 128)], one for every 128 columns of a part."""
+
+    def __init__(self, q, scale):
+        if q.dtype != torch.int8 or q.dim() != 2 or not q.is_contiguous():
+            raise ValueError(f"q: expected contiguous int8 rows, got {q.dtype} of {tuple(q.shape)}")
+        n, width = q.shape
+        parts = scale.shape[1] if scale.dim() == 3 else 0
+        if scale.dtype != torch.bfloat16 or not scale.is_contiguous() or parts < 1 or width % parts or (
+                scale.shape != (n, parts, (width // parts + 127) // 128)):
+            raise ValueError(f"scale: expected contiguous bfloat16 [rows, parts, groups of 128 columns], got "
+                             f"{scale.dtype} of {tuple(scale.shape)} for q of {tuple(q.shape)}")
+        if scale.get_device() != q.get_device():
+            raise ValueError("q and scale must be on one device")
+        self.q, self.scale, self.parts, self.width = q, scale, parts, width // parts
+
+    def _ptrs(self, name, n, parts, width, here):
+        """Pointers of q and scale, if they hold at least n rows of that layout on the current device."""
+        if self.q.shape[0] < n or (self.parts, self.width) != (parts, width) or self.q.get_device() != here:
+            raise ValueError(f"{name}: expected a checkpoint of {n} rows of {parts} x {width} on the current device, got "
+                             f"{self.q.shape[0]} of {self.parts} x {self.width} on {self.q.device}")
+        return self.q.data_ptr(), self.scale.data_ptr()
+
+
+def _new_checkpoint(n, parts, width, device, stream):
+    q = _empty((n, parts * width), torch.int8, device, stream)
+    return Checkpoint(q, _empty((n, parts, (width + 127) // 128), torch.bfloat16, device, stream))
+
+
+def checkpoint(rows, parts=1, out=None, stream=None):
+    """``rows`` [n, width] (f32 or bf16) as a Checkpoint (lrmoe_checkpoint). ``parts``: equal column parts that share no
+    scale (2 for [gate | up]). ``out``: a Checkpoint of that layout, overwritten."""
+    here = torch._C._cuda_getDevice()
+    if rows.dtype not in (torch.float32, torch.bfloat16) or rows.dim() != 2:
+        raise ValueError("rows: expected f32 or bf16 [n, width]")
+    n, width, parts = rows.shape[0], rows.shape[1], int(parts)
+    if parts < 1 or width % (8 * parts) or not width:
+        raise ValueError("rows: the width must be a multiple of 8 in each part")
+    x = _want(rows, "rows", rows.shape, rows.dtype, here)
+    c = _new_checkpoint(n, parts, width // parts, rows.device, stream) if out is None else out
+    q, s = c._ptrs("out", n, parts, width // parts, here)
+    _lib.check(library().lrmoe_checkpoint(n, parts, width // parts, BF16 if rows.dtype == torch.bfloat16 else F32, x, q,
+                                          s, _stream(stream)), "lrmoe_checkpoint")
+    return c
+
+
+def restore(c: Checkpoint, dtype=torch.bfloat16, out=None, stream=None):
+    """The rows that a Checkpoint stands for (lrmoe_restore), bf16 or f32 [n, width]."""
+    here = torch._C._cuda_getDevice()
+    n, width = c.q.shape
+    if out is not None:
+        dtype = out.dtype
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("dtype must be f32 or bf16")
+    q, s = c._ptrs("c", n, c.parts, c.width, here)
+    if out is None:
+        out = _empty((n, width), dtype, c.q.device, stream)
+    _lib.check(library().lrmoe_restore(n, c.parts, c.width, q, s, BF16 if dtype == torch.bfloat16 else F32,
+                                       _want(out, "out", (n, width), dtype, here), _stream(stream)), "lrmoe_restore")
+    return out
+
+
+def expert_forward_checkpoint(p: Problem, X, tok, alpha, W1, W2, out=None, stream=None):
+    """expert_forward that saves [gate | up] as a Checkpoint ("H") of the N pairs (lrmoe_expert_forward_checkpoint).
+    "Phi" is what FC2 reads; a backward from the checkpoint does without it."""
+    here, dt, o = torch._C._cuda_getDevice(), torch.bfloat16, out or {}
+    n = max(p.N, 1)
+    H = o.get("H") if o.get("H") is not None else _new_checkpoint(n, 2, p.F, p.device, stream)
+    Phi = o.get("Phi") if o.get("Phi") is not None else _empty((n, p.F), dt, p.device, stream)
+    Y = o.get("Y") if o.get("Y") is not None else _empty((n, p.D), dt, p.device, stream)
+    q, s = H._ptrs("H", p.N, 2, p.F, here)
+    _lib.check(library().lrmoe_expert_forward_checkpoint(
+        ctypes.byref(p.c), _ptr(p.seg_off_d), _ptr(X), _ptr(tok), _ptr(alpha), _ptr(W1), _ptr(W2), q, s, _ptr(Phi),
+        _ptr(Y), _stream(stream)), "lrmoe_expert_forward_checkpoint")
+    return {"H": Checkpoint(H.q[:p.N], H.scale[:p.N]), "Phi": Phi[:p.N], "Y": Y[:p.N]}
+
+
+def _saved(p, H, here):
+    """Pointers of the pairs' saved rows in 8 bits: [gate | up], or Phi of FC2-only problems."""
+    return H._ptrs("H", p.N, 2 if p.swiglu else 1, p.F, here)
+
+
+def score_checkpoint(p: Problem, G, H: Checkpoint, alpha, tok, R=None, stream=None):
+    """Step 1 from a Checkpoint of the pairs' [gate | up] rows (of their Phi rows, if FC2-only)."""
+    q, s = _saved(p, H, torch._C._cuda_getDevice())
+    if R is None:
+        R = _empty((p.N,), torch.float32, p.device, stream)
+    ws = p.workspace()
+    _lib.check(library().lrmoe_score_checkpoint(ctypes.byref(p.c), _ptr(G), q, s, _ptr(alpha), _ptr(tok), _ptr(R),
+                                                _ptr(ws), ws.numel(), _stream(stream)), "lrmoe_score_checkpoint")
+    return R
+
+
+def compact_checkpoint(p: Problem, sel, H: Checkpoint, alpha, out=None, stream=None):
+    """compact_weighted from a Checkpoint: PhiW of the K_tot packed rows."""
+    q, s = _saved(p, H, torch._C._cuda_getDevice())
+    PhiW = out if out is not None else _empty((max(p.K_tot, 1), p.F), p.torch_dtype, p.device, stream)
+    _lib.check(library().lrmoe_compact_checkpoint(ctypes.byref(p.c), _ptr(sel), q, s, _ptr(alpha), _ptr(PhiW),
+                                                  _stream(stream)), "lrmoe_compact_checkpoint")
+    return PhiW[:p.K_tot]
+
+
+def grouped_gemm_bwd_checkpoint(p: Problem, G, alpha, sel, ctok, PhiW, W2, X, H: Checkpoint, W1, out=None,
+                                accumulate=False, din_ready=None, stream=None):
+    """grouped_gemm_bwd_gathered with [gate | up] from a Checkpoint (SwiGLU problems). X: rows of the storage dtype."""
+    q, s = _saved(p, H, torch._C._cuda_getDevice())
+    o = _gemm_outputs(p, p.K_tot, out)
+    ws = p.workspace(COMPACT_PHYSICAL)
+    _lib.check(library().lrmoe_grouped_gemm_bwd_checkpoint(
+        ctypes.byref(p.c), _ptr(p.cseg_off_d), _ptr(G), _ptr(alpha), _ptr(sel), _ptr(ctok), _ptr(PhiW), _ptr(X), q, s,
+        _ptr(W2), _ptr(W1), _ptr(o["dW2"]), _ptr(o["dW1"]), _ptr(o["dH"]), _ptr(o["dIn"]), int(bool(accumulate)),
+        _ptr(ws), ws.numel(), _stream(stream), _event(din_ready, stream)), "lrmoe_grouped_gemm_bwd_checkpoint")
+    return _gemm_results(p, p.K_tot, o)
 
 
 class Router:
@@ -513,7 +675,8 @@ def _capturing(stream):
 def _empty(shape, dtype, device, stream):
     """An output of a call on `stream` (None: the current one), allocated there: memory that other
     work of the current stream gave back is not written before that work is done."""
-    strides = (1,) if len(shape) == 1 else (shape[1], 1)  # given, they save a third of torch.empty's host time
+    # strides given save a third of torch.empty's host time
+    strides = (1,) if len(shape) == 1 else (shape[1], 1) if len(shape) == 2 else (shape[1] * shape[2], shape[2], 1)
     if stream is None:
         return torch.empty_strided(shape, strides, dtype=dtype, device=device)
     with torch.cuda.stream(stream):

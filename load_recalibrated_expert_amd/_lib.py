@@ -27,7 +27,9 @@ EXPORTS = ("lrmoe_status_string", "lrmoe_version", "lrmoe_validate", "lrmoe_work
            "lrmoe_select_noalloc", "lrmoe_compact_weighted", "lrmoe_grouped_gemm_bwd_gathered",
            "lrmoe_router_workspace_size", "lrmoe_route", "lrmoe_balance_loss", "lrmoe_route_bwd", "lrmoe_alpha_grad",
            "lrmoe_adamw_step_scalars", "lrmoe_adamw_plan", "lrmoe_adamw", "lrmoe_scoring_check", "lrmoe_route_scored",
-           "lrmoe_balance_loss_scored", "lrmoe_route_bwd_scored", "lrmoe_bias_update")
+           "lrmoe_balance_loss_scored", "lrmoe_route_bwd_scored", "lrmoe_bias_update", "lrmoe_checkpoint", "lrmoe_restore",
+           "lrmoe_expert_forward_checkpoint", "lrmoe_score_checkpoint", "lrmoe_compact_checkpoint",
+           "lrmoe_grouped_gemm_bwd_checkpoint")
 
 
 class LrmoeError(RuntimeError):
@@ -121,6 +123,12 @@ def load() -> ctypes.CDLL:
         "lrmoe_route_bwd_scored": [ctypes.POINTER(CRouter), ctypes.POINTER(CScoring), vp, vp, vp, vp, vp, i64, vp, i32,
                                    vp, vp, vp, vp, vp],
         "lrmoe_bias_update": [ctypes.POINTER(CRouter), vp, ctypes.c_float, vp, vp, vp],
+        "lrmoe_checkpoint": [i64, i32, i32, ctypes.c_int, vp, vp, vp, vp],
+        "lrmoe_restore": [i64, i32, i32, vp, vp, ctypes.c_int, vp, vp],
+        "lrmoe_expert_forward_checkpoint": [P] + [vp] * 11,
+        "lrmoe_score_checkpoint": [P, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+        "lrmoe_compact_checkpoint": [P, vp, vp, vp, vp, vp, vp],
+        "lrmoe_grouped_gemm_bwd_checkpoint": [P] + [vp] * 15 + [i32, vp, sz, vp, vp],
         "lrmoe_alpha_grad": [P, vp, vp, vp, vp, vp, vp, vp],
         "lrmoe_adamw_step_scalars": [ctypes.POINTER(CAdamwConfig), ctypes.POINTER(CAdamwScalars)],
         "lrmoe_adamw": [ctypes.POINTER(CAdamwTensor), i32, ctypes.POINTER(CAdamwConfig), vp, vp, vp],

@@ -122,6 +122,8 @@ constexpr int64_t kMaxTokens = (int64_t)1 << 26, kMaxSequences = (int64_t)1 << 2
 
 lrmoe_status launch_score(const lrmoe_problem* p, const void* G, const void* Phi, const float* alpha,
                           const int32_t* tok, float* R, double* gn, hipStream_t s);
+// ||G[t]||^2 of every token (the first launch of every score)
+void launch_token_sqnorm(const lrmoe_problem* p, const void* G, double* gn, hipStream_t s);
 lrmoe_status launch_score_gradient(const lrmoe_problem* p, bool magnitude, const void* G, const int32_t* tok,
                                     float* R, double* gs, hipStream_t s);
 
@@ -146,13 +148,14 @@ size_t compact_ws_bytes(const lrmoe_problem* p);
 lrmoe_status launch_compact_weighted_phi(const lrmoe_problem* p, int64_t rows, const int32_t* sel,
                                          const void* Phi, const float* alpha, void* PhiW, hipStream_t s);
 
+// hscale: H (HC below) holds 8-bit codes with these scales; NULL: rows of the storage dtype
 lrmoe_status launch_expert_forward(const lrmoe_problem* p, const int64_t* seg_off_d, const void* X,
                                    const int32_t* tok, const float* alpha, const void* W1, const void* W2, void* H,
-                                   void* Phi, void* Y, hipStream_t s);
+                                   uint16_t* hscale, void* Phi, void* Y, hipStream_t s);
 size_t gemm_ws_bytes(const lrmoe_problem* p, const int64_t* row_off_h);
 lrmoe_status launch_grouped_gemm_bwd(const lrmoe_problem* p, const int64_t* row_off_h,
                                      const int64_t* row_off_d, const void* Dlt, const void* PhiC,
-                                     const void* XC, const void* HC, const int32_t* hc_rows,
+                                     const void* XC, const void* HC, const uint16_t* hscale, const int32_t* hc_rows,
                                      const int32_t* phi_rows, const int32_t* x_rows, const int32_t* dlt_rows,
                                      const float* alpha, const void* W2, const void* W1,
                                      float* dW2, float* dW1, void* dH, void* dIn, int accumulate,
@@ -181,6 +184,16 @@ lrmoe_status launch_route_bwd(const lrmoe_router* r, bool sigmoid, const void* l
                               const float* gloss, void* dlogits, hipStream_t s);
 lrmoe_status launch_alpha_grad(const lrmoe_problem* p, const void* G, const void* Y, const float* alpha,
                                const int32_t* pmap, const uint8_t* keep, float* dalpha, hipStream_t s);
+
+int64_t checkpoint_units(int64_t n, int32_t parts, int32_t width);
+lrmoe_status launch_checkpoint(int64_t n, int32_t parts, int32_t width, int dtype, const void* rows, int8_t* q,
+                               uint16_t* scale, hipStream_t s);
+lrmoe_status launch_restore(int64_t n, int32_t parts, int32_t width, const int8_t* q, const uint16_t* scale, int dtype,
+                            void* rows, hipStream_t s);
+lrmoe_status launch_score_checkpoint(const lrmoe_problem* p, const void* G, const int8_t* q, const uint16_t* scale,
+                                     const float* alpha, const int32_t* tok, float* R, double* gn, hipStream_t s);
+lrmoe_status launch_compact_checkpoint(const lrmoe_problem* p, int64_t rows, const int32_t* sel, const int8_t* q,
+                                       const uint16_t* scale, const float* alpha, void* PhiW, hipStream_t s);
 
 constexpr int kAdamwTensors = 48;  // tensors of one launch: their table travels in the kernel arguments
 lrmoe_status launch_adamw(const lrmoe_adamw_tensor* tensors, int32_t n_tensors, const lrmoe_adamw_config* c,

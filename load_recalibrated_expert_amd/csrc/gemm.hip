@@ -37,7 +37,7 @@
 #include <mutex>
 #include <vector>
 
-#include "common.h"
+#include "checkpoint_device.h"
 
 namespace lrmoe {
 namespace {
@@ -665,7 +665,7 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float (&v)[8]) {
 
 // ---------------------------------------------------------------- data-gradient kernel
 
-enum { EPI_SWIGLU = 0, EPI_STORE = 1 };
+enum { EPI_SWIGLU = 0, EPI_STORE = 1, EPI_SWIGLU_CODES = 2 };  // CODES: the saved rows are 8-bit codes
 
 struct DgradArgs {
   const uint16_t* A;   // [rows x K] packed rows (Dlt or dH), or the matrix a_rows gathers from
@@ -681,7 +681,8 @@ struct DgradArgs {
   const int64_t* row_off;
   int E;
   // epilogue
-  const uint16_t* HC;  // SwiGLU: saved [gate | up] rows, 2F wide
+  const uint16_t* HC;  // SwiGLU: saved [gate | up] rows, 2F wide (CODES: the codes, bytes)
+  const uint16_t* hscale;  // CODES: the scales of a row's 128-column groups [hc_nrows x 2 x ceil(F / 128)]
   const int32_t* hc_rows;  // row of HC (and pair of alpha) for packed row c (nullptr: row c)
   int64_t hc_nrows;        // rows of HC: a mapped row outside [0, hc_nrows) reads as zeros
   uint16_t* out;       // SwiGLU: dH [rows x 2F]; STORE: [rows x N]
@@ -710,7 +711,9 @@ struct HcBatch {
   uint4 gw[B], uw[B];
 };
 
-template <class C, int B, bool AHEAD, class Pre>
+// CODES: the chunks are 8 bytes of codes, and their groups' scales come beside them in the batch's third words. A row
+// outside HC counts as zeros there, since row 0 may hold a scale of NaN.
+template <class C, int B, bool AHEAD, bool CODES, class Pre>
 __device__ __forceinline__ void swiglu_half(StageBufs<C>& sm, const acc_t<C>& acc, int wm, int wn, int lane,
                                             const DgradArgs& g, const int32_t* ep_rows, const float* ep_alpha,
                                             int64_t row0, int rows_valid, int n0, int n_valid, int half, Pre pre) {
@@ -731,8 +734,17 @@ __device__ __forceinline__ void swiglu_half(StageBufs<C>& sm, const acc_t<C>& ac
     for (int b = 0; b < B; ++b) {
       const int32_t hr = ep_rows[half * (BM / C::WM) + tr0 + kRowStep * (i0 + b)];
       const int64_t hb = hr >= 0 && col_ok ? (int64_t)hr * ld + n0 + tc : 0;
-      bt.gw[b] = *(const uint4*)(hc + hb);
-      bt.uw[b] = *(const uint4*)(hc + hb + F);
+      if constexpr (CODES) {
+        const int8_t* codes = (const int8_t*)hc + hb;
+        const uint2 qg = *(const uint2*)codes, qu = *(const uint2*)(codes + F);
+        const int groups = scale_groups(F);
+        const uint16_t* sc = g.hscale + (hr >= 0 && col_ok ? (int64_t)hr * 2 * groups + (n0 + tc) / kGroupCols : 0);
+        bt.gw[b] = make_uint4(qg.x, qg.y, sc[0], 0);
+        bt.uw[b] = make_uint4(qu.x, qu.y, sc[groups], 0);
+      } else {
+        bt.gw[b] = *(const uint4*)(hc + hb);
+        bt.uw[b] = *(const uint4*)(hc + hb + F);
+      }
     }
   };
   auto finish = [&](HcBatch<B>& bt, int i0) {
@@ -748,10 +760,22 @@ __device__ __forceinline__ void swiglu_half(StageBufs<C>& sm, const acc_t<C>& ac
       const uint32_t gg[4] = {bt.gw[b].x, bt.gw[b].y, bt.gw[b].z, bt.gw[b].w};
       const uint32_t uu[4] = {bt.uw[b].x, bt.uw[b].y, bt.uw[b].z, bt.uw[b].w};
       float dg[8], du[8];
+      float sg8 = 0.0f, su8 = 0.0f;
+      if constexpr (CODES) {
+        const bool there = ep_rows[half * (BM / C::WM) + r] >= 0;
+        sg8 = there ? __uint_as_float(gg[2] << 16) : 0.0f;
+        su8 = there ? __uint_as_float(uu[2] << 16) : 0.0f;
+      }
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        const float gate = (c & 1) ? bf16_hi(gg[c >> 1]) : bf16_lo(gg[c >> 1]);
-        const float up = (c & 1) ? bf16_hi(uu[c >> 1]) : bf16_lo(uu[c >> 1]);
+        float gate, up;
+        if constexpr (CODES) {
+          gate = (float)(int8_t)(gg[c >> 2] >> (8 * (c & 3))) * sg8;
+          up = (float)(int8_t)(uu[c >> 2] >> (8 * (c & 3))) * su8;
+        } else {
+          gate = (c & 1) ? bf16_hi(gg[c >> 1]) : bf16_lo(gg[c >> 1]);
+          up = (c & 1) ? bf16_hi(uu[c >> 1]) : bf16_lo(uu[c >> 1]);
+        }
         // sigmoid from the hardware base-2 exponential and reciprocal (about 1 ulp each; the
         // result is rounded to bf16): 1 / (1 + 2^(-gate log2 e))
         const float sg = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(gate * -1.44269504088896341f));
@@ -790,7 +814,7 @@ __device__ __forceinline__ void swiglu_half(StageBufs<C>& sm, const acc_t<C>& ac
 // my_row: for threads below BM, the HC row of tile row threadIdx.x (-1: none), loaded before
 // the K loop. Its routing weight is loaded here, beside the first [gate | up] loads, and
 // written to LDS before the first half is staged.
-template <class C>
+template <class C, bool CODES>
 __device__ __forceinline__ void epilogue_swiglu(StageBufs<C>& sm, const acc_t<C>& acc, int wm, int wn, int lane,
                                                 const DgradArgs& g, int32_t* ep_rows, float* ep_alpha,
                                                 int32_t my_row, int64_t row0, int rows_valid, int n0,
@@ -805,8 +829,8 @@ __device__ __forceinline__ void epilogue_swiglu(StageBufs<C>& sm, const acc_t<C>
     if (t < BM) ep_alpha[t] = my_alpha;
   };
   auto pre1 = [] {};
-  swiglu_half<C, 4, true>(sm, acc, wm, wn, lane, g, ep_rows, ep_alpha, row0, rows_valid, n0, n_valid, 0, pre0);
-  swiglu_half<C, 4, true>(sm, acc, wm, wn, lane, g, ep_rows, ep_alpha, row0, rows_valid, n0, n_valid, 1, pre1);
+  swiglu_half<C, 4, true, CODES>(sm, acc, wm, wn, lane, g, ep_rows, ep_alpha, row0, rows_valid, n0, n_valid, 0, pre0);
+  swiglu_half<C, 4, true, CODES>(sm, acc, wm, wn, lane, g, ep_rows, ep_alpha, row0, rows_valid, n0, n_valid, 1, pre1);
 }
 
 // The kernel's one LDS object: the stage buffers (both forms), then for EPI_SWIGLU the
@@ -827,6 +851,8 @@ struct DgradShared<C, EPI_SWIGLU> {
   int32_t ep_rows[BM];  // SwiGLU epilogue: HC row of each tile row (-1: none)
   float ep_alpha[BM];   // and its routing weight
 };
+template <class C>
+struct DgradShared<C, EPI_SWIGLU_CODES> : DgradShared<C, EPI_SWIGLU> {};
 
 // One output tile per block.
 template <int EPI>
@@ -858,7 +884,7 @@ __global__ LRMOE_GEMM_ATTR(CfgD) void dgrad_kernel(DgradArgs g) {
   // SwiGLU epilogue: thread t < BM fetches tile row t's HC row now, so that the value is in a
   // register by the end of the K loop
   int32_t my_row = -1;
-  if (EPI == EPI_SWIGLU && (int)threadIdx.x < rows_valid) {
+  if (EPI != EPI_STORE && (int)threadIdx.x < rows_valid) {
     const int64_t j = g.hc_rows != nullptr ? (int64_t)g.hc_rows[row0 + threadIdx.x] : row0 + threadIdx.x;
     my_row = j >= 0 && j < g.hc_nrows ? (int32_t)j : -1;
   }
@@ -876,8 +902,8 @@ __global__ LRMOE_GEMM_ATTR(CfgD) void dgrad_kernel(DgradArgs g) {
   init(la, lb);
   gemm_mainloop_k64<C>(lds_all.k64, la, lb, g.K, acc, wm, wn, lane);
 
-  if constexpr (EPI == EPI_SWIGLU) {
-    epilogue_swiglu<C>(lds, acc, wm, wn, lane, g, lds_all.ep_rows, lds_all.ep_alpha, my_row, row0, rows_valid, n0,
+  if constexpr (EPI != EPI_STORE) {
+    epilogue_swiglu<C, EPI == EPI_SWIGLU_CODES>(lds, acc, wm, wn, lane, g, lds_all.ep_rows, lds_all.ep_alpha, my_row, row0, rows_valid, n0,
                        n_valid);
   } else if (g.alpha == nullptr) {  // uniform
     uint16_t* __restrict__ out = g.out;
@@ -916,7 +942,8 @@ struct FwdArgs {
   const float* alpha;   // [N] routing weights
   const uint16_t* W1;   // [E x D x 2F]
   const uint16_t* W2;   // [E x F x D]
-  uint16_t* H;          // [N x 2F] out
+  uint16_t* H;          // [N x 2F] out (CODES: 8-bit codes, bytes)
+  uint16_t* hscale;     // CODES: out, the scales of their groups [N x 2 x ceil(F / 128)]
   uint16_t* Phi;        // [N x F] out (FC1 launch) / in (FC2 launch)
   uint16_t* Y;          // [N x D] out
   const int64_t* row_off;
@@ -945,7 +972,9 @@ __device__ __forceinline__ bool fwd_tile(const FwdArgs& g, int b, int& e, int64_
 // FC1 tile: 256 pair rows x [128 gate | 128 up] columns j0 = 128 nt; the SwiGLU forward in the
 // epilogue, staged through LDS like epilogue_staged. A thread takes 8 gate columns of a row
 // with the matching 8 up columns and writes both to H and phi = silu(gate) * up (from the
-// fp32 sums, rounded once) to Phi.
+// fp32 sums, rounded once) to Phi. CODES: H leaves as 8-bit codes of the bf16 values; the sixteen lanes of a staged row hold
+// one 128-column group of the gate and one of up.
+template <bool CODES>
 __global__ LRMOE_GEMM_ATTR(CfgW) void fwd_fc1_kernel(FwdArgs g) {
   using C = CfgW;
   __shared__ StageBufs<C> lds;
@@ -975,7 +1004,8 @@ __global__ LRMOE_GEMM_ATTR(CfgW) void fwd_fc1_kernel(FwdArgs g) {
       const int id = threadIdx.x + C::NTHR * i;
       const int r = id / 16, c8 = id % 16;
       const int tr = half * (BM / C::WM) + r, f = j0 + c8 * 8;
-      if (tr < rows_valid && f < F) {
+      const bool on = tr < rows_valid && f < F;
+      if (CODES || on) {
         const float4 g0 = st[r * P + ((2 * c8) ^ (r & 15))], g1 = st[r * P + ((2 * c8 + 1) ^ (r & 15))];
         const float4 u0 = st[r * P + ((32 + 2 * c8) ^ (r & 15))], u1 = st[r * P + ((32 + 2 * c8 + 1) ^ (r & 15))];
         const float gt[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
@@ -988,9 +1018,33 @@ __global__ LRMOE_GEMM_ATTR(CfgW) void fwd_fc1_kernel(FwdArgs g) {
           ph[k] = gt[k] * sg * ut[k];
         }
         const int64_t row = row0 + tr;
-        *(uint4*)(g.H + row * ldh + f) = pack_bf16x8(gt);
-        *(uint4*)(g.H + row * ldh + F + f) = pack_bf16x8(ut);
-        *(uint4*)(g.Phi + row * F + f) = pack_bf16x8(ph);
+        if constexpr (CODES) {
+          const uint4 gw = pack_bf16x8(gt), uw = pack_bf16x8(ut);
+          const uint32_t gb[4] = {gw.x, gw.y, gw.z, gw.w}, ub[4] = {uw.x, uw.y, uw.z, uw.w};
+          float vg[8], vu[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // columns at and past F are zeros (the operand's loads give them)
+            vg[2 * k] = bf16_lo(gb[k]), vg[2 * k + 1] = bf16_hi(gb[k]);
+            vu[2 * k] = bf16_lo(ub[k]), vu[2 * k + 1] = bf16_hi(ub[k]);
+          }
+          uint16_t sg, su;
+          const uint2 cg = group_codes(vg, &sg), cu = group_codes(vu, &su);
+          if (on) {
+            int8_t* q = (int8_t*)g.H + row * ldh + f;
+            *(uint2*)q = cg;
+            *(uint2*)(q + F) = cu;
+            if (c8 == 0) {
+              const int groups = scale_groups(F);
+              g.hscale[row * 2 * groups + nt] = sg;
+              g.hscale[(row * 2 + 1) * groups + nt] = su;
+            }
+            *(uint4*)(g.Phi + row * F + f) = pack_bf16x8(ph);
+          }
+        } else {
+          *(uint4*)(g.H + row * ldh + f) = pack_bf16x8(gt);
+          *(uint4*)(g.H + row * ldh + F + f) = pack_bf16x8(ut);
+          *(uint4*)(g.Phi + row * F + f) = pack_bf16x8(ph);
+        }
       }
     }
   }
@@ -1324,6 +1378,7 @@ __global__ __launch_bounds__(kAuxThr) void f32_dgrad_kernel(const float* __restr
                                                          int64_t w_estride, int N, int K,
                                                          const int64_t* __restrict__ row_off, int E,
                                                          const float* __restrict__ HC,
+                                                         const uint16_t* __restrict__ hscale,
                                                          const int32_t* __restrict__ hc_rows, int64_t hc_nrows,
                                                          float* __restrict__ out, int64_t ldo, int F) {
   const int64_t r = blockIdx.x;
@@ -1340,8 +1395,17 @@ __global__ __launch_bounds__(kAuxThr) void f32_dgrad_kernel(const float* __restr
   const int64_t hr = hc_rows != nullptr ? (int64_t)hc_rows[r] : r;
   const bool ok = hr >= 0 && hr < hc_nrows;  // rows outside HC read as zeros
   if (alpha != nullptr) acc *= ok ? alpha[hr] : 0.0f;
-  if (EPI == EPI_SWIGLU) {
-    const float gate = ok ? HC[hr * 2 * F + n] : 0.0f, up = ok ? HC[hr * 2 * F + F + n] : 0.0f;
+  if (EPI != EPI_STORE) {
+    float gate = 0.0f, up = 0.0f;
+    if (ok && EPI == EPI_SWIGLU_CODES) {
+      const int8_t* q = (const int8_t*)HC + hr * 2 * F + n;
+      const uint16_t* sc = hscale + hr * 2 * scale_groups(F) + n / kGroupCols;
+      gate = (float)q[0] * scale_of(sc[0]);
+      up = (float)q[F] * scale_of(sc[scale_groups(F)]);
+    } else if (ok) {
+      gate = HC[hr * 2 * F + n];
+      up = HC[hr * 2 * F + F + n];
+    }
     const float s = 1.0f / (1.0f + expf(-gate));
     out[r * 2 * F + n] = acc * up * (s * (1.0f + gate * (1.0f - s)));
     out[r * 2 * F + F + n] = acc * (gate * s);
@@ -1524,7 +1588,7 @@ WgradSchedule wgrad_schedule(const lrmoe_problem* p, const int64_t* row_off_h) {
 
 lrmoe_status launch_expert_forward(const lrmoe_problem* p, const int64_t* seg_off_d, const void* X,
                                    const int32_t* tok, const float* alpha, const void* W1, const void* W2, void* H,
-                                   void* Phi, void* Y, hipStream_t s) {
+                                   uint16_t* hscale, void* Phi, void* Y, hipStream_t s) {
   int64_t mtiles = 0;
   for (int e = 0; e < p->E; ++e) mtiles += ceil_div(p->seg_off[e + 1] - p->seg_off[e], BM);
   if (mtiles == 0) return LRMOE_OK;
@@ -1536,6 +1600,7 @@ lrmoe_status launch_expert_forward(const lrmoe_problem* p, const int64_t* seg_of
   g.W1 = (const uint16_t*)W1;
   g.W2 = (const uint16_t*)W2;
   g.H = (uint16_t*)H;
+  g.hscale = hscale;
   g.Phi = (uint16_t*)Phi;
   g.Y = (uint16_t*)Y;
   g.row_off = seg_off_d;
@@ -1543,7 +1608,8 @@ lrmoe_status launch_expert_forward(const lrmoe_problem* p, const int64_t* seg_of
   g.D = p->D;
   g.F = p->F;
   g.ntn = (int)ceil_div(p->F, 128);
-  fwd_fc1_kernel<<<(unsigned)(mtiles * g.ntn), CfgW::NTHR, 0, s>>>(g);
+  if (hscale) fwd_fc1_kernel<true><<<(unsigned)(mtiles * g.ntn), CfgW::NTHR, 0, s>>>(g);
+  else fwd_fc1_kernel<false><<<(unsigned)(mtiles * g.ntn), CfgW::NTHR, 0, s>>>(g);
   g.ntn = (int)ceil_div(p->D, BN);
   fwd_fc2_kernel<<<(unsigned)(mtiles * g.ntn), CfgW::NTHR, 0, s>>>(g);
   return launch_status();
@@ -1557,7 +1623,7 @@ size_t gemm_ws_bytes(const lrmoe_problem* p, const int64_t* row_off_h) {
 
 lrmoe_status launch_grouped_gemm_bwd(const lrmoe_problem* p, const int64_t* row_off_h,
                                      const int64_t* row_off_d, const void* Dlt, const void* PhiC,
-                                     const void* XC, const void* HC, const int32_t* hc_rows,
+                                     const void* XC, const void* HC, const uint16_t* hscale, const int32_t* hc_rows,
                                      const int32_t* phi_rows, const int32_t* x_rows, const int32_t* dlt_rows,
                                      const float* alpha, const void* W2, const void* W1,
                                      float* dW2, float* dW1, void* dH, void* dIn, int accumulate,
@@ -1578,12 +1644,15 @@ lrmoe_status launch_grouped_gemm_bwd(const lrmoe_problem* p, const int64_t* row_
     const float* dl = (const float*)Dlt;
     if (p->swiglu) {
       if (rows > 0) {
-        f32_dgrad_kernel<EPI_SWIGLU><<<dim3((unsigned)rows, (unsigned)ceil_div(F, kAuxThr)), kAuxThr, 0, s>>>(
-            dl, D, dlt_rows, dlt_nrows, alpha, (const float*)W2, D, (int64_t)F * D, F, D, row_off_d, E,
-            (const float*)HC, hc_rows, hc_nrows, (float*)dH, 2 * F, F);
+        auto fc2 = [&](auto kernel) {
+          kernel<<<dim3((unsigned)rows, (unsigned)ceil_div(F, kAuxThr)), kAuxThr, 0, s>>>(
+              dl, D, dlt_rows, dlt_nrows, alpha, (const float*)W2, D, (int64_t)F * D, F, D, row_off_d, E,
+              (const float*)HC, hscale, hc_rows, hc_nrows, (float*)dH, 2 * F, F);
+        };
+        hscale ? fc2(f32_dgrad_kernel<EPI_SWIGLU_CODES>) : fc2(f32_dgrad_kernel<EPI_SWIGLU>);
         f32_dgrad_kernel<EPI_STORE><<<dim3((unsigned)rows, (unsigned)ceil_div(D, kAuxThr)), kAuxThr, 0, s>>>(
             (const float*)dH, 2 * F, nullptr, 0, nullptr, (const float*)W1, 2 * F, (int64_t)D * 2 * F, D, 2 * F,
-            row_off_d, E, nullptr, nullptr, 0, (float*)dIn, D, F);
+            row_off_d, E, nullptr, nullptr, nullptr, 0, (float*)dIn, D, F);
       }
       if (mark_din() != LRMOE_OK) return LRMOE_ERR_HIP;
       if (E > 0) {
@@ -1597,7 +1666,7 @@ lrmoe_status launch_grouped_gemm_bwd(const lrmoe_problem* p, const int64_t* row_
       if (rows > 0)
         f32_dgrad_kernel<EPI_STORE><<<dim3((unsigned)rows, (unsigned)ceil_div(F, kAuxThr)), kAuxThr, 0, s>>>(
             dl, D, dlt_rows, dlt_nrows, alpha, (const float*)W2, D, (int64_t)F * D, F, D, row_off_d, E, nullptr,
-            hc_rows, hc_nrows, (float*)dIn, F, F);
+            nullptr, hc_rows, hc_nrows, (float*)dIn, F, F);
       if (mark_din() != LRMOE_OK) return LRMOE_ERR_HIP;
       if (E > 0)
         f32_wgrad_kernel<<<dim3((unsigned)ceil_div(D, kAuxThr), F, E), kAuxThr, 0, s>>>(
@@ -1628,9 +1697,13 @@ lrmoe_status launch_grouped_gemm_bwd(const lrmoe_problem* p, const int64_t* row_
   d2.F = F;
   if (p->swiglu) {
     d2.HC = (const uint16_t*)HC;
+    d2.hscale = hscale;
     d2.out = (uint16_t*)dH;
     d2.ldo = 2 * F;
-    if (mtiles > 0) dgrad_kernel<EPI_SWIGLU><<<(unsigned)(mtiles * d2.ntn), CfgD::NTHR, 0, s>>>(d2);
+    if (mtiles > 0) {
+      if (hscale) dgrad_kernel<EPI_SWIGLU_CODES><<<(unsigned)(mtiles * d2.ntn), CfgD::NTHR, 0, s>>>(d2);
+      else dgrad_kernel<EPI_SWIGLU><<<(unsigned)(mtiles * d2.ntn), CfgD::NTHR, 0, s>>>(d2);
+    }
     DgradArgs d1 = d2;
     d1.A = (const uint16_t*)dH;
     d1.lda = 2 * F;

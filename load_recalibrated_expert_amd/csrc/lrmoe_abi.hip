@@ -266,17 +266,75 @@ lrmoe_status lrmoe_score_criterion(const lrmoe_problem* p, lrmoe_criterion crite
                                (hipStream_t)stream);
 }
 
-lrmoe_status lrmoe_expert_forward(const lrmoe_problem* p, const int64_t* seg_off_d, const void* X,
-                                  const int32_t* tok, const float* alpha, const void* W1, const void* W2,
-                                  void* H, void* Phi, void* Y, lrmoe_stream_t stream) {
-  LRMOE_TRY(check_problem(p, nullptr, nullptr));
+static lrmoe_status forward_checked(const lrmoe_problem* p, const int64_t* seg_off_d, const void* X, const int32_t* tok,
+                                    const float* alpha, const void* W1, const void* W2, void* H, uint16_t* hscale,
+                                    void* Phi, void* Y, lrmoe_stream_t stream) {
   if (p->dtype != LRMOE_BF16 || p->swiglu != 1) return LRMOE_ERR_UNSUPPORTED;
   if (p->N == 0) return LRMOE_OK;
   if (!seg_off_d || !X || !tok || !alpha || !W1 || !W2 || !H || !Phi || !Y) return LRMOE_ERR_INVALID_ARG;
   const int64_t lim = (int64_t)1 << 31;
   if ((int64_t)p->T * p->D * 2 >= lim || (int64_t)p->D * 2 * p->F * 2 >= lim || (int64_t)p->F * p->D * 2 >= lim)
     return LRMOE_ERR_UNSUPPORTED;
-  return launch_expert_forward(p, seg_off_d, X, tok, alpha, W1, W2, H, Phi, Y, (hipStream_t)stream);
+  return launch_expert_forward(p, seg_off_d, X, tok, alpha, W1, W2, H, hscale, Phi, Y, (hipStream_t)stream);
+}
+
+lrmoe_status lrmoe_expert_forward(const lrmoe_problem* p, const int64_t* seg_off_d, const void* X,
+                                  const int32_t* tok, const float* alpha, const void* W1, const void* W2,
+                                  void* H, void* Phi, void* Y, lrmoe_stream_t stream) {
+  LRMOE_TRY(check_problem(p, nullptr, nullptr));
+  return forward_checked(p, seg_off_d, X, tok, alpha, W1, W2, H, nullptr, Phi, Y, stream);
+}
+
+lrmoe_status lrmoe_expert_forward_checkpoint(const lrmoe_problem* p, const int64_t* seg_off_d, const void* X,
+                                             const int32_t* tok, const float* alpha, const void* W1, const void* W2,
+                                             int8_t* q, uint16_t* scale, void* Phi, void* Y, lrmoe_stream_t stream) {
+  LRMOE_TRY(check_problem(p, nullptr, nullptr));
+  if ((p->N > 0 && !scale) || !aligned(q, 16) || !aligned(scale, 2)) return LRMOE_ERR_INVALID_ARG;
+  return forward_checked(p, seg_off_d, X, tok, alpha, W1, W2, q, scale, Phi, Y, stream);
+}
+
+static lrmoe_status check_rows(int64_t n, int32_t parts, int32_t width, lrmoe_dtype dtype) {
+  if (n < 0 || parts < 1 || width < 8) return LRMOE_ERR_INVALID_ARG;
+  if (dtype != LRMOE_F32 && dtype != LRMOE_BF16) return LRMOE_ERR_UNSUPPORTED;
+  if (width % 8 != 0 || n >= ((int64_t)1 << 40) || parts >= (1 << 16)) return LRMOE_ERR_UNSUPPORTED;
+  // four threads to a group, of which a launch takes fewer than 2^32
+  return (double)n * parts * ((width + 127) / 128) >= (double)(1 << 30) ? LRMOE_ERR_UNSUPPORTED : LRMOE_OK;
+}
+
+lrmoe_status lrmoe_checkpoint(int64_t n, int32_t parts, int32_t width, lrmoe_dtype dtype, const void* rows, int8_t* q,
+                              uint16_t* scale, lrmoe_stream_t stream) {
+  LRMOE_TRY(check_rows(n, parts, width, dtype));
+  if (n == 0) return LRMOE_OK;
+  if (!rows || !q || !scale || !aligned(rows, 16) || !aligned(q, 16) || !aligned(scale, 2)) return LRMOE_ERR_INVALID_ARG;
+  return launch_checkpoint(n, parts, width, dtype, rows, q, scale, (hipStream_t)stream);
+}
+
+lrmoe_status lrmoe_restore(int64_t n, int32_t parts, int32_t width, const int8_t* q, const uint16_t* scale,
+                           lrmoe_dtype dtype, void* rows, lrmoe_stream_t stream) {
+  LRMOE_TRY(check_rows(n, parts, width, dtype));
+  if (n == 0) return LRMOE_OK;
+  if (!rows || !q || !scale || !aligned(rows, 16) || !aligned(q, 16) || !aligned(scale, 2)) return LRMOE_ERR_INVALID_ARG;
+  return launch_restore(n, parts, width, q, scale, dtype, rows, (hipStream_t)stream);
+}
+
+lrmoe_status lrmoe_score_checkpoint(const lrmoe_problem* p, const void* G, const int8_t* q, const uint16_t* scale,
+                                    const float* alpha, const int32_t* tok, float* R, void* ws, size_t ws_bytes,
+                                    lrmoe_stream_t stream) {
+  LRMOE_TRY(check_problem(p, nullptr, nullptr));
+  if ((p->T > 0 && !G) || (p->N > 0 && (!q || !scale || !alpha || !tok || !R))) return LRMOE_ERR_INVALID_ARG;
+  if (!aligned(G, 16) || !aligned(q, 16) || !aligned(scale, 2)) return LRMOE_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < align_up(sizeof(double) * (size_t)p->T, 256)) return LRMOE_ERR_WORKSPACE;
+  return launch_score_checkpoint(p, G, q, scale, alpha, tok, R, (double*)ws, (hipStream_t)stream);
+}
+
+lrmoe_status lrmoe_compact_checkpoint(const lrmoe_problem* p, const int32_t* sel, const int8_t* q,
+                                      const uint16_t* scale, const float* alpha, void* PhiW, lrmoe_stream_t stream) {
+  int64_t K_tot = 0;
+  LRMOE_TRY(check_problem(p, &K_tot, nullptr));
+  if (K_tot == 0) return LRMOE_OK;
+  if (!sel || !q || !scale || !alpha || !PhiW) return LRMOE_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(scale, 2) || !aligned(PhiW, 16)) return LRMOE_ERR_INVALID_ARG;
+  return launch_compact_checkpoint(p, K_tot, sel, q, scale, alpha, PhiW, (hipStream_t)stream);
 }
 
 lrmoe_status lrmoe_select(const lrmoe_problem* p, const float* R, const int64_t* seg_off_d,
@@ -364,7 +422,7 @@ lrmoe_status lrmoe_grouped_gemm_bwd(const lrmoe_problem* p, lrmoe_compact_mode m
     return LRMOE_ERR_UNSUPPORTED;
   if (ws_bytes < gemm_ws_bytes(p, row_off_h) || (!ws && gemm_ws_bytes(p, row_off_h) > 0))
     return LRMOE_ERR_WORKSPACE;
-  return launch_grouped_gemm_bwd(p, row_off_h, row_off_d, Dlt, PhiC, XC, HC, hc_rows, phi_rows, x_rows, nullptr,
+  return launch_grouped_gemm_bwd(p, row_off_h, row_off_d, Dlt, PhiC, XC, HC, nullptr, hc_rows, phi_rows, x_rows, nullptr,
                                  nullptr, W2, W1, dW2, dW1, dH, dIn, accumulate, ws, (hipStream_t)stream,
                                  (hipEvent_t)din_ready);
 }
@@ -378,12 +436,11 @@ lrmoe_status lrmoe_compact_weighted(const lrmoe_problem* p, const int32_t* sel, 
   return launch_compact_weighted_phi(p, K_tot, sel, Phi, alpha, PhiW, (hipStream_t)stream);
 }
 
-lrmoe_status lrmoe_grouped_gemm_bwd_gathered(const lrmoe_problem* p, const int64_t* cseg_off_d, const void* G,
-                                             const float* alpha, const int32_t* sel, const int32_t* ctok,
-                                             const void* PhiW, const void* X, const void* H, const void* W2,
-                                             const void* W1, float* dW2, float* dW1, void* dH, void* dIn,
-                                             int32_t accumulate, void* ws, size_t ws_bytes, lrmoe_stream_t stream,
-                                             lrmoe_event_t din_ready) {
+static lrmoe_status gathered_checked(const lrmoe_problem* p, const int64_t* cseg_off_d, const void* G,
+                                     const float* alpha, const int32_t* sel, const int32_t* ctok, const void* PhiW,
+                                     const void* X, const void* H, const uint16_t* hscale, const void* W2,
+                                     const void* W1, float* dW2, float* dW1, void* dH, void* dIn, int32_t accumulate,
+                                     void* ws, size_t ws_bytes, lrmoe_stream_t stream, lrmoe_event_t din_ready) {
   std::vector<int64_t> cseg;
   int64_t K_tot = 0;
   LRMOE_TRY(check_problem(p, &K_tot, &cseg));
@@ -400,9 +457,32 @@ lrmoe_status lrmoe_grouped_gemm_bwd_gathered(const lrmoe_problem* p, const int64
   if ((int64_t)p->T * p->D * esz >= ((int64_t)1 << 31)) return LRMOE_ERR_UNSUPPORTED;
   const size_t need = gemm_ws_bytes(p, cseg.data());
   if (ws_bytes < need || (!ws && need > 0)) return LRMOE_ERR_WORKSPACE;
-  return launch_grouped_gemm_bwd(p, cseg.data(), cseg_off_d, G, PhiW, X, H, sel, nullptr, p->swiglu ? ctok : nullptr,
-                                 ctok, alpha, W2, W1, dW2, dW1, dH, dIn, accumulate, ws, (hipStream_t)stream,
-                                 (hipEvent_t)din_ready);
+  return launch_grouped_gemm_bwd(p, cseg.data(), cseg_off_d, G, PhiW, X, H, hscale, sel, nullptr,
+                                 p->swiglu ? ctok : nullptr, ctok, alpha, W2, W1, dW2, dW1, dH, dIn, accumulate, ws,
+                                 (hipStream_t)stream, (hipEvent_t)din_ready);
+}
+
+lrmoe_status lrmoe_grouped_gemm_bwd_gathered(const lrmoe_problem* p, const int64_t* cseg_off_d, const void* G,
+                                             const float* alpha, const int32_t* sel, const int32_t* ctok,
+                                             const void* PhiW, const void* X, const void* H, const void* W2,
+                                             const void* W1, float* dW2, float* dW1, void* dH, void* dIn,
+                                             int32_t accumulate, void* ws, size_t ws_bytes, lrmoe_stream_t stream,
+                                             lrmoe_event_t din_ready) {
+  return gathered_checked(p, cseg_off_d, G, alpha, sel, ctok, PhiW, X, H, nullptr, W2, W1, dW2, dW1, dH, dIn, accumulate,
+                          ws, ws_bytes, stream, din_ready);
+}
+
+lrmoe_status lrmoe_grouped_gemm_bwd_checkpoint(const lrmoe_problem* p, const int64_t* cseg_off_d, const void* G,
+                                               const float* alpha, const int32_t* sel, const int32_t* ctok,
+                                               const void* PhiW, const void* X, const int8_t* q, const uint16_t* scale,
+                                               const void* W2, const void* W1, float* dW2, float* dW1, void* dH,
+                                               void* dIn, int32_t accumulate, void* ws, size_t ws_bytes,
+                                               lrmoe_stream_t stream, lrmoe_event_t din_ready) {
+  LRMOE_TRY(check_problem(p, nullptr, nullptr));
+  if (!p->swiglu) return LRMOE_ERR_UNSUPPORTED;  // nothing of it reads the saved rows
+  if (!scale || !aligned(q, 16) || !aligned(scale, 2)) return LRMOE_ERR_INVALID_ARG;
+  return gathered_checked(p, cseg_off_d, G, alpha, sel, ctok, PhiW, X, q, scale, W2, W1, dW2, dW1, dH, dIn, accumulate,
+                          ws, ws_bytes, stream, din_ready);
 }
 
 lrmoe_status lrmoe_scatter(const lrmoe_problem* p, lrmoe_scatter_mode mode, int64_t n_rows, int32_t width,

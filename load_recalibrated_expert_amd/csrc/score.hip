@@ -105,18 +105,22 @@ lrmoe_status launch_score_gradient(const lrmoe_problem* p, bool magnitude, const
   return launch_status();
 }
 
+void launch_token_sqnorm(const lrmoe_problem* p, const void* G, double* gn, hipStream_t s) {
+  const bool bf16 = p->dtype == LRMOE_BF16;
+  const int gch = p->D * (bf16 ? 2 : 4) / 16;
+  if (p->T <= 0) return;
+  dim3 grid((unsigned)ceil_div(p->T, kScoreThreads / kWave));
+  if (bf16)
+    token_sqnorm_kernel<true><<<grid, kScoreThreads, 0, s>>>((const uint4*)G, p->T, gch, gn);
+  else
+    token_sqnorm_kernel<false><<<grid, kScoreThreads, 0, s>>>((const uint4*)G, p->T, gch, gn);
+}
+
 lrmoe_status launch_score(const lrmoe_problem* p, const void* G, const void* Phi, const float* alpha,
                           const int32_t* tok, float* R, double* gn, hipStream_t s) {
   const bool bf16 = p->dtype == LRMOE_BF16;
-  const int esz = bf16 ? 2 : 4;
-  const int gch = p->D * esz / 16, pch = p->F * esz / 16;
-  if (p->T > 0) {
-    dim3 grid((unsigned)ceil_div(p->T, kScoreThreads / kWave));
-    if (bf16)
-      token_sqnorm_kernel<true><<<grid, kScoreThreads, 0, s>>>((const uint4*)G, p->T, gch, gn);
-    else
-      token_sqnorm_kernel<false><<<grid, kScoreThreads, 0, s>>>((const uint4*)G, p->T, gch, gn);
-  }
+  const int pch = p->F * (bf16 ? 2 : 4) / 16;
+  launch_token_sqnorm(p, G, gn, s);
   if (p->N > 0) {
     dim3 grid((unsigned)ceil_div(p->N, kScoreThreads / 16));
     if (bf16)
