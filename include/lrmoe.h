@@ -517,9 +517,10 @@ lrmoe_status lrmoe_scoring_check(const lrmoe_router* r, const lrmoe_scoring* c);
  * the lower index first; -1 in slots without one.
  *   w[t, k] = scale * s_k                     renorm = 0
  *             scale * s_k / sum_j s_idx_j     renorm = 1, over the token's chosen experts; no sum underflows
- * The bias is no part of w. Choice scores are f64 and compared to 42 bits (scores that differ by less, relative,
- * may count as equal); sigmoid scores without bias and groups are chosen by the logits, exactly. A sigmoid logit below
- * -700 counts as -700 in the choice. Deterministic. */
+ * The bias is no part of w. Without a bias experts are chosen by their logits (whose order is that of the scores),
+ * exactly. Choice scores with a bias, and groups' sums of scores, are f64; choice scores are compared to 42 bits and sums
+ * to 44 (what differs by less, relative, may count as equal). A sigmoid logit below -700 counts as -700 in the choice.
+ * Deterministic. */
 lrmoe_status lrmoe_route_scored(const lrmoe_router* r, const lrmoe_scoring* c, const void* logits, const float* bias,
                                 const uint8_t* mask, int32_t* idx, float* w, int32_t* counts, int64_t* seg_off,
                                 int32_t* tok, int32_t* slot, float* alpha, int32_t* pmap, void* ws, size_t ws_bytes,

@@ -21,12 +21,12 @@ namespace {
 // smaller ones than the scan loses by more rows: above 320 experts, where a token has sixteen or more
 // lanes whatever K (16384 x 512 in chunks of 128 22 us, of 64 14.5 us), and with more than 256 chunks
 // (50021 x 257 in chunks of 128 23.6 us, of 104 21.8 us). With 9 to 32 slots sixteen lanes begin at 257
-// experts; chunks of 64 there were not measured.
-int route_chunk(const lrmoe_router* r) {
+// experts; chunks of 64 there were not measured. Routing by scores costs more a token: 64 tokens always.
+int route_chunk(const lrmoe_router* r, bool scored) {
   if (r->T <= kOneChunk) return kOneChunk;
   const int64_t even = align_up((size_t)ceil_div(r->T, r->T <= 256 * 128 ? 256 : 512), 8);
   const int64_t room = (int64_t)kPlaceLds / 4 / r->local * 32;  // whose bits fit
-  return (int)std::min(std::max(even, (int64_t)(r->E > 320 || r->T > 256 * 128 ? 64 : 128)),
+  return (int)std::min(std::max(even, (int64_t)(scored || r->E > 320 || r->T > 256 * 128 ? 64 : 128)),
                        std::min<int64_t>(room, 1024));
 }
 
@@ -762,7 +762,7 @@ lrmoe_status by_slots(const lrmoe_router* r, F&& f) {
 }  // namespace
 
 size_t route_ws_bytes(const lrmoe_router* r) {
-  const size_t rows = (size_t)ceil_div(r->T, route_chunk(r)), E8 = align_up(r->E, 8);
+  const size_t rows = (size_t)ceil_div(r->T, route_chunk(r, true)), E8 = align_up(r->E, 8);  // the smaller chunks
   const size_t hist = align_up(rows * E8 * 2, 256);
   return std::max<size_t>(256, rows > kOwnRows ? hist + align_up((rows + 1) * E8 * 4, 256) : hist);
 }
@@ -770,7 +770,7 @@ size_t route_ws_bytes(const lrmoe_router* r) {
 lrmoe_status launch_route(const lrmoe_router* r, const lrmoe_scoring* c, const void* logits, const float* bias,
                           const uint8_t* mask, int32_t* idx, float* w, int32_t* counts, int64_t* seg_off, int32_t* tok,
                           int32_t* slot, float* alpha, int32_t* pmap, void* ws, hipStream_t s) {
-  const int C = route_chunk(r), rows = (int)ceil_div(r->T, C);
+  const int C = route_chunk(r, c != nullptr), rows = (int)ceil_div(r->T, C);
   const size_t E8 = align_up(r->E, 8);
   int* prefix = rows > kOwnRows ? (int*)((char*)ws + align_up((size_t)rows * E8 * 2, 256)) : nullptr;
   const size_t bits = 4 * (size_t)bit_words(C, r->local), cnt = (size_t)r->E * 4, pairs = (size_t)C * r->K * 8;

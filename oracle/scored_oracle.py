@@ -39,8 +39,8 @@ def choice_scores(x, score, bias=None):
     return np.where((x > -np.inf) & (b > -np.inf)[None], s + np.where(b > -np.inf, b, 0)[None], -np.inf)
 
 
-# The GPU computes scores and their group sums in f64 and compares choice scores to 42 bits, so scores whose f64 values
-# here and there agree to this, relative, may come in either order.
+# The GPU compares choice scores to 42 bits and group sums to 44, so those that agree to this, relative, may come in
+# either order.
 NEAR = 2.0 ** -41
 
 
@@ -52,10 +52,10 @@ def _of_groups(c, groups, group_best):
     return found
 
 
-def _check_near(c, idx, groups, top_groups, group_best):
-    """That the choice of a token is one of those that NEAR allows."""
+def _check_near(c, scores, by_logit, idx, groups, top_groups, group_best):
+    """That the choice of a token is one of those that NEAR allows; logits are compared exactly."""
     size, chosen = len(c) // groups, [int(e) for e in idx if e >= 0]
-    of_group = _of_groups(c, groups, group_best)
+    of_group = _of_groups(scores, groups, group_best)
     there = sorted((g for g in range(groups) if of_group[g] > -np.inf), key=lambda g: (-of_group[g], g))
     kept = there[:top_groups]
     if len(there) > top_groups:
@@ -70,7 +70,7 @@ def _check_near(c, idx, groups, top_groups, group_best):
     assert len(set(chosen)) == len(chosen) == min(len(idx), len(left)) and set(chosen) <= set(left)
     for k, e in enumerate(chosen):
         best = max(c[f] for f in left if f not in chosen[:k])
-        assert c[e] >= best - NEAR * abs(best)
+        assert c[e] >= best - (0 if by_logit else NEAR * abs(best))
 
 
 def route(logits, K, score, bias=None, groups=1, top_groups=1, group_best=1, mask=None, first=0, local=None, renorm=False,
@@ -79,17 +79,17 @@ def route(logits, K, score, bias=None, groups=1, top_groups=1, group_best=1, mas
     x = clean(logits, mask)
     T, E = x.shape
     local, size = E - first if local is None else local, E // groups
-    by_logit = score == "sigmoid" and bias is None and groups == top_groups
-    c = np.where(x > -np.inf, x, -np.inf) if by_logit else choice_scores(x, score, bias)
+    scores = choice_scores(x, score, bias)
+    c = x if bias is None else scores  # without a bias by the logits, whose order is that of the scores
     idx = np.full((T, K), -1, np.int32)
     for t in range(T):
-        of_group = _of_groups(c[t], groups, group_best)
+        of_group = _of_groups(scores[t], groups, group_best)
         kept = sorted((g for g in range(groups) if of_group[g] > -np.inf), key=lambda g: (-of_group[g], g))[:top_groups]
         order = sorted((e for g in kept for e in range(g * size, (g + 1) * size) if c[t, e] > -np.inf),
                        key=lambda e: (-c[t, e], e))[:K]
         idx[t, :len(order)] = order
-        if given is not None and not by_logit and not np.array_equal(given[t], idx[t]):
-            _check_near(c[t], given[t], groups, top_groups, group_best)
+        if given is not None and not np.array_equal(given[t], idx[t]):
+            _check_near(c[t], scores[t], bias is None, given[t], groups, top_groups, group_best)
             idx[t] = given[t]
     ok = idx >= 0
     at = np.maximum(idx, 0)

@@ -109,7 +109,7 @@ def _outs(r, fill=-7):
 
 
 def _reference(r, x, b, mask, o):
-    # scores over 0.5 that differ by less than 2^-41 come from logits over 28 here ("large"): 1 - s = exp(-28) = 7e-13
+    # group sums of scores that differ by less than 2^-41 come from logits over 28 here ("large"): exp(-28) = 7e-13
     return so.route(_host(x), r.K, r.score, _host(b), r.groups, r.top_groups, r.group_best, _host(mask), r.first, r.local,
                     r.renorm, r.scale, given=o["idx"].cpu().numpy())
 
