@@ -2,7 +2,10 @@
 // from codes, and the weighted rows of the retained pairs.
 //
 // All are one pass over memory: a code and a scale's part (1.016 bytes a value) beside the 2 or 4 bytes of the rows.
+#include <type_traits>
+
 #include "checkpoint_device.h"
+#include "score_device.h"
 
 namespace lrmoe {
 namespace {
@@ -10,6 +13,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kUnits = 4;                                    // groups of a lane in flight
 constexpr int kPerBlock = kThreads / kGroupLanes * kUnits;   // groups of a block
+
+// Words of 16 bytes of gradient rows, read once a pair, up to which scoring takes one launch (8 pairs to a token, rows of
+// 2048 bf16: 512 tokens 8.5 us with one launch and 10.7 with two, 1024 tokens 10.9 and 10.8, 2048 tokens 16.7 and 13.6).
+constexpr int64_t kFewWords = 1 << 21;
 
 // Where the eight columns of this lane's group `unit` are: rows of `width` in groups of 128, the last one short.
 struct Place {
@@ -105,18 +112,13 @@ __global__ __launch_bounds__(kThreads) void restore_kernel(Place p, const int8_t
   }
 }
 
-// Sixteen lanes to a pair, four groups of its row in flight. Squares and sums in fp64.
+// Sum of squares of phi of pair j, by sixteen lanes, four groups of its row in flight; sums over chunks in fp64.
 template <bool SWIGLU>
-__global__ __launch_bounds__(kThreads) void pair_score_codes_kernel(const int8_t* __restrict__ q,
-                                                                    const uint16_t* __restrict__ scale,
-                                                                    const float* __restrict__ alpha,
-                                                                    const int32_t* __restrict__ tok,
-                                                                    const double* __restrict__ gn, int64_t N, int T, int F,
-                                                                    float* __restrict__ R) {
+__device__ __forceinline__ double pair_sqnorm(const int8_t* __restrict__ q, const uint16_t* __restrict__ scale, int64_t j,
+                                              bool on, int F) {
   const int lane = threadIdx.x & (kGroupLanes - 1), groups = scale_groups(F), chunks = F / 8;
-  const int64_t j = (int64_t)blockIdx.x * (kThreads / kGroupLanes) + threadIdx.x / kGroupLanes;
   double acc = 0.0;
-  if (j < N) {
+  if (on) {
     for (int c0 = lane; c0 < chunks; c0 += kGroupLanes * kUnits) {
       PhiChunk<SWIGLU> p[kUnits];
 #pragma unroll
@@ -126,22 +128,74 @@ __global__ __launch_bounds__(kThreads) void pair_score_codes_kernel(const int8_t
         else p[u].zero();
       }
 #pragma unroll
-      for (int u = 0; u < kUnits; ++u) {
-        float v[8];
-        p[u].phi(v);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) acc = __builtin_fma((double)v[k], (double)v[k], acc);
-      }
+      for (int u = 0; u < kUnits; ++u) acc = __builtin_fma((double)p[u].sqnorm_of_codes(), p[u].scale_sq(), acc);
     }
   }
 #pragma unroll
   for (int o = kGroupLanes / 2; o > 0; o >>= 1) acc += __shfl_xor(acc, o, kGroupLanes);
-  if (lane == 0 && j < N) {
-    const int t = tok[j];
-    const double g = (t >= 0 && t < T) ? gn[t] : 0.0;  // out-of-range tokens score 0
-    const double a = (double)alpha[j];
-    R[j] = (float)(a * a * g * acc);
+  return acc;
+}
+
+__device__ __forceinline__ float pair_score(float alpha, double gn, double pn) {
+  const double a = (double)alpha;
+  return (float)(a * a * gn * pn);
+}
+
+// OWN: each pair's lanes take the norm of its gradient row themselves (few pairs, one launch). Else gn has it.
+template <bool SWIGLU, bool BF16, bool OWN>
+__global__ __launch_bounds__(kThreads) void pair_score_codes_kernel(const uint4* __restrict__ G, int T, int words,
+                                                                    const double* __restrict__ gn,
+                                                                    const int8_t* __restrict__ q,
+                                                                    const uint16_t* __restrict__ scale,
+                                                                    const float* __restrict__ alpha,
+                                                                    const int32_t* __restrict__ tok, int64_t N, int F,
+                                                                    float* __restrict__ R) {
+  const int lane = threadIdx.x & (kGroupLanes - 1);
+  const int64_t j = (int64_t)blockIdx.x * (kThreads / kGroupLanes) + threadIdx.x / kGroupLanes;
+  const int t = j < N ? tok[j] : -1;
+  const bool there = t >= 0 && t < T;  // out-of-range tokens score 0
+  double g = 0.0;
+  if (there && !OWN) g = gn[t];
+  if (OWN) {
+    if (there) {
+      const uint4* row = G + (int64_t)t * words;
+#pragma unroll 4
+      for (int c = lane; c < words; c += kGroupLanes) g += BF16 ? sumsq_bf16x8(row[c]) : sumsq_f32x4(row[c]);
+    }
+#pragma unroll
+    for (int o = kGroupLanes / 2; o > 0; o >>= 1) g += __shfl_xor(g, o, kGroupLanes);
   }
+  const double pn = pair_sqnorm<SWIGLU>(q, scale, j, j < N, F);
+  if (lane == 0 && j < N) R[j] = pair_score(alpha[j], g, pn);
+}
+
+// Tokens and pairs in one launch, their blocks mixed evenly: the pairs are bound by arithmetic (two transcendental
+// instructions a value), the tokens' rows by HBM. The 32768-token share (262144 pairs of 768): 115 us with the join behind
+// it, 4.7 TB/s; tokens and pairs one after the other 125 us. Block b is the tokens' i-th if the count floor(b step / 2^32) passes i there.
+template <bool SWIGLU, bool BF16>
+__global__ __launch_bounds__(kThreads) void norms_kernel(uint64_t step, const uint4* __restrict__ G, int T, int words,
+                                                         double* __restrict__ gn, const int8_t* __restrict__ q,
+                                                         const uint16_t* __restrict__ scale, int64_t N, int F,
+                                                         double* __restrict__ pn) {
+  const uint64_t before = (blockIdx.x * step) >> 32;
+  if (((blockIdx.x + 1ull) * step) >> 32 != before) {
+    token_sqnorm<BF16, false>(G, T, words, (int64_t)before, gn);
+    return;
+  }
+  const int64_t j = (int64_t)(blockIdx.x - before) * (kThreads / kGroupLanes) + threadIdx.x / kGroupLanes;
+  const double n = pair_sqnorm<SWIGLU>(q, scale, j, j < N, F);
+  if ((threadIdx.x & (kGroupLanes - 1)) == 0 && j < N) pn[j] = n;
+}
+
+__global__ __launch_bounds__(kThreads) void join_scores_kernel(const double* __restrict__ pn,
+                                                               const float* __restrict__ alpha,
+                                                               const int32_t* __restrict__ tok,
+                                                               const double* __restrict__ gn, int64_t N, int T,
+                                                               float* __restrict__ R) {
+  const int64_t j = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (j >= N) return;
+  const int t = tok[j];
+  R[j] = pair_score(alpha[j], t >= 0 && t < T ? gn[t] : 0.0, pn[j]);  // out-of-range tokens score 0
 }
 
 // Sixteen lanes to a packed row.
@@ -216,13 +270,40 @@ lrmoe_status launch_restore(int64_t n, int32_t parts, int32_t width, const int8_
 }
 
 lrmoe_status launch_score_checkpoint(const lrmoe_problem* p, const void* G, const int8_t* q, const uint16_t* scale,
-                                     const float* alpha, const int32_t* tok, float* R, double* gn, hipStream_t s) {
-  launch_token_sqnorm(p, G, gn, s);
-  if (p->N > 0) {
-    const unsigned g = (unsigned)ceil_div(p->N, kThreads / kGroupLanes);
-    if (p->swiglu) pair_score_codes_kernel<true><<<g, kThreads, 0, s>>>(q, scale, alpha, tok, gn, p->N, p->T, p->F, R);
-    else pair_score_codes_kernel<false><<<g, kThreads, 0, s>>>(q, scale, alpha, tok, gn, p->N, p->T, p->F, R);
+                                     const float* alpha, const int32_t* tok, float* R, void* ws, size_t ws_bytes,
+                                     hipStream_t s) {
+  double* gn = (double*)ws;
+  const bool bf16 = p->dtype == LRMOE_BF16;
+  const size_t tokens = align_up(sizeof(double) * (size_t)p->T, 256);
+  const int words = p->D * (bf16 ? 2 : 4) / 16;
+  const int64_t pairs = ceil_div(p->N, kThreads / kGroupLanes), rows = ceil_div(p->T, kThreads / kWave);
+  if (p->N == 0) return LRMOE_OK;
+  // by_type(f): f with SWIGLU and BF16 as constants
+  auto by_type = [&](auto f) {
+    using std::bool_constant;
+    if (bf16) p->swiglu ? f(bool_constant<true>(), bool_constant<true>()) : f(bool_constant<false>(), bool_constant<true>());
+    else p->swiglu ? f(bool_constant<true>(), bool_constant<false>()) : f(bool_constant<false>(), bool_constant<false>());
+  };
+  const bool few = p->N * words <= kFewWords;
+  if (!few && ws_bytes >= tokens + sizeof(double) * (size_t)p->N && pairs + rows < (1 << 24)) {
+    // both norms in one launch: the pairs' need a place until the tokens' are there
+    double* pn = (double*)((char*)ws + tokens);
+    const uint64_t all = (uint64_t)(pairs + rows), step = (((uint64_t)rows << 32) + all - 1) / all;
+    by_type([&](auto sw, auto bf) {
+      norms_kernel<decltype(sw)::value, decltype(bf)::value><<<(unsigned)all, kThreads, 0, s>>>(
+          step, (const uint4*)G, p->T, words, gn, q, scale, p->N, p->F, pn);
+    });
+    join_scores_kernel<<<(unsigned)ceil_div(p->N, kThreads), kThreads, 0, s>>>(pn, alpha, tok, gn, p->N, p->T, R);
+    return launch_status();
   }
+  if (!few) launch_token_sqnorm(p, G, gn, s);
+  by_type([&](auto sw, auto bf) {
+    auto run = [&](auto kernel) {
+      kernel<<<(unsigned)pairs, kThreads, 0, s>>>((const uint4*)G, p->T, words, gn, q, scale, alpha, tok, p->N, p->F, R);
+    };
+    constexpr bool kSw = decltype(sw)::value, kBf = decltype(bf)::value;
+    few ? run(pair_score_codes_kernel<kSw, kBf, true>) : run(pair_score_codes_kernel<kSw, true, false>);
+  });
   return launch_status();
 }
 

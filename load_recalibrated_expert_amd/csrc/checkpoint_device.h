@@ -121,6 +121,28 @@ struct PhiChunk {
       v[i] = v[i] * sg * up[i];
     }
   }
+  // Sum of squares of the chunk's phi over scale_sq(), to 17 U relative (U = 2^-24; the exponent's rounding aside): terms
+  // of at most 127^2 in magnitude, so nothing overflows whatever the scales, and codes' products are exact.
+  __device__ __forceinline__ float sqnorm_of_codes() const {
+    const uint32_t qa[2] = {a.x, a.y}, qb[2] = {b.x, b.y};
+    const float s = scale_of(sa);
+    float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float g = (float)(int8_t)(qa[i >> 2] >> (8 * (i & 3)));
+      float t = g;
+      if (SWIGLU) {
+        const float u = (float)(int8_t)(qb[i >> 2] >> (8 * (i & 3)));
+        t = g * u * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * s * -1.44269504088896341f));
+      }
+      sum[i & 1] = __builtin_fmaf(t, t, sum[i & 1]);
+    }
+    return sum[0] + sum[1];
+  }
+  __device__ __forceinline__ double scale_sq() const {
+    const double f = SWIGLU ? (double)scale_of(sa) * (double)scale_of(sb) : (double)scale_of(sa);
+    return f * f;
+  }
 };
 
 }  // namespace lrmoe

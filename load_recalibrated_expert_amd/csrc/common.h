@@ -191,7 +191,8 @@ lrmoe_status launch_checkpoint(int64_t n, int32_t parts, int32_t width, int dtyp
 lrmoe_status launch_restore(int64_t n, int32_t parts, int32_t width, const int8_t* q, const uint16_t* scale, int dtype,
                             void* rows, hipStream_t s);
 lrmoe_status launch_score_checkpoint(const lrmoe_problem* p, const void* G, const int8_t* q, const uint16_t* scale,
-                                     const float* alpha, const int32_t* tok, float* R, double* gn, hipStream_t s);
+                                     const float* alpha, const int32_t* tok, float* R, void* ws, size_t ws_bytes,
+                                     hipStream_t s);
 lrmoe_status launch_compact_checkpoint(const lrmoe_problem* p, int64_t rows, const int32_t* sel, const int8_t* q,
                                        const uint16_t* scale, const float* alpha, void* PhiW, hipStream_t s);
 

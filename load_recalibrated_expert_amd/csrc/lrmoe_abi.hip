@@ -324,7 +324,7 @@ lrmoe_status lrmoe_score_checkpoint(const lrmoe_problem* p, const void* G, const
   if ((p->T > 0 && !G) || (p->N > 0 && (!q || !scale || !alpha || !tok || !R))) return LRMOE_ERR_INVALID_ARG;
   if (!aligned(G, 16) || !aligned(q, 16) || !aligned(scale, 2)) return LRMOE_ERR_INVALID_ARG;
   if (!ws || ws_bytes < align_up(sizeof(double) * (size_t)p->T, 256)) return LRMOE_ERR_WORKSPACE;
-  return launch_score_checkpoint(p, G, q, scale, alpha, tok, R, (double*)ws, (hipStream_t)stream);
+  return launch_score_checkpoint(p, G, q, scale, alpha, tok, R, ws, ws_bytes, (hipStream_t)stream);
 }
 
 lrmoe_status lrmoe_compact_checkpoint(const lrmoe_problem* p, const int32_t* sel, const int8_t* q,

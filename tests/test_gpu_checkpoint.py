@@ -130,6 +130,37 @@ def test_score(case):
     assert np.all(d <= err), np.max(d / err)
 
 
+@pytest.mark.parametrize("swiglu,dt", [(True, "bf16"), (False, "bf16"), (True, "f32")])
+def test_score_by_launch_plan(swiglu, dt):
+    """Many gradient words: both norms in one launch where the workspace has room for the pairs', else in two; and few
+    words, each pair on its own. Tokens outside [0, T) score 0 in each."""
+    T, K, E, D, F = 1100, 8, 3, 2048 if dt == "bf16" else 1024, 136
+    rng = np.random.default_rng(9)
+    seg = np.array([0, 3000, 3000, T * K])
+    H = _rows(T * K, F * (2 if swiglu else 1), dt, "normal")
+    G = torch.from_numpy(rng.standard_normal((T, D)).astype(np.float32)).to(DEV).to(TYPES[dt])
+    tok = rng.integers(0, T, T * K).astype(np.int32)
+    tok[::97], tok[5] = -1, T
+    alpha = rng.random(T * K).astype(np.float32)
+    c = lr.checkpoint(H, parts=2 if swiglu else 1)
+    q, scale = c.q.cpu().numpy().astype(np.float64), as_f64(c.scale)
+    out = (tok < 0) | (tok >= T)
+    ref, err = co.score(as_f64(G), q, scale, alpha, np.where(out, 0, tok), swiglu)
+    for t_of, few in ((T, False), (T // 10, True)):  # the fewer tokens: pairs of the first T // 10 tokens' count
+        n = t_of * K
+        p = lr.Problem(E=E, T=T if not few else t_of, K=K, D=D, F=F, swiglu=swiglu, dtype=lr.BF16 if dt == "bf16" else lr.F32,
+                       seg_off=np.minimum(seg, n), quota=np.diff(np.minimum(seg, n)), device=DEV)
+        tk = torch.from_numpy(np.where(tok[:n] < p.T, tok[:n], -1)).to(DEV)
+        part = lr.Checkpoint(c.q[:n], c.scale[:n])
+        gone = tk.cpu().numpy() < 0
+        for room in (8 * (p.T + 64), 8 * (p.T + 64 + p.N)):
+            log(f"score plan {swiglu} {dt} {p.T} tokens, {room} bytes")
+            p.workspace = lambda mode=0, b=room: torch.empty(b, dtype=torch.uint8, device=DEV)
+            R = as_f64(lr.score_checkpoint(p, G[:p.T], part, torch.from_numpy(alpha[:n]).to(DEV), tk))
+            assert not R[gone].any()
+            assert np.all((np.abs(R - ref[:n]) <= err[:n])[~gone])
+
+
 def test_compact(case):
     name, pr, s, c, q, scale = case
     N = s.P.N
