@@ -490,6 +490,13 @@ class Checkpoint:
             raise ValueError("q and scale must be on one device")
         self.q, self.scale, self.parts, self.width = q, scale, parts, width // parts
 
+    @classmethod
+    def _of(cls, q, scale, parts, width):
+        """Of tensors that need no checks (which take a third of a small call's host time)."""
+        c = object.__new__(cls)
+        c.q, c.scale, c.parts, c.width = q, scale, parts, width
+        return c
+
     def _ptrs(self, name, n, parts, width, here):
         """Pointers of q and scale, if they hold at least n rows of that layout on the current device."""
         if self.q.shape[0] < n or (self.parts, self.width) != (parts, width) or self.q.get_device() != here:
@@ -500,39 +507,50 @@ class Checkpoint:
 
 def _new_checkpoint(n, parts, width, device, stream):
     q = _empty((n, parts * width), torch.int8, device, stream)
-    return Checkpoint(q, _empty((n, parts, (width + 127) // 128), torch.bfloat16, device, stream))
+    return Checkpoint._of(q, _empty((n, parts, (width + 127) // 128), torch.bfloat16, device, stream), parts, width)
 
 
 def checkpoint(rows, parts=1, out=None, stream=None):
     """``rows`` [n, width] (f32 or bf16) as a Checkpoint (lrmoe_checkpoint). ``parts``: equal column parts that share no
     scale (2 for [gate | up]). ``out``: a Checkpoint of that layout, overwritten."""
-    here = torch._C._cuda_getDevice()
-    if rows.dtype not in (torch.float32, torch.bfloat16) or rows.dim() != 2:
+    here, dtype = torch._C._cuda_getDevice(), rows.dtype
+    if (dtype is not torch.bfloat16 and dtype is not torch.float32) or rows.dim() != 2:
         raise ValueError("rows: expected f32 or bf16 [n, width]")
-    n, width, parts = rows.shape[0], rows.shape[1], int(parts)
+    (n, width), parts = rows.shape, int(parts)
     if parts < 1 or width % (8 * parts) or not width:
         raise ValueError("rows: the width must be a multiple of 8 in each part")
-    x = _want(rows, "rows", rows.shape, rows.dtype, here)
-    c = _new_checkpoint(n, parts, width // parts, rows.device, stream) if out is None else out
-    q, s = c._ptrs("out", n, parts, width // parts, here)
-    _lib.check(library().lrmoe_checkpoint(n, parts, width // parts, BF16 if rows.dtype == torch.bfloat16 else F32, x, q,
-                                          s, _stream(stream)), "lrmoe_checkpoint")
-    return c
+    width //= parts
+    if rows.get_device() != here or not rows.is_contiguous():
+        raise ValueError(f"rows: expected contiguous rows on the current device, got them on {rows.device}")
+    raw = _stream(stream)
+    if out is None:
+        out = _new_checkpoint(n, parts, width, rows.device, stream)
+        q, s = out.q.data_ptr(), out.scale.data_ptr()
+    else:
+        q, s = out._ptrs("out", n, parts, width, here)
+    _lib.check(library().lrmoe_checkpoint(n, parts, width, BF16 if dtype is torch.bfloat16 else F32, rows.data_ptr(), q, s,
+                                          raw), "lrmoe_checkpoint")
+    return out
 
 
 def restore(c: Checkpoint, dtype=torch.bfloat16, out=None, stream=None):
     """The rows that a Checkpoint stands for (lrmoe_restore), bf16 or f32 [n, width]."""
-    here = torch._C._cuda_getDevice()
-    n, width = c.q.shape
+    here, q = torch._C._cuda_getDevice(), c.q
+    shape = q.shape
     if out is not None:
         dtype = out.dtype
-    if dtype not in (torch.float32, torch.bfloat16):
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise ValueError("dtype must be f32 or bf16")
-    q, s = c._ptrs("c", n, c.parts, c.width, here)
+    if q.get_device() != here:
+        raise ValueError(f"c: expected a checkpoint on the current device, got it on {q.device}")
+    raw = _stream(stream)
     if out is None:
-        out = _empty((n, width), dtype, c.q.device, stream)
-    _lib.check(library().lrmoe_restore(n, c.parts, c.width, q, s, BF16 if dtype == torch.bfloat16 else F32,
-                                       _want(out, "out", (n, width), dtype, here), _stream(stream)), "lrmoe_restore")
+        out = _empty(shape, dtype, q.device, stream)
+        rows = out.data_ptr()
+    else:
+        rows = _want(out, "out", shape, dtype, here)
+    _lib.check(library().lrmoe_restore(shape[0], c.parts, c.width, q.data_ptr(), c.scale.data_ptr(),
+                                       BF16 if dtype is torch.bfloat16 else F32, rows, raw), "lrmoe_restore")
     return out
 
 
@@ -548,7 +566,7 @@ def expert_forward_checkpoint(p: Problem, X, tok, alpha, W1, W2, out=None, strea
     _lib.check(library().lrmoe_expert_forward_checkpoint(
         ctypes.byref(p.c), _ptr(p.seg_off_d), _ptr(X), _ptr(tok), _ptr(alpha), _ptr(W1), _ptr(W2), q, s, _ptr(Phi),
         _ptr(Y), _stream(stream)), "lrmoe_expert_forward_checkpoint")
-    return {"H": Checkpoint(H.q[:p.N], H.scale[:p.N]), "Phi": Phi[:p.N], "Y": Y[:p.N]}
+    return {"H": Checkpoint._of(H.q[:p.N], H.scale[:p.N], 2, p.F), "Phi": Phi[:p.N], "Y": Y[:p.N]}
 
 
 def _saved(p, H, here):

@@ -101,11 +101,11 @@ __global__ __launch_bounds__(topk_threads(Lay::L, N)) void route_topk_kernel(Rou
   blk.finish(a);
 }
 
-// Rows of counts up to which every placing block sums them itself, a thread to an expert and one row
-// after the other; above, a launch scans them first. 64 rows of 128 experts: 7.3 us of placing against
-// 3.2 us of scan and 5.7 us of placing; 128 rows: 9.9 against 3.1 and 6.1 us. (With 128 experts that
-// loop leaves seven eighths of the block's threads idle; sums by all of them were not measured.)
-constexpr int kOwnRows = 64;
+// Words of counts (two experts' each) up to which every placing block sums all rows itself; above, a launch scans them
+// first. 4096 x 128 (32 rows of 64 words) 15.1 us with the scan, 12.4 without; 32768 x 128 (256 rows) 18.3 and 16.4;
+// 65536 x 128 (512 rows) 24.9 and 26.6; 16384 x 512 (256 rows of 256 words) 22.4 and 24.6.
+constexpr int kOwnWords = 24 * kRouteThreads;
+bool sums_own(int64_t rows, int64_t E8) { return rows * (E8 / 2) <= kOwnWords; }
 constexpr int kScanExperts = 32;
 constexpr int kScanKept = 8;  // rows of a run: all of them up to 512 chunks
 
@@ -174,21 +174,30 @@ __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs a)
   const int e0 = tid < n ? a.idx[i0 + tid] : -1;  // on its way meanwhile
   const float w0 = tid < n ? a.w[i0 + tid] : 0.0f;
   for (int i = tid; i < words; i += kRouteThreads) bits[i] = 0;
-  if (tid < a.E) {
-    int sum = 0, low = 0;
-    if (a.prefix) {
-      sum = a.total[tid];
-      low = a.prefix[(int64_t)c * E8 + tid];
-    } else {
-#pragma unroll 8
-      for (int r = 0; r < a.rows; ++r) {
-        const int h = a.hist[(int64_t)r * E8 + tid];
-        sum += h;
-        low += r < c ? h : 0;
-      }
+  if (a.prefix) {
+    if (tid < a.E) {
+      total[tid] = a.total[tid];
+      before[tid] = a.prefix[(int64_t)c * E8 + tid];
     }
-    total[tid] = sum;
-    before[tid] = low;
+  } else {
+    // a thread has one word of every `step`-th row
+    if (tid < a.E) total[tid] = before[tid] = 0;
+    __syncthreads();
+    const int pairs = E8 / 2, step = kRouteThreads / pairs, w = tid % pairs;
+    const uint32_t* h = (const uint32_t*)a.hist + w;
+    int s0 = 0, s1 = 0, l0 = 0, l1 = 0;
+    if (tid < step * pairs) {
+#pragma unroll 8
+      for (int r = tid / pairs; r < a.rows; r += step) {
+        const uint32_t v = h[(int64_t)r * pairs];
+        const int lo = (int)(v & 0xFFFFu), hi = (int)(v >> 16);
+        s0 += lo, s1 += hi;
+        l0 += r < c ? lo : 0, l1 += r < c ? hi : 0;
+      }
+      // whole numbers: their order does not matter
+      if (2 * w < a.E) atomicAdd(&total[2 * w], s0), atomicAdd(&before[2 * w], l0);
+      if (2 * w + 1 < a.E) atomicAdd(&total[2 * w + 1], s1), atomicAdd(&before[2 * w + 1], l1);
+    }
   }
   __syncthreads();
   place_chunk<kRouteThreads>(
@@ -539,9 +548,29 @@ __global__ __launch_bounds__(kGradThreads) void route_bwd_kernel(
   for (int v = 0; v < V; ++v) top = fmaxf(top, x[v]);
   top = group_max<L>(top);
   const bool live = top > kNegInf;
+  float xe[S];  // logits of the slots' experts
+  if (SIG) {
+    if (dalpha) {  // (through the row, as below, took the same time)
+#pragma unroll
+      for (int q = 0; q < S; ++q) xe[q] = e[q] >= 0 && e[q] < E ? clean(Lay::load_one(logits, t * E + e[q])) : kNegInf;
+    }
+    if (__any(top < 0.0f)) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) p[v] = exp_below(fminf(x[v], 0.0f) - fminf(top, 0.0f));
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) p[v] = x[v] >= 0.0f ? 1.0f : exp_below(-fabsf(x[v]));
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float z = exp_below(-fabsf(x[v])), r = __builtin_amdgcn_rcpf(1.0f + z);
+      p[v] *= r;
+      x[v] = (x[v] >= 0.0f ? z : 1.0f) * r;
+    }
+  }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    p[v] = SIG ? sigmoid_over(x[v], top) : exp_below(x[v] - top);
+    if (!SIG) p[v] = exp_below(x[v] - top);
     Z += p[v];
     dx[v] = 0.0f;
   }
@@ -552,12 +581,8 @@ __global__ __launch_bounds__(kGradThreads) void route_bwd_kernel(
   if (dalpha) {
     // the row passes the logits of the chosen experts to their slots, then the slots' results back
     float* row = rows[threadIdx.x / L];
-    float xe[S], ref = top, r = rz, q_of[S], s = 0.0f;
-    if (SIG) {
-#pragma unroll
-      for (int q = 0; q < S; ++q)
-        xe[q] = e[q] >= 0 && e[q] < E ? clean(Lay::load_one(logits, t * E + e[q])) : kNegInf;
-    } else {
+    float ref = top, r = rz, q_of[S], s = 0.0f;
+    if (!SIG) {
 #pragma unroll
       for (int v = 0; v < V; ++v) row[Lay::expert(lane, v)] = x[v];
       wave_sync();
@@ -623,9 +648,10 @@ __global__ __launch_bounds__(kGradThreads) void route_bwd_kernel(
     // would leave its rounding there. Counts of 2^17 +- 1 over 64 experts: an error of 1.6e-2 of the
     // gradient without, 1.1e-7 with it; 32768 x 128 takes 7.5 and 7.85 us.
     int32_t n[V], ref = INT32_MIN;
+    const float least = SIG ? sigmoid_over(-top, 0.0f) : 0.0f;  // 1 - s of the most probable expert
     Lay::load_counts(counts, s, E, inside, lane, n);
 #pragma unroll
-    for (int v = 0; v < V; ++v) ref = max(ref, (SIG ? x[v] >= top : p[v] >= rz) ? n[v] : INT32_MIN);
+    for (int v = 0; v < V; ++v) ref = max(ref, (SIG ? x[v] <= least : p[v] >= rz) ? n[v] : INT32_MIN);
     ref = group_reduce<L>(ref, [](int a, int b) { return max(a, b); });
     float c[V], dot = 0.0f;
 #pragma unroll
@@ -637,7 +663,7 @@ __global__ __launch_bounds__(kGradThreads) void route_bwd_kernel(
     const float f = inside ? norm[s] * (gloss ? gloss[0] : 1.0f) : 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v)  // zeros where f or, not live, p is 0
-      dx[v] += f * (p[v] * (SIG ? sigmoid_over(-x[v], 0.0f) : 1.0f) * (c[v] - dot));
+      dx[v] += f * (p[v] * (SIG ? x[v] : 1.0f) * (c[v] - dot));
   }
   if (!in) return;
   Lay::store(dlogits, t, E, lane, dx);
@@ -764,7 +790,7 @@ lrmoe_status by_slots(const lrmoe_router* r, F&& f) {
 size_t route_ws_bytes(const lrmoe_router* r) {
   const size_t rows = (size_t)ceil_div(r->T, route_chunk(r, true)), E8 = align_up(r->E, 8);  // the smaller chunks
   const size_t hist = align_up(rows * E8 * 2, 256);
-  return std::max<size_t>(256, rows > kOwnRows ? hist + align_up((rows + 1) * E8 * 4, 256) : hist);
+  return std::max<size_t>(256, hist + align_up((rows + 1) * E8 * 4, 256));
 }
 
 lrmoe_status launch_route(const lrmoe_router* r, const lrmoe_scoring* c, const void* logits, const float* bias,
@@ -772,7 +798,7 @@ lrmoe_status launch_route(const lrmoe_router* r, const lrmoe_scoring* c, const v
                           int32_t* slot, float* alpha, int32_t* pmap, void* ws, hipStream_t s) {
   const int C = route_chunk(r, c != nullptr), rows = (int)ceil_div(r->T, C);
   const size_t E8 = align_up(r->E, 8);
-  int* prefix = rows > kOwnRows ? (int*)((char*)ws + align_up((size_t)rows * E8 * 2, 256)) : nullptr;
+  int* prefix = sums_own(rows, E8) ? nullptr : (int*)((char*)ws + align_up((size_t)rows * E8 * 2, 256));
   const size_t bits = 4 * (size_t)bit_words(C, r->local), cnt = (size_t)r->E * 4, pairs = (size_t)C * r->K * 8;
   // a chunk's pairs are sorted where they fit beside its bits; without tokens there are no counts to sort by
   const int sorted = rows > 0 && bits + pairs <= kPlaceLds;
