@@ -71,7 +71,7 @@ __global__ __launch_bounds__(kThreads) void checkpoint_kernel(Place p, const voi
   for (int u = 0; u < kUnits; ++u) {
     const uint32_t unit = u0 + u * (kThreads / kGroupLanes);
     uint16_t s;
-    const uint2 c = group_codes(x[u], &s);
+    const uint2 c = group_codes<BF16>(x[u], &s);
     if (on[u]) *(uint2*)(q + i[u]) = c;
     if (lane == 0 && unit < p.units) scale[unit] = s;
   }

@@ -39,12 +39,25 @@ __device__ __forceinline__ float scale_for(float amax) {
   return fmaxf(s, 0x1p-126f);
 }
 
+constexpr float kRound = 12582912.0f;  // 1.5 2^23: what is added to it is rounded to a whole number, ties to even
+
+// The lowest bytes of eight whole numbers that kRound has been added to.
+__device__ __forceinline__ uint2 pack_codes(const float t[8]) {
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(t[4 * i + 1]), __float_as_uint(t[4 * i]), 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(t[4 * i + 3]), __float_as_uint(t[4 * i + 2]), 0x04000c0cu);
+    w[i] = lo | hi;
+  }
+  return make_uint2(w[0], w[1]);
+}
+
 // Codes of eight values of one group, whose sixteen lanes call this together: nearest whole numbers of scales, ties to
 // even, exactly. u = x / s is rounded by adding 1.5 2^23, with the reciprocal to 1 ulp instead of the quotient, so next to
 // a half the code may be the other neighbour. The remainder r = x - q s tells: it is exact (|r| <= |x| and both are whole
 // multiples of the smaller of their last places), and under s / 2 in magnitude where q is right and no tie.
 __device__ __forceinline__ uint2 codes8(const float x[8], float s, float inv) {
-  constexpr float kRound = 12582912.0f;
   const float half = 0.5f * s;
   float t[8], far = 0.0f;
 #pragma unroll
@@ -60,14 +73,29 @@ __device__ __forceinline__ uint2 codes8(const float x[8], float s, float inv) {
       if (fabsf(r) > half || (fabsf(r) == half && odd)) t[i] += r > 0.0f ? 1.0f : -1.0f;
     }
   }
-  uint32_t w[2];
+  return pack_codes(t);
+}
+
+// The same for values that are bf16 numbers, without the second look: the quotient of two 8-bit significands is a half
+// exactly or at least 2^-10 away from one (2 x - (2 q + 1) s is a whole multiple of a last place of x or s, and x is at
+// least s / 2 there), and the quotient as corrected by its remainder is exact where f32 holds it, as it does all halves.
+// The remainder has places down to 2^-31 of s, so tiny scales are taken away from the subnormal numbers first.
+__device__ __forceinline__ uint2 codes8_bf16(const float x[8], float s, float inv) {
+  float t[8];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {  // the lowest byte of each is the code
-    const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(t[4 * i + 1]), __float_as_uint(t[4 * i]), 0x0c0c0400u);
-    const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(t[4 * i + 3]), __float_as_uint(t[4 * i + 2]), 0x04000c0cu);
-    w[i] = lo | hi;
+  for (int i = 0; i < 8; ++i) t[i] = x[i];
+  if (s < 0x1p-100f) {
+    s *= 0x1p64f;
+    inv *= 0x1p-64f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] *= 0x1p64f;
   }
-  return make_uint2(w[0], w[1]);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float u = t[i] * inv;
+    t[i] = __builtin_fmaf(__builtin_fmaf(-u, s, t[i]), inv, u) + kRound;
+  }
+  return pack_codes(t);
 }
 
 // Largest bits of |x| over the group: of finite values the largest magnitude's, else at least infinity's.
@@ -78,16 +106,15 @@ __device__ __forceinline__ uint32_t group_amax_bits(const float x[8]) {
   return (uint32_t)group_reduce<kGroupLanes>((int)m, [](int a, int b) { return max(a, b); });
 }
 
-// A group's codes and the bits of its scale, from the eight values of each of its lanes.
-__device__ __forceinline__ uint2 group_codes(float x[8], uint16_t* scale) {
+// A group's codes and the bits of its scale, from the eight values of each of its lanes. BF16: they are bf16 numbers.
+template <bool BF16>
+__device__ __forceinline__ uint2 group_codes(const float x[8], uint16_t* scale) {
   const uint32_t m = group_amax_bits(x);
-  if (m >= 0x7F800000u) {  // infinities or NaN: all of the group counts as NaN
-    *scale = 0x7FC0;
-    return make_uint2(0, 0);
-  }
-  const float s = scale_for(__uint_as_float(m));
-  *scale = (uint16_t)(__float_as_uint(s) >> 16);
-  return codes8(x, s, __builtin_amdgcn_rcpf(s));
+  const bool bad = m >= 0x7F800000u;  // infinities or NaN: all of the group counts as NaN
+  const float s = scale_for(__uint_as_float(m)), inv = __builtin_amdgcn_rcpf(s);
+  const uint2 c = BF16 ? codes8_bf16(x, s, inv) : codes8(x, s, inv);
+  *scale = bad ? 0x7FC0 : (uint16_t)(__float_as_uint(s) >> 16);
+  return bad ? make_uint2(0, 0) : c;
 }
 
 // Eight columns of phi, as an expert's FC2 read it: silu(gate) up from the restored values, or the restored value itself.

@@ -1028,7 +1028,7 @@ __global__ LRMOE_GEMM_ATTR(CfgW) void fwd_fc1_kernel(FwdArgs g) {
             vu[2 * k] = bf16_lo(ub[k]), vu[2 * k + 1] = bf16_hi(ub[k]);
           }
           uint16_t sg, su;
-          const uint2 cg = group_codes(vg, &sg), cu = group_codes(vu, &su);
+          const uint2 cg = group_codes<true>(vg, &sg), cu = group_codes<true>(vu, &su);
           if (on) {
             int8_t* q = (int8_t*)g.H + row * ldh + f;
             *(uint2*)q = cg;

@@ -35,6 +35,10 @@ def _rows(n, width, dt, kind, seed=0):
         x = x * rng.choice([1.0, 1 + 2.0 ** -7, 1.1640625], (n, 1)) * (1 + rng.integers(-2, 3, (n, width)) * 2.0 ** -23)
     elif kind == "spread":
         x *= np.exp(rng.standard_normal((n, width)) * 4)
+    elif kind == "tiny_ties":  # ties and their neighbours of scales just over the smallest
+        x = rng.integers(-254, 255, (n, width)) / 2.0
+        x[:, ::128] = 127.0
+        x *= rng.integers(128, 160, (n, 1)) * 2.0 ** (rng.integers(0, 4, (n, 1)) - 133.0)
     elif kind == "tiny":  # down to subnormal values, and rows of zeros
         x *= 2.0 ** rng.integers(-150, -115, (n, 1))
         x[::5] = 0
@@ -58,7 +62,7 @@ def _same(got, ref):
     (65, 1, 128, "bf16", "ties"), (64, 2, 128, "f32", "ties"), (33, 1, 136, "bf16", "near_ties"),
     (50, 1, 1536, "f32", "near_ties"), (257, 2, 768, "bf16", "normal"), (257, 2, 768, "bf16", "ties"),
     (100, 2, 1408, "bf16", "spread"), (999, 1, 520, "f32", "normal"), (40, 3, 264, "bf16", "tiny"),
-    (40, 3, 264, "f32", "tiny"), (40, 2, 264, "bf16", "huge"), (40, 1, 384, "f32", "huge"), (300, 2, 256, "bf16", "bad"),
+    (40, 3, 264, "f32", "tiny"), (3000, 1, 256, "bf16", "tiny_ties"), (3000, 1, 256, "f32", "tiny_ties"), (40, 2, 264, "bf16", "huge"), (40, 1, 384, "f32", "huge"), (300, 2, 256, "bf16", "bad"),
     (300, 1, 200, "f32", "bad"), (5, 1, 20000, "bf16", "normal"), (30011, 1, 24, "f32", "spread"),
     (3001, 2, 640, "bf16", "near_ties")])
 def test_codes_and_values(n, parts, width, dt, kind):
