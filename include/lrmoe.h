@@ -400,7 +400,7 @@ lrmoe_status lrmoe_expert_forward_checkpoint(const lrmoe_problem* p, const int64
                                              int8_t* q, uint16_t* scale, void* Phi, void* Y, lrmoe_stream_t stream);
 
 /* lrmoe_score with phi_j from the codes of pair j: silu(gate) * up (swiglu; in f32, not rounded to the storage dtype),
- * or the value itself (q, scale of one part of F). */
+ * or the value itself (q, scale of one part of F). A sigmoid of the gate below 2^-126 counts as 0. A workspace with 8 bytes a pair more than lrmoe_score needs saves time. */
 lrmoe_status lrmoe_score_checkpoint(const lrmoe_problem* p, const void* G, const int8_t* q, const uint16_t* scale,
                                     const float* alpha, const int32_t* tok, float* R, void* ws, size_t ws_bytes,
                                     lrmoe_stream_t stream);

@@ -402,6 +402,8 @@ def backward(p: Problem, *, G, Phi=None, alpha, tok, slot, W2, X=None, H=None, W
         if not phys or packed_dlt:
             raise ValueError("checkpoints need physical compaction without packed_dlt")
         if isinstance(X, Checkpoint):
+            if not p.swiglu:
+                raise ValueError("FC2-only problems take no X")
             X._ptrs("X", p.T, 1, p.D, torch._C._cuda_getDevice())
     if saved is None:
         b["R"] = score(p, G, Phi, alpha, tok, R=b.get("R"), stream=stream)

@@ -11,7 +11,10 @@ namespace lrmoe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnits = 4;                                    // groups of a lane in flight
+// Groups of a lane in flight. 262144 rows of 2 x 768 bf16 saved and restored / their pairs scored (squares in f32) / 60 % of
+// them compacted: 393 / 100 / 77 us with one, 360 / 100 / 78 with two, 378 / 119 / 79 with four, 430 / 128 / 83 with eight
+// (the restored rows written past the caches, without which four take 414 us; codes written so as well: 381 instead of 360).
+constexpr int kUnits = 2;
 constexpr int kPerBlock = kThreads / kGroupLanes * kUnits;   // groups of a block
 
 // Words of 16 bytes of gradient rows, read once a pair, up to which scoring takes one launch (8 pairs to a token, rows of
@@ -103,16 +106,19 @@ __global__ __launch_bounds__(kThreads) void restore_kernel(Place p, const int8_t
     values8(c[u], scale_of(s[u]), v);
     if (!on[u]) continue;
     if (BF16) {
-      *(uint4*)((uint16_t*)rows + i[u]) =
-          make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+      const u32x4_t w = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                         pack_bf16x2(v[6], v[7])};
+      __builtin_nontemporal_store(w, (u32x4_t*)((uint16_t*)rows + i[u]));
     } else {
-      ((float4*)((float*)rows + i[u]))[0] = make_float4(v[0], v[1], v[2], v[3]);
-      ((float4*)((float*)rows + i[u]))[1] = make_float4(v[4], v[5], v[6], v[7]);
+      typedef float f32x4_t __attribute__((ext_vector_type(4)));
+      f32x4_t* o = (f32x4_t*)((float*)rows + i[u]);
+      __builtin_nontemporal_store(f32x4_t{v[0], v[1], v[2], v[3]}, o);
+      __builtin_nontemporal_store(f32x4_t{v[4], v[5], v[6], v[7]}, o + 1);
     }
   }
 }
 
-// Sum of squares of phi of pair j, by sixteen lanes, four groups of its row in flight; sums over chunks in fp64.
+// Sum of squares of phi of pair j, by sixteen lanes, two groups of its row in flight; squares and sums in fp64.
 template <bool SWIGLU>
 __device__ __forceinline__ double pair_sqnorm(const int8_t* __restrict__ q, const uint16_t* __restrict__ scale, int64_t j,
                                               bool on, int F) {
@@ -128,7 +134,7 @@ __device__ __forceinline__ double pair_sqnorm(const int8_t* __restrict__ q, cons
         else p[u].zero();
       }
 #pragma unroll
-      for (int u = 0; u < kUnits; ++u) acc = __builtin_fma((double)p[u].sqnorm_of_codes(), p[u].scale_sq(), acc);
+      for (int u = 0; u < kUnits; ++u) acc = __builtin_fma(p[u].sqnorm_of_codes(), p[u].scale_sq(), acc);
     }
   }
 #pragma unroll
@@ -170,8 +176,9 @@ __global__ __launch_bounds__(kThreads) void pair_score_codes_kernel(const uint4*
 }
 
 // Tokens and pairs in one launch, their blocks mixed evenly: the pairs are bound by arithmetic (two transcendental
-// instructions a value), the tokens' rows by HBM. The 32768-token share (262144 pairs of 768): 115 us with the join behind
-// it, 4.7 TB/s; tokens and pairs one after the other 125 us. Block b is the tokens' i-th if the count floor(b step / 2^32) passes i there.
+// instructions a value), the tokens' rows by HBM. The 32768-token share (262144 pairs of 768): 104 us with the join behind
+// it, 5.2 TB/s (98 us with squares in f32, which small ones leave; with those and four groups in flight 115 us, and 125 us
+// with tokens and pairs one after the other). Block b is the tokens' i-th if the count floor(b step / 2^32) passes i there.
 template <bool SWIGLU, bool BF16>
 __global__ __launch_bounds__(kThreads) void norms_kernel(uint64_t step, const uint4* __restrict__ G, int T, int words,
                                                          double* __restrict__ gn, const int8_t* __restrict__ q,

@@ -148,12 +148,12 @@ struct PhiChunk {
       v[i] = v[i] * sg * up[i];
     }
   }
-  // Sum of squares of the chunk's phi over scale_sq(), to 17 U relative (U = 2^-24; the exponent's rounding aside): terms
-  // of at most 127^2 in magnitude, so nothing overflows whatever the scales, and codes' products are exact.
-  __device__ __forceinline__ float sqnorm_of_codes() const {
+  // Sum of squares of the chunk's phi over scale_sq(), in fp64: with a gate of -50 a term is 1e-18, and its square is
+  // close to the subnormal f32 numbers.
+  __device__ __forceinline__ double sqnorm_of_codes() const {
     const uint32_t qa[2] = {a.x, a.y}, qb[2] = {b.x, b.y};
     const float s = scale_of(sa);
-    float sum[2] = {0.0f, 0.0f};
+    double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float g = (float)(int8_t)(qa[i >> 2] >> (8 * (i & 3)));
@@ -162,9 +162,9 @@ struct PhiChunk {
         const float u = (float)(int8_t)(qb[i >> 2] >> (8 * (i & 3)));
         t = g * u * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * s * -1.44269504088896341f));
       }
-      sum[i & 1] = __builtin_fmaf(t, t, sum[i & 1]);
+      sum = __builtin_fma((double)t, (double)t, sum);
     }
-    return sum[0] + sum[1];
+    return sum;
   }
   __device__ __forceinline__ double scale_sq() const {
     const double f = SWIGLU ? (double)scale_of(sa) * (double)scale_of(sb) : (double)scale_of(sa);

@@ -478,9 +478,10 @@ lrmoe_status lrmoe_grouped_gemm_bwd_checkpoint(const lrmoe_problem* p, const int
                                                const void* W2, const void* W1, float* dW2, float* dW1, void* dH,
                                                void* dIn, int32_t accumulate, void* ws, size_t ws_bytes,
                                                lrmoe_stream_t stream, lrmoe_event_t din_ready) {
-  LRMOE_TRY(check_problem(p, nullptr, nullptr));
+  int64_t K_tot = 0;
+  LRMOE_TRY(check_problem(p, &K_tot, nullptr));
   if (!p->swiglu) return LRMOE_ERR_UNSUPPORTED;  // nothing of it reads the saved rows
-  if (!scale || !aligned(q, 16) || !aligned(scale, 2)) return LRMOE_ERR_INVALID_ARG;
+  if ((K_tot > 0 && !scale) || !aligned(q, 16) || !aligned(scale, 2)) return LRMOE_ERR_INVALID_ARG;
   return gathered_checked(p, cseg_off_d, G, alpha, sel, ctok, PhiW, X, q, scale, W2, W1, dW2, dW1, dH, dIn, accumulate,
                           ws, ws_bytes, stream, din_ready);
 }

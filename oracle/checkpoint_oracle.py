@@ -48,8 +48,9 @@ def values(q, scale):
 
 def phi(h, swiglu):
     """(phi, err): err bounds an fp32 evaluation from the same h. exp(-g) has the rounding of g log2 e, a relative |g| U,
-    of which sigmoid keeps the part 1 - sigmoid(g); exponential, sum, reciprocal and two products stay under 8 U. For g
-    under -88 the exponential overflows and phi is 0: less than 2^-120 |u| lost."""
+    of which sigmoid keeps the part 1 - sigmoid(g); exponential, sum, reciprocal and two products stay under 8 U. A sigmoid
+    below 2^-126 (g under -87.3) is a subnormal number, which the reciprocal gives as 0: |g| sigmoid(g) is at most
+    87.4 * 2^-126 = 2^-119.55 there, as it falls with g."""
     if not swiglu:
         return h, np.zeros_like(h)
     F = h.shape[1] // 2
@@ -57,7 +58,7 @@ def phi(h, swiglu):
     with np.errstate(over="ignore"):
         sg = 1.0 / (1.0 + np.exp(-g))
     p = g * sg * u
-    return p, np.abs(p) * ((1 - sg) * np.abs(g) + 8) * U + np.abs(u) * 2.0 ** -120
+    return p, np.abs(p) * ((1 - sg) * np.abs(g) + 8) * U + np.abs(u) * 2.0 ** -119.5
 
 
 def score(G, q, scale, alpha, tok, swiglu):

@@ -191,4 +191,6 @@ def test_python_refusals(gpu):  # noqa: F811
             lr.backward(p, **common, **kw)
     with pytest.raises(ValueError):
         lr.backward(lin, **common, H=good)
+    with pytest.raises(ValueError):
+        lr.backward(lin, **common, Phi=lr.Checkpoint(Tensor((9, 32), i8, 0), Tensor((9, 1, 1), bf, 0)), X=x8)
     assert gpu.lib.launched == []

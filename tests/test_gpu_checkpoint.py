@@ -206,8 +206,7 @@ def _run(s, pr, c, X, **kw):
 @pytest.mark.parametrize("x8", [False, True])
 def test_backward(case, x8):
     name, pr, s, c, q, scale = case
-    if x8 and not pr.cfg.swiglu:
-        pytest.skip("FC2-only problems read no X")
+    x8 = x8 and pr.cfg.swiglu  # FC2-only problems read no X
     bf = pr.cfg.dtype == "bf16"
     X = lr.checkpoint(s.X) if x8 else s.X
     log(f"backward {name} {'X in 8 bits' if x8 else ''}")
@@ -272,6 +271,55 @@ def test_pairs_outside_and_a_bad_first_row():
     for t in (PhiW, g["dH"], g["dIn"]):
         assert not t[out_of].any() and torch.isfinite(t.float()).all()
     assert torch.isfinite(g["dW1"]).all() and torch.isfinite(g["dW2"]).all()
+
+
+@pytest.mark.parametrize("pairs,quota", [(0, 0), (40, 0)])
+def test_nothing_retained(pairs, quota):
+    """No pairs at all, and pairs of which none is kept: zero gradients."""
+    T, K, D, F = 30, 2, 64, 40
+    bf = lambda *d: torch.randn(*d, device=DEV).bfloat16()  # noqa: E731
+    p = lr.Problem(E=2, T=T, K=K, D=D, F=F, swiglu=True, dtype=lr.BF16, seg_off=[0, pairs // 4, pairs],
+                   quota=[quota, quota], device=DEV)
+    tok = torch.arange(max(pairs, 1), dtype=torch.int32, device=DEV) % T
+    slot = torch.arange(max(pairs, 1), dtype=torch.int32, device=DEV) // T
+    alpha, X, W1, W2 = torch.rand(max(pairs, 1), device=DEV), bf(T, D), bf(2, D, 2 * F), bf(2, F, D)
+    log(f"nothing retained of {pairs}")
+    f = lr.expert_forward_checkpoint(p, X, tok, alpha, W1, W2)
+    assert f["H"].q.shape == (pairs, 2 * F)
+    res = lr.backward(p, G=bf(T, D), H=f["H"], X=lr.checkpoint(X), alpha=alpha, tok=tok, slot=slot, W2=W2, W1=W1)
+    torch.cuda.synchronize()
+    assert res["sel"].numel() == 0 and not res["dW1"].any() and not res["dW2"].any() and not res["out"][:T].any()
+
+
+def test_offsets_past_32_bits():
+    """Codes, rows and packed rows behind the 2^32nd value."""
+    T, K, F = 360_000, 8, 768
+    N = T * K  # 2880000 rows of 1536: 4.4e9 values
+    keep = 5000
+    x = torch.zeros(N, 2 * F, dtype=torch.bfloat16, device=DEV)
+    x[-keep:] = _rows(keep, 2 * F, "bf16", "spread")
+    log("checkpoint of 4.4e9 values")
+    c = lr.checkpoint(x, parts=2)
+    q, s = co.checkpoint(as_f64(x[-keep:]), 2)
+    _same(c.q[-keep:].cpu().numpy().astype(np.float64), q)
+    _same(as_f64(c.scale[-keep:]), s)
+    assert not c.q[:-keep].any()
+    lr.restore(c, out=x)
+    _same(as_f64(x[-keep:]), torch.from_numpy(co.values(q, s).astype(np.float32)).bfloat16().double().numpy())
+    assert not x[:-keep].any()
+    del x
+    p = lr.Problem(E=2, T=T, K=K, D=8, F=F, swiglu=True, dtype=lr.BF16, seg_off=[0, 100, N], quota=[0, N - 100], device=DEV)
+    G = torch.ones(T, 8, dtype=torch.bfloat16, device=DEV)
+    tok = (torch.arange(N, device=DEV) // K).int()
+    alpha = torch.rand(N, device=DEV)
+    log("scores and packed rows")
+    R = lr.score_checkpoint(p, G, c, alpha, tok)
+    a = alpha[-keep:].cpu().numpy()
+    ref, err = co.score(np.ones((1, 8)), q, s, a, np.zeros(keep, np.int64), True)
+    assert np.all(np.abs(as_f64(R[-keep:]) - ref) <= err) and not R[:-keep].any()
+    P = lr.compact_checkpoint(p, torch.arange(100, N, dtype=torch.int32, device=DEV), c, alpha)
+    ref, err = co.compact(np.arange(keep), q, s, a, True, True)
+    assert np.all(np.abs(as_f64(P[-keep:]) - ref) <= err) and not P[:-keep].any()
 
 
 FORWARD = {

@@ -240,6 +240,29 @@ def test_route_no_tokens():
     assert lr.route_bwd(r, empty, o["idx"], balance=b, seq_off=[0, 0, 0]).shape == (0, 9)
 
 
+@pytest.mark.parametrize("T,E,K,score", [(600007, 96, 1, "softmax"), (600007, 96, 1, "sigmoid"), (66001, 128, 3, "sigmoid"),
+                                         (24000, 128, 2, "sigmoid"), (49999, 130, 2, "softmax")])
+def test_many_rows_of_counts(T, E, K, score):
+    """Numbers of chunks on both sides of what the placing blocks sum themselves, and more than a scan keeps in registers.
+    The lists against stable sorts by torch."""
+    x = torch.randn(T, E, device=DEV, generator=torch.Generator(device=DEV).manual_seed(T))
+    r = lr.Router(T=T, E=E, K=K, first=1, local=E - 2, score=score, device=DEV)
+    log(f"pair lists of {T} x {E}")
+    o = lr.route(r, x)
+    idx = torch.sort(x, dim=1, descending=True, stable=True).indices[:, :K]
+    assert torch.equal(o["idx"].long(), idx) and torch.equal(o["counts"].long(), torch.bincount(idx.view(-1), minlength=E))
+    e = idx.reshape(-1) - 1
+    here = (e >= 0) & (e < E - 2)
+    order = torch.argsort(torch.where(here, e, E), stable=True)[:int(here.sum())]
+    n = len(order)
+    assert torch.equal(o["seg_off"][1:], torch.cumsum(o["counts"][1:-1].long(), 0)) and int(o["seg_off"][-1]) == n
+    assert torch.equal(o["tok"][:n].long(), order // K) and torch.equal(o["slot"][:n].long(), order % K)
+    assert torch.equal(o["alpha"][:n], o["w"].view(-1)[order])
+    row = torch.full((T * K,), -1, device=DEV)
+    row[order] = torch.arange(n, device=DEV)
+    assert torch.equal(o["pmap"].view(-1).long(), row)
+
+
 @pytest.mark.parametrize("E", [1, 3, 64, 65, 1024])
 def test_bias_update(E):
     rng = np.random.default_rng(E)
