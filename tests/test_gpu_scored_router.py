@@ -249,7 +249,7 @@ def test_many_rows_of_counts(T, E, K, score):
     r = lr.Router(T=T, E=E, K=K, first=1, local=E - 2, score=score, device=DEV)
     log(f"pair lists of {T} x {E}")
     o = lr.route(r, x)
-    idx = torch.sort(x, dim=1, descending=True, stable=True).indices[:, :K]
+    idx = torch.sort(x, dim=1, descending=True, stable=True).indices[:, :K].contiguous()
     assert torch.equal(o["idx"].long(), idx) and torch.equal(o["counts"].long(), torch.bincount(idx.view(-1), minlength=E))
     e = idx.reshape(-1) - 1
     here = (e >= 0) & (e < E - 2)
