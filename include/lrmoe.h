@@ -389,7 +389,9 @@ lrmoe_status lrmoe_scatter(const lrmoe_problem* p, lrmoe_scatter_mode mode, int6
 lrmoe_status lrmoe_checkpoint(int64_t n, int32_t parts, int32_t width, lrmoe_dtype dtype, const void* rows, int8_t* q,
                               uint16_t* scale, lrmoe_stream_t stream);
 
-/* rows = q * scale, rounded to dtype (f32: exact). Restored X rows are what lrmoe_grouped_gemm_bwd_checkpoint reads. */
+/* rows = q * scale, rounded to dtype. f32: exact, and finite where the scale is. bf16: a value may round past the largest
+ * finite number to an infinity if its group's largest magnitude is within 2^-8 of it or above it. Restored X rows are
+ * what lrmoe_grouped_gemm_bwd_checkpoint reads. */
 lrmoe_status lrmoe_restore(int64_t n, int32_t parts, int32_t width, const int8_t* q, const uint16_t* scale,
                            lrmoe_dtype dtype, void* rows, lrmoe_stream_t stream);
 
@@ -400,7 +402,8 @@ lrmoe_status lrmoe_expert_forward_checkpoint(const lrmoe_problem* p, const int64
                                              int8_t* q, uint16_t* scale, void* Phi, void* Y, lrmoe_stream_t stream);
 
 /* lrmoe_score with phi_j from the codes of pair j: silu(gate) * up (swiglu; in f32, not rounded to the storage dtype),
- * or the value itself (q, scale of one part of F). A sigmoid of the gate below 2^-126 counts as 0. A workspace with 8 bytes a pair more than lrmoe_score needs saves time. */
+ * or the value itself (q, scale of one part of F). A sigmoid of the gate below 2^-126 counts as 0. A workspace with
+ * 8 bytes a pair more than lrmoe_score needs saves time. */
 lrmoe_status lrmoe_score_checkpoint(const lrmoe_problem* p, const void* G, const int8_t* q, const uint16_t* scale,
                                     const float* alpha, const int32_t* tok, float* R, void* ws, size_t ws_bytes,
                                     lrmoe_stream_t stream);

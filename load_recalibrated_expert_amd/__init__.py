@@ -10,8 +10,9 @@ section 3.3) are calls into ``liblrmoe.so`` (hand-written HIP for gfx950):
 The functions here have the C entry points' names and only marshal arguments:
 torch tensors supply device memory and the current HIP stream. ``backward`` chains
 the five calls. ``Checkpoint`` holds saved activations in 8 bits: expert_forward_checkpoint
-(or checkpoint) makes one, and backward takes it in the place of H and Phi, and of X. Around the experts, ``Router`` with route, balance_loss, alpha_grad and
-route_bwd makes the pair lists and trains the router, and ``AdamW`` applies the gradients.
+(or checkpoint) makes one, and backward takes it in the place of H and Phi, and of X. Around the
+experts, ``Router`` with route, balance_loss, alpha_grad and route_bwd makes the pair lists and trains
+the router, bias_update balances it, and ``AdamW`` applies the gradients.
 Nothing falls back to another implementation; if the library is not built, the first call
 raises ImportError.
 """
@@ -599,6 +600,8 @@ def compact_checkpoint(p: Problem, sel, H: Checkpoint, alpha, out=None, stream=N
 def grouped_gemm_bwd_checkpoint(p: Problem, G, alpha, sel, ctok, PhiW, W2, X, H: Checkpoint, W1, out=None,
                                 accumulate=False, din_ready=None, stream=None):
     """grouped_gemm_bwd_gathered with [gate | up] from a Checkpoint (SwiGLU problems). X: rows of the storage dtype."""
+    if not p.swiglu:
+        raise ValueError("FC2-only problems have no [gate | up]: grouped_gemm_bwd_gathered")
     q, s = _saved(p, H, torch._C._cuda_getDevice())
     o = _gemm_outputs(p, p.K_tot, out)
     ws = p.workspace(COMPACT_PHYSICAL)

@@ -194,3 +194,13 @@ def test_python_refusals(gpu):  # noqa: F811
     with pytest.raises(ValueError):
         lr.backward(lin, **common, Phi=lr.Checkpoint(Tensor((9, 32), i8, 0), Tensor((9, 1, 1), bf, 0)), X=x8)
     assert gpu.lib.launched == []
+
+
+def test_gemm_is_for_gate_and_up(gpu):  # noqa: F811
+    bf = torch.bfloat16
+    lin = types.SimpleNamespace(N=9, T=8, K=2, D=8, F=32, K_tot=5, swiglu=False, torch_dtype=bf, device="cuda:0",
+                                c=_lib.CProblem(), workspace=lambda mode=0: Tensor((512,), torch.uint8, 0))
+    phi, t = lr.Checkpoint(Tensor((9, 32), torch.int8, 0), Tensor((9, 1, 1), bf, 0)), Tensor((9,), torch.float32, 0)
+    with pytest.raises(ValueError):
+        lr.grouped_gemm_bwd_checkpoint(lin, t, t, t, t, t, t, t, phi, t, out=dict(dW2=t, dIn=t))
+    assert gpu.lib.launched == []

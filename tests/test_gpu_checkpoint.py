@@ -402,3 +402,24 @@ def test_on_another_stream():
     assert torch.equal(c.q, ref.q) and torch.equal(back, lr.restore(ref))
     f2 = lr.expert_forward_checkpoint(s.P, s.X, s.tok, s.alpha, s.W1, s.W2)
     assert torch.equal(f["H"].q, f2["H"].q) and torch.equal(R, lr.score_checkpoint(s.P, s.G, f2["H"], s.alpha, s.tok))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_largest_values(dt):
+    """Groups whose largest magnitude is at or next to the type's largest finite number: codes are the definition's, and
+    f32 values stay finite; bf16 ones may round to an infinity, as the nearest bf16 number of code times scale does."""
+    rng = np.random.default_rng(3)
+    big = torch.finfo(TYPES[dt]).max
+    x = rng.uniform(-1, 1, (40, 256)) * big
+    x[:, 5] = big * np.where(np.arange(40) % 2, 1.0, -1.0)
+    x[:, 200] = big * (1 - 2.0 ** -np.arange(40).clip(1, 22 if dt == "f32" else 8))
+    rows = torch.from_numpy(x).to(TYPES[dt]).to(DEV)
+    log("rows at the end of the range")
+    c = lr.checkpoint(rows)
+    back, back16 = lr.restore(c, dtype=torch.float32), lr.restore(c, dtype=torch.bfloat16)
+    torch.cuda.synchronize()
+    q, scale = co.checkpoint(as_f64(rows), 1)
+    assert np.array_equal(c.q.cpu().numpy(), q) and np.array_equal(as_f64(c.scale), scale)
+    v = co.values(q, scale)
+    assert np.isfinite(as_f64(back)).all() and np.array_equal(as_f64(back), v)
+    assert torch.equal(back16.cpu(), torch.from_numpy(v).float().bfloat16())
