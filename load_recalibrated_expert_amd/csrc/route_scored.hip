@@ -118,8 +118,11 @@ __device__ __forceinline__ bool is_kept(uint64_t marks, uint32_t g) {
   return ((g < 32 ? (uint32_t)marks : (uint32_t)(marks >> 32)) >> (g & 31) & 1u) != 0;
 }
 
+// Threads of a block: 1024 where they have the registers, which is up to sixteen values to a lane (the layouts with 128
+// experts and more; 32768 tokens of 128 experts with eight lanes each: 24.9 us with 512, 24.5 us with 1024; of 256: 38.3
+// and 34.4 us; 131072 of 128: 73 and 63 us, all with the masks kept, see below). With groups their rows of LDS do not fit so many tokens.
 constexpr int scored_threads(bool groups, int L, int V) {
-  return V <= 8 && L >= 16 && !groups ? 1024 : groups && V > 24 ? 256 : 512;
+  return !groups && V <= 16 && L >= 8 && L * V >= 128 ? 1024 : groups && V > 24 ? 256 : 512;
 }
 
 // As route_topk_kernel, with keys of choice scores instead of logits.
@@ -131,7 +134,7 @@ __global__ __launch_bounds__(scored_threads(GROUPS, Lay::L, Lay::V)) void route_
   extern __shared__ uint32_t lds[];
   __shared__ double rows[GROUPS ? kTokens : 1][GROUPS ? L * V + kMaxGroups + 1 : 1];
   RouteBlock<NT> blk(a, lds);
-  const int lane = threadIdx.x & (L - 1);
+  int lane = threadIdx.x & (L - 1);
   const int64_t t0 = (int64_t)blockIdx.x * a.C, t1 = min(t0 + a.C, (int64_t)a.T);
   uint32_t of[V];  // the group of each of the lane's experts; behind the last expert the number of groups
   if (GROUPS)
@@ -141,11 +144,17 @@ __global__ __launch_bounds__(scored_threads(GROUPS, Lay::L, Lay::V)) void route_
   for (int64_t tb = t0 + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) * (kWave / L); tb < t1; tb += kTokens) {
     const int64_t t = tb + (threadIdx.x & (kWave - 1)) / L;
     const bool in = t < t1;
+    int E = a.E;
+    // What only the lane and E decide (the masks of the experts below E, keys' places) is computed where it is used: kept
+    // over the loop it takes up to 160 scalar registers that there are not (32768 tokens of 128 experts: 24.9 us, 23.4 so).
+    asm volatile("" : "+v"(lane));
+    asm volatile("" : "+s"(E));
     double* row = rows[GROUPS ? threadIdx.x / L : 0];
     float x[V], bias[V], top = kNegInf, Z = 0.0f;
-    Lay::load(a.logits, t, a.E, in && unmasked(a.mask, t), lane, x);
+    Lay::load(a.logits, t, E, in && unmasked(a.mask, t), lane, x);
     if (s.bias) {  // an expert whose logit or bias is -inf (or NaN) has the bias -inf from here on
-      Layout<L, V, false>::load(s.bias, 0, a.E, true, lane, bias);
+      asm volatile("" : "+s"(E));
+      Layout<L, V, false>::load(s.bias, 0, E, true, lane, bias);
 #pragma unroll
       for (int v = 0; v < V; ++v) bias[v] = x[v] > kNegInf ? bias[v] : kNegInf;
     }
@@ -215,7 +224,7 @@ __global__ __launch_bounds__(scored_threads(GROUPS, Lay::L, Lay::V)) void route_
     float xk[S], p[S], ref = kNegInf, sum = 0.0f;
 #pragma unroll
     for (int q = 0; q < S; ++q) {
-      xk[q] = e[q] >= 0 ? clean(Lay::load_one(a.logits, t * a.E + e[q])) : kNegInf;
+      xk[q] = e[q] >= 0 ? clean(Lay::load_one(a.logits, t * E + e[q])) : kNegInf;
       ref = fmaxf(ref, s.sigmoid ? fminf(xk[q], 0.0f) : xk[q]);
     }
     ref = a.renorm ? group_max<L>(ref) : s.sigmoid ? 0.0f : top;
@@ -282,6 +291,23 @@ void by_group_lists(int E, int K, F&& f) {
   }
 }
 
+// Layouts without groups: those of route, but up to 8 slots sixteen values to a lane where that fits the experts, whose
+// f64 scores leave registers for blocks of 1024 (32768 tokens of 128 experts: 24.6 us with four lanes of 32 values, 23.4 us
+// with eight of sixteen; 512 tokens 13.5 and 12.6 us; 131072 63.2 and 60.6 us; 32768 of 256: 34.2 and 32.8 us; 16384 of 500:
+// 34.8 and 33.9 us; 8192 of 1000: 56.8 and 53.9 us; but of 192 28.4 us with eight lanes of 24 and 31.3 us with sixteen of
+// sixteen, of 300 41.6 us with eight of forty and 46.7 us with sixteen of 24, and with 16 slots of 128 27.4 us with
+// four lanes and 37.0 us with sixteen).
+template <bool BF16, class F>
+void by_score_lists(int T, int E, int K, F&& f) {
+  std::integral_constant<int, 8> n;
+  if (K > 8 || T <= kFewTokens) by_lists<BF16>(T, E, K, f);
+  else if (E > 64 && E <= 128) f(Layout<8, 16, BF16>(), n);
+  else if (E > 192 && E <= 256) f(Layout<16, 16, BF16>(), n);
+  else if (E > 320 && E <= 512) f(Layout<32, 16, BF16>(), n);
+  else if (E > 512) f(Layout<64, 16, BF16>(), n);
+  else by_lists<BF16>(T, E, K, f);
+}
+
 template <bool BF16>
 void run_scored(const RouteArgs& a, const ScoreArgs& s, size_t lds, hipStream_t st) {
   if (s.groups > 1) {
@@ -291,7 +317,7 @@ void run_scored(const RouteArgs& a, const ScoreArgs& s, size_t lds, hipStream_t 
           <<<a.rows, scored_threads(true, Lay::L, Lay::V), lds, st>>>(a, s);
     });
   } else {
-    by_lists<BF16>(a.T, a.E, a.K, [&](auto lay, auto n) {
+    by_score_lists<BF16>(a.T, a.E, a.K, [&](auto lay, auto n) {
       using Lay = decltype(lay);
       route_scored_kernel<Lay, decltype(n)::value, false>
           <<<a.rows, scored_threads(false, Lay::L, Lay::V), lds, st>>>(a, s);
