@@ -114,9 +114,8 @@ __device__ __forceinline__ uint64_t kept_groups(const ScoreArgs& s, int lane, do
   return (uint64_t)high << 32 | low;
 }
 
-__device__ __forceinline__ bool is_kept(uint64_t marks, uint32_t g) {
-  return ((g < 32 ? (uint32_t)marks : (uint32_t)(marks >> 32)) >> (g & 31) & 1u) != 0;
-}
+// g may be the number of groups, of which what is behind the last expert is: its scores are none whatever this gives.
+__device__ __forceinline__ bool is_kept(uint64_t marks, uint32_t g) { return (marks >> (g & 63u) & 1u) != 0; }
 
 // Threads of a block: 1024 where they have the registers, which is up to sixteen values to a lane (the layouts with 128
 // experts and more; 32768 tokens of 128 experts with eight lanes each: 24.9 us with 512, 24.5 us with 1024; of 256: 38.3
