@@ -195,7 +195,7 @@ def prepare(case, seed):
         if own:
             s["p"] = lr.Problem(E=case["E"], T=case["T"], K=case["K"], D=case.get("D", 8), F=case["F"],
                                 swiglu=case["swiglu"], seg_off=seg, quota=quota, device=DEV, dtype=kind)
-            s["H"] = lr.Checkpoint(s["q"], s["scale"])
+            s["H"] = lr.Checkpoint(s["q"].contiguous(), s["scale"].contiguous())
     return s
 
 
