@@ -2,6 +2,7 @@
 // from codes, and the weighted rows of the retained pairs.
 //
 // All are one pass over memory: a code and a scale's part (1.016 bytes a value) beside the 2 or 4 bytes of the rows.
+#include <algorithm>
 #include <type_traits>
 
 #include "checkpoint_device.h"
@@ -249,9 +250,20 @@ __global__ __launch_bounds__(kThreads) void compact_codes_kernel(int64_t rows, i
   }
 }
 
-Place place(int64_t n, int32_t parts, int32_t width) {
+// Groups of one launch, eight threads to each, which fewer than 2^32 threads take.
+constexpr int64_t kLaunchUnits = (((int64_t)1 << 32) / kThreads - 1) * kPerBlock;
+
+// Calls f for as many launches as n * parts rows of `width` need (one below 2^29 groups), each with its place, its blocks and
+// the values and scales before it.
+template <class F>
+void by_launches(int64_t n, int32_t parts, int32_t width, F&& f) {
   const int groups = scale_groups(width);
-  return Place{(uint32_t)(n * parts * groups), width, groups, 1.0 / groups, width % kGroupCols == 0};
+  const int64_t rows = n * parts, step = kLaunchUnits / groups;
+  for (int64_t r = 0; r < rows; r += step) {
+    const int64_t units = std::min(step, rows - r) * groups;
+    f(Place{(uint32_t)units, width, groups, 1.0 / groups, width % kGroupCols == 0}, (unsigned)ceil_div(units, kPerBlock),
+      r * width, r * groups);
+  }
 }
 
 }  // namespace
@@ -260,19 +272,19 @@ int64_t checkpoint_units(int64_t n, int32_t parts, int32_t width) { return n * p
 
 lrmoe_status launch_checkpoint(int64_t n, int32_t parts, int32_t width, int dtype, const void* rows, int8_t* q,
                                uint16_t* scale, hipStream_t s) {
-  const Place p = place(n, parts, width);
-  const unsigned g = (unsigned)ceil_div(p.units, kPerBlock);
-  if (dtype == LRMOE_BF16) checkpoint_kernel<true><<<g, kThreads, 0, s>>>(p, rows, q, scale);
-  else checkpoint_kernel<false><<<g, kThreads, 0, s>>>(p, rows, q, scale);
+  by_launches(n, parts, width, [&](const Place& p, unsigned g, int64_t v, int64_t u) {
+    if (dtype == LRMOE_BF16) checkpoint_kernel<true><<<g, kThreads, 0, s>>>(p, (const uint16_t*)rows + v, q + v, scale + u);
+    else checkpoint_kernel<false><<<g, kThreads, 0, s>>>(p, (const float*)rows + v, q + v, scale + u);
+  });
   return launch_status();
 }
 
 lrmoe_status launch_restore(int64_t n, int32_t parts, int32_t width, const int8_t* q, const uint16_t* scale, int dtype,
                             void* rows, hipStream_t s) {
-  const Place p = place(n, parts, width);
-  const unsigned g = (unsigned)ceil_div(p.units, kPerBlock);
-  if (dtype == LRMOE_BF16) restore_kernel<true><<<g, kThreads, 0, s>>>(p, q, scale, rows);
-  else restore_kernel<false><<<g, kThreads, 0, s>>>(p, q, scale, rows);
+  by_launches(n, parts, width, [&](const Place& p, unsigned g, int64_t v, int64_t u) {
+    if (dtype == LRMOE_BF16) restore_kernel<true><<<g, kThreads, 0, s>>>(p, q + v, scale + u, (uint16_t*)rows + v);
+    else restore_kernel<false><<<g, kThreads, 0, s>>>(p, q + v, scale + u, (float*)rows + v);
+  });
   return launch_status();
 }
 

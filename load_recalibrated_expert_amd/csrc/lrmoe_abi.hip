@@ -297,7 +297,7 @@ static lrmoe_status check_rows(int64_t n, int32_t parts, int32_t width, lrmoe_dt
   if (n < 0 || parts < 1 || width < 8) return LRMOE_ERR_INVALID_ARG;
   if (dtype != LRMOE_F32 && dtype != LRMOE_BF16) return LRMOE_ERR_UNSUPPORTED;
   if (width % 8 != 0 || n >= ((int64_t)1 << 40) || parts >= (1 << 16)) return LRMOE_ERR_UNSUPPORTED;
-  // four threads to a group, of which a launch takes fewer than 2^32
+  // the header's limit; from 2^29 groups on a call takes several launches
   return (double)n * parts * ((width + 127) / 128) >= (double)(1 << 30) ? LRMOE_ERR_UNSUPPORTED : LRMOE_OK;
 }
 

@@ -1,0 +1,39 @@
+"""Launches of the largest sizes that calls accept: fewer than 2^32 threads each, and together they cover the call. Without
+a GPU, from the launches that the library asks the runtime for."""
+import pytest
+
+import launch_shim
+
+LIMIT = 1 << 32  # threads of one launch, a limit of the runtime's own
+ROWS, Q, SCALE = 1 << 40, 1 << 42, 1 << 44
+
+
+@pytest.fixture(scope="module")
+def shim(tmp_path_factory):
+    return launch_shim.build(str(tmp_path_factory.mktemp("shim")))
+
+
+@pytest.mark.parametrize("n,parts,width", [
+    (1, 1, 8), (1000, 2, 264), (2 ** 29 - 32, 1, 8), (2 ** 29 - 31, 1, 8), (2 ** 29, 1, 8), (2 ** 30 - 1, 1, 8),
+    ((2 ** 30 - 1) // 3, 3, 8), ((2 ** 30 - 1) // 9, 3, 264), (1, 2, 2 ** 31 - 128)])
+def test_codes_of_many_groups(shim, n, parts, width):
+    code = f"""
+for dtype in (0, 1):
+    say(lib.lrmoe_checkpoint(i64({n}), {parts}, {width}, dtype, vp({ROWS}), vp({Q}), vp({SCALE}), None))
+    say(lib.lrmoe_restore(i64({n}), {parts}, {width}, vp({Q}), vp({SCALE}), dtype, vp({ROWS}), None))
+"""
+    groups = (width + 127) // 128
+    calls = launch_shim.run(shim, code)
+    assert len(calls) == 4
+    for i, (status, launches) in enumerate(calls):
+        size, saves = (4, 2)[i // 2], i % 2 == 0
+        assert status == "0" and launches
+        done = 0  # rows of one part
+        for at in launches:
+            assert at.threads < LIMIT and at.grid[1:] == [1, 1]
+            rows, q, scale = at.args[1:] if saves else (at.args[3], *at.args[1:3])
+            assert (rows - ROWS, q - Q, scale - SCALE) == (done * width * size, done * width, done * groups * 2)
+            units = at.args[0] & 0xFFFFFFFF  # Place begins with them
+            assert units % groups == 0 and at.threads // 8 - 32 < units <= at.threads // 8
+            done += units // groups
+        assert done == n * parts
