@@ -10,7 +10,8 @@ namespace lrmoe {
 
 constexpr int kGroupCols = 128, kGroupLanes = 16;
 
-__host__ __device__ constexpr int scale_groups(int width) { return (width + kGroupCols - 1) / kGroupCols; }
+// unsigned: the sum may be past 2^31
+__host__ __device__ constexpr int scale_groups(int width) { return (int)(((uint32_t)width + kGroupCols - 1) / kGroupCols); }
 
 __device__ __forceinline__ uint2 ld_stream8(const void* p) {
   const unsigned long long v = __builtin_nontemporal_load((const unsigned long long*)p);

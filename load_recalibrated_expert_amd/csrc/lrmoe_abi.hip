@@ -298,7 +298,7 @@ static lrmoe_status check_rows(int64_t n, int32_t parts, int32_t width, lrmoe_dt
   if (dtype != LRMOE_F32 && dtype != LRMOE_BF16) return LRMOE_ERR_UNSUPPORTED;
   if (width % 8 != 0 || n >= ((int64_t)1 << 40) || parts >= (1 << 16)) return LRMOE_ERR_UNSUPPORTED;
   // the header's limit; from 2^29 groups on a call takes several launches
-  return (double)n * parts * ((width + 127) / 128) >= (double)(1 << 30) ? LRMOE_ERR_UNSUPPORTED : LRMOE_OK;
+  return (double)n * parts * (((int64_t)width + 127) / 128) >= (double)(1 << 30) ? LRMOE_ERR_UNSUPPORTED : LRMOE_OK;
 }
 
 lrmoe_status lrmoe_checkpoint(int64_t n, int32_t parts, int32_t width, lrmoe_dtype dtype, const void* rows, int8_t* q,

@@ -1,5 +1,6 @@
-"""Launches of the built library as it would make them, without a GPU: a small preloaded library takes the place of the HIP
-runtime's launch calls and notes grid, block and the kernel's first arguments. Nothing runs on a device."""
+"""Launches of the built library as it would make them, without a GPU: a small library in the scope of a process of its own
+takes the place of the HIP runtime's launch calls and notes grid, block and the kernel's first arguments. Nothing runs on a
+device."""
 import os
 import subprocess
 import sys
@@ -36,7 +37,7 @@ int hipLaunchKernel(const void* f, dims grid, dims block, void** args, size_t ld
 
 
 def build(folder):
-    """The preloaded library, compiled into ``folder``."""
+    """That small library, compiled into ``folder``."""
     src, lib = os.path.join(folder, "shim.c"), os.path.join(folder, "shim.so")
     with open(src, "w") as f:
         f.write(SHIM)
@@ -54,14 +55,14 @@ class Launch:
         return self.grid[0] * self.block
 
 
-def run(lib, code, timeout=120):
-    """Runs ``code`` in a process of its own, with ``lib`` (liblrmoe.so by ctypes) in its scope. Returns (launches, other
-    lines that it printed), in order: [(text, launches since the last text)]."""
-    head = ("import ctypes\nlib = ctypes.CDLL('load_recalibrated_expert_amd/liblrmoe.so')\n"
+def run(lib, code, timeout=60):
+    """Runs ``code`` in a process of its own, where ``lib`` is liblrmoe.so (by ctypes). Returns what it printed and the
+    launches before: [(text, launches since the last text)]."""
+    head = (f"import ctypes\nshim = ctypes.CDLL({lib!r}, mode=ctypes.RTLD_GLOBAL)\n"  # before the runtime: its symbols win
+            "lib = ctypes.CDLL('load_recalibrated_expert_amd/liblrmoe.so')\n"
             "vp, i64, i32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float\n"
             "say = lambda t: print(t, flush=True)\n")
-    out = subprocess.run([sys.executable, "-c", head + code], cwd=ROOT, env={**os.environ, "LD_PRELOAD": lib},
-                         capture_output=True, text=True, timeout=timeout)
+    out = subprocess.run([sys.executable, "-c", head + code], cwd=ROOT, capture_output=True, text=True, timeout=timeout)
     assert out.returncode == 0, out.stderr[-2000:]
     found, launches = [], []
     for line in out.stdout.splitlines():

@@ -15,7 +15,8 @@ def shim(tmp_path_factory):
 
 @pytest.mark.parametrize("n,parts,width", [
     (1, 1, 8), (1000, 2, 264), (2 ** 29 - 32, 1, 8), (2 ** 29 - 31, 1, 8), (2 ** 29, 1, 8), (2 ** 30 - 1, 1, 8),
-    ((2 ** 30 - 1) // 3, 3, 8), ((2 ** 30 - 1) // 9, 3, 264), (1, 2, 2 ** 31 - 128)])
+    ((2 ** 30 - 1) // 3, 3, 8), ((2 ** 30 - 1) // 9, 3, 264), (1, 2, 2 ** 31 - 128), (1, 2, 2 ** 31 - 120),
+    (20, 3, 2 ** 31 - 8)])
 def test_codes_of_many_groups(shim, n, parts, width):
     code = f"""
 for dtype in (0, 1):
