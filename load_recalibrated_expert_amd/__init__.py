@@ -476,6 +476,9 @@ def backward(p: Problem, *, G, Phi=None, alpha, tok, slot, W2, X=None, H=None, W
     return {"R": b["R"], "sel": sel, "keep": keep, **c, **g, "out": out}
 
 
+_MOST_COLUMNS, _MOST_PARTS = (1 << 31) - 8, (1 << 16) - 1  # of a part and of a row: the C calls count them in 32 bits
+
+
 class Checkpoint:
     """Activation rows in 8 bits (the header's section on saved activations): codes ``q`` int8 [n, width] and ``scale``
     bf16 [n, parts, ceil(width / parts / 128)], one for every 128 columns of a part."""
@@ -491,6 +494,8 @@ class Checkpoint:
                              f"{scale.dtype} of {tuple(scale.shape)} for q of {tuple(q.shape)}")
         if scale.get_device() != q.get_device():
             raise ValueError("q and scale must be on one device")
+        if width // parts > _MOST_COLUMNS or parts > _MOST_PARTS:
+            raise ValueError(f"q: {parts} parts of {width // parts} columns are more than the library counts")
         self.q, self.scale, self.parts, self.width = q, scale, parts, width // parts
 
     @classmethod
@@ -523,6 +528,8 @@ def checkpoint(rows, parts=1, out=None, stream=None):
     if parts < 1 or width % (8 * parts) or not width:
         raise ValueError("rows: the width must be a multiple of 8 in each part")
     width //= parts
+    if width > _MOST_COLUMNS or parts > _MOST_PARTS:
+        raise ValueError(f"rows: {parts} parts of {width} columns are more than the library counts")
     if rows.get_device() != here or not rows.is_contiguous():
         raise ValueError(f"rows: expected contiguous rows on the current device, got them on {rows.device}")
     raw = _stream(stream)
