@@ -294,7 +294,7 @@ lrmoe_status launch_score_checkpoint(const lrmoe_problem* p, const void* G, cons
   double* gn = (double*)ws;
   const bool bf16 = p->dtype == LRMOE_BF16;
   const size_t tokens = align_up(sizeof(double) * (size_t)p->T, 256);
-  const int words = p->D * (bf16 ? 2 : 4) / 16;
+  const int words = p->D / (bf16 ? 8 : 4);
   const int64_t pairs = ceil_div(p->N, kThreads / kGroupLanes), rows = ceil_div(p->T, kThreads / kWave);
   if (p->N == 0) return LRMOE_OK;
   // by_type(f): f with SWIGLU and BF16 as constants

@@ -402,7 +402,7 @@ void launch(int64_t rows, bool masked, const lrmoe_problem* p, const int32_t* se
             const int32_t* slot, void* Dlt, void* PhiC, void* XC, void* HC, int32_t* ctok, int32_t* cslot,
             const int32_t* pmap, int32_t* map, hipStream_t s) {
   const int esz = BF16 ? 2 : 4;
-  const int dch = p->D * esz / 16, fch = p->F * esz / 16;
+  const int dch = p->D / (16 / esz), fch = p->F / (16 / esz);
   if (masked) {
     compact_masked_kernel<BF16, SWIGLU><<<(unsigned)ceil_div(rows, kRowsPerBlock), kThreads, 0, s>>>(
         rows, p->T, dch, fch, keep, (const uint4*)G, (const uint4*)X, alpha, tok, slot, (uint4*)Dlt, (uint4*)XC, ctok,
@@ -441,7 +441,7 @@ lrmoe_status launch_compact_weighted_phi(const lrmoe_problem* p, int64_t rows, c
                                          const void* Phi, const float* alpha, void* PhiW, hipStream_t s) {
   if (rows <= 0) return LRMOE_OK;
   const bool bf16 = p->dtype == LRMOE_BF16;
-  const int fch = p->F * (bf16 ? 2 : 4) / 16;
+  const int fch = p->F / (bf16 ? 8 : 4);
   const unsigned grid = (unsigned)ceil_div(rows, kWRows);
   if (bf16)
     compact_weighted_phi_kernel<true><<<grid, kThreads, 0, s>>>(rows, p->N, fch, sel, (const uint4*)Phi, alpha,

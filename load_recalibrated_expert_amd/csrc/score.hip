@@ -68,7 +68,7 @@ __global__ __launch_bounds__(kScoreThreads) void pair_gather_kernel(const int32_
 lrmoe_status launch_score_gradient(const lrmoe_problem* p, bool magnitude, const void* G, const int32_t* tok,
                                    float* R, double* gs, hipStream_t s) {
   const bool bf16 = p->dtype == LRMOE_BF16;
-  const int gch = p->D * (bf16 ? 2 : 4) / 16;
+  const int gch = p->D / (bf16 ? 8 : 4);
   if (p->T > 0) {
     dim3 grid((unsigned)ceil_div(p->T, kScoreThreads / kWave));
     if (bf16 && magnitude) token_sqnorm_kernel<true, true><<<grid, kScoreThreads, 0, s>>>((const uint4*)G, p->T, gch, gs);
@@ -83,7 +83,7 @@ lrmoe_status launch_score_gradient(const lrmoe_problem* p, bool magnitude, const
 
 void launch_token_sqnorm(const lrmoe_problem* p, const void* G, double* gn, hipStream_t s) {
   const bool bf16 = p->dtype == LRMOE_BF16;
-  const int gch = p->D * (bf16 ? 2 : 4) / 16;
+  const int gch = p->D / (bf16 ? 8 : 4);
   if (p->T <= 0) return;
   dim3 grid((unsigned)ceil_div(p->T, kScoreThreads / kWave));
   if (bf16)
@@ -95,7 +95,7 @@ void launch_token_sqnorm(const lrmoe_problem* p, const void* G, double* gn, hipS
 lrmoe_status launch_score(const lrmoe_problem* p, const void* G, const void* Phi, const float* alpha,
                           const int32_t* tok, float* R, double* gn, hipStream_t s) {
   const bool bf16 = p->dtype == LRMOE_BF16;
-  const int pch = p->F * (bf16 ? 2 : 4) / 16;
+  const int pch = p->F / (bf16 ? 8 : 4);
   launch_token_sqnorm(p, G, gn, s);
   if (p->N > 0) {
     dim3 grid((unsigned)ceil_div(p->N, kScoreThreads / 16));

@@ -38,3 +38,47 @@ for dtype in (0, 1):
             assert units % groups == 0 and at.threads // 8 - 32 < units <= at.threads // 8
             done += units // groups
         assert done == n * parts
+
+
+PROBLEM = """
+class Problem(ctypes.Structure):
+    _fields_ = [(n, i32) for n in ("E", "T", "K", "D", "F", "swiglu", "dtype", "reserved")] + [
+        ("N", i64), ("seg_off", vp), ("quota", vp)]
+
+
+def problem(T, K, D, F, N, swiglu=1, dtype=0, kept=None):
+    kept = N if kept is None else kept
+    p = Problem(E=1, T=T, K=K, D=D, F=F, N=N, swiglu=swiglu, dtype=dtype)
+    p.keep = (i64 * 2)(0, N), (i32 * 1)(kept)
+    p.seg_off, p.quota = (ctypes.cast(a, vp) for a in p.keep)
+    return ctypes.byref(p)
+
+
+def score(p, ws=1 << 60):
+    return lib.lrmoe_score_checkpoint(p, vp(4096), vp(4096), vp(4096), vp(4096), vp(4096), vp(4096), vp(4096),
+                                      ctypes.c_size_t(ws), None)
+
+
+def compact(p):
+    return lib.lrmoe_compact_checkpoint(p, vp(4096), vp(4096), vp(4096), vp(4096), vp(4096), None)
+"""
+
+
+@pytest.mark.parametrize("dtype,D", [(0, 64), (1, 64), (0, 2 ** 29), (1, 2 ** 30), (0, 2 ** 31 - 8), (1, 2 ** 31 - 8)])
+def test_words_of_a_wide_row(shim, dtype, D):
+    """A row's words of 16 bytes, counted without its bytes passing 32 bits."""
+    code = PROBLEM + f"""
+p = problem(40000, 1, {D}, {D}, 40000, swiglu=0, dtype={dtype})
+say(score(p))
+say(score(p, ws=8 * 40064))
+say(lib.lrmoe_score(p, *[vp(4096)] * 6, ctypes.c_size_t(1 << 30), None))
+say(lib.lrmoe_compact_weighted(p, *[vp(4096)] * 4, None))
+"""
+    words = D // (8 if dtype else 4)
+    calls = launch_shim.run(shim, code)
+    assert [status for status, _ in calls] == ["0"] * 4
+    (_, fused), (_, two), (_, plain), (_, compact) = calls
+    low = lambda launch, i: launch.args[i] & 0xFFFFFFFF  # noqa: E731
+    if 40000 * words > 2 ** 21:
+        assert low(fused[0], 3) == words and low(two[0], 2) == words
+    assert low(plain[0], 2) == low(compact[0], 2) == words
