@@ -403,12 +403,14 @@ lrmoe_status lrmoe_expert_forward_checkpoint(const lrmoe_problem* p, const int64
 
 /* lrmoe_score with phi_j from the codes of pair j: silu(gate) * up (swiglu; in f32, not rounded to the storage dtype),
  * or the value itself (q, scale of one part of F). A sigmoid of the gate below 2^-126 counts as 0. A workspace with
- * 8 bytes a pair more than lrmoe_score needs saves time. */
+ * 8 bytes a pair more than lrmoe_score needs saves time. Up to 2^28 - 16 pairs and 2^26 - 4 tokens (any number of tokens
+ * where the pairs are few), else LRMOE_ERR_UNSUPPORTED. */
 lrmoe_status lrmoe_score_checkpoint(const lrmoe_problem* p, const void* G, const int8_t* q, const uint16_t* scale,
                                     const float* alpha, const int32_t* tok, float* R, void* ws, size_t ws_bytes,
                                     lrmoe_stream_t stream);
 
-/* lrmoe_compact_weighted with the same phi_j: PhiW[c] = alpha[j] * phi_j, j = sel[c], rounded to the storage dtype. */
+/* lrmoe_compact_weighted with the same phi_j: PhiW[c] = alpha[j] * phi_j, j = sel[c], rounded to the storage dtype. Up to
+ * 2^28 - 16 retained pairs, else LRMOE_ERR_UNSUPPORTED. */
 lrmoe_status lrmoe_compact_checkpoint(const lrmoe_problem* p, const int32_t* sel, const int8_t* q,
                                       const uint16_t* scale, const float* alpha, void* PhiW, lrmoe_stream_t stream);
 

@@ -250,8 +250,9 @@ __global__ __launch_bounds__(kThreads) void compact_codes_kernel(int64_t rows, i
   }
 }
 
-// Groups of one launch, eight threads to each, which fewer than 2^32 threads take.
-constexpr int64_t kLaunchUnits = (((int64_t)1 << 32) / kThreads - 1) * kPerBlock;
+// A launch has fewer than 2^32 threads.
+constexpr int64_t kMaxBlocks = ((int64_t)1 << 32) / kThreads;
+constexpr int64_t kLaunchUnits = (kMaxBlocks - 1) * kPerBlock;  // groups of one launch
 
 // Calls f for as many launches as n * parts rows of `width` need (one below 2^29 groups), each with its place, its blocks and
 // the values and scales before it.
@@ -297,14 +298,15 @@ lrmoe_status launch_score_checkpoint(const lrmoe_problem* p, const void* G, cons
   const int words = p->D / (bf16 ? 8 : 4);
   const int64_t pairs = ceil_div(p->N, kThreads / kGroupLanes), rows = ceil_div(p->T, kThreads / kWave);
   if (p->N == 0) return LRMOE_OK;
+  const bool few = p->N * words <= kFewWords;
+  if (pairs >= kMaxBlocks || (!few && rows >= kMaxBlocks)) return LRMOE_ERR_UNSUPPORTED;
   // by_type(f): f with SWIGLU and BF16 as constants
   auto by_type = [&](auto f) {
     using std::bool_constant;
     if (bf16) p->swiglu ? f(bool_constant<true>(), bool_constant<true>()) : f(bool_constant<false>(), bool_constant<true>());
     else p->swiglu ? f(bool_constant<true>(), bool_constant<false>()) : f(bool_constant<false>(), bool_constant<false>());
   };
-  const bool few = p->N * words <= kFewWords;
-  if (!few && ws_bytes >= tokens + sizeof(double) * (size_t)p->N && pairs + rows < (1 << 24)) {
+  if (!few && ws_bytes >= tokens + sizeof(double) * (size_t)p->N && pairs + rows < kMaxBlocks) {
     // both norms in one launch: the pairs' need a place until the tokens' are there
     double* pn = (double*)((char*)ws + tokens);
     const uint64_t all = (uint64_t)(pairs + rows), step = (((uint64_t)rows << 32) + all - 1) / all;
@@ -329,8 +331,9 @@ lrmoe_status launch_score_checkpoint(const lrmoe_problem* p, const void* G, cons
 lrmoe_status launch_compact_checkpoint(const lrmoe_problem* p, int64_t rows, const int32_t* sel, const int8_t* q,
                                        const uint16_t* scale, const float* alpha, void* PhiW, hipStream_t s) {
   if (rows <= 0) return LRMOE_OK;
-  const unsigned g = (unsigned)ceil_div(rows, kThreads / kGroupLanes);
-  auto run = [&](auto kernel) { kernel<<<g, kThreads, 0, s>>>(rows, p->N, p->F, sel, q, scale, alpha, PhiW); };
+  const int64_t g = ceil_div(rows, kThreads / kGroupLanes);
+  if (g >= kMaxBlocks) return LRMOE_ERR_UNSUPPORTED;
+  auto run = [&](auto kernel) { kernel<<<(unsigned)g, kThreads, 0, s>>>(rows, p->N, p->F, sel, q, scale, alpha, PhiW); };
   if (p->dtype == LRMOE_BF16) p->swiglu ? run(compact_codes_kernel<true, true>) : run(compact_codes_kernel<false, true>);
   else p->swiglu ? run(compact_codes_kernel<true, false>) : run(compact_codes_kernel<false, false>);
   return launch_status();

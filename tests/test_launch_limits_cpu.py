@@ -6,6 +6,7 @@ import launch_shim
 
 LIMIT = 1 << 32  # threads of one launch, a limit of the runtime's own
 ROWS, Q, SCALE = 1 << 40, 1 << 42, 1 << 44
+UNSUPPORTED = "3"
 
 
 @pytest.fixture(scope="module")
@@ -82,3 +83,30 @@ say(lib.lrmoe_compact_weighted(p, *[vp(4096)] * 4, None))
     if 40000 * words > 2 ** 21:
         assert low(fused[0], 3) == words and low(two[0], 2) == words
     assert low(plain[0], 2) == low(compact[0], 2) == words
+
+
+@pytest.mark.parametrize("T,K,N,D,ws,ok", [
+    (2 ** 26 - 8, 8, 2 ** 28 - 16, 64, 1 << 60, True), (2 ** 26 - 8, 8, 2 ** 28 - 15, 64, 1 << 60, False),
+    (2 ** 26 - 8, 8, 2 ** 28, 64, 8 << 26, False), (2 ** 24, 32, 2 ** 29 - 32, 8, 1 << 60, False),
+    (2 ** 26 - 4, 1, 2 ** 22, 64, 8 << 26, True), (2 ** 26 - 4, 1, 2 ** 22, 64, 1 << 60, True),
+    (2 ** 26 - 3, 1, 2 ** 22, 64, 8 << 28, False), (2 ** 27, 1, 2 ** 22, 64, 1 << 60, False),
+    (2 ** 30, 1, 1000, 64, 8 << 30, True)])  # few pairs read their tokens' rows themselves
+def test_scores_of_many_pairs(shim, T, K, N, D, ws, ok):
+    for dtype in (0, 1):
+        code = PROBLEM + f"say(score(problem({T}, {K}, {D}, 8, {N}, dtype={dtype}), ws={ws}))"
+        (status, launches), = launch_shim.run(shim, code)
+        if ok:
+            assert status == "0" and launches and all(at.threads < LIMIT for at in launches)
+        else:
+            assert status == UNSUPPORTED and not launches
+
+
+@pytest.mark.parametrize("kept,ok", [(1, True), (2 ** 28 - 16, True), (2 ** 28 - 15, False), (2 ** 28, False),
+                                     (2 ** 31 - 32, False)])
+def test_many_retained_pairs(shim, kept, ok):
+    code = PROBLEM + f"say(compact(problem({2 ** 26 - 1}, 32, 8, 8, {2 ** 31 - 32}, kept={kept})))"
+    (status, launches), = launch_shim.run(shim, code)
+    if ok:
+        assert status == "0" and len(launches) == 1 and launches[0].threads < LIMIT and launches[0].args[0] == kept
+    else:
+        assert status == UNSUPPORTED and not launches
