@@ -493,7 +493,8 @@ lrmoe_status lrmoe_balance_loss(const lrmoe_router* r, const void* logits, const
  *   with gloss a device f32 (NULL: 1), the gradient of the loss value. The counts' differences are
  *   taken as whole numbers before anything is rounded, so nearly equal counts lose nothing.
  * The probability p_e of an expert that is not chosen counts as 0 below 2^-126.
- * A token's idx entries have to be different; an entry outside [0, E) is an empty slot. */
+ * A token's idx entries have to be different; an entry outside [0, E) is an empty slot. Above 512 experts
+ * T is at most 2^26 - 4. */
 lrmoe_status lrmoe_route_bwd(const lrmoe_router* r, const void* logits, const uint8_t* mask, const int32_t* idx,
                              const float* dalpha, const int32_t* pmap, int64_t n_pairs, const int64_t* seq_off_d,
                              int32_t n_seq, const int32_t* counts, const float* norm, const float* gloss,
@@ -561,7 +562,7 @@ lrmoe_status lrmoe_bias_update(const lrmoe_router* r, const int32_t* counts, flo
  * the storage dtype. pmap [T x K]: the pair row of each (token, slot) position, as lrmoe_route
  * wrote it; each pair has one position. An entry outside [0, N) is none, and pairs without a
  * position keep what dalpha held. Products and sums in fp64; what Y lost to subnormal values of the
- * storage dtype (alpha near 2^-126) cannot be had back. T must be under 2^26. No workspace. */
+ * storage dtype (alpha near 2^-126) cannot be had back. T is at most 2^26 - 4. No workspace. */
 lrmoe_status lrmoe_alpha_grad(const lrmoe_problem* p, const void* G, const void* Y, const float* alpha,
                               const int32_t* pmap, const uint8_t* keep, float* dalpha, lrmoe_stream_t stream);
 

@@ -117,6 +117,8 @@ inline lrmoe_status launch_status() {
 // A launch has fewer than 2^32 threads along a dimension, a limit of the runtime's own. One wavefront to
 // a token, and a block of 1024 threads to a tile of tokens and to a sequence, stay below it under these:
 constexpr int64_t kMaxTokens = (int64_t)1 << 26, kMaxSequences = (int64_t)1 << 21;
+// but for whole blocks of four tokens, which the last three below kMaxTokens are not:
+constexpr int64_t kMaxFours = kMaxTokens - 4;
 
 // ---------------------------------------------------------------- launchers (one per .hip file)
 

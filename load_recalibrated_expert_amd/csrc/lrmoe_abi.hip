@@ -621,6 +621,7 @@ lrmoe_status lrmoe_alpha_grad(const lrmoe_problem* p, const void* G, const void*
   LRMOE_TRY(check_problem(p, nullptr, nullptr));
   if (p->T >= kMaxTokens) return LRMOE_ERR_UNSUPPORTED;
   if (p->N == 0) return LRMOE_OK;
+  if (p->T > kMaxFours) return LRMOE_ERR_UNSUPPORTED;
   if (!G || !Y || !alpha || !pmap || !dalpha) return LRMOE_ERR_INVALID_ARG;
   if (!aligned(G, 16) || !aligned(Y, 16)) return LRMOE_ERR_INVALID_ARG;
   return launch_alpha_grad(p, G, Y, alpha, pmap, keep, dalpha, (hipStream_t)stream);

@@ -858,6 +858,7 @@ lrmoe_status launch_route_bwd(const lrmoe_router* r, bool sigmoid, const void* l
                               const int32_t* idx, const float* dalpha, const int32_t* pmap, int64_t n_pairs,
                               const int64_t* seq_off_d, int32_t n_seq, const int32_t* counts, const float* norm,
                               const float* gloss, void* dlogits, hipStream_t s) {
+  if (r->E > 512 && r->T > kMaxFours) return LRMOE_ERR_UNSUPPORTED;
   return by_layout(r, true, [&](auto lay) {
     using Lay = decltype(lay);
     constexpr int L = Lay::L, most = std::min(32, L * Lay::V);  // slots: no more than experts

@@ -110,3 +110,38 @@ def test_many_retained_pairs(shim, kept, ok):
         assert status == "0" and len(launches) == 1 and launches[0].threads < LIMIT and launches[0].args[0] == kept
     else:
         assert status == UNSUPPORTED and not launches
+
+
+ROUTER = """
+class Router(ctypes.Structure):
+    _fields_ = [(n, i32) for n in ("T", "E", "K", "first", "local", "dtype", "renorm", "reserved")] + [("scale", f32)]
+
+
+class Scoring(ctypes.Structure):
+    _fields_ = [(n, i32) for n in ("score", "groups", "top_groups", "group_best")]
+
+
+note(0)
+F, ws = vp(4096), ctypes.c_size_t(1 << 60)
+"""
+
+
+@pytest.mark.parametrize("T", [2 ** 26 - 4, 2 ** 26 - 3, 2 ** 26 - 1])
+@pytest.mark.parametrize("E,K", [(1024, 8), (513, 31), (512, 8), (64, 20), (8, 4), (1, 1)])
+def test_router_of_most_tokens(shim, T, E, K):
+    code = PROBLEM + ROUTER + f"""
+r = ctypes.byref(Router(T={T}, E={E}, K={K}, local={E}, dtype=1, renorm=1, scale=1.0))
+for score in (0, 1):
+    c = ctypes.byref(Scoring(score, 1, 1, 1))
+    say(f"route {{lib.lrmoe_route_scored(r, c, F, F, None, F, F, F, F, F, F, F, F, F, ws, None)}}")
+    for n in (1, min(2 ** 21 - 1, (2 ** 31 - 1) // {E})):
+        say(f"loss {{lib.lrmoe_balance_loss_scored(r, c, F, None, F, F, n, f32(1), F, F, F, F, F, ws, None)}}")
+    say(f"gradient {{lib.lrmoe_route_bwd_scored(r, c, F, None, F, F, F, i64(5), F, 3, F, F, None, F, None)}}")
+say(f"weights {{lib.lrmoe_alpha_grad(problem({T}, {K}, 8, 8, 1000), F, F, F, F, None, F, None)}}")
+"""
+    for text, launches in launch_shim.run(shim, code):
+        call, status = text.split()
+        if T > 2 ** 26 - 4 and (call == "weights" or call == "gradient" and E > 512):
+            assert status == UNSUPPORTED and not launches, text
+        else:
+            assert status == "0" and launches and all(at.threads < LIMIT for at in launches), text
