@@ -648,10 +648,11 @@ __global__ __launch_bounds__(kGradThreads) void route_bwd_kernel(
     // would leave its rounding there. Counts of 2^17 +- 1 over 64 experts: an error of 1.6e-2 of the
     // gradient without, 1.1e-7 with it; 32768 x 128 takes 7.5 and 7.85 us.
     int32_t n[V], ref = INT32_MIN;
-    const float least = SIG ? sigmoid_over(-top, 0.0f) : 0.0f;  // 1 - s of the most probable expert
+    // p of the most probable expert, by the same operations (not by 1 - s, which is 1 for all of them below -17)
+    const float most = SIG ? __builtin_amdgcn_rcpf(1.0f + exp_below(-fabsf(top))) * rz : rz;
     Lay::load_counts(counts, s, E, inside, lane, n);
 #pragma unroll
-    for (int v = 0; v < V; ++v) ref = max(ref, (SIG ? x[v] <= least : p[v] >= rz) ? n[v] : INT32_MIN);
+    for (int v = 0; v < V; ++v) ref = max(ref, p[v] >= most ? n[v] : INT32_MIN);
     ref = group_reduce<L>(ref, [](int a, int b) { return max(a, b); });
     float c[V], dot = 0.0f;
 #pragma unroll
