@@ -167,7 +167,8 @@ lrmoe_status lrmoe_workspace_size(const lrmoe_problem* p, lrmoe_compact_mode mod
  *   dW2 [E x F x D] (SwiGLU: dW1 [E x D x 2F]); the scatter output f32 [T x w]
  * (storage dtype where not marked; w = D for SwiGLU experts, F for FC2-only ones). This is
  * the memory the retention quotas decide: the estimate quota admission compares with the
- * available HBM. */
+ * available HBM. Rows of X that the caller restores for the call (lrmoe_restore) are not in
+ * it: T * D of the storage dtype to add, or to take from hbm_avail below. */
 lrmoe_status lrmoe_backward_bytes(const lrmoe_problem* p, int32_t packed, size_t* bytes);
 
 /* Host-only. Quota admission on one GPU: Algorithm 1's forward-time admission (section

@@ -124,22 +124,30 @@ class Problem:
         return self.cseg_off_d if mode == COMPACT_PHYSICAL else self.seg_off_d
 
 
-def backward_bytes(p: Problem, packed=False) -> int:
+def _restored_bytes(T, D, dtype, restored_x):
+    """The rows of X that ``backward`` restores from a Checkpoint, whatever the quotas."""
+    return int(T) * int(D) * (2 if dtype == BF16 else 4) if restored_x else 0
+
+
+def backward_bytes(p: Problem, packed=False, restored_x=False) -> int:
     """Device bytes one physical-compaction backward holds at p's quotas besides its
     inputs: its buffers and its workspace (host-only; the list is in the header,
-    lrmoe_backward_bytes)."""
+    lrmoe_backward_bytes). ``restored_x``: X is a Checkpoint, whose rows the backward holds too."""
     n = ctypes.c_size_t(0)
     _lib.check(library().lrmoe_backward_bytes(ctypes.byref(p.c), int(bool(packed)), ctypes.byref(n)),
                "lrmoe_backward_bytes")
-    return int(n.value)
+    return int(n.value) + _restored_bytes(p.T, p.D, p.dtype, restored_x)
 
 
-def plan_quotas(E, T, K, D, F, swiglu, dtype, seg_off, rhos, hbm_avail, packed=False):
+def plan_quotas(E, T, K, D, F, swiglu, dtype, seg_off, rhos, hbm_avail, packed=False, restored_x=False):
     """Quota admission on one GPU (host-only): the largest candidate ratio in ``rhos``
     (exact decimals such as "0.6", or Fractions) whose backward (buffers and workspace)
     fits ``hbm_avail`` bytes. Returns (index into rhos, quotas [E] int32, bytes); raises InfeasibleQuotaError
-    when none fits (Algorithm 1's "return Infeasible")."""
+    when none fits (Algorithm 1's "return Infeasible"). ``restored_x``: as in backward_bytes."""
     from fractions import Fraction
+    restored = _restored_bytes(T, D, dtype, restored_x)
+    if restored:  # no estimate is 0 bytes
+        hbm_avail = max(int(hbm_avail) - restored, 0)
     fr = [Fraction(r) for r in rhos]
     num = np.array([f.numerator for f in fr], dtype=np.int32)
     den = np.array([f.denominator for f in fr], dtype=np.int32)
@@ -150,7 +158,7 @@ def plan_quotas(E, T, K, D, F, swiglu, dtype, seg_off, rhos, hbm_avail, packed=F
     _lib.check(library().lrmoe_plan_quotas(ctypes.byref(c), num.ctypes.data_as(I32), den.ctypes.data_as(I32),
                                            len(fr), int(bool(packed)), int(hbm_avail), ctypes.byref(chosen),
                                            q.ctypes.data_as(I32), ctypes.byref(nb)), "lrmoe_plan_quotas")
-    return int(chosen.value), q, int(nb.value)
+    return int(chosen.value), q, int(nb.value) + restored
 
 
 CRITERIA = {"lrm": 0, "grad_sqnorm": 1, "grad_abs": 2}
@@ -386,7 +394,7 @@ def backward(p: Problem, *, G, Phi=None, alpha, tok, slot, W2, X=None, H=None, W
 
     Saved activations in 8 bits: ``H`` may be a Checkpoint of the [gate | up] rows (``Phi`` is then left out), or
     ``Phi`` one of the Phi rows of an FC2-only problem, and ``X`` one of the FC1 inputs, which are restored for the
-    call. Physical compaction without ``packed_dlt`` only.
+    call (``backward_bytes`` counts them with ``restored_x``). Physical compaction without ``packed_dlt`` only.
 
     ``bufs`` (a dict, optional) carries preallocated outputs between calls; it is
     filled on first use. With ``overlap_scatter`` the scatter runs on a second stream as
@@ -426,7 +434,8 @@ def backward(p: Problem, *, G, Phi=None, alpha, tok, slot, W2, X=None, H=None, W
         else:
             PhiW = compact_checkpoint(p, sel, saved, alpha, out=b.get("PhiW"), stream=stream)
         if isinstance(X, Checkpoint):
-            X = b["X"] = restore(X, dtype=p.torch_dtype, out=b.get("X"), stream=stream)
+            rows = Checkpoint._of(X.q[:p.T], X.scale[:p.T], 1, p.D)
+            X = b["X"] = restore(rows, dtype=p.torch_dtype, out=b.get("X"), stream=stream)
         b.setdefault("PhiW", PhiW)
         c = {"PhiW": PhiW, "ctok": maps["ctok"], "cslot": maps["cslot"]}
     else:  # the weighted gradient rows; the GEMMs read Phi, X and H in place through sel and ctok
