@@ -377,7 +377,7 @@ def _saved_in_8_bits(p, Phi, H):
         if p.swiglu:
             raise ValueError("a SwiGLU problem takes a checkpoint of [gate | up], not of Phi")
         return Phi
-    if Phi is None:
+    if Phi is None and p.N:  # without pairs there are no rows to give
         raise ValueError("Phi is missing")
     return None
 
