@@ -101,11 +101,17 @@ __global__ __launch_bounds__(topk_threads(Lay::L, N)) void route_topk_kernel(Rou
   blk.finish(a);
 }
 
-// Words of counts (two experts' each) up to which every placing block sums all rows itself; above, a launch scans them
-// first. 4096 x 128 (32 rows of 64 words) 15.1 us with the scan, 12.4 without; 32768 x 128 (256 rows) 18.3 and 16.4;
-// 65536 x 128 (512 rows) 24.9 and 26.6; 16384 x 512 (256 rows of 256 words) 22.4 and 24.6.
-constexpr int kOwnWords = 24 * kRouteThreads;
-bool sums_own(int64_t rows, int64_t E8) { return rows * (E8 / 2) <= kOwnWords; }
+// Whether every placing block sums all rows of counts itself, a word (two experts' 16-bit counts) of every so many rows to a
+// thread, or a launch scans them first. Up to 64 rows, and up to 24 words a thread (22 where a compute unit has more than one
+// block); the loads of a thread's last rows go out together too, one after the other they cost 0.7 us. With the scan and
+// without: 3584 x 1024 (56 rows of 512 words) 25.0 and 24.5 us, 32768 x 128 (256 rows, 16 words a thread) 17.8 and 15.8,
+// 32768 x 192 (256 rows, 24) 20.8 and 20.0, 700000 x 64 (684 rows, 21.4) 147 and 141, 6000000 x 8 (5860 rows, 22.9) 217 and
+// 218; but 40000 x 96 (500 rows, 23.4) 20.4 and 20.7.
+constexpr int kOwnRows = 64, kOneEach = 256;
+bool sums_own(int64_t rows, int64_t E8) {
+  return rows <= kOwnRows || rows * (E8 / 2) <= (rows <= kOneEach ? 24 : 22) * kRouteThreads;
+}
+constexpr int kSumAhead = 8;
 constexpr int kScanExperts = 32;
 constexpr int kScanKept = 8;  // rows of a run: all of them up to 512 chunks
 
@@ -187,13 +193,21 @@ __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs a)
     const uint32_t* h = (const uint32_t*)a.hist + w;
     int s0 = 0, s1 = 0, l0 = 0, l1 = 0;
     if (tid < step * pairs) {
-#pragma unroll 8
-      for (int r = tid / pairs; r < a.rows; r += step) {
-        const uint32_t v = h[(int64_t)r * pairs];
-        const int lo = (int)(v & 0xFFFFu), hi = (int)(v >> 16);
-        s0 += lo, s1 += hi;
-        l0 += r < c ? lo : 0, l1 += r < c ? hi : 0;
-      }
+      auto add = [&](auto whole, int r) {  // eight rows whose loads are in flight together, or the fewer that are left
+        uint32_t v[kSumAhead];
+#pragma unroll
+        for (int q = 0; q < kSumAhead; ++q)
+          v[q] = decltype(whole)::value || r + q * step < a.rows ? h[(int64_t)(r + q * step) * pairs] : 0;
+#pragma unroll
+        for (int q = 0; q < kSumAhead; ++q) {
+          const int lo = (int)(v[q] & 0xFFFFu), hi = (int)(v[q] >> 16);
+          s0 += lo, s1 += hi;
+          l0 += r + q * step < c ? lo : 0, l1 += r + q * step < c ? hi : 0;
+        }
+      };
+      int r = tid / pairs;
+      for (; r + (kSumAhead - 1) * step < a.rows; r += kSumAhead * step) add(std::true_type(), r);
+      if (r < a.rows) add(std::false_type(), r);
       // whole numbers: their order does not matter
       if (2 * w < a.E) atomicAdd(&total[2 * w], s0), atomicAdd(&before[2 * w], l0);
       if (2 * w + 1 < a.E) atomicAdd(&total[2 * w + 1], s1), atomicAdd(&before[2 * w + 1], l1);

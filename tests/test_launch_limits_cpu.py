@@ -145,3 +145,16 @@ say(f"weights {{lib.lrmoe_alpha_grad(problem({T}, {K}, 8, 8, 1000), F, F, F, F, 
             assert status == UNSUPPORTED and not launches, text
         else:
             assert status == "0" and launches and all(at.threads < LIMIT for at in launches), text
+
+
+@pytest.mark.parametrize("T,E,launches", [
+    (128, 1024, 1), (129, 8, 2), (3073, 1024, 2), (4096, 1024, 2), (4096, 777, 2), (4097, 1024, 3), (32768, 128, 2),
+    (65536, 128, 3), (24000, 256, 2), (32768, 256, 3), (40000, 96, 3), (700_000, 64, 2), (4_000_000, 8, 2), (6_000_000, 8, 3)])
+def test_launches_of_routing(shim, T, E, launches):
+    """Top-K alone, with the placing, or with a scan of the counts between: as each was measured to be faster."""
+    code = ROUTER + f"""
+r = ctypes.byref(Router(T={T}, E={E}, K=1, local={E}, dtype=0, renorm=1, scale=1.0))
+say(lib.lrmoe_route(r, F, None, F, F, F, F, F, F, F, F, F, ws, None))
+"""
+    (status, found), = launch_shim.run(shim, code)
+    assert status == "0" and len(found) == launches
