@@ -269,8 +269,6 @@ void by_launches(int64_t n, int32_t parts, int32_t width, F&& f) {
 
 }  // namespace
 
-int64_t checkpoint_units(int64_t n, int32_t parts, int32_t width) { return n * parts * scale_groups(width); }
-
 lrmoe_status launch_checkpoint(int64_t n, int32_t parts, int32_t width, int dtype, const void* rows, int8_t* q,
                                uint16_t* scale, hipStream_t s) {
   by_launches(n, parts, width, [&](const Place& p, unsigned g, int64_t v, int64_t u) {

@@ -187,7 +187,6 @@ lrmoe_status launch_route_bwd(const lrmoe_router* r, bool sigmoid, const void* l
 lrmoe_status launch_alpha_grad(const lrmoe_problem* p, const void* G, const void* Y, const float* alpha,
                                const int32_t* pmap, const uint8_t* keep, float* dalpha, hipStream_t s);
 
-int64_t checkpoint_units(int64_t n, int32_t parts, int32_t width);
 lrmoe_status launch_checkpoint(int64_t n, int32_t parts, int32_t width, int dtype, const void* rows, int8_t* q,
                                uint16_t* scale, hipStream_t s);
 lrmoe_status launch_restore(int64_t n, int32_t parts, int32_t width, const int8_t* q, const uint16_t* scale, int dtype,
