@@ -526,8 +526,9 @@ lrmoe_status lrmoe_scoring_check(const lrmoe_router* r, const lrmoe_scoring* c);
  *             scale * s_k / sum_j s_idx_j     renorm = 1, over the token's chosen experts; no sum underflows
  * The bias is no part of w. Without a bias experts are chosen by their logits (whose order is that of the scores),
  * exactly. Choice scores with a bias, and groups' sums of scores, are f64; choice scores are compared to 42 bits and sums
- * to 44 (what differs by less, relative, may count as equal). A sigmoid logit below -700 counts as -700 in the choice.
- * Deterministic. */
+ * to 44: what differs by less, relative to the scores and to their sum with the bias, may come in either order, which may
+ * be another one for another T, E or K, as softmax sums are. A sigmoid logit below -700 counts as -700 in the choice, and
+ * softmax scores below 2^-1022 are compared to 2^-1064. The same call gives the same result. */
 lrmoe_status lrmoe_route_scored(const lrmoe_router* r, const lrmoe_scoring* c, const void* logits, const float* bias,
                                 const uint8_t* mask, int32_t* idx, float* w, int32_t* counts, int64_t* seg_off,
                                 int32_t* tok, int32_t* slot, float* alpha, int32_t* pmap, void* ws, size_t ws_bytes,

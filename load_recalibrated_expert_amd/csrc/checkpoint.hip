@@ -177,9 +177,11 @@ __global__ __launch_bounds__(kThreads) void pair_score_codes_kernel(const uint4*
 }
 
 // Tokens and pairs in one launch, their blocks mixed evenly: the pairs are bound by arithmetic (two transcendental
-// instructions a value), the tokens' rows by HBM. The 32768-token share (262144 pairs of 768): 104 us with the join behind
-// it, 5.2 TB/s (98 us with squares in f32, which small ones leave; with those and four groups in flight 115 us, and 125 us
-// with tokens and pairs one after the other). Block b is the tokens' i-th if the count floor(b step / 2^32) passes i there.
+// instructions a value), the tokens' rows by HBM. The 32768-token share (262144 pairs of 768): 98 us and 4.8 us of the join
+// behind it, 100 to 104 us a call, 5.2 TB/s (98 us with squares in f32, which small ones leave), against 116 us with tokens
+// and pairs one after the other (20.8 + 99 us); 65536 pairs 31.2 and 33.1 us, in f32 32.1 and 36.3; of 768 without gate and up
+// 262144 55.8 and 67.0. The workspace has to have room for the pairs' norms: one that lrmoe_workspace_size gives has it where
+// something else needs as much. Block b is the tokens' i-th if the count floor(b step / 2^32) passes i there.
 template <bool SWIGLU, bool BF16>
 __global__ __launch_bounds__(kThreads) void norms_kernel(uint64_t step, const uint4* __restrict__ G, int T, int words,
                                                          double* __restrict__ gn, const int8_t* __restrict__ q,
