@@ -582,15 +582,24 @@ def expert_forward_checkpoint(p: Problem, X, tok, alpha, W1, W2, out=None, strea
     Phi = o.get("Phi") if o.get("Phi") is not None else _empty((n, p.F), dt, p.device, stream)
     Y = o.get("Y") if o.get("Y") is not None else _empty((n, p.D), dt, p.device, stream)
     q, s = H._ptrs("H", p.N, 2, p.F, here)
+    _on_current(p, here)
     _lib.check(library().lrmoe_expert_forward_checkpoint(
         ctypes.byref(p.c), _ptr(p.seg_off_d), _ptr(X), _ptr(tok), _ptr(alpha), _ptr(W1), _ptr(W2), q, s, _ptr(Phi),
         _ptr(Y), _stream(stream)), "lrmoe_expert_forward_checkpoint")
     return {"H": Checkpoint._of(H.q[:p.N], H.scale[:p.N], 2, p.F), "Phi": Phi[:p.N], "Y": Y[:p.N]}
 
 
+def _on_current(p, here):
+    """The problem's arrays, workspace and the outputs allocated for it have to be on the current device."""
+    if p.seg_off_d.get_device() != here:
+        raise ValueError(f"the problem is on {p.seg_off_d.device}, which is not the current device")
+
+
 def _saved(p, H, here):
     """Pointers of the pairs' saved rows in 8 bits: [gate | up], or Phi of FC2-only problems."""
-    return H._ptrs("H", p.N, 2 if p.swiglu else 1, p.F, here)
+    ptrs = H._ptrs("H", p.N, 2 if p.swiglu else 1, p.F, here)
+    _on_current(p, here)
+    return ptrs
 
 
 def score_checkpoint(p: Problem, G, H: Checkpoint, alpha, tok, R=None, stream=None):
