@@ -552,7 +552,8 @@ lrmoe_status lrmoe_route_bwd_scored(const lrmoe_router* r, const lrmoe_scoring* 
                                     const float* norm, const float* gloss, void* dlogits, lrmoe_stream_t stream);
 
 /* out[e] = bias[e] + rate * sign(mean of counts - counts[e])   f32 [E]; counts [E] int32 as lrmoe_route_scored gives
- * them (summed over the GPUs, where each routes tokens of its own), compared as whole numbers. out may be bias. */
+ * them (summed over the GPUs, where each routes tokens of its own), compared as whole numbers. out may be bias, or
+ * share elements with it. */
 lrmoe_status lrmoe_bias_update(const lrmoe_router* r, const int32_t* counts, float rate, const float* bias, float* out,
                                lrmoe_stream_t stream);
 

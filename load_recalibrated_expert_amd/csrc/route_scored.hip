@@ -251,6 +251,7 @@ __global__ __launch_bounds__(1024) void bias_update_kernel(int E, const int32_t*
   __shared__ int64_t part[1024 / kWave];
   const int e = threadIdx.x, lane = e & (kWave - 1);
   const int64_t n = e < E ? counts[e] : 0;
+  const float b = e < E ? bias[e] : 0.0f;  // all are read before any is written: out may share elements with bias
   int64_t sum = n;
 #pragma unroll
   for (int o = 1; o < kWave; o <<= 1) sum += __shfl_xor(sum, o, kWave);
@@ -259,7 +260,7 @@ __global__ __launch_bounds__(1024) void bias_update_kernel(int E, const int32_t*
   sum = 0;
 #pragma unroll
   for (int q = 0; q < 1024 / kWave; ++q) sum += part[q];
-  if (e < E) out[e] = bias[e] + (sum > E * n ? rate : sum < E * n ? -rate : 0.0f);
+  if (e < E) out[e] = b + (sum > E * n ? rate : sum < E * n ? -rate : 0.0f);
 }
 
 // Layouts with groups, whose rows of LDS leave room for a block of eight wavefronts. Eight lanes to a token up to 192

@@ -73,3 +73,20 @@ def test_balance_gradient_is_of_the_counts_differences(E, dt, counts, kind):
     assert np.all(got[~live] == 0)
     worst = float(np.max((np.abs(got - want) / err)[live]))
     assert worst <= 1
+
+
+@pytest.mark.parametrize("shift", [1, 63, 64, 65, 500])
+@pytest.mark.parametrize("ahead", [True, False])
+def test_bias_update_into_a_part_of_the_bias(ahead, shift):
+    """``out`` and ``bias`` as two rows of one buffer that share elements: every bias is read before any is written."""
+    E = 1024
+    rng = np.random.default_rng(shift)
+    buf = (rng.standard_normal(E + shift) * 0.1).astype(np.float32)
+    counts = rng.integers(0, 50, E).astype(np.int32)
+    t = torch.from_numpy(buf).to(DEV)
+    low, high = t[:E], t[shift:shift + E]
+    out, bias = (high, low) if ahead else (low, high)
+    ref = so.bias_update(bias.cpu().numpy(), counts, 1e-3)
+    r = lr.Router(T=4, E=E, K=1, score="sigmoid", device=DEV)
+    log(f"bias update, {shift} apart")
+    assert np.array_equal(lr.bias_update(r, bias, torch.from_numpy(counts).to(DEV), 1e-3, out=out).cpu().numpy(), ref)
